@@ -177,7 +177,7 @@ def quantise(x):
     b = x.unflatten(-1, (-1, 32))
     a = b.abs().amax(-1, keepdim=True)
     e = (torch.frexp(a)[1] - 3).clamp(-127, 127)
-    e = torch.where(a == 0, -127, e)
+    e = torch.where(a == 0, 0, e)
     y = torch.ldexp(torch.ldexp(b.abs(), -e // 2), -e - (-e // 2))
     # the values between 0, .5, 1, 1.5, 2, 3, 4, 6: a tie goes to the even code
     code = ((y > 0.25).to(torch.uint8) + (y >= 0.75) + (y > 1.25) + (y >= 1.75) + (y > 2.5) + (y >= 3.5) + (y > 5.0))
