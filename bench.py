@@ -109,12 +109,13 @@ def read_peaks_file():
 
 def kernel_sources_sha():
     """sha256 prefix of the layer's device-code sources (the C-ABI's host code,
-    the bench's copy/read kernels and the expert-centric comparison layer are
-    left out)."""
+    the bench's copy/read kernels, the expert-centric comparison layer and the
+    cache of keys and values are left out)."""
     h = hashlib.sha256()
     for f in sorted(os.listdir(os.path.join(ROOT, "moe_decode_gate_gb300", "csrc"))):
         if not f.endswith((".cu", ".cuh", ".h")) or f in ("wd_capi.cu", "wd_bench.cu",
-                                                          "wd_expert_centric.cu"):
+                                                          "wd_expert_centric.cu") or \
+                f.startswith("wd_kv"):
             continue
         with open(os.path.join(ROOT, "moe_decode_gate_gb300", "csrc", f), "rb") as fh:
             h.update(fh.read())

@@ -99,7 +99,9 @@ typedef enum wd_status {
   WD_ERR_WORKSPACE_TOO_SMALL = 3, /* workspace_bytes < wd_moe_workspace_size(...) */
   WD_ERR_CUDA = 4,                /* a CUDA runtime call or launch failed        */
   WD_ERR_BAD_EXPERT_ID = 5,       /* reported by wd_moe_read_error_flag only     */
-  WD_ERR_PIPELINE_TIMEOUT = 6     /* reported by wd_moe_read_error_flag only     */
+  WD_ERR_PIPELINE_TIMEOUT = 6,    /* reported by the read_error_flag calls only  */
+  WD_ERR_BAD_INDEX = 7,           /* reported by wd_kv_read_error_flag only      */
+  WD_ERR_OUT_OF_PAGES = 8         /* reported by wd_kv_read_error_flag only      */
 } wd_status;
 
 /* Human-readable name of a status code (static string, never NULL). */

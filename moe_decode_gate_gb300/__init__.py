@@ -9,6 +9,9 @@ each routed row is read and dequantised once for all of its tokens:
 ``moe_gate_up_mma`` (tensor-core products, one CTA per SM), then
 ``moe_h_encode`` and ``moe_down_dimblock`` (one CTA per 16 output dims over
 every routed expert); ``wd_moe_describe_plan`` names the kernels a shape gets.
+Next to the layer, ``KVCache`` (include/wd_kv.h) is the attention half of a
+decode step: a paged cache of keys and values in MXFP4, the attention that reads
+it, and forking, freeing and compacting its pages.
 This package is the thin Python binding over that library; PyTorch only
 supplies device memory and streams.
 
@@ -45,5 +48,12 @@ from ._native import (  # noqa: F401
     wd_moe_workspace_init,
     wd_moe_workspace_size,
     wd_status_string,
+)
+from .kv_cache import (  # noqa: F401
+    KV_FLAG_BAD_INDEX,
+    KV_FLAG_NO_PAGES,
+    KV_FLAG_TIMEOUT,
+    KVCache,
+    wd_kv_page_bytes,
 )
 from .layer import MoEDecodeLayer  # noqa: F401

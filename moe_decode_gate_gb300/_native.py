@@ -1,4 +1,5 @@
-"""ctypes binding of the C-ABI in include/wd_moe.h and include/wd_bench.h.
+"""ctypes binding of the C-ABI in include/wd_moe.h, include/wd_kv.h and include/wd_bench.h
+(the calls of wd_kv.h are wrapped by kv_cache.py).
 
 Argument marshalling only: shapes are read off the tensors, pointers and the
 current CUDA stream are passed through, and a non-OK status raises WdError.
@@ -20,13 +21,14 @@ _LIB = None
 WD_OK = 0
 STATUS_NAMES = {0: "WD_OK", 1: "WD_ERR_INVALID_ARG", 2: "WD_ERR_UNSUPPORTED_SHAPE",
                 3: "WD_ERR_WORKSPACE_TOO_SMALL", 4: "WD_ERR_CUDA", 5: "WD_ERR_BAD_EXPERT_ID",
-                6: "WD_ERR_PIPELINE_TIMEOUT"}
+                6: "WD_ERR_PIPELINE_TIMEOUT", 7: "WD_ERR_BAD_INDEX", 8: "WD_ERR_OUT_OF_PAGES"}
 # bits of the workspace error flag (wd_moe_read_error_flag)
 FLAG_BAD_EXPERT_ID = 1
 FLAG_PIPELINE_TIMEOUT = 2
 
 # (name, restype, argtypes) for every symbol the headers declare
 _P, _I, _SZ, _U32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint32
+_I64 = ctypes.c_int64
 SIGNATURES = {
     "wd_status_string": (ctypes.c_char_p, [_I]),
     "wd_moe_workspace_size": (_SZ, [_I, _I, _I]),
@@ -44,6 +46,17 @@ SIGNATURES = {
     "wd_moe_set_plan": (_I, [ctypes.c_char_p]),
     "wd_last_error_string": (ctypes.c_char_p, []),
     "wd_moe_describe_plan": (_I, [ctypes.c_int] * 5 + [ctypes.c_char_p, ctypes.c_size_t]),
+    "wd_kv_page_bytes": (_SZ, [_I, _I, _I, _I]),
+    "wd_kv_workspace_size": (_SZ, [_P]),
+    "wd_kv_workspace_init": (_I, [_P, _P]),
+    "wd_kv_read_error_flag": (_I, [_P, _P, ctypes.POINTER(_I)]),
+    "wd_kv_reserve": (_I, [_P, _P, _P, _I, _P, _P]),
+    "wd_kv_append": (_I, [_P, _I, _P, _P, _I, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _I, _I, _P]),
+    "wd_kv_attention": (_I, [_P, _I, _P, _I, _I64, _I64, _I, _P, _P, _P, _P, _I, _I, _I,
+                             ctypes.c_float, _I, _P]),
+    "wd_kv_fork": (_I, [_P, _P, _P, _I, _P, _P]),
+    "wd_kv_free": (_I, [_P, _P, _I, _P]),
+    "wd_kv_compact": (_I, [_P, _P, _P, _P, _P]),
     "wd_bench_copy": (_I, [_P, _P, _SZ, _I, _P]),
     "wd_bench_read": (_I, [_P, _SZ, _P, _I, _P]),
     "wd_bench_fill": (_I, [_P, _SZ, _U32, _I, _P]),

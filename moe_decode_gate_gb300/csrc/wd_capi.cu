@@ -302,6 +302,8 @@ const char* wd_status_string(wd_status s) {
     case WD_ERR_CUDA: return "WD_ERR_CUDA";
     case WD_ERR_BAD_EXPERT_ID: return "WD_ERR_BAD_EXPERT_ID";
     case WD_ERR_PIPELINE_TIMEOUT: return "WD_ERR_PIPELINE_TIMEOUT";
+    case WD_ERR_BAD_INDEX: return "WD_ERR_BAD_INDEX";
+    case WD_ERR_OUT_OF_PAGES: return "WD_ERR_OUT_OF_PAGES";
   }
   return "WD_ERR_UNKNOWN";
 }

@@ -1,0 +1,450 @@
+// wd_kv_pages.cu - handing out, forking, freeing and compacting the pages of
+// the 4-bit cache (declared in include/wd_kv.h).
+//
+// A page is free when refs[page] == 0; there is no free list to keep in order,
+// and the lowest free pages go first, so results do not depend on the timing of
+// anything.  Each operation is a plan (who gets which page: scans over refs and
+// over the requests) and the work that it describes (table rows, counts, and the
+// pages' bytes, which are what it costs: a page of 48 layers is over a megabyte).
+// Counts change by integer atomics, whose order does not show.
+#include "wd_kv.cuh"
+
+namespace wd {
+namespace {
+
+constexpr int kPlan = 1024;  // threads of the planning CTA
+constexpr int kCopy = 256;   // threads of a copying CTA
+
+// Exclusive scan of one int per thread of a kPlan-thread CTA; `total` is the sum.
+__device__ __forceinline__ int block_scan(int v, int& total, int* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int t = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+    if (lane >= off) incl += t;
+  }
+  __syncthreads();  // the sums of the scan before have been read
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    const int mine = warp_sums[lane];
+    int s = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int t = __shfl_up_sync(0xFFFFFFFFu, s, off);
+      if (lane >= off) s += t;
+    }
+    warp_sums[lane] = s - mine;
+    if (lane == 31) warp_sums[32] = s;
+  }
+  __syncthreads();
+  total = warp_sums[32];
+  return warp_sums[warp] + incl - v;
+}
+
+// Calls take(rank, page) for the lowest free pages, rank 0 first, until
+// `wanted` are found or the pool ends; returns how many there are of them.
+// All threads of the CTA.
+template <typename F>
+__device__ __forceinline__ int find_free(const KvView& v, int wanted, int* warp_sums, F take) {
+  constexpr int kEach = 16;
+  int found = 0;
+  for (int base = 0; base < v.num_pages && found < wanted; base += kPlan * kEach) {
+    const int at = base + threadIdx.x * kEach;
+    uint32_t free_bits = 0;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      if (at + k < v.num_pages && v.refs[at + k] == 0) free_bits |= 1u << k;
+    int total;
+    int rank = found + block_scan(__popc(free_bits), total, warp_sums);
+    while (free_bits) {
+      const int k = __ffs(free_bits) - 1;
+      free_bits &= free_bits - 1;
+      if (rank < wanted) take(rank, at + k);
+      ++rank;
+    }
+    found += total;
+  }
+  return min(found, wanted);
+}
+
+// Marks, for each slot that the call names, the first request that names it.
+__device__ __forceinline__ void mark_owners(const KvView& v, const int32_t* slots_of, int n,
+                                            int32_t* owner) {
+  for (int i = threadIdx.x; i < n; i += kPlan) {
+    const int s = slots_of ? slots_of[i] : i;
+    if ((unsigned)s < (unsigned)v.slots) __stcg(owner + s, 0x7FFFFFFF);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kPlan) {
+    const int s = slots_of ? slots_of[i] : i;
+    if ((unsigned)s < (unsigned)v.slots) atomicMin(owner + s, i);
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------- reserve ---
+
+__global__ void __launch_bounds__(kPlan)
+    kv_reserve(const KvView v, const KvScratch w, const int32_t* seqs, const int32_t* counts,
+               int n, int32_t* ok) {
+  __shared__ int warp_sums[33];
+  __shared__ int wanted_sh;
+  int32_t* begin = w.plan;              // pages that the requests before i ask for
+  int32_t* need = w.plan + v.slots;     // pages of request i, -1: refused
+  mark_owners(v, seqs, n, w.owner);
+  int before = 0;
+  for (int base = 0; base < n; base += kPlan) {
+    const int i = base + threadIdx.x;
+    int pages = -1;
+    if (i < n) {
+      const int s = seqs ? seqs[i] : i;
+      const int add = counts[i];
+      if ((unsigned)s < (unsigned)v.slots && add >= 0 && __ldcg(w.owner + s) == i) {
+        const long long len = kv_length(v, s);
+        const long long most = (long long)v.columns << v.page_shift;
+        if (len + add <= most)
+          pages = (int)(((len + add + v.page_size - 1) >> v.page_shift) -
+                        ((len + v.page_size - 1) >> v.page_shift));
+      } else {
+        atomicOr(v.flag, WD_KV_FLAG_BAD_INDEX);
+      }
+    }
+    int total;
+    const int excl = block_scan(pages > 0 ? pages : 0, total, warp_sums);
+    if (i < n) {
+      begin[i] = before + excl;
+      need[i] = pages;
+    }
+    before += total;
+  }
+  if (threadIdx.x == 0) wanted_sh = before;
+  __syncthreads();
+  const int wanted = wanted_sh;
+  // the pages, in rank order: list_a[rank]
+  const int found = find_free(v, wanted, warp_sums,
+                              [&](int rank, int page) { __stcg(w.list_a + rank, page); });
+  __syncthreads();
+  for (int i = threadIdx.x >> 5; i < n; i += kPlan / 32) {  // a warp to a request
+    const int lane = threadIdx.x & 31;
+    const int s = seqs ? seqs[i] : i;
+    const int pages = need[i];
+    const bool served = pages == 0 || (pages > 0 && begin[i] + pages <= found);
+    if (served) {
+      const int len = kv_length(v, s);
+      const int have = (len + v.page_size - 1) >> v.page_shift;
+      for (int k = lane; k < pages; k += 32) {
+        const int page = __ldcg(w.list_a + begin[i] + k);
+        v.table[(long long)s * v.columns + have + k] = page;
+        v.refs[page] = 1;
+      }
+      __syncwarp();
+      if (lane == 0) v.lengths[s] = len + counts[i];
+    } else if (lane == 0) {
+      atomicOr(v.flag, pages > 0 ? WD_KV_FLAG_NO_PAGES : WD_KV_FLAG_BAD_INDEX);
+    }
+    if (ok && lane == 0) ok[i] = served ? 1 : 0;
+  }
+}
+
+// ---------------------------------------------------------------- fork ---
+
+// The plan of a fork, per request: what becomes of the slot.
+struct ForkPlan {
+  int32_t* whole;  // pages shared with the source, -1: the slot stays as it is
+  int32_t* page;   // the new last page, -1: none
+  int32_t* from;   // the page that it is a copy of
+  int32_t* old;    // pages that the slot held
+  int32_t* length; // its new length
+};
+__device__ __host__ __forceinline__ ForkPlan fork_plan(const KvScratch& w, int slots) {
+  const long long n = slots;
+  return ForkPlan{w.plan, w.plan + n, w.plan + 2 * n, w.plan + 3 * n, w.plan + 4 * n};
+}
+
+__global__ void __launch_bounds__(kPlan)
+    kv_fork_plan(const KvView v, const KvScratch w, const int32_t* src, const int32_t* dst, int n,
+                 int32_t* ok) {
+  __shared__ int warp_sums[33];
+  const ForkPlan p = fork_plan(w, v.slots);
+  mark_owners(v, dst, n, w.owner);
+  int before = 0;
+  for (int base = 0; base < n; base += kPlan) {
+    const int i = base + threadIdx.x;
+    bool copy = false;
+    if (i < n) {
+      const int d = dst[i], s = src ? src[i] : -1;
+      int whole = -1, from = -1, old = 0, len = 0;
+      if ((unsigned)d < (unsigned)v.slots && s >= -1 && s < v.slots && __ldcg(w.owner + d) == i) {
+        old = (kv_length(v, d) + v.page_size - 1) >> v.page_shift;
+        len = s < 0 ? 0 : kv_length(v, s);
+        if (s == d) {
+          whole = -2;  // stays, but not refused
+        } else {
+          whole = len >> v.page_shift;
+          copy = (len & (v.page_size - 1)) != 0;
+          if (copy) from = kv_page(v, s, whole);
+        }
+      } else {
+        atomicOr(v.flag, WD_KV_FLAG_BAD_INDEX);
+      }
+      p.whole[i] = whole;
+      p.from[i] = from;
+      p.old[i] = old;
+      p.length[i] = len;
+    }
+    int total;
+    const int rank = before + block_scan(copy ? 1 : 0, total, warp_sums);
+    if (i < n) p.page[i] = copy ? rank : -1;
+    before += total;
+  }
+  const int found = find_free(v, before, warp_sums,
+                              [&](int rank, int page) { __stcg(w.list_a + rank, page); });
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kPlan) {
+    const int rank = p.page[i];
+    if (rank >= 0) {
+      const bool have = rank < found;
+      p.page[i] = have ? __ldcg(w.list_a + rank) : -1;
+      if (!have) {
+        p.whole[i] = -1;
+        p.from[i] = -1;
+        atomicOr(v.flag, WD_KV_FLAG_NO_PAGES);
+      }
+    }
+    if (ok) ok[i] = p.whole[i] != -1 ? 1 : 0;
+  }
+}
+
+// `bytes` (a multiple of 16) from src to dst by the threads of a CTA, four
+// 16-byte loads in flight each.
+__device__ __forceinline__ void copy_bytes(uint8_t* dst, const uint8_t* src, int bytes) {
+  const uint4* in = reinterpret_cast<const uint4*>(src);
+  uint4* out = reinterpret_cast<uint4*>(dst);
+  const int n = bytes >> 4;
+  int i = threadIdx.x;
+  for (; i + 3 * kCopy < n; i += 4 * kCopy) {
+    const uint4 a = in[i], b = in[i + kCopy], c = in[i + 2 * kCopy], d = in[i + 3 * kCopy];
+    out[i] = a;
+    out[i + kCopy] = b;
+    out[i + 2 * kCopy] = c;
+    out[i + 3 * kCopy] = d;
+  }
+  for (; i < n; i += kCopy) out[i] = in[i];
+}
+
+constexpr int kPiece = 4 * kCopy * 16;  // bytes that a CTA copies at a time
+
+// Stage the new table rows (the table itself is still being read), change the
+// counts, and copy the partly filled pages.
+__global__ void __launch_bounds__(kCopy) kv_fork_work(const KvView v, const KvScratch w,
+                                                      const int32_t* src, const int32_t* dst,
+                                                      int n) {
+  const ForkPlan p = fork_plan(w, v.slots);
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const int whole = p.whole[i];
+    if (whole < 0) continue;
+    const int d = dst[i], s = src ? src[i] : -1, page = p.page[i], old = p.old[i];
+    const int most = max(old, whole + 1);
+    for (int j = threadIdx.x; j < v.columns && j < most; j += kCopy) {
+      int next = -1;
+      if (j < whole) {
+        next = v.table[(long long)s * v.columns + j];
+        if ((unsigned)next < (unsigned)v.num_pages)
+          atomicAdd(v.refs + next, 1);
+        else
+          atomicOr(v.flag, WD_KV_FLAG_BAD_INDEX);
+      } else if (j == whole && page >= 0) {
+        next = page;
+        atomicAdd(v.refs + next, 1);
+      }
+      if (j < old) {
+        const int gone = v.table[(long long)d * v.columns + j];
+        if ((unsigned)gone < (unsigned)v.num_pages)
+          atomicSub(v.refs + gone, 1);
+        else
+          atomicOr(v.flag, WD_KV_FLAG_BAD_INDEX);
+      }
+      w.rows[(long long)i * v.columns + j] = next;
+    }
+  }
+  const int pieces = (int)((v.page_bytes + kPiece - 1) / kPiece);
+  for (long long t = blockIdx.x; t < (long long)n * pieces; t += gridDim.x) {
+    const int i = (int)(t / pieces), piece = (int)(t % pieces);
+    if (p.whole[i] < 0 || p.page[i] < 0) continue;
+    const long long off = (long long)piece * kPiece;
+    copy_bytes(v.pool + p.page[i] * v.page_bytes + off, v.pool + p.from[i] * v.page_bytes + off,
+               (int)min((long long)kPiece, v.page_bytes - off));
+  }
+}
+
+// The rows and lengths, now that nothing reads the old ones any more.
+__global__ void __launch_bounds__(kCopy) kv_fork_rows(const KvView v, const KvScratch w,
+                                                      const int32_t* dst, int n) {
+  const ForkPlan p = fork_plan(w, v.slots);
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const int whole = p.whole[i];
+    if (whole < 0) continue;
+    const int d = dst[i];
+    const int most = min(v.columns, max(p.old[i], whole + 1));
+    for (int j = threadIdx.x; j < most; j += kCopy)
+      v.table[(long long)d * v.columns + j] = w.rows[(long long)i * v.columns + j];
+    if (threadIdx.x == 0) v.lengths[d] = p.length[i];
+  }
+}
+
+// ------------------------------------------------------------- compact ---
+
+// Live pages of each chunk of kKvChunkPages pages.
+__global__ void __launch_bounds__(kPlan) kv_compact_count(const KvView v, const KvScratch w) {
+  __shared__ int sums[32];
+  const int base = blockIdx.x * kKvChunkPages;
+  int live = 0;
+#pragma unroll
+  for (int k = 0; k < kKvChunkPages / kPlan; ++k) {
+    const int at = base + k * kPlan + threadIdx.x;
+    if (at < v.num_pages && v.refs[at] > 0) ++live;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) live += __shfl_xor_sync(0xFFFFFFFFu, live, off);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = live;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int t = 0;
+    for (int k = 0; k < 32; ++k) t += sums[k];
+    w.chunk[blockIdx.x] = t;
+  }
+}
+
+// list_a: where each page goes, -1 for a free one, -2 - k for the k-th mover;
+// list_b: the movers; list_c: the holes that they move to.  chunk[chunks] =
+// live pages, chunk[chunks + 1] = movers.
+__global__ void __launch_bounds__(kPlan)
+    kv_compact_plan(const KvView v, const KvScratch w, int chunks) {
+  __shared__ int warp_sums[33];
+  int live_total = 0, live_before = 0, live_to_split = 0, total;
+  for (int base = 0; base < chunks; base += kPlan) {
+    const int k = base + threadIdx.x;
+    const int c = k < chunks ? w.chunk[k] : 0;
+    block_scan(c, total, warp_sums);
+    live_total += total;
+    block_scan(k < (int)blockIdx.x ? c : 0, total, warp_sums);
+    live_before += total;
+  }
+  const int split = live_total / kKvChunkPages;  // the chunk that page live_total is in
+  for (int base = 0; base < split; base += kPlan) {
+    const int k = base + threadIdx.x;
+    block_scan(k < split ? w.chunk[k] : 0, total, warp_sums);
+    live_to_split += total;
+  }
+  int in_split = 0;
+  for (int at = split * kKvChunkPages + threadIdx.x; at < live_total; at += kPlan)
+    in_split += v.refs[at] > 0 ? 1 : 0;
+  block_scan(in_split, total, warp_sums);
+  const int below = live_to_split + total;  // live pages below live_total
+  constexpr int kEach = kKvChunkPages / kPlan;
+  const int at = blockIdx.x * kKvChunkPages + threadIdx.x * kEach;
+  bool live[kEach];
+  int mine = 0;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    live[k] = at + k < v.num_pages && v.refs[at + k] > 0;
+    mine += live[k] ? 1 : 0;
+  }
+  int rank = live_before + block_scan(mine, total, warp_sums);  // live pages before `at`
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int page = at + k;
+    if (page < v.num_pages) {
+      int to = -1;
+      if (live[k]) {
+        to = page;
+        if (page >= live_total) {
+          w.list_b[rank - below] = page;
+          to = -2 - (rank - below);
+        }
+      } else if (page < live_total) {
+        w.list_c[page - rank] = page;
+      }
+      w.list_a[page] = to;
+    }
+    rank += live[k] ? 1 : 0;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    w.chunk[chunks] = live_total;
+    w.chunk[chunks + 1] = live_total - below;
+  }
+}
+
+// Move the pages and rewrite the bookkeeping.  Movers lie at or above the live
+// count and holes below it, so no page is read after it was written.
+__global__ void __launch_bounds__(kCopy)
+    kv_compact_work(const KvView v, const KvScratch w, int chunks, int32_t* table_out,
+                    int32_t* refs_out, int32_t* page_map) {
+  const int movers = w.chunk[chunks + 1];
+  const long long threads = (long long)gridDim.x * kCopy;
+  const long long me = (long long)blockIdx.x * kCopy + threadIdx.x;
+  for (long long e = me; e < (long long)v.slots * v.columns; e += threads) {
+    const int page = v.table[e];
+    int to = -1;
+    if (page >= 0) {
+      if (page < v.num_pages) {
+        to = w.list_a[page];
+        if (to <= -2) to = w.list_c[-2 - to];
+      } else {
+        atomicOr(v.flag, WD_KV_FLAG_BAD_INDEX);
+      }
+    }
+    table_out[e] = to;
+  }
+  for (long long page = me; page < v.num_pages; page += threads) {
+    const int to = w.list_a[page];
+    if (to == page) {
+      if (refs_out != v.refs) refs_out[page] = v.refs[page];
+    } else if (to <= -2) {  // a mover: its count goes with it
+      const int hole = w.list_c[-2 - to];
+      refs_out[hole] = v.refs[page];
+      refs_out[page] = 0;
+    } else if (page >= w.chunk[chunks]) {  // free, and no mover's place
+      refs_out[page] = 0;
+    }
+    if (page_map) page_map[page] = to <= -2 ? w.list_c[-2 - to] : to;
+  }
+  const int pieces = (int)((v.page_bytes + kPiece - 1) / kPiece);
+  for (long long t = blockIdx.x; t < (long long)movers * pieces; t += gridDim.x) {
+    const int k = (int)(t / pieces), piece = (int)(t % pieces);
+    const long long off = (long long)piece * kPiece;
+    copy_bytes(v.pool + w.list_c[k] * v.page_bytes + off, v.pool + w.list_b[k] * v.page_bytes + off,
+               (int)min((long long)kPiece, v.page_bytes - off));
+  }
+}
+
+constexpr int kWorkCtas = 152 * 8;
+
+}  // namespace
+
+cudaError_t launch_kv_reserve(const KvView& v, const KvScratch& w, const int32_t* seqs,
+                              const int32_t* counts, int n, int32_t* ok, cudaStream_t s) {
+  kv_reserve<<<1, kPlan, 0, s>>>(v, w, seqs, counts, n, ok);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_fork(const KvView& v, const KvScratch& w, const int32_t* src,
+                           const int32_t* dst, int n, int32_t* ok, cudaStream_t s) {
+  kv_fork_plan<<<1, kPlan, 0, s>>>(v, w, src, dst, n, ok);
+  kv_fork_work<<<kWorkCtas, kCopy, 0, s>>>(v, w, src, dst, n);
+  kv_fork_rows<<<n < 1024 ? n : 1024, kCopy, 0, s>>>(v, w, dst, n);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_compact(const KvView& v, const KvScratch& w, int32_t* table_out,
+                              int32_t* refs_out, int32_t* page_map, cudaStream_t s) {
+  const int chunks = (v.num_pages + kKvChunkPages - 1) / kKvChunkPages;
+  kv_compact_count<<<chunks, kPlan, 0, s>>>(v, w);
+  kv_compact_plan<<<chunks, kPlan, 0, s>>>(v, w, chunks);
+  kv_compact_work<<<kWorkCtas, kCopy, 0, s>>>(v, w, chunks, table_out, refs_out, page_map);
+  return cudaGetLastError();
+}
+
+}  // namespace wd
