@@ -33,7 +33,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 32;     // keys of a warp's step: two groups
-constexpr int kPad = 36;      // floats to a row of the merge buffer
+constexpr int kCached = 256;  // entries whose slot and length are kept in shared memory
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 template <int D, int NT>
@@ -43,15 +43,24 @@ struct Shape {
   static constexpr int kStageBytes = 2 * G::kBytes;
   static constexpr int kStages = D == 64 ? 4 : 2;
   static constexpr int kCtasPerSm = D <= 128 && NT == 1 ? 2 : 1;
+  // the warps' outputs are joined through shared memory, in one round where it has room for all
+  static constexpr int kRounds = D == 256 ? 2 * NT : D == 128 && NT == 4 ? 2 : 1;
+  static constexpr int kRoundBlocks = G::kBlocks / kRounds;
+  static constexpr int kMergeRow = 32 * kRoundBlocks + 4;  // floats
   // shared memory, in bytes from its start
   static constexpr int kRing = 0;
   static constexpr int kQ = kRing + kWarps * kStages * kStageBytes;  // fragments [NT][blocks][32] uint4
-  static constexpr int kMerge = kQ + NT * G::kBlocks * 512;          // float [kWarps][kRows][kPad]
-  static constexpr int kStats = kMerge + kWarps * kRows * kPad * 4;  // float m, l [kWarps][kRows] each
-  static constexpr int kRowInfo = kStats + 2 * kWarps * kRows * 4;   // factor, lo, hi, max, sum [kRows]
-  static constexpr int kBars = kRowInfo + 5 * kRows * 4;             // uint64 [kWarps][kStages]
-  static constexpr int kScan = kBars + kWarps * kStages * 8;         // long long [16]
-  static constexpr int kPrefix = kScan + 16 * 8;                     // long long [entries + 1]
+  static constexpr int kMerge = kQ + NT * G::kBlocks * 512;  // float [kWarps][kRows][kMergeRow]
+  static constexpr int kStats = kMerge + kWarps * kRows * kMergeRow * 4;  // float m, l [kWarps][kRows]
+  static constexpr int kRowInfo = kStats + 2 * kWarps * kRows * 4;   // factor, lo, hi [kRows]
+  static constexpr int kBars = kRowInfo + 3 * kRows * 4 + (kRows * 4) % 8;  // uint64 [kWarps][kStages]
+  static constexpr int kScan = kBars + kWarps * kStages * 8;         // long long [2][kWarps]
+  static constexpr int kPrefix = kScan + 2 * kWarps * 8;             // long long [entries + 1]
+  static constexpr int shared_bytes(int entries) {  // ... and int2 [min(entries, kCached)]
+    return kPrefix + 8 * (entries + 1) + 8 * (entries < kCached ? entries : kCached);
+  }
+  static_assert(kWarps * kMergeRow >= kKvMaxCtas, "the last join's factors fit the merge buffer");
+  static_assert(kPrefix + 8 * (WD_KV_MAX_ENTRIES + 1) + 8 * kCached <= 227 * 1024, "shared memory");
 };
 
 // Four E2M1 pairs (the bytes of w, low half first) -> four f16x2, exactly.
@@ -124,13 +133,6 @@ __device__ __forceinline__ Words<(CB + 3) / 4> lds_scales(const uint8_t* p) {
 struct Entry {
   int slot, len, first, n;
 };
-__device__ __forceinline__ Entry load_entry(const KvAttentionArgs& a, int b) {
-  Entry e;
-  e.slot = kv_slot(a.cache, a.batch, b);
-  e.len = e.slot < 0 ? 0 : kv_length(a.cache, e.slot);
-  kv_tokens(a.cache, a.batch, b, e.first, e.n);
-  return e;
-}
 
 // The steps of keys that a tile of query rows sees: at least one, so that a tile that sees
 // nothing is written too.
@@ -140,8 +142,11 @@ struct Span {
 };
 template <int kRows>
 __device__ __forceinline__ Span tile_span(const Entry& e, int tile, int group, int window) {
-  const int i0 = tile * kRows / group;
-  const int i1 = min(e.n - 1, (tile * kRows + kRows - 1) / group);
+  int i0 = 0, i1 = e.n - 1;
+  if (e.n > 1) {
+    i0 = tile * kRows / group;
+    i1 = min(i1, (tile * kRows + kRows - 1) / group);
+  }
   const int hi = e.len - e.n + i1;
   const int lo = window > 0 ? max(0, e.len - e.n + i0 - window + 1) : 0;
   Span s;
@@ -150,36 +155,84 @@ __device__ __forceinline__ Span tile_span(const Entry& e, int tile, int group, i
   s.end = hi + 1;
   return s;
 }
+template <int kRows>
+__device__ __forceinline__ int tiles_of(const Entry& e, int group) {
+  return (e.n * group + kRows - 1) / kRows;
+}
 
-// A place in the order of all steps.
+// All steps of the call in a row: entries, their tiles, the key heads, the item's steps (rounded
+// up to a multiple of `pad`).
+struct Order {
+  const long long* prefix;  // steps of the entries before each entry
+  const int2* cached;       // slot and length of the first kCached entries
+  int pad, group;
+};
+__device__ __forceinline__ Entry load_entry(const KvAttentionArgs& a, int b) {
+  Entry e;
+  e.slot = kv_slot(a.cache, a.batch, b);
+  e.len = e.slot < 0 ? 0 : kv_length(a.cache, e.slot);
+  kv_tokens(a.cache, a.batch, b, e.first, e.n);
+  return e;
+}
 struct Place {
   int entry, tile, head, step;
   Span span;
+  int padded;  // steps with the padding
 };
 template <int kRows>
-__device__ __forceinline__ Place locate(const KvAttentionArgs& a, const long long* prefix,
-                                        long long p, int group, Entry& e) {
+__device__ __forceinline__ Place locate(const KvAttentionArgs& a, const Order& o, long long p,
+                                        Entry& e) {
   int lo = 0, hi = a.batch.entries;  // the last entry whose steps begin at or before p
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (prefix[mid] <= p) lo = mid; else hi = mid;
+    if (o.prefix[mid] <= p) lo = mid; else hi = mid;
   }
   Place at;
   at.entry = lo;
-  e = load_entry(a, lo);
-  long long rest = p - prefix[lo];
+  if (lo < kCached) {
+    const int2 c = o.cached[lo];
+    e.slot = c.x;
+    e.len = c.y;
+    kv_tokens(a.cache, a.batch, lo, e.first, e.n);
+  } else {
+    e = load_entry(a, lo);
+  }
+  long long rest = p - o.prefix[lo];
   const int heads = a.cache.kv_heads;
   // (the last tile and head are also where it ends if someone rewrites the lengths meanwhile)
-  const int tiles = max(1, (e.n * group + kRows - 1) / kRows);
+  const int tiles = max(1, tiles_of<kRows>(e, o.group));
   for (at.tile = 0;; ++at.tile) {
-    at.span = tile_span<kRows>(e, at.tile, group, a.window);
-    const long long cost = (long long)at.span.steps * heads;
+    at.span = tile_span<kRows>(e, at.tile, o.group, a.window);
+    at.padded = (at.span.steps + o.pad - 1) / o.pad * o.pad;
+    const long long cost = (long long)at.padded * heads;
     if (rest < cost || at.tile + 1 == tiles) break;
     rest -= cost;
   }
-  at.head = min((int)((uint32_t)rest / (uint32_t)at.span.steps), heads - 1);
-  at.step = (int)((uint32_t)rest % (uint32_t)at.span.steps);
+  at.head = min((int)((uint32_t)rest / (uint32_t)at.padded), heads - 1);
+  at.step = (int)((uint32_t)rest % (uint32_t)at.padded);
   return at;
+}
+
+// Eight values of a query row, from wherever they lie.
+__device__ __forceinline__ void load8(const KvAttentionArgs& a, long long off, bool vec,
+                                      float (&x)[8]) {
+  const uint16_t* s = static_cast<const uint16_t*>(a.q) + off;
+  uint32_t w[4];
+  if (vec) {
+    const uint4 v = *reinterpret_cast<const uint4*>(s);
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = s[2 * k] | ((uint32_t)s[2 * k + 1] << 16);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = a.half ? __half22float2(*reinterpret_cast<const __half2*>(&w[k]))
+                            : make_float2(__uint_as_float(w[k] << 16),
+                                          __uint_as_float(w[k] & 0xFFFF0000u));
+    x[2 * k] = f.x;
+    x[2 * k + 1] = f.y;
+  }
 }
 
 template <int D, int NT>
@@ -201,10 +254,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
   float* factor_sh = reinterpret_cast<float*>(smem + L::kRowInfo);
   int* lo_sh = reinterpret_cast<int*>(factor_sh + kRows);
   int* hi_sh = lo_sh + kRows;
-  float* max_sh = reinterpret_cast<float*>(hi_sh + kRows);
-  float* sum_sh = max_sh + kRows;
   long long* scan = reinterpret_cast<long long*>(smem + L::kScan);
   long long* prefix = reinterpret_cast<long long*>(smem + L::kPrefix);
+  int2* cached = reinterpret_cast<int2*>(prefix + a.batch.entries + 1);
   uint8_t* ring = smem + L::kRing + warp * kStages * L::kStageBytes;
   const uint32_t bar = smem_u32(smem + L::kBars) + warp * kStages * 8;
   __shared__ int last_sh;
@@ -213,128 +265,164 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
     for (int s = 0; s < kStages; ++s) mbar_init(bar + 8 * s, 1);
     mbar_init_fence();
   }
-  // prefix[b] = steps of the entries before b
-  long long before = 0;
-  for (int base = 0; base < a.batch.entries; base += kThreads) {
-    const int b = base + threadIdx.x;
-    long long cost = 0;
-    if (b < a.batch.entries) {
-      const Entry e = load_entry(a, b);
-      const int tiles = (e.n * group + kRows - 1) / kRows;
-      for (int t = 0; t < tiles; ++t) cost += tile_span<kRows>(e, t, group, a.window).steps;
-      cost *= heads;
-    }
-    long long incl = cost;
+  // The order of the steps.  A call with little work pads its items to whole rounds of the eight
+  // warps, and a CTA takes at least as many rounds as an item has, up to kLeast: an item that one CTA finishes
+  // needs no join through memory, which costs more than a few rounds do.  (One short sequence
+  // of 17 steps, four heads: 9 CTAs and a join 19.2 us, 4 CTAs without 11.0 us.)
+  constexpr int kLeast = 3;
+  Order order{prefix, cached, 1, group};
+  long long total = 0;
+  int longest = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long before = 0;
+    for (int base = 0; base < a.batch.entries; base += kThreads) {
+      const int b = base + threadIdx.x;
+      long long cost = 0;
+      if (b < a.batch.entries) {
+        const Entry e = load_entry(a, b);
+        if (b < kCached) cached[b] = make_int2(e.slot, e.len);
+        const int tiles = tiles_of<kRows>(e, group);
+        for (int t = 0; t < tiles; ++t) {
+          const int steps = tile_span<kRows>(e, t, group, a.window).steps;
+          cost += (steps + order.pad - 1) / order.pad * order.pad;
+          longest = max(longest, steps);
+        }
+        cost *= heads;
+      }
+      long long incl = cost;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long long t = __shfl_up_sync(kAll, incl, off);
-      if (lane >= off) incl += t;
-    }
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    long long below = before, all = 0;
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long t = __shfl_up_sync(kAll, incl, off);
+        if (lane >= off) incl += t;
+      }
+      if (lane == 31) scan[warp] = incl;
+      const int top = __reduce_max_sync(kAll, longest);
+      if (lane == 0) scan[kWarps + warp] = top;
+      __syncthreads();
+      long long below = before, all = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) below += scan[w];
-      all += scan[w];
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) below += scan[w];
+        all += scan[w];
+        longest = max(longest, (int)scan[kWarps + w]);
+      }
+      if (b < a.batch.entries) prefix[b] = below + incl - cost;
+      before += all;
+      __syncthreads();
     }
-    if (b < a.batch.entries) prefix[b] = below + incl - cost;
-    before += all;
+    if (threadIdx.x == 0) prefix[a.batch.entries] = before;
     __syncthreads();
+    total = before;
+    if (total > (long long)gridDim.x * kLeast * kWarps) break;
+    order.pad = kWarps;
   }
-  if (threadIdx.x == 0) prefix[a.batch.entries] = before;
-  __syncthreads();
-  const long long total = before;
   // steps to a CTA: a whole number for each of its warps
-  const long long quota = (total + (long long)gridDim.x * kWarps - 1) /
-                          ((long long)gridDim.x * kWarps) * kWarps;
-  const long long begin = blockIdx.x * quota, end = min(total, begin + quota);
-  if (begin >= end) return;
+  const long long rounds = (total + (long long)gridDim.x * kWarps - 1) /
+                           ((long long)gridDim.x * kWarps);
+  const int least = order.pad == 1 ? 1 : min(kLeast, (longest + kWarps - 1) / kWarps);
+  const int quota = (int)max(rounds, (long long)least) * kWarps;
+  const long long begin = (long long)blockIdx.x * quota;
+  if (begin >= total) return;
+  const int mine = (int)min(total - begin, (long long)quota);  // steps of this CTA
 
-  // The warp's steps are begin + warp, + kWarps, ...: its k-th step's groups are worked out by
-  // lane k % 32, 32 steps at a time, and copied into stage k % kStages.
+  // The warp's steps are warp, warp + kWarps, ... of the CTA's: its k-th step's groups are
+  // worked out by lane k % 32, 32 steps at a time, and copied into stage k % kStages.
   const uint8_t *src0 = nullptr, *src1 = nullptr;
   const auto plan = [&](int k0) {
-    const long long p = begin + warp + (long long)kWarps * (k0 + lane);
+    const int r = warp + kWarps * (k0 + lane);
     src0 = src1 = nullptr;
-    if (p >= end) return;
+    if (r >= mine) return;
     Entry e;
-    const Place at = locate<kRows>(a, prefix, p, group, e);
+    const Place at = locate<kRows>(a, order, begin + r, e);
+    if (at.step >= at.span.steps) return;
     const int pos = (at.span.first + at.step) * kStep;
     if (pos < at.span.end)
       src0 = kv_group(cache, kv_page(cache, e.slot, pos >> cache.page_shift), a.layer, at.head,
                       pos, G::kBytes);
-    if (pos + 16 < at.span.end)
-      src1 = kv_group(cache, kv_page(cache, e.slot, (pos + 16) >> cache.page_shift), a.layer,
-                      at.head, pos + 16, G::kBytes);
+    if (pos + 16 < at.span.end) {
+      if (cache.page_size >= kStep)  // a step lies within a page, its groups side by side
+        src1 = src0 + G::kBytes;
+      else
+        src1 = kv_group(cache, kv_page(cache, e.slot, (pos + 16) >> cache.page_shift), a.layer,
+                        at.head, pos + 16, G::kBytes);
+    }
   };
+  const uint32_t ring_at = smem_u32(ring);
   const auto issue = [&](int stage) {
-    const uint32_t to = smem_u32(ring) + stage * L::kStageBytes;
-    mbar_arrive_expect_tx(bar + 8 * stage, (src0 ? G::kBytes : 0) + (src1 ? G::kBytes : 0));
-    if (src0) bulk_g2s_nohint(to, src0, G::kBytes, bar + 8 * stage);
-    if (src1) bulk_g2s_nohint(to + G::kBytes, src1, G::kBytes, bar + 8 * stage);
+    const uint32_t to = ring_at + stage * L::kStageBytes, full = bar + 8 * stage;
+    if (src1 && src1 == src0 + G::kBytes) {
+      mbar_arrive_expect_tx(full, 2 * G::kBytes);
+      bulk_g2s_nohint(to, src0, 2 * G::kBytes, full);
+    } else {
+      mbar_arrive_expect_tx(full, (src0 ? G::kBytes : 0) + (src1 ? G::kBytes : 0));
+      if (src0) bulk_g2s_nohint(to, src0, G::kBytes, full);
+      if (src1) bulk_g2s_nohint(to + G::kBytes, src1, G::kBytes, full);
+    }
   };
   plan(0);
-  if (lane < kStages && begin + warp + (long long)kWarps * lane < end) issue(lane);
+  if (lane < kStages && warp + kWarps * lane < mine) issue(lane);
   __syncwarp();
 
+  const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.q_token % 8 == 0 &&
+                   a.q_head % 8 == 0;
+  int r = warp;  // the warp's next step, of the CTA's
   int k = 0, stage = 0;
   uint32_t phase = 0;
   bool dead = false;  // a wait ran out
+  // refill the stage that the k-th step has used, and go on to the next
+  const auto issue_next = [&]() {
+    __syncwarp();
+    const int next = k + kStages;
+    if ((next & 31) == 0) plan(next);
+    if (lane == (next & 31) && warp + kWarps * next < mine) issue(stage);
+    __syncwarp();
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  };
   Entry entry;
-  for (long long p0 = begin; p0 < end;) {
-    const Place at = locate<kRows>(a, prefix, p0, group, entry);
-    const long long item = p0 - at.step;                      // the item's first step
-    const long long p1 = min(end, item + at.span.steps);      // the segment is [p0, p1)
+  for (int r0 = 0; r0 < mine;) {
+    const Place at = locate<kRows>(a, order, begin + r0, entry);
+    const int r1 = min(mine, r0 + at.padded - at.step);  // the segment is [r0, r1)
+    const int rows = entry.n * group - at.tile * kRows;  // of the tile's, those that are real
 
-    // the tile's queries, as fragments: channel 32c + 8t + 4j + 2r + {0,1} of row 8nt + g is
-    // register r of product j in lane 4g + t
+    // the tile's queries, as fragments: channel 32c + 8t + 4j + 2i + {0,1} of row 8nt + g is
+    // register i of product j in lane 4g + t.  Four lanes to a block of 32 channels.
     __syncthreads();
-    for (int row = warp; row < kRows; row += kWarps) {
+    for (int i = threadIdx.x; i < kRows * (D / 8); i += kThreads) {
+      const int row = i / (D / 8), e8 = i % (D / 8);
       const int flat = at.tile * kRows + row;
-      const bool real = flat < entry.n * group;
-      const int i = flat / group;
+      const int token = flat / group;
+      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (row < rows)
+        load8(a, (entry.first + token) * a.q_token + (at.head * group + flat % group) * a.q_head +
+                     8 * e8, vec, x);
       uint32_t bits = 0;
-      float x[D / 32];
 #pragma unroll
-      for (int q = 0; q < D / 64; ++q) {
-        float lo = 0.f, hi = 0.f;
-        if (real) {
-          const long long off = (entry.first + i) * a.q_token +
-                                (at.head * group + flat % group) * a.q_head + 64 * q + 2 * lane;
-          if (a.half) {
-            const __half* s = static_cast<const __half*>(a.q) + off;
-            lo = __half2float(s[0]);
-            hi = __half2float(s[1]);
-          } else {
-            const __nv_bfloat16* s = static_cast<const __nv_bfloat16*>(a.q) + off;
-            lo = __bfloat162float(s[0]);
-            hi = __bfloat162float(s[1]);
-          }
-        }
-        x[2 * q] = lo;
-        x[2 * q + 1] = hi;
-        bits = max(bits, max(__float_as_uint(lo) & 0x7FFFFFFFu, __float_as_uint(hi) & 0x7FFFFFFFu));
-      }
-      bits = __reduce_max_sync(kAll, bits);
+      for (int q = 0; q < 8; ++q) bits = max(bits, __float_as_uint(x[q]) & 0x7FFFFFFFu);
+#pragma unroll
+      for (int off = 1; off < D / 8; off <<= 1)
+        bits = max(bits, __shfl_xor_sync(kAll, bits, off));
       // 2^k brings the largest magnitude into [2^14, 2^15); subnormals are scaled as if 2^-126
       const bool bad = bits >= 0x7F800000u;
       const int k2 = bad || bits == 0u ? 0 : 14 - (max((int)(bits >> 23), 1) - 127);
       const float up = exp2_int(k2 / 2), up2 = exp2_int(k2 - k2 / 2);
-#pragma unroll
-      for (int q = 0; q < D / 64; ++q) {
-        const int ch = 64 * q + 2 * lane;
-        const int c = ch >> 5, t = (ch & 31) >> 3, r = (ch & 7) >> 1;
-        *reinterpret_cast<uint32_t*>(smem + L::kQ + (((row >> 3) * CB + c) * 32 + (row & 7) * 4 + t) * 16 +
-                                     r * 4) = pack_half2(x[2 * q] * up * up2, x[2 * q + 1] * up * up2);
-      }
-      if (lane == 0) {
-        const int pos = entry.len - entry.n + i;
+      uint4 f;
+      f.x = pack_half2(x[0] * up * up2, x[1] * up * up2);
+      f.y = pack_half2(x[2] * up * up2, x[3] * up * up2);
+      f.z = pack_half2(x[4] * up * up2, x[5] * up * up2);
+      f.w = pack_half2(x[6] * up * up2, x[7] * up * up2);
+      *reinterpret_cast<uint4*>(smem + L::kQ + (((row >> 3) * CB + (e8 >> 2)) * 32 +
+                                                (row & 7) * 4 + (e8 & 3)) * 16) = f;
+      if (e8 == 0) {
+        const int pos = entry.len - entry.n + token;
         // a row with an infinity or NaN has no finite logit
         factor_sh[row] = bad ? __uint_as_float(0x7FC00000u)
                              : a.scale * 1.4426950408889634f / up / up2;
+        const bool real = row < rows;  // no row: nothing to hide, never stored
         lo_sh[row] = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
-        hi_sh[row] = real ? pos : at.span.end - 1;  // no row: nothing to hide, never stored
+        hi_sh[row] = real ? pos : at.span.end - 1;
       }
     }
     __syncthreads();
@@ -380,14 +468,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
 #pragma unroll
     for (int w = 0; w < NW; ++w) ref[w] = 0x10101010u;
 
-    for (; begin + warp + (long long)kWarps * k < p1; ++k) {
-      const int j0 = (at.span.first + (int)(begin + warp + (long long)kWarps * k - item)) * kStep;
+    for (; r < r1; r += kWarps, ++k) {
+      const int step = at.step + r - r0;
+      const int j0 = (at.span.first + step) * kStep;
       if (!dead && !mbar_wait(bar + 8 * stage, phase)) {
         dead = true;
         if (lane == 0) atomicOr(cache.flag, WD_KV_FLAG_TIMEOUT);
       }
       dead = __any_sync(kAll, dead);
       if (dead) break;
+      if (step >= at.span.steps) {  // padding, the last of the item: nothing was copied
+        issue_next();
+        continue;
+      }
       const uint8_t* buf = ring + stage * L::kStageBytes;
 
       // ---- S^T = K Q^T
@@ -694,16 +787,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
             }
       }
 
-      // ---- refill the stage
-      __syncwarp();
-      const int next = k + kStages;
-      if ((next & 31) == 0) plan(next);
-      if (lane == (next & 31) && begin + warp + (long long)kWarps * next < end) issue(stage);
-      __syncwarp();
-      if (++stage == kStages) {
-        stage = 0;
-        phase ^= 1u;
-      }
+      issue_next();
     }
 
     // ---- join the warps
@@ -720,77 +804,90 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
           l_sh[warp * kRows + 8 * nt + 2 * tq + e] = t;
         }
       }
-    __syncthreads();
-    if (threadIdx.x < kRows) {
-      const int row = threadIdx.x;
-      float top = -INFINITY, sum = 0.f;
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_sh[w * kRows + row]);
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = top == -INFINITY ? 0.f : exp2_fast(m_sh[w * kRows + row] - top);
-        // a warp whose keys were all NaN has no maximum but a NaN sum
-        const float lw = l_sh[w * kRows + row];
-        sum += lw != lw ? lw : lw * f;
-        m_sh[w * kRows + row] = f;
-      }
-      max_sh[row] = top;
-      sum_sh[row] = sum;
-    }
-    __syncthreads();
-    const bool alone = p0 == item && p1 == item + at.span.steps;
+    const long long item = begin + r0 - at.step;  // the item's first step
+    const bool alone = at.step == 0 && r1 - r0 == at.padded;
     const int first_cta = (int)(item / quota);
-    const int last_cta = (int)((item + at.span.steps - 1) / quota);
-    const long long slot_floats = (long long)kKvMaxRows * (D + 2);
-    float* part = a.partial + (2 * (long long)blockIdx.x + (p0 > begin ? 1 : 0)) * slot_floats;
-    const auto store_out = [&](int row, int ch, float y) {
+    const int last_cta = (int)((item + at.padded - 1) / quota);
+    constexpr long long kSlot = (long long)kKvMaxRows * (D + 2);
+    const auto part_of = [&](int x) {
+      return a.partial + (2 * (long long)x + (item > (long long)x * quota ? 1 : 0)) * kSlot;
+    };
+    float* part = part_of(blockIdx.x);
+    const auto store_out = [&](int row, int ch, const float4& y, float sum) {
+      if (row >= rows) return;
       const int flat = at.tile * kRows + row;
-      if (flat >= entry.n * group) return;
       const long long o_at = ((long long)(entry.first + flat / group) * a.q_heads + at.head * group +
                               flat % group) * D + ch;
-      if (a.half)
-        static_cast<__half*>(a.out)[o_at] = __float2half_rn(y);
-      else
-        static_cast<__nv_bfloat16*>(a.out)[o_at] = __float2bfloat16_rn(y);
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      uint16_t* to = static_cast<uint16_t*>(a.out) + o_at;
+      const float v[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (a.half)
+          reinterpret_cast<__half*>(to)[q] = __float2half_rn(v[q]);
+        else
+          reinterpret_cast<__nv_bfloat16*>(to)[q] = __float2bfloat16_rn(v[q]);
+      }
     };
     const auto store_lse = [&](int row, float top, float sum) {
+      if (!a.lse || row >= rows) return;
       const int flat = at.tile * kRows + row;
-      if (!a.lse || flat >= entry.n * group) return;
       a.lse[(long long)(entry.first + flat / group) * a.q_heads + at.head * group + flat % group] =
           sum == 0.f ? -INFINITY : (top - 14.f) * 0.6931471805599453f + logf(sum);
     };
 #pragma unroll
-    for (int c = 0; c < CB; ++c) {
-      const float unit = exp2f((float)((int)((ref[c / 4] >> (8 * (c % 4))) & 0xFFu) - 128));
+    for (int round = 0; round < L::kRounds; ++round) {
+      if (round > 0) __syncthreads();
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int cr = 0; cr < L::kRoundBlocks; ++cr) {
+        const int c = round * L::kRoundBlocks + cr;
+        const float unit = exp2_int((int)((ref[c / 4] >> (8 * (c % 4))) & 0xFFu) - 128);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int row = 8 * nt + 2 * tq + e;
-          const float f = m_sh[warp * kRows + row] * unit;
-          float* to = merge + (warp * kRows + row) * kPad + 4 * g;
-          *reinterpret_cast<float4*>(to) =
-              make_float4(o[c][0][nt][e] * f, o[c][0][nt][2 + e] * f, o[c][1][nt][e] * f,
-                          o[c][1][nt][2 + e] * f);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float4*>(
+                merge + (warp * kRows + 8 * nt + 2 * tq + e) * L::kMergeRow + 32 * cr + 4 * g) =
+                make_float4(o[c][0][nt][e] * unit, o[c][0][nt][2 + e] * unit,
+                            o[c][1][nt][e] * unit, o[c][1][nt][2 + e] * unit);
+      }
+      __syncthreads();
+      constexpr int kQuads = 8 * L::kRoundBlocks;  // four channels each, of a row
+      for (int i = threadIdx.x; i < kRows * kQuads; i += kThreads) {
+        const int row = i / kQuads, ch = 4 * (i % kQuads);
+        float mw[kWarps], top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          mw[w] = m_sh[w * kRows + row];
+          top = fmaxf(top, mw[w]);
         }
-      __syncthreads();
-      for (int i = threadIdx.x; i < kRows * 32; i += kThreads) {
-        const int row = i >> 5, ch = i & 31;
-        float y = 0.f;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) y += merge[(w * kRows + row) * kPad + ch];
-        if (alone)
-          store_out(row, 32 * c + ch, sum_sh[row] == 0.f ? 0.f : y / sum_sh[row]);
-        else
-          part[row * D + 32 * c + ch] = y;
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = top == -INFINITY ? 0.f : exp2_fast(mw[w] - top);
+          const float lw = l_sh[w * kRows + row];
+          // a warp whose keys were all NaN has no maximum, but a NaN sum
+          sum += lw != lw ? lw : lw * f;
+          const float4 v = *reinterpret_cast<const float4*>(merge + (w * kRows + row) * L::kMergeRow + ch);
+          y.x = fmaf(v.x, f, y.x);
+          y.y = fmaf(v.y, f, y.y);
+          y.z = fmaf(v.z, f, y.z);
+          y.w = fmaf(v.w, f, y.w);
+        }
+        const int at_ch = 32 * round * L::kRoundBlocks + ch;
+        if (alone) {
+          store_out(row, at_ch, y, sum);
+          if (at_ch == 0) store_lse(row, top, sum);
+        } else {
+          __stcg(reinterpret_cast<float4*>(part + row * D + at_ch), y);
+          if (at_ch == 0) {
+            __stcg(part + kRows * D + row, top);
+            __stcg(part + kRows * D + kRows + row, sum);
+          }
+        }
       }
-      __syncthreads();
     }
-    if (alone) {
-      if (threadIdx.x < kRows) store_lse(threadIdx.x, max_sh[threadIdx.x], sum_sh[threadIdx.x]);
-    } else {
-      if (threadIdx.x < kRows) {
-        part[kRows * D + threadIdx.x] = max_sh[threadIdx.x];
-        part[kRows * D + kRows + threadIdx.x] = sum_sh[threadIdx.x];
-      }
+    if (!alone) {
       __threadfence();
       __syncthreads();
       if (threadIdx.x == 0)
@@ -800,36 +897,50 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
         // every part is there: join them in their order
         __threadfence();
         if (threadIdx.x == 0) a.counters[first_cta] = 0;
-        const auto part_of = [&](int x) {
-          return a.partial + (2 * (long long)x + (item > x * quota ? 1 : 0)) * slot_floats;
-        };
-        if (threadIdx.x < kRows) {
-          float top = -INFINITY, sum = 0.f;
-          for (int x = first_cta; x <= last_cta; ++x)
-            top = fmaxf(top, __ldcg(part_of(x) + kRows * D + threadIdx.x));
-          for (int x = first_cta; x <= last_cta; ++x) {
-            const float mx = __ldcg(part_of(x) + kRows * D + threadIdx.x);
-            const float lx = __ldcg(part_of(x) + kRows * D + kRows + threadIdx.x);
-            sum += lx != lx ? lx : lx * (top == -INFINITY ? 0.f : exp2_fast(mx - top));
+        const int parts = last_cta - first_cta + 1;
+        float* factors = merge;  // [kRows][parts]
+        for (int row = warp; row < kRows; row += kWarps) {
+          float top = -INFINITY;
+          for (int x = lane; x < parts; x += 32)
+            top = fmaxf(top, __ldcg(part_of(first_cta + x) + kRows * D + row));
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
+          float sum = 0.f;
+          for (int x = lane; x < parts; x += 32) {
+            const float* from = part_of(first_cta + x) + kRows * D + row;
+            const float f = top == -INFINITY ? 0.f : exp2_fast(__ldcg(from) - top);
+            const float lx = __ldcg(from + kRows);
+            sum += lx != lx ? lx : lx * f;
+            factors[row * parts + x] = f;
           }
-          max_sh[threadIdx.x] = top;
-          sum_sh[threadIdx.x] = sum;
-          store_lse(threadIdx.x, top, sum);
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
+          if (lane == 0) {
+            l_sh[row] = sum;
+            store_lse(row, top, sum);
+          }
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < kRows * D; i += kThreads) {
-          const int row = i / D;
-          const float top = max_sh[row];
-          float y = 0.f;
-          for (int x = first_cta; x <= last_cta; ++x) {
-            const float mx = __ldcg(part_of(x) + kRows * D + row);
-            y += __ldcg(part_of(x) + i) * (top == -INFINITY ? 0.f : exp2_fast(mx - top));
+        for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
+          const int row = i / (D / 4), ch = 4 * (i % (D / 4));
+          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int x = 0; x < parts; ++x) {
+            const float4 v = __ldcg(
+                reinterpret_cast<const float4*>(part_of(first_cta + x) + row * D + ch));
+            const float f = factors[row * parts + x];
+            y.x = fmaf(v.x, f, y.x);
+            y.y = fmaf(v.y, f, y.y);
+            y.z = fmaf(v.z, f, y.z);
+            y.w = fmaf(v.w, f, y.w);
           }
-          store_out(row, i % D, sum_sh[row] == 0.f ? 0.f : y / sum_sh[row]);
+          store_out(row, ch, y, l_sh[row]);
         }
+        __syncthreads();
       }
     }
-    p0 = p1;
+    r0 = r1;
   }
   if (dead) {
     // give up, but not before the copies in flight have landed (or as long again has passed)
@@ -840,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
 template <int D, int NT>
 cudaError_t run(const KvAttentionArgs& a, cudaStream_t s) {
   using L = Shape<D, NT>;
-  const int bytes = L::kPrefix + 8 * (a.batch.entries + 1);
+  const int bytes = L::shared_bytes(a.batch.entries);
   const void* fn = reinterpret_cast<const void*>(kv_attention<D, NT>);
   cudaError_t e = ensure_dynamic_smem(fn, bytes);
   if (e != cudaSuccess) return e;
