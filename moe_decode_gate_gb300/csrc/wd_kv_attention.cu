@@ -50,16 +50,16 @@ struct Shape {
   // shared memory, in bytes from its start
   static constexpr int kRing = 0;
   static constexpr int kQ = kRing + kWarps * kStages * kStageBytes;  // fragments [NT][blocks][32] uint4
-  static constexpr int kMerge = kQ + NT * G::kBlocks * 512;  // float [kWarps][kRows][kMergeRow]
+  static constexpr int kQBytes = NT * G::kBlocks * 512;                // twice: this segment's, the next's
+  static constexpr int kMerge = kQ + 2 * kQBytes;  // float [kWarps][kRows][kMergeRow]
   static constexpr int kStats = kMerge + kWarps * kRows * kMergeRow * 4;  // float m, l [kWarps][kRows]
-  static constexpr int kRowInfo = kStats + 2 * kWarps * kRows * 4;   // factor, lo, hi [kRows]
-  static constexpr int kBars = kRowInfo + 3 * kRows * 4 + (kRows * 4) % 8;  // uint64 [kWarps][kStages]
-  static constexpr int kScan = kBars + kWarps * kStages * 8;         // long long [2][kWarps]
-  static constexpr int kPrefix = kScan + 2 * kWarps * 8;             // long long [entries + 1]
+  static constexpr int kRowInfo = kStats + 2 * kWarps * kRows * 4;   // twice: factor, lo, hi [kRows]
+  static constexpr int kBars = kRowInfo + 2 * 3 * kRows * 4;         // uint64 [kWarps][kStages]
+  static constexpr int kScan = kBars + kWarps * kStages * 8;         // long long [kWarps], int [kWarps][8]
+  static constexpr int kPrefix = kScan + kWarps * 8 + kWarps * 32;   // long long [entries + 1]
   static constexpr int shared_bytes(int entries) {  // ... and int2 [min(entries, kCached)]
     return kPrefix + 8 * (entries + 1) + 8 * (entries < kCached ? entries : kCached);
   }
-  static_assert(kWarps * kMergeRow >= kKvMaxCtas, "the last join's factors fit the merge buffer");
   static_assert(kPrefix + 8 * (WD_KV_MAX_ENTRIES + 1) + 8 * kCached <= 227 * 1024, "shared memory");
 };
 
@@ -71,6 +71,15 @@ __device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t& r0, uint32_t& r1, u
       "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
       : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
       : "r"(w));
+}
+
+// Two E8M0 scale bytes (the low 16 bits of w) -> BF16 2^(s-127), NaN for 255, exactly.
+__device__ __forceinline__ uint32_t e8m0x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.bf16x2.ue8m0x2 %0, a;\n\t}"
+      : "=r"(r)
+      : "r"(w));
+  return r;
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -235,6 +244,42 @@ __device__ __forceinline__ void load8(const KvAttentionArgs& a, long long off, b
   }
 }
 
+// Part of an item that one CTA has done, and where the whole item's output goes.
+struct Part {
+  long long item;           // the item's first step
+  int first_cta, last_cta;  // that have parts of it
+  int tile, head, first, n;
+};
+// Where CTA x leaves its part: it has at most two, the first if the item began before it.
+__device__ __forceinline__ float* part_at(const KvAttentionArgs& a, const Part& p, int x,
+                                          int quota) {
+  const long long slot = 2 * (long long)x + (p.item > (long long)x * quota ? 1 : 0);
+  return a.partial + slot * kKvMaxRows * (a.cache.head_dim + 2);
+}
+
+// Four channels of a finished row: y / sum, and with the first of them the row's lse.
+template <int D, int kRows>
+__device__ __forceinline__ void store_row(const KvAttentionArgs& a, const Part& p, int row, int ch,
+                                          const float4& y, float top, float sum) {
+  const int group = a.q_heads / a.cache.kv_heads;
+  const int flat = p.tile * kRows + row;
+  if (flat >= p.n * group) return;
+  const long long at =
+      (long long)(p.first + flat / group) * a.q_heads + p.head * group + flat % group;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const float v[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
+  uint16_t* to = static_cast<uint16_t*>(a.out) + at * D + ch;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (a.half)
+      reinterpret_cast<__half*>(to)[q] = __float2half_rn(v[q]);
+    else
+      reinterpret_cast<__nv_bfloat16*>(to)[q] = __float2bfloat16_rn(v[q]);
+  }
+  if (a.lse && ch == 0)
+    a.lse[at] = sum == 0.f ? -INFINITY : (top - 14.f) * 0.6931471805599453f + logf(sum);
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
     kv_attention(const KvAttentionArgs a) {
@@ -251,76 +296,134 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
   float* merge = reinterpret_cast<float*>(smem + L::kMerge);
   float* m_sh = reinterpret_cast<float*>(smem + L::kStats);
   float* l_sh = m_sh + kWarps * kRows;
-  float* factor_sh = reinterpret_cast<float*>(smem + L::kRowInfo);
-  int* lo_sh = reinterpret_cast<int*>(factor_sh + kRows);
-  int* hi_sh = lo_sh + kRows;
   long long* scan = reinterpret_cast<long long*>(smem + L::kScan);
+  int* scan2 = reinterpret_cast<int*>(scan + kWarps);
   long long* prefix = reinterpret_cast<long long*>(smem + L::kPrefix);
   int2* cached = reinterpret_cast<int2*>(prefix + a.batch.entries + 1);
   uint8_t* ring = smem + L::kRing + warp * kStages * L::kStageBytes;
   const uint32_t bar = smem_u32(smem + L::kBars) + warp * kStages * 8;
-  __shared__ int last_sh;
+  __shared__ Part parts_sh[2];
+  __shared__ int last_sh[2];
 
   if (lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(bar + 8 * s, 1);
     mbar_init_fence();
   }
-  // The order of the steps.  A call with little work pads its items to whole rounds of the eight
-  // warps, and a CTA takes at least as many rounds as an item has, up to kLeast: an item that one CTA finishes
-  // needs no join through memory, which costs more than a few rounds do.  (One short sequence
-  // of 17 steps, four heads: 9 CTAs and a join 19.2 us, 4 CTAs without 11.0 us.)
+  // The division of the work.  Where there are no more items than CTAs, each item gets CTAs of
+  // its own (its steps are padded to a multiple of a CTA's), so that a CTA has one item to do;
+  // else the CTAs' ranges cross the items' bounds and are all of the same length.  A CTA takes at
+  // least kLeast rounds of its warps where an item has as many: fewer would only add parts to
+  // join, and a join through memory costs as much as two rounds.
   constexpr int kLeast = 3;
+  constexpr int kTries = 8;
   Order order{prefix, cached, 1, group};
+  Entry own{-1, 0, 0, 0};
+  if ((int)threadIdx.x < a.batch.entries) own = load_entry(a, threadIdx.x);
   long long total = 0;
-  int longest = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    long long before = 0;
-    for (int base = 0; base < a.batch.entries; base += kThreads) {
-      const int b = base + threadIdx.x;
-      long long cost = 0;
-      if (b < a.batch.entries) {
-        const Entry e = load_entry(a, b);
-        if (b < kCached) cached[b] = make_int2(e.slot, e.len);
+  int longest = 0, items = 0;
+  {
+    long long steps_here = 0;
+    for (int b = threadIdx.x; b < a.batch.entries; b += kThreads) {
+      const Entry e = b < kThreads ? own : load_entry(a, b);
+      if (b < kCached) cached[b] = make_int2(e.slot, e.len);
+      const int tiles = tiles_of<kRows>(e, group);
+      for (int t = 0; t < tiles; ++t) {
+        const int steps = tile_span<kRows>(e, t, group, a.window).steps;
+        steps_here += steps;
+        longest = max(longest, steps);
+      }
+      items += tiles * heads;
+    }
+    steps_here *= heads;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) steps_here += __shfl_xor_sync(kAll, steps_here, off);
+    longest = __reduce_max_sync(kAll, longest);
+    items = __reduce_add_sync(kAll, min(items, 1 << 24));
+    if (lane == 0) {
+      scan[warp] = steps_here;
+      scan2[warp * 8] = longest;
+      scan2[warp * 8 + 1] = items;
+    }
+    __syncthreads();
+    items = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      total += scan[w];
+      longest = max(longest, scan2[w * 8]);
+      items += min(scan2[w * 8 + 1], 1 << 24);
+    }
+  }
+  const long long rounds = (total + (long long)gridDim.x * kWarps - 1) /
+                           ((long long)gridDim.x * kWarps);
+  int quota = (int)max(rounds, 1ll) * kWarps;
+  if (items <= (int)gridDim.x) {
+    // the shortest of some quotas at which the CTAs suffice
+    const int lowest = max(quota, min(kLeast, (longest + kWarps - 1) / kWarps) * kWarps);
+    const auto try_quota = [&](int i) {  // times 16, 17, 18, 20, 24, 32, 48, 64 sixteenths
+      constexpr int kBy[kTries] = {16, 17, 18, 20, 24, 32, 48, 64};
+      return (int)(((long long)lowest * kBy[i] / 16 + kWarps - 1) / kWarps) * kWarps;
+    };
+    int need[kTries] = {0};
+    if (longest <= lowest) {  // no item needs two CTAs
+      order.pad = quota = lowest;
+    } else {
+      for (int b = threadIdx.x; b < a.batch.entries; b += kThreads) {
+        const Entry e = b < kThreads ? own : load_entry(a, b);
         const int tiles = tiles_of<kRows>(e, group);
         for (int t = 0; t < tiles; ++t) {
           const int steps = tile_span<kRows>(e, t, group, a.window).steps;
-          cost += (steps + order.pad - 1) / order.pad * order.pad;
-          longest = max(longest, steps);
+#pragma unroll
+          for (int i = 0; i < kTries; ++i) need[i] += (steps + try_quota(i) - 1) / try_quota(i);
         }
-        cost *= heads;
       }
-      long long incl = cost;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const long long t = __shfl_up_sync(kAll, incl, off);
-        if (lane >= off) incl += t;
-      }
-      if (lane == 31) scan[warp] = incl;
-      const int top = __reduce_max_sync(kAll, longest);
-      if (lane == 0) scan[kWarps + warp] = top;
       __syncthreads();
-      long long below = before, all = 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) below += scan[w];
-        all += scan[w];
-        longest = max(longest, (int)scan[kWarps + w]);
+      for (int i = 0; i < kTries; ++i) {
+        need[i] = __reduce_add_sync(kAll, need[i]);
+        if (lane == 0) scan2[warp * 8 + i] = need[i];
       }
-      if (b < a.batch.entries) prefix[b] = below + incl - cost;
-      before += all;
       __syncthreads();
+#pragma unroll
+      for (int i = kTries - 1; i >= 0; --i) {
+        int all = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) all += scan2[w * 8 + i];
+        if ((long long)all * heads <= (long long)gridDim.x) order.pad = quota = try_quota(i);
+      }
     }
-    if (threadIdx.x == 0) prefix[a.batch.entries] = before;
-    __syncthreads();
-    total = before;
-    if (total > (long long)gridDim.x * kLeast * kWarps) break;
-    order.pad = kWarps;
   }
-  // steps to a CTA: a whole number for each of its warps
-  const long long rounds = (total + (long long)gridDim.x * kWarps - 1) /
-                           ((long long)gridDim.x * kWarps);
-  const int least = order.pad == 1 ? 1 : min(kLeast, (longest + kWarps - 1) / kWarps);
-  const int quota = (int)max(rounds, (long long)least) * kWarps;
+  // prefix[b] = steps, with the padding, of the entries before b
+  total = 0;
+  for (int base = 0; base < a.batch.entries; base += kThreads) {
+    const int b = base + threadIdx.x;
+    long long cost = 0;
+    if (b < a.batch.entries) {
+      const Entry e = b < kThreads ? own : load_entry(a, b);
+      const int tiles = tiles_of<kRows>(e, group);
+      for (int t = 0; t < tiles; ++t)
+        cost += (tile_span<kRows>(e, t, group, a.window).steps + order.pad - 1) / order.pad * order.pad;
+      cost *= heads;
+    }
+    long long incl = cost;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long t = __shfl_up_sync(kAll, incl, off);
+      if (lane >= off) incl += t;
+    }
+    __syncthreads();
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    long long below = total, all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) below += scan[w];
+      all += scan[w];
+    }
+    if (b < a.batch.entries) prefix[b] = below + incl - cost;
+    total += all;
+  }
+  if (threadIdx.x == 0) prefix[a.batch.entries] = total;
+  __syncthreads();
   const long long begin = (long long)blockIdx.x * quota;
   if (begin >= total) return;
   const int mine = (int)min(total - begin, (long long)quota);  // steps of this CTA
@@ -328,20 +431,22 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
   // The warp's steps are warp, warp + kWarps, ... of the CTA's: its k-th step's groups are
   // worked out by lane k % 32, 32 steps at a time, and copied into stage k % kStages.
   const uint8_t *src0 = nullptr, *src1 = nullptr;
+  uint32_t bytes0 = 0;
   const auto plan = [&](int k0) {
     const int r = warp + kWarps * (k0 + lane);
     src0 = src1 = nullptr;
+    bytes0 = 0;
     if (r >= mine) return;
     Entry e;
     const Place at = locate<kRows>(a, order, begin + r, e);
-    if (at.step >= at.span.steps) return;
     const int pos = (at.span.first + at.step) * kStep;
-    if (pos < at.span.end)
-      src0 = kv_group(cache, kv_page(cache, e.slot, pos >> cache.page_shift), a.layer, at.head,
-                      pos, G::kBytes);
+    if (at.step >= at.span.steps || pos >= at.span.end) return;
+    src0 = kv_group(cache, kv_page(cache, e.slot, pos >> cache.page_shift), a.layer, at.head, pos,
+                    G::kBytes);
+    bytes0 = G::kBytes;
     if (pos + 16 < at.span.end) {
-      if (cache.page_size >= kStep)  // a step lies within a page, its groups side by side
-        src1 = src0 + G::kBytes;
+      if (cache.page_size >= kStep)  // the step lies within a page, its groups side by side
+        bytes0 = 2 * G::kBytes;
       else
         src1 = kv_group(cache, kv_page(cache, e.slot, (pos + 16) >> cache.page_shift), a.layer,
                         at.head, pos + 16, G::kBytes);
@@ -350,14 +455,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
   const uint32_t ring_at = smem_u32(ring);
   const auto issue = [&](int stage) {
     const uint32_t to = ring_at + stage * L::kStageBytes, full = bar + 8 * stage;
-    if (src1 && src1 == src0 + G::kBytes) {
-      mbar_arrive_expect_tx(full, 2 * G::kBytes);
-      bulk_g2s_nohint(to, src0, 2 * G::kBytes, full);
-    } else {
-      mbar_arrive_expect_tx(full, (src0 ? G::kBytes : 0) + (src1 ? G::kBytes : 0));
-      if (src0) bulk_g2s_nohint(to, src0, G::kBytes, full);
-      if (src1) bulk_g2s_nohint(to + G::kBytes, src1, G::kBytes, full);
-    }
+    mbar_arrive_expect_tx(full, bytes0 + (src1 ? G::kBytes : 0));
+    if (bytes0) bulk_g2s_nohint(to, src0, bytes0, full);
+    if (src1) bulk_g2s_nohint(to + G::kBytes, src1, G::kBytes, full);
   };
   plan(0);
   if (lane < kStages && warp + kWarps * lane < mine) issue(lane);
@@ -381,15 +481,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
       phase ^= 1u;
     }
   };
-  Entry entry;
-  for (int r0 = 0; r0 < mine;) {
-    const Place at = locate<kRows>(a, order, begin + r0, entry);
-    const int r1 = min(mine, r0 + at.padded - at.step);  // the segment is [r0, r1)
+  // A tile's queries as fragments: channel 32c + 8t + 4j + 2i + {0,1} of row 8nt + g is register
+  // i of product j in lane 4g + t.  Four lanes to a block of 32 channels.
+  const auto load_queries = [&](const Place& at, const Entry& entry, int which) {
     const int rows = entry.n * group - at.tile * kRows;  // of the tile's, those that are real
-
-    // the tile's queries, as fragments: channel 32c + 8t + 4j + 2i + {0,1} of row 8nt + g is
-    // register i of product j in lane 4g + t.  Four lanes to a block of 32 channels.
-    __syncthreads();
+    float* factor_sh = reinterpret_cast<float*>(smem + L::kRowInfo) + which * 3 * kRows;
+    int* lo_sh = reinterpret_cast<int*>(factor_sh + kRows);
+    int* hi_sh = lo_sh + kRows;
     for (int i = threadIdx.x; i < kRows * (D / 8); i += kThreads) {
       const int row = i / (D / 8), e8 = i % (D / 8);
       const int flat = at.tile * kRows + row;
@@ -413,25 +511,36 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
       f.y = pack_half2(x[2] * up * up2, x[3] * up * up2);
       f.z = pack_half2(x[4] * up * up2, x[5] * up * up2);
       f.w = pack_half2(x[6] * up * up2, x[7] * up * up2);
-      *reinterpret_cast<uint4*>(smem + L::kQ + (((row >> 3) * CB + (e8 >> 2)) * 32 +
-                                                (row & 7) * 4 + (e8 & 3)) * 16) = f;
+      *reinterpret_cast<uint4*>(smem + L::kQ + which * L::kQBytes +
+                                (((row >> 3) * CB + (e8 >> 2)) * 32 + (row & 7) * 4 + (e8 & 3)) * 16) = f;
       if (e8 == 0) {
         const int pos = entry.len - entry.n + token;
-        // a row with an infinity or NaN has no finite logit
+        // a row with an infinity or NaN has no finite logit; never 0, so that -inf stays -inf
         factor_sh[row] = bad ? __uint_as_float(0x7FC00000u)
-                             : a.scale * 1.4426950408889634f / up / up2;
+                             : fmaxf(a.scale * 1.4426950408889634f / up / up2, 1.2e-38f);
         const bool real = row < rows;  // no row: nothing to hide, never stored
         lo_sh[row] = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
         hi_sh[row] = real ? pos : at.span.end - 1;
       }
     }
-    __syncthreads();
+  };
+  Entry entry;
+  Place at = locate<kRows>(a, order, begin, entry);
+  load_queries(at, entry, 0);
+  __syncthreads();
+  int pending = 0;  // parts of items that other CTAs have parts of: at most the first and the last
+  for (int r0 = 0, which = 0; r0 < mine; which ^= 1) {
+    const int r1 = min(mine, r0 + at.padded - at.step);  // the segment is [r0, r1)
+    const uint8_t* q_sh = smem + L::kQ + which * L::kQBytes;
+    const float* factor_sh = reinterpret_cast<const float*>(smem + L::kRowInfo) + which * 3 * kRows;
+    const int* lo_sh = reinterpret_cast<const int*>(factor_sh + kRows);
+    const int* hi_sh = lo_sh + kRows;
 
     uint4 qf[kQInRegs ? CB : 1];
     if constexpr (kQInRegs) {
 #pragma unroll
       for (int c = 0; c < CB; ++c)
-        qf[c] = *reinterpret_cast<const uint4*>(smem + L::kQ + (c * 32 + lane) * 16);
+        qf[c] = *reinterpret_cast<const uint4*>(q_sh + (c * 32 + lane) * 16);
     }
     float factor[NT][2];
     int seen_lo = 0, seen_hi = 0x7FFFFFFF;  // keys that every row of the tile sees
@@ -470,17 +579,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
 
     for (; r < r1; r += kWarps, ++k) {
       const int step = at.step + r - r0;
+      if (step >= at.span.steps) break;  // padding: the CTA has no other item
       const int j0 = (at.span.first + step) * kStep;
-      if (!dead && !mbar_wait(bar + 8 * stage, phase)) {
-        dead = true;
-        if (lane == 0) atomicOr(cache.flag, WD_KV_FLAG_TIMEOUT);
-      }
-      dead = __any_sync(kAll, dead);
       if (dead) break;
-      if (step >= at.span.steps) {  // padding, the last of the item: nothing was copied
-        issue_next();
-        continue;
-      }
+      const bool landed = mbar_wait(bar + 8 * stage, phase);
       const uint8_t* buf = ring + stage * L::kStageBytes;
 
       // ---- S^T = K Q^T
@@ -491,12 +593,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[u][nt][e] = 0.f;
-      Words<NW> ks[2][2];
+      uint32_t kf[2][2][CB / 2];  // the scales of keys 16u + 8h + g, BF16, two blocks to a word
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          ks[u][h] = lds_scales<CB>(buf + u * G::kBytes + G::kKScale + (8 * h + g) * CB);
+        for (int h = 0; h < 2; ++h) {
+          const Words<NW> w = lds_scales<CB>(buf + u * G::kBytes + G::kKScale + (8 * h + g) * CB);
+#pragma unroll
+          for (int c = 0; c < CB / 2; ++c) kf[u][h][c] = e8m0x2(w.v[c / 2] >> (16 * (c & 1)));
+        }
 #pragma unroll
       for (int sl = 0; sl < NS; ++sl) {
         Words<SB> kw[2][2];
@@ -514,14 +619,16 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
           for (int nt = 0; nt < NT; ++nt)
             q[nt] = kQInRegs ? qf[kQInRegs ? cb : 0]
                              : *reinterpret_cast<const uint4*>(
-                                   smem + L::kQ + ((nt * CB + cb) * 32 + lane) * 16);
+                                   q_sh + ((nt * CB + cb) * 32 + lane) * 16);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
             e2m1x8(kw[u][0].v[c], a0, a2, b0, b2);
             e2m1x8(kw[u][1].v[c], a1, a3, b1, b3);
-            const float s0 = __uint_as_float(((ks[u][0].v[cb / 4] >> (8 * (cb % 4))) & 0xFFu) << 23);
-            const float s1 = __uint_as_float(((ks[u][1].v[cb / 4] >> (8 * (cb % 4))) & 0xFFu) << 23);
+            const float s0 = __uint_as_float(cb & 1 ? kf[u][0][cb / 2] & 0xFFFF0000u
+                                                    : kf[u][0][cb / 2] << 16);
+            const float s1 = __uint_as_float(cb & 1 ? kf[u][1][cb / 2] & 0xFFFF0000u
+                                                    : kf[u][1][cb / 2] << 16);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float t[4];
@@ -536,55 +643,97 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
         }
       }
 
-      // ---- the scales of token j0 + lane: are all of them in range?
-      const bool inside = j0 + lane < at.span.end;
-      bool slow = false;
-      {
-        const uint8_t* sc = buf + (lane >> 4) * G::kBytes + (lane & 15) * CB;
-        const Words<NW> kt = lds_scales<CB>(sc + G::kKScale);
-        Words<NW> vt = lds_scales<CB>(sc + G::kVScale);
-        bool odd = false, nan_k = false;
+      // ---- does anything change: a larger logit, a V scale out of range, keys behind the end?
+      const bool whole = j0 >= seen_lo && j0 + kStep - 1 <= seen_hi;
+      float top[NT][2];
+      bool odd = !landed;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          if (CB == 2) vt.v[w] |= ref[w] & 0xFFFF0000u;
-          nan_k |= (((kt.v[w] & 0x7F7F7F7Fu) + 0x01010101u) & kt.v[w] & 0x80808080u) != 0u;
-          const uint32_t t0 = ((ref[w] & 0x00FF00FFu) | 0x80008000u) - (vt.v[w] & 0x00FF00FFu);
-          const uint32_t t1 =
-              (((ref[w] >> 8) & 0x00FF00FFu) | 0x80008000u) - ((vt.v[w] >> 8) & 0x00FF00FFu);
-          odd |= ((t0 | t1) & 0x7FF07FF0u) != 0u;
-        }
-        if (__any_sync(kAll, inside && (odd || nan_k))) {
-          const uint32_t nan_tokens = __ballot_sync(kAll, inside && nan_k);
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float t = -INFINITY;
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (nan_tokens >> (16 * u + 8 * (e >> 1) + g) & 1u)
+            for (int h = 0; h < 2; ++h) {
+              float& x = s[u][nt][2 * h + e];
+              if (!whole) {
+                const int row = 8 * nt + 2 * tq + e, key = j0 + 16 * u + 8 * h + g;
+                if (key < lo_sh[row] || key > hi_sh[row]) x = -INFINITY;
+              }
+              t = fmaxf(t, x);
+            }
+          top[nt][e] = t * factor[nt][e];
+          odd |= top[nt][e] > m[nt][e];
+        }
+      // the V scales of key j0 + lane: all within [r - 15, r]?
+      const bool inside = j0 + lane < at.span.end;
+      Words<NW> vt = lds_scales<CB>(buf + (lane >> 4) * G::kBytes + G::kVScale + (lane & 15) * CB);
+      const auto out_of_range = [&]() {
+        bool bad = false;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) s[u][nt][e] = __uint_as_float(0x7FC00000u);
-          // raise the reference scales, and what stands on them
-          uint32_t bad = 0;
+        for (int w = 0; w < NW; ++w) {
+          const uint32_t v = CB == 2 ? vt.v[w] | (ref[w] & 0xFFFF0000u) : vt.v[w];
+          const uint32_t t0 = ((ref[w] & 0x00FF00FFu) | 0x80008000u) - (v & 0x00FF00FFu);
+          const uint32_t t1 = (((ref[w] >> 8) & 0x00FF00FFu) | 0x80008000u) - ((v >> 8) & 0x00FF00FFu);
+          bad |= ((t0 | t1) & 0x7FF07FF0u) != 0u;
+        }
+        return bad;
+      };
+      odd |= inside ? out_of_range() : true;
+      bool slow = false;
+      if (__any_sync(kAll, odd)) {
+        if (__any_sync(kAll, !landed)) {
+          dead = true;
+          if (lane == 0) atomicOr(cache.flag, WD_KV_FLAG_TIMEOUT);
+          break;
+        }
+        // the maxima, and what stands on them
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float t = fmaxf(m[nt][e], top[nt][e]);
+            t = fmaxf(t, __shfl_xor_sync(kAll, t, 4));
+            t = fmaxf(t, __shfl_xor_sync(kAll, t, 8));
+            t = fmaxf(t, __shfl_xor_sync(kAll, t, 16));
+            // both -inf: nothing stands yet
+            const float keep = m[nt][e] == -INFINITY ? 0.f : exp2_fast(m[nt][e] - t);
+            // (a NaN that stands there stays: a sum of NaN is not forgotten)
+            l[nt][e] = m[nt][e] == -INFINITY ? l[nt][e] : l[nt][e] * keep;
+            m[nt][e] = t;
+#pragma unroll
+            for (int c = 0; c < CB; ++c)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                o[c][j][nt][e] *= keep;
+                o[c][j][nt][2 + e] *= keep;
+              }
+          }
+        // the largest V scales, and what stands on them
+        if (__any_sync(kAll, inside && out_of_range())) {
+          bool bad = false;
 #pragma unroll
           for (int c = 0; c < CB; ++c) {
-            const uint32_t sh = 8 * (c % 4), mine = (vt.v[c / 4] >> sh) & 0xFFu;
+            const uint32_t sh = 8 * (c % 4), mine_c = (vt.v[c / 4] >> sh) & 0xFFu;
             const uint32_t old = (ref[c / 4] >> sh) & 0xFFu;
-            const uint32_t top =
-                max(old, __reduce_max_sync(kAll, inside && mine != 255u ? mine : 0u));
-            if (top != old) {
-              const float down = exp2_fast((float)(int)old - (float)(int)top);
+            const uint32_t most =
+                max(old, __reduce_max_sync(kAll, inside && mine_c != 255u ? mine_c : 0u));
+            if (most != old) {
+              const float down = exp2_fast((float)(int)old - (float)(int)most);
 #pragma unroll
               for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                   for (int e = 0; e < 4; ++e) o[c][j][nt][e] *= down;
-              ref[c / 4] = (ref[c / 4] & ~(0xFFu << sh)) | (top << sh);
+              ref[c / 4] = (ref[c / 4] & ~(0xFFu << sh)) | (most << sh);
             }
-            bad |= inside && (mine > top || mine + 15u < top) ? 1u : 0u;
+            bad |= inside && (mine_c > most || mine_c + 15u < most);
           }
-          slow = __any_sync(kAll, bad != 0u);
+          slow = __any_sync(kAll, bad);
         }
-        // keys behind the end get a scale in range; their probabilities are zero
+        // keys behind the end get scales in range; their probabilities are zero
         if (j0 + kStep > at.span.end) {
           if (!inside) {
             uint8_t* to = ring + stage * L::kStageBytes + (lane >> 4) * G::kBytes + G::kVScale +
@@ -600,59 +749,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
         }
       }
 
-      // ---- softmax
-      const bool whole = j0 >= seen_lo && j0 + kStep - 1 <= seen_hi;
-      float top[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float t = -INFINITY;
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float x = s[u][nt][2 * h + e] * factor[nt][e];
-              if (!whole) {
-                const int row = 8 * nt + 2 * tq + e, key = j0 + 16 * u + 8 * h + g;
-                if (key < lo_sh[row] || key > hi_sh[row]) x = -INFINITY;
-              }
-              s[u][nt][2 * h + e] = x;
-              t = fmaxf(t, x);
-            }
-          top[nt][e] = t;
-        }
-      bool grow = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float t = top[nt][e];
-          t = fmaxf(t, __shfl_xor_sync(kAll, t, 4));
-          t = fmaxf(t, __shfl_xor_sync(kAll, t, 8));
-          t = fmaxf(t, __shfl_xor_sync(kAll, t, 16));
-          top[nt][e] = fmaxf(m[nt][e], t);
-          grow |= t > m[nt][e];
-        }
-      if (__any_sync(kAll, grow)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            // both -inf: nothing stands yet, and 0 is kept
-            const float keep =
-                m[nt][e] == -INFINITY ? 0.f : exp2_fast(m[nt][e] - top[nt][e]);
-            m[nt][e] = top[nt][e];
-            l[nt][e] *= keep;
-#pragma unroll
-            for (int c = 0; c < CB; ++c)
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                o[c][j][nt][e] *= keep;
-                o[c][j][nt][2 + e] *= keep;
-              }
-          }
-      }
+      // ---- P = 2^14 exp2(x - max)
       uint32_t p[2][2][NT];  // P^T fragments: tokens 16u + 8h + 2tq + {0, 1} of column g
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -662,11 +759,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float p0 = exp2_fast(s[u][nt][2 * h] + z0);
-            const float p1_ = exp2_fast(s[u][nt][2 * h + 1] + z1);
+            const float p0 = exp2_fast(fmaf(s[u][nt][2 * h], factor[nt][0], z0));
+            const float p1 = exp2_fast(fmaf(s[u][nt][2 * h + 1], factor[nt][1], z1));
             l[nt][0] += p0;
-            l[nt][1] += p1_;
-            p[u][h][nt] = transpose8(pack_half2(p0, p1_));
+            l[nt][1] += p1;
+            p[u][h][nt] = transpose8(pack_half2(p0, p1));
           }
       }
 
@@ -791,6 +888,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
     }
 
     // ---- join the warps
+    if (r0 > 0) __syncthreads();  // the segment before has been read
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -804,43 +902,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
           l_sh[warp * kRows + 8 * nt + 2 * tq + e] = t;
         }
       }
-    const long long item = begin + r0 - at.step;  // the item's first step
-    const bool alone = at.step == 0 && r1 - r0 == at.padded;
-    const int first_cta = (int)(item / quota);
-    const int last_cta = (int)((item + at.padded - 1) / quota);
-    constexpr long long kSlot = (long long)kKvMaxRows * (D + 2);
-    const auto part_of = [&](int x) {
-      return a.partial + (2 * (long long)x + (item > (long long)x * quota ? 1 : 0)) * kSlot;
-    };
-    float* part = part_of(blockIdx.x);
-    const auto store_out = [&](int row, int ch, const float4& y, float sum) {
-      if (row >= rows) return;
-      const int flat = at.tile * kRows + row;
-      const long long o_at = ((long long)(entry.first + flat / group) * a.q_heads + at.head * group +
-                              flat % group) * D + ch;
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      uint16_t* to = static_cast<uint16_t*>(a.out) + o_at;
-      const float v[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
+    const auto write_round = [&](int round) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (a.half)
-          reinterpret_cast<__half*>(to)[q] = __float2half_rn(v[q]);
-        else
-          reinterpret_cast<__nv_bfloat16*>(to)[q] = __float2bfloat16_rn(v[q]);
-      }
-    };
-    const auto store_lse = [&](int row, float top, float sum) {
-      if (!a.lse || row >= rows) return;
-      const int flat = at.tile * kRows + row;
-      a.lse[(long long)(entry.first + flat / group) * a.q_heads + at.head * group + flat % group] =
-          sum == 0.f ? -INFINITY : (top - 14.f) * 0.6931471805599453f + logf(sum);
-    };
-#pragma unroll
-    for (int round = 0; round < L::kRounds; ++round) {
-      if (round > 0) __syncthreads();
-#pragma unroll
-      for (int cr = 0; cr < L::kRoundBlocks; ++cr) {
-        const int c = round * L::kRoundBlocks + cr;
+      for (int c = 0; c < CB; ++c) {
+        const int cr = c - round * L::kRoundBlocks;
+        if (cr < 0 || cr >= L::kRoundBlocks) continue;
         const float unit = exp2_int((int)((ref[c / 4] >> (8 * (c % 4))) & 0xFFu) - 128);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -850,6 +916,33 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
                 merge + (warp * kRows + 8 * nt + 2 * tq + e) * L::kMergeRow + 32 * cr + 4 * g) =
                 make_float4(o[c][0][nt][e] * unit, o[c][0][nt][2 + e] * unit,
                             o[c][1][nt][e] * unit, o[c][1][nt][2 + e] * unit);
+      }
+    };
+    write_round(0);
+    Part part;
+    part.item = begin + r0 - at.step;
+    part.first_cta = (int)(part.item / quota);
+    part.last_cta = (int)((part.item + at.padded - 1) / quota);
+    part.tile = at.tile;
+    part.head = at.head;
+    part.first = entry.first;
+    part.n = entry.n;
+    const bool alone = at.step == 0 && r1 - r0 == at.padded;
+    float* to = part_at(a, part, blockIdx.x, quota);
+    if (!alone) {
+      if (threadIdx.x == 0) parts_sh[pending] = part;
+      ++pending;
+    }
+    // what comes next, while the slower warps finish
+    if (r1 < mine) {
+      at = locate<kRows>(a, order, begin + r1, entry);
+      load_queries(at, entry, which ^ 1);
+    }
+#pragma unroll
+    for (int round = 0; round < L::kRounds; ++round) {
+      if (round > 0) {
+        __syncthreads();
+        write_round(round);
       }
       __syncthreads();
       constexpr int kQuads = 8 * L::kRoundBlocks;  // four channels each, of a row
@@ -876,71 +969,80 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
         }
         const int at_ch = 32 * round * L::kRoundBlocks + ch;
         if (alone) {
-          store_out(row, at_ch, y, sum);
-          if (at_ch == 0) store_lse(row, top, sum);
+          store_row<D, kRows>(a, part, row, at_ch, y, top, sum);
         } else {
-          __stcg(reinterpret_cast<float4*>(part + row * D + at_ch), y);
+          __stcg(reinterpret_cast<float4*>(to + row * D + at_ch), y);
           if (at_ch == 0) {
-            __stcg(part + kRows * D + row, top);
-            __stcg(part + kRows * D + kRows + row, sum);
+            __stcg(to + kRows * D + row, top);
+            __stcg(to + kRows * D + kRows + row, sum);
           }
         }
-      }
-    }
-    if (!alone) {
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0)
-        last_sh = atomicAdd(a.counters + first_cta, 1u) == (uint32_t)(last_cta - first_cta);
-      __syncthreads();
-      if (last_sh) {
-        // every part is there: join them in their order
-        __threadfence();
-        if (threadIdx.x == 0) a.counters[first_cta] = 0;
-        const int parts = last_cta - first_cta + 1;
-        float* factors = merge;  // [kRows][parts]
-        for (int row = warp; row < kRows; row += kWarps) {
-          float top = -INFINITY;
-          for (int x = lane; x < parts; x += 32)
-            top = fmaxf(top, __ldcg(part_of(first_cta + x) + kRows * D + row));
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(kAll, top, off));
-          float sum = 0.f;
-          for (int x = lane; x < parts; x += 32) {
-            const float* from = part_of(first_cta + x) + kRows * D + row;
-            const float f = top == -INFINITY ? 0.f : exp2_fast(__ldcg(from) - top);
-            const float lx = __ldcg(from + kRows);
-            sum += lx != lx ? lx : lx * f;
-            factors[row * parts + x] = f;
-          }
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
-          if (lane == 0) {
-            l_sh[row] = sum;
-            store_lse(row, top, sum);
-          }
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
-          const int row = i / (D / 4), ch = 4 * (i % (D / 4));
-          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int x = 0; x < parts; ++x) {
-            const float4 v = __ldcg(
-                reinterpret_cast<const float4*>(part_of(first_cta + x) + row * D + ch));
-            const float f = factors[row * parts + x];
-            y.x = fmaf(v.x, f, y.x);
-            y.y = fmaf(v.y, f, y.y);
-            y.z = fmaf(v.z, f, y.z);
-            y.w = fmaf(v.w, f, y.w);
-          }
-          store_out(row, ch, y, l_sh[row]);
-        }
-        __syncthreads();
       }
     }
     r0 = r1;
+  }
+  if (pending > 0) {
+    // the CTA that arrives last at an item joins its parts, in their order
+    __syncthreads();
+    if (threadIdx.x < pending) {
+      __threadfence();
+      const Part part = parts_sh[threadIdx.x];
+      const uint32_t others = (uint32_t)(part.last_cta - part.first_cta);
+      const bool last = atomicAdd(a.counters + part.first_cta, 1u) == others;
+      if (last) a.counters[part.first_cta] = 0;
+      __threadfence();
+      last_sh[threadIdx.x] = last;
+    }
+    __syncthreads();
+    for (int which = 0; which < pending; ++which) {
+      if (!last_sh[which]) continue;
+      const Part part = parts_sh[which];
+      const int parts = part.last_cta - part.first_cta + 1;
+      for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
+        const int row = i / (D / 4), ch = 4 * (i % (D / 4));
+        float top = -INFINITY, sum = 0.f;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kBatch = 8;  // parts on their way at a time
+        for (int x0 = 0; x0 < parts; x0 += kBatch) {
+          float mx[kBatch], lx[kBatch];
+          float4 v[kBatch];
+#pragma unroll
+          for (int x = 0; x < kBatch; ++x) {
+            mx[x] = -INFINITY;
+            lx[x] = 0.f;
+            v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x0 + x < parts) {
+              const float* from = part_at(a, part, part.first_cta + x0 + x, quota);
+              mx[x] = __ldcg(from + kRows * D + row);
+              lx[x] = __ldcg(from + kRows * D + kRows + row);
+              v[x] = __ldcg(reinterpret_cast<const float4*>(from + row * D + ch));
+            }
+          }
+          float next = top;
+#pragma unroll
+          for (int x = 0; x < kBatch; ++x) next = fmaxf(next, mx[x]);
+          const float keep = top == -INFINITY ? 0.f : exp2_fast(top - next);
+          if (x0 > 0) {
+            sum = sum != sum ? sum : sum * keep;
+            y.x *= keep;
+            y.y *= keep;
+            y.z *= keep;
+            y.w *= keep;
+          }
+          top = next;
+#pragma unroll
+          for (int x = 0; x < kBatch; ++x) {
+            const float f = top == -INFINITY ? 0.f : exp2_fast(mx[x] - top);
+            sum += lx[x] != lx[x] ? lx[x] : lx[x] * f;
+            y.x = fmaf(v[x].x, f, y.x);
+            y.y = fmaf(v[x].y, f, y.y);
+            y.z = fmaf(v[x].z, f, y.z);
+            y.w = fmaf(v[x].w, f, y.w);
+          }
+        }
+        store_row<D, kRows>(a, part, row, ch, y, top, sum);
+      }
+    }
   }
   if (dead) {
     // give up, but not before the copies in flight have landed (or as long again has passed)

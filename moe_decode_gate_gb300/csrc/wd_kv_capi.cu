@@ -197,6 +197,7 @@ wd_status wd_kv_attention(const wd_kv_cache* cache, int layer, const void* q, wd
       q_heads % cache->kv_heads || max_q < 0 || window < 0)
     return WD_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !(scale < INFINITY)) return WD_ERR_INVALID_ARG;
+  if ((long long)tokens * q_heads >= (1ll << 31)) return WD_ERR_UNSUPPORTED_SHAPE;
   if (tokens == 0 || entries == 0) return WD_OK;
   if (!q || !out || !aligned(q, 2) || !aligned(out, 2) || !aligned(lse, 4))
     return WD_ERR_INVALID_ARG;
