@@ -18,8 +18,10 @@
 //   - K: the sums over a block of 32 channels are scaled by the block's 2^(s-127) in FP32.
 //   - Queries are FP16 x 2^k with k per row (exact for BF16 and FP16 within 2^31 of the row's
 //     largest magnitude), 2^-k folded into the softmax scale.
-//   - P = 2^14 exp2(x - max) is rounded to FP16 once (11 bits; below 2^-28 of the largest it
-//     loses bits, below 2^-39 it is zero); the row sums are of the unrounded values, in FP32.
+//   - P = 2^8 exp2(x - m) is rounded to FP16 once; the row sums are of the unrounded values, in
+//     FP32.  m follows the running maximum only when that has grown by more than 2^6, so that
+//     hardly any step has to rescale what stands on it: P stays below 2^14 and has its 11 bits
+//     down to 2^-22 of 2^m (2^-16 of the largest at worst) and an error of 2^-33 of 2^m below.
 //   - V: the scales lie along the channels that are the product's rows, so each of P's
 //     columns is multiplied by 2^(s - r + 1) for every block, with r the largest scale that the warp
 //     has met for that block of channels: exact while s >= r - 15. A step that holds other
@@ -34,6 +36,8 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 32;     // keys of a warp's step: two groups
 constexpr int kCached = 256;  // entries whose slot and length are kept in shared memory
+constexpr float kBias = 8.f;  // P = 2^kBias at the reference m ...
+constexpr float kSlack = 6.f; // ... which may fall this far behind the maximum (log2)
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 template <int D, int NT>
@@ -176,10 +180,16 @@ struct Order {
   const int2* cached;       // slot and length of the first kCached entries
   int pad, group;
 };
-__device__ __forceinline__ Entry load_entry(const KvAttentionArgs& a, int b) {
+__device__ __forceinline__ Entry load_entry(const KvAttentionArgs& a, int b,
+                                            const int2* cached = nullptr) {
   Entry e;
-  e.slot = kv_slot(a.cache, a.batch, b);
-  e.len = e.slot < 0 ? 0 : kv_length(a.cache, e.slot);
+  if (cached && b < kCached) {
+    e.slot = cached[b].x;
+    e.len = cached[b].y;
+  } else {
+    e.slot = kv_slot(a.cache, a.batch, b);
+    e.len = e.slot < 0 ? 0 : kv_length(a.cache, e.slot);
+  }
   kv_tokens(a.cache, a.batch, b, e.first, e.n);
   return e;
 }
@@ -198,14 +208,7 @@ __device__ __forceinline__ Place locate(const KvAttentionArgs& a, const Order& o
   }
   Place at;
   at.entry = lo;
-  if (lo < kCached) {
-    const int2 c = o.cached[lo];
-    e.slot = c.x;
-    e.len = c.y;
-    kv_tokens(a.cache, a.batch, lo, e.first, e.n);
-  } else {
-    e = load_entry(a, lo);
-  }
+  e = load_entry(a, lo, o.cached);
   long long rest = p - o.prefix[lo];
   const int heads = a.cache.kv_heads;
   // (the last tile and head are also where it ends if someone rewrites the lengths meanwhile)
@@ -222,23 +225,25 @@ __device__ __forceinline__ Place locate(const KvAttentionArgs& a, const Order& o
   return at;
 }
 
-// Eight values of a query row, from wherever they lie.
-__device__ __forceinline__ void load8(const KvAttentionArgs& a, long long off, bool vec,
-                                      float (&x)[8]) {
+// Eight 16-bit values of a query row, from wherever they lie.
+__device__ __forceinline__ Words<4> load8(const KvAttentionArgs& a, long long off, bool vec) {
   const uint16_t* s = static_cast<const uint16_t*>(a.q) + off;
-  uint32_t w[4];
+  Words<4> w;
   if (vec) {
     const uint4 v = *reinterpret_cast<const uint4*>(s);
-    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+    w.v[0] = v.x; w.v[1] = v.y; w.v[2] = v.z; w.v[3] = v.w;
   } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = s[2 * k] | ((uint32_t)s[2 * k + 1] << 16);
+    for (int k = 0; k < 4; ++k) w.v[k] = s[2 * k] | ((uint32_t)s[2 * k + 1] << 16);
   }
+  return w;
+}
+__device__ __forceinline__ void widen8(const Words<4>& w, bool half, float (&x)[8]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float2 f = a.half ? __half22float2(*reinterpret_cast<const __half2*>(&w[k]))
-                            : make_float2(__uint_as_float(w[k] << 16),
-                                          __uint_as_float(w[k] & 0xFFFF0000u));
+    const float2 f = half ? __half22float2(*reinterpret_cast<const __half2*>(&w.v[k]))
+                          : make_float2(__uint_as_float(w.v[k] << 16),
+                                        __uint_as_float(w.v[k] & 0xFFFF0000u));
     x[2 * k] = f.x;
     x[2 * k + 1] = f.y;
   }
@@ -277,7 +282,7 @@ __device__ __forceinline__ void store_row(const KvAttentionArgs& a, const Part& 
       reinterpret_cast<__nv_bfloat16*>(to)[q] = __float2bfloat16_rn(v[q]);
   }
   if (a.lse && ch == 0)
-    a.lse[at] = sum == 0.f ? -INFINITY : (top - 14.f) * 0.6931471805599453f + logf(sum);
+    a.lse[at] = sum == 0.f ? -INFINITY : (top - kBias) * 0.6931471805599453f + logf(sum);
 }
 
 template <int D, int NT>
@@ -315,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
   // least kLeast rounds of its warps where an item has as many: fewer would only add parts to
   // join, and a join through memory costs as much as two rounds.
   constexpr int kLeast = 3;
-  constexpr int kTries = 8;
+  constexpr int kTries = kWarps;
   Order order{prefix, cached, 1, group};
   Entry own{-1, 0, 0, 0};
   if ((int)threadIdx.x < a.batch.entries) own = load_entry(a, threadIdx.x);
@@ -341,16 +346,16 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
     items = __reduce_add_sync(kAll, min(items, 1 << 24));
     if (lane == 0) {
       scan[warp] = steps_here;
-      scan2[warp * 8] = longest;
-      scan2[warp * 8 + 1] = items;
+      scan2[8 + 2 * warp] = longest;
+      scan2[9 + 2 * warp] = items;
     }
     __syncthreads();
     items = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       total += scan[w];
-      longest = max(longest, scan2[w * 8]);
-      items += min(scan2[w * 8 + 1], 1 << 24);
+      longest = max(longest, scan2[8 + 2 * w]);
+      items += min(scan2[9 + 2 * w], 1 << 24);
     }
   }
   const long long rounds = (total + (long long)gridDim.x * kWarps - 1) /
@@ -360,36 +365,26 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
     // the shortest of some quotas at which the CTAs suffice
     const int lowest = max(quota, min(kLeast, (longest + kWarps - 1) / kWarps) * kWarps);
     const auto try_quota = [&](int i) {  // times 16, 17, 18, 20, 24, 32, 48, 64 sixteenths
-      constexpr int kBy[kTries] = {16, 17, 18, 20, 24, 32, 48, 64};
-      return (int)(((long long)lowest * kBy[i] / 16 + kWarps - 1) / kWarps) * kWarps;
+      const int by = i < 3 ? 16 + i : i < 5 ? 12 + 4 * (i - 1) : i < 6 ? 32 : 16 * (i - 3);
+      return (int)((((long long)lowest * by >> 4) + kWarps - 1) >> 3 << 3);
     };
-    int need[kTries] = {0};
     if (longest <= lowest) {  // no item needs two CTAs
       order.pad = quota = lowest;
     } else {
-      for (int b = threadIdx.x; b < a.batch.entries; b += kThreads) {
-        const Entry e = b < kThreads ? own : load_entry(a, b);
+      const unsigned q = try_quota(warp);  // a warp to each
+      int need = 0;
+      for (int b = lane; b < a.batch.entries; b += 32) {
+        const Entry e = load_entry(a, b, cached);
         const int tiles = tiles_of<kRows>(e, group);
-        for (int t = 0; t < tiles; ++t) {
-          const int steps = tile_span<kRows>(e, t, group, a.window).steps;
-#pragma unroll
-          for (int i = 0; i < kTries; ++i) need[i] += (steps + try_quota(i) - 1) / try_quota(i);
-        }
+        for (int t = 0; t < tiles; ++t)
+          need += (int)((unsigned)tile_span<kRows>(e, t, group, a.window).steps + q - 1) / q;
       }
+      need = __reduce_add_sync(kAll, need);
+      if (lane == 0) scan2[warp] = need;
       __syncthreads();
 #pragma unroll
-      for (int i = 0; i < kTries; ++i) {
-        need[i] = __reduce_add_sync(kAll, need[i]);
-        if (lane == 0) scan2[warp * 8 + i] = need[i];
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = kTries - 1; i >= 0; --i) {
-        int all = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) all += scan2[w * 8 + i];
-        if ((long long)all * heads <= (long long)gridDim.x) order.pad = quota = try_quota(i);
-      }
+      for (int i = kTries - 1; i >= 0; --i)
+        if ((long long)scan2[i] * heads <= (long long)gridDim.x) order.pad = quota = try_quota(i);
     }
   }
   // prefix[b] = steps, with the padding, of the entries before b
@@ -459,9 +454,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
     if (bytes0) bulk_g2s_nohint(to, src0, bytes0, full);
     if (src1) bulk_g2s_nohint(to + G::kBytes, src1, G::kBytes, full);
   };
-  plan(0);
-  if (lane < kStages && warp + kWarps * lane < mine) issue(lane);
-  __syncwarp();
 
   const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.q_token % 8 == 0 &&
                    a.q_head % 8 == 0;
@@ -483,19 +475,33 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
   };
   // A tile's queries as fragments: channel 32c + 8t + 4j + 2i + {0,1} of row 8nt + g is register
   // i of product j in lane 4g + t.  Four lanes to a block of 32 channels.
-  const auto load_queries = [&](const Place& at, const Entry& entry, int which) {
+  constexpr int kQueryPasses = (kRows * (D / 8) + kThreads - 1) / kThreads;
+  Words<4> query[kQueryPasses];
+  const auto fetch_queries = [&](const Place& at, const Entry& entry) {
     const int rows = entry.n * group - at.tile * kRows;  // of the tile's, those that are real
+#pragma unroll
+    for (int pass = 0; pass < kQueryPasses; ++pass) {
+      const int i = threadIdx.x + pass * kThreads;
+      const int row = i / (D / 8), e8 = i % (D / 8);
+      const int flat = at.tile * kRows + row;
+      query[pass] = Words<4>{{0u, 0u, 0u, 0u}};
+      if (row < kRows && row < rows)
+        query[pass] = load8(a, (entry.first + flat / group) * a.q_token +
+                                   (at.head * group + flat % group) * a.q_head + 8 * e8, vec);
+    }
+  };
+  const auto put_queries = [&](const Place& at, const Entry& entry, int which) {
+    const int rows = entry.n * group - at.tile * kRows;
     float* factor_sh = reinterpret_cast<float*>(smem + L::kRowInfo) + which * 3 * kRows;
     int* lo_sh = reinterpret_cast<int*>(factor_sh + kRows);
     int* hi_sh = lo_sh + kRows;
-    for (int i = threadIdx.x; i < kRows * (D / 8); i += kThreads) {
+#pragma unroll
+    for (int pass = 0; pass < kQueryPasses; ++pass) {
+      const int i = threadIdx.x + pass * kThreads;
       const int row = i / (D / 8), e8 = i % (D / 8);
-      const int flat = at.tile * kRows + row;
-      const int token = flat / group;
-      float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (row < rows)
-        load8(a, (entry.first + token) * a.q_token + (at.head * group + flat % group) * a.q_head +
-                     8 * e8, vec, x);
+      if (row >= kRows) break;  // (whole warps)
+      float x[8];
+      widen8(query[pass], a.half, x);
       uint32_t bits = 0;
 #pragma unroll
       for (int q = 0; q < 8; ++q) bits = max(bits, __float_as_uint(x[q]) & 0x7FFFFFFFu);
@@ -514,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
       *reinterpret_cast<uint4*>(smem + L::kQ + which * L::kQBytes +
                                 (((row >> 3) * CB + (e8 >> 2)) * 32 + (row & 7) * 4 + (e8 & 3)) * 16) = f;
       if (e8 == 0) {
-        const int pos = entry.len - entry.n + token;
+        const int pos = entry.len - entry.n + (at.tile * kRows + row) / group;
         // a row with an infinity or NaN has no finite logit; never 0, so that -inf stays -inf
         factor_sh[row] = bad ? __uint_as_float(0x7FC00000u)
                              : fmaxf(a.scale * 1.4426950408889634f / up / up2, 1.2e-38f);
@@ -526,7 +532,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
   };
   Entry entry;
   Place at = locate<kRows>(a, order, begin, entry);
-  load_queries(at, entry, 0);
+  fetch_queries(at, entry);
+  plan(0);
+  if (lane < kStages && warp + kWarps * lane < mine) issue(lane);
+  __syncwarp();
+  put_queries(at, entry, 0);
   __syncthreads();
   int pending = 0;  // parts of items that other CTAs have parts of: at most the first and the last
   for (int r0 = 0, which = 0; r0 < mine; which ^= 1) {
@@ -664,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
               t = fmaxf(t, x);
             }
           top[nt][e] = t * factor[nt][e];
-          odd |= top[nt][e] > m[nt][e];
+          odd |= top[nt][e] > m[nt][e] + kSlack;
         }
       // the V scales of key j0 + lane: all within [r - 15, r]?
       const bool inside = j0 + lane < at.span.end;
@@ -697,6 +707,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
             t = fmaxf(t, __shfl_xor_sync(kAll, t, 4));
             t = fmaxf(t, __shfl_xor_sync(kAll, t, 8));
             t = fmaxf(t, __shfl_xor_sync(kAll, t, 16));
+            if (t <= m[nt][e] + kSlack) t = m[nt][e];
             // both -inf: nothing stands yet
             const float keep = m[nt][e] == -INFINITY ? 0.f : exp2_fast(m[nt][e] - t);
             // (a NaN that stands there stays: a sum of NaN is not forgotten)
@@ -749,12 +760,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
         }
       }
 
-      // ---- P = 2^14 exp2(x - max)
+      // ---- P = 2^kBias exp2(x - m)
       uint32_t p[2][2][NT];  // P^T fragments: tokens 16u + 8h + 2tq + {0, 1} of column g
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float z0 = m[nt][0] == -INFINITY ? 0.f : 14.f - m[nt][0];
-        const float z1 = m[nt][1] == -INFINITY ? 0.f : 14.f - m[nt][1];
+        const float z0 = m[nt][0] == -INFINITY ? 0.f : kBias - m[nt][0];
+        const float z1 = m[nt][1] == -INFINITY ? 0.f : kBias - m[nt][1];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -936,7 +947,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
     // what comes next, while the slower warps finish
     if (r1 < mine) {
       at = locate<kRows>(a, order, begin + r1, entry);
-      load_queries(at, entry, which ^ 1);
+      fetch_queries(at, entry);
+      put_queries(at, entry, which ^ 1);
     }
 #pragma unroll
     for (int round = 0; round < L::kRounds; ++round) {
