@@ -114,16 +114,16 @@ __device__ __forceinline__ uint8_t* kv_group(const KvView& v, int page, int laye
          ((pos & (v.page_size - 1)) >> 4) * group_bytes;
 }
 
-// Scratch inside a cache's workspace.  Attention: one arrival counter per CTA
-// and two partial results per CTA.  Pages: lists of page ids, chunk counts,
-// staged table rows and per-slot owners.
-constexpr int kKvMaxCtas = 304;       // attention CTAs that a workspace has room for
-constexpr int kKvMaxRows = 32;        // query rows of one attention tile
+// Scratch inside a cache's workspace.  Attention: an arrival counter and two
+// partial results per unit (what a CTA does in one pass).  Pages: lists of page ids, chunk
+// counts, staged table rows and per-slot owners.
+constexpr int kKvSms = 152;           // what the attention's grid is made for
+constexpr int kKvMaxUnits = 8 * kKvSms;  // units of 8 query rows that there is room for
 constexpr int kKvChunkPages = 4096;   // pages that one CTA counts in wd_kv_compact
 
 struct KvScratch {
-  uint32_t* counters;  // [kKvMaxCtas], zero between calls
-  float* partial;      // [2 * kKvMaxCtas][kKvMaxRows][head_dim + 2]
+  uint32_t* counters;  // [kKvMaxUnits], zero between calls
+  float* partial;      // [2 * kKvMaxUnits][8][head_dim + 2]
   int32_t* list_a;     // [num_pages]
   int32_t* list_b;     // [num_pages]
   int32_t* list_c;     // [num_pages]

@@ -1,20 +1,21 @@
 // wd_kv_attention.cu - attention over the 4-bit cache (declared in include/wd_kv.h).
 //
 // Work.  An item is (entry, tile of 8 * NT query rows, key head); the rows of a tile are the
-// heads that share the key head and, behind them, further new tokens.  An item is cut into steps
-// of 32 keys, and all steps of the call, in order, are dealt out evenly over a grid of as many
-// CTAs as fit the GPU: a CTA takes a contiguous range of steps and its eight warps take turns in
-// it.  The lengths are known to the device alone, so every CTA derives the whole division from
-// them; a captured graph can be replayed while the sequences grow.  A CTA that has all of an
-// item writes its output; else it leaves a partial result (maximum, sum, output) in the
-// workspace, and the CTA that arrives last joins the parts in their order.
+// heads that share the key head and, behind them, further new tokens.  An item is cut into pieces
+// of q steps of 32 keys, a warp to a piece, and the pieces of the call, in order, are dealt out
+// to the warps of as many CTAs as fit the GPU (eight pieces to a CTA, in several passes if they
+// are many).  The lengths are known to the device alone, so every CTA derives q and the whole
+// division from them; a captured graph can be replayed while the sequences grow.  A warp that
+// has all of an item writes its output; the pieces of one CTA meet in shared memory; and where an
+// item has pieces in several CTAs, each leaves a partial result (maximum, sum, output) in
+// the workspace, and the CTA that arrives last joins them in their order.
 //
 // A step.  Each warp streams its steps' groups (2176 bytes per 16 keys at head_dim 128) with
 // bulk copies into a ring of its own.  With K as the left operand, S^T = K Q^T and O^T = V^T P^T
 // are m16n8k16 products whose 16 rows are keys or channels and whose 8 columns are query rows,
-// so eight query heads fill a tile, where a 16-row query tile would be half empty.  The groups are stored in
-// fragment order: one 16-byte shared-memory read per lane brings 32 codes, which the hardware
-// conversion turns into FP16 (exactly) in place.
+// so eight query heads fill a tile, where a 16-row query tile would be half empty.  The groups are
+// stored in fragment order: one 16-byte shared-memory read per lane brings 32 codes, which the
+// hardware conversion turns into FP16 (exactly) in place.
 //   - K: the sums over a block of 32 channels are scaled by the block's 2^(s-127) in FP32.
 //   - Queries are FP16 x 2^k with k per row (exact for BF16 and FP16 within 2^31 of the row's
 //     largest magnitude), 2^-k folded into the softmax scale.
@@ -34,11 +35,19 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStep = 32;     // keys of a warp's step: two groups
-constexpr int kCached = 256;  // entries whose slot and length are kept in shared memory
-constexpr float kBias = 8.f;  // P = 2^kBias at the reference m ...
-constexpr float kSlack = 6.f; // ... which may fall this far behind the maximum (log2)
+constexpr int kStep = 32;      // keys of a step: two groups
+constexpr int kCached = 256;   // entries whose slot and length are kept in shared memory
+constexpr int kChoices = 32;   // divisions of the work that are compared
+constexpr float kBias = 8.f;   // P = 2^kBias at the reference m ...
+constexpr float kSlack = 6.f;  // ... which may fall this far behind the maximum (log2)
 constexpr uint32_t kAll = 0xFFFFFFFFu;
+
+// A warp's piece of an item, and where the item's output goes.
+struct Part {
+  long long slot0;  // the place of the item's first piece among all pieces
+  int pieces;       // of the item; 0: nothing to do
+  int tile, head, first, n;
+};
 
 template <int D, int NT>
 struct Shape {
@@ -47,6 +56,9 @@ struct Shape {
   static constexpr int kStageBytes = 2 * G::kBytes;
   static constexpr int kStages = D == 64 ? 4 : 2;
   static constexpr int kCtasPerSm = D <= 128 && NT == 1 ? 2 : 1;
+  // One tile of queries fits the registers; more are shared by the CTA's warps, whose
+  // pieces are then always of one item.
+  static constexpr bool kShared = NT > 1;
   // the warps' outputs are joined through shared memory, in one round where it has room for all
   static constexpr int kRounds = D == 256 ? 2 * NT : D == 128 && NT == 4 ? 2 : 1;
   static constexpr int kRoundBlocks = G::kBlocks / kRounds;
@@ -54,16 +66,18 @@ struct Shape {
   // shared memory, in bytes from its start
   static constexpr int kRing = 0;
   static constexpr int kQ = kRing + kWarps * kStages * kStageBytes;  // fragments [NT][blocks][32] uint4
-  static constexpr int kQBytes = NT * G::kBlocks * 512;                // twice: this segment's, the next's
-  static constexpr int kMerge = kQ + 2 * kQBytes;  // float [kWarps][kRows][kMergeRow]
+  static constexpr int kMerge = kQ + (kShared ? NT * G::kBlocks * 512 : 0);  // float [kWarps][kRows][kMergeRow]
   static constexpr int kStats = kMerge + kWarps * kRows * kMergeRow * 4;  // float m, l [kWarps][kRows]
-  static constexpr int kRowInfo = kStats + 2 * kWarps * kRows * 4;   // twice: factor, lo, hi [kRows]
-  static constexpr int kBars = kRowInfo + 2 * 3 * kRows * 4;         // uint64 [kWarps][kStages]
-  static constexpr int kScan = kBars + kWarps * kStages * 8;         // long long [kWarps], int [kWarps][8]
-  static constexpr int kPrefix = kScan + kWarps * 8 + kWarps * 32;   // long long [entries + 1]
+  static constexpr int kRowInfo = kStats + 2 * kWarps * kRows * 4;  // factor, lo, hi [kRows], of each warp or all
+  static constexpr int kParts = kRowInfo + (kShared ? 1 : kWarps) * 3 * kRows * 4;  // Part [kWarps]
+  static constexpr int kBars = kParts + kWarps * (int)sizeof(Part);  // uint64 [kWarps][kStages]
+  static constexpr int kScan = kBars + kWarps * kStages * 8;         // long long [kWarps]
+  static constexpr int kScan2 = kScan + kWarps * 8;                  // int [kChoices]
+  static constexpr int kPrefix = kScan2 + kChoices * 4;              // long long [entries + 1]
   static constexpr int shared_bytes(int entries) {  // ... and int2 [min(entries, kCached)]
     return kPrefix + 8 * (entries + 1) + 8 * (entries < kCached ? entries : kCached);
   }
+  static_assert(kBars % 8 == 0 && kParts % 8 == 0, "alignment");
   static_assert(kPrefix + 8 * (WD_KV_MAX_ENTRIES + 1) + 8 * kCached <= 227 * 1024, "shared memory");
 };
 
@@ -146,40 +160,6 @@ __device__ __forceinline__ Words<(CB + 3) / 4> lds_scales(const uint8_t* p) {
 struct Entry {
   int slot, len, first, n;
 };
-
-// The steps of keys that a tile of query rows sees: at least one, so that a tile that sees
-// nothing is written too.
-struct Span {
-  int first, steps;  // in steps of kStep keys
-  int end;           // keys from here on are not seen
-};
-template <int kRows>
-__device__ __forceinline__ Span tile_span(const Entry& e, int tile, int group, int window) {
-  int i0 = 0, i1 = e.n - 1;
-  if (e.n > 1) {
-    i0 = tile * kRows / group;
-    i1 = min(i1, (tile * kRows + kRows - 1) / group);
-  }
-  const int hi = e.len - e.n + i1;
-  const int lo = window > 0 ? max(0, e.len - e.n + i0 - window + 1) : 0;
-  Span s;
-  s.first = lo / kStep;
-  s.steps = hi < 0 ? 1 : max(1, hi / kStep + 1 - s.first);
-  s.end = hi + 1;
-  return s;
-}
-template <int kRows>
-__device__ __forceinline__ int tiles_of(const Entry& e, int group) {
-  return (e.n * group + kRows - 1) / kRows;
-}
-
-// All steps of the call in a row: entries, their tiles, the key heads, the item's steps (rounded
-// up to a multiple of `pad`).
-struct Order {
-  const long long* prefix;  // steps of the entries before each entry
-  const int2* cached;       // slot and length of the first kCached entries
-  int pad, group;
-};
 __device__ __forceinline__ Entry load_entry(const KvAttentionArgs& a, int b,
                                             const int2* cached = nullptr) {
   Entry e;
@@ -193,36 +173,46 @@ __device__ __forceinline__ Entry load_entry(const KvAttentionArgs& a, int b,
   kv_tokens(a.cache, a.batch, b, e.first, e.n);
   return e;
 }
-struct Place {
-  int entry, tile, head, step;
-  Span span;
-  int padded;  // steps with the padding
+template <int kRows>
+__device__ __forceinline__ int tiles_of(const Entry& e, int group) {
+  return (e.n * group + kRows - 1) / kRows;
+}
+
+// Steps that each of an entry's tiles is given: what the tile that sees the most needs, at least
+// one (a tile that sees nothing is written too).  The tiles of a causal chunk see unlike numbers
+// of keys; they are taken from both ends in turn, so that what is given and not needed
+// spreads over the warps.
+template <int kRows>
+__device__ __forceinline__ int steps_of(const Entry& e, int group, int window) {
+  if (e.len <= 0) return 1;
+  int steps = (e.len - 1) / kStep + 1;
+  if (window > 0) {
+    if (e.n == 1) {
+      steps -= max(0, e.len - window) / kStep;
+    } else {
+      const int tokens = min(e.n - 1, (kRows - 1) / group + 1);  // between a tile's ends
+      const long long keys = (long long)window + tokens;
+      steps = (int)min((long long)steps, (keys + kStep - 2) / kStep + 1);
+    }
+  }
+  return steps;
+}
+
+// The keys that a tile sees: from those of step `first` up to `end`.
+struct Span {
+  int first, end;
 };
 template <int kRows>
-__device__ __forceinline__ Place locate(const KvAttentionArgs& a, const Order& o, long long p,
-                                        Entry& e) {
-  int lo = 0, hi = a.batch.entries;  // the last entry whose steps begin at or before p
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (o.prefix[mid] <= p) lo = mid; else hi = mid;
+__device__ __forceinline__ Span tile_span(const Entry& e, int tile, int group, int window) {
+  int i0 = 0, i1 = e.n - 1;
+  if (e.n > 1) {
+    i0 = tile * kRows / group;
+    i1 = min(i1, (tile * kRows + kRows - 1) / group);
   }
-  Place at;
-  at.entry = lo;
-  e = load_entry(a, lo, o.cached);
-  long long rest = p - o.prefix[lo];
-  const int heads = a.cache.kv_heads;
-  // (the last tile and head are also where it ends if someone rewrites the lengths meanwhile)
-  const int tiles = max(1, tiles_of<kRows>(e, o.group));
-  for (at.tile = 0;; ++at.tile) {
-    at.span = tile_span<kRows>(e, at.tile, o.group, a.window);
-    at.padded = (at.span.steps + o.pad - 1) / o.pad * o.pad;
-    const long long cost = (long long)at.padded * heads;
-    if (rest < cost || at.tile + 1 == tiles) break;
-    rest -= cost;
-  }
-  at.head = min((int)((uint32_t)rest / (uint32_t)at.padded), heads - 1);
-  at.step = (int)((uint32_t)rest % (uint32_t)at.padded);
-  return at;
+  Span s;
+  s.first = window > 0 ? max(0, e.len - e.n + i0 - window + 1) / kStep : 0;
+  s.end = e.len - e.n + i1 + 1;
+  return s;
 }
 
 // Eight 16-bit values of a query row, from wherever they lie.
@@ -249,17 +239,12 @@ __device__ __forceinline__ void widen8(const Words<4>& w, bool half, float (&x)[
   }
 }
 
-// Part of an item that one CTA has done, and where the whole item's output goes.
-struct Part {
-  long long item;           // the item's first step
-  int first_cta, last_cta;  // that have parts of it
-  int tile, head, first, n;
-};
-// Where CTA x leaves its part: it has at most two, the first if the item began before it.
-__device__ __forceinline__ float* part_at(const KvAttentionArgs& a, const Part& p, int x,
-                                          int quota) {
-  const long long slot = 2 * (long long)x + (p.item > (long long)x * quota ? 1 : 0);
-  return a.partial + slot * kKvMaxRows * (a.cache.head_dim + 2);
+// Where CTA `unit` leaves its part of an item: it has at most two, that of an item that began
+// before it and that of one that goes on behind it.
+template <int kRows>
+__device__ __forceinline__ float* part_at(const KvAttentionArgs& a, const Part& p, int unit) {
+  const long long slot = 2 * (long long)unit + (p.slot0 >= (long long)unit * kWarps ? 1 : 0);
+  return a.partial + slot * kRows * (a.cache.head_dim + 2);
 }
 
 // Four channels of a finished row: y / sum, and with the first of them the row's lse.
@@ -285,6 +270,47 @@ __device__ __forceinline__ void store_row(const KvAttentionArgs& a, const Part& 
     a.lse[at] = sum == 0.f ? -INFINITY : (top - kBias) * 0.6931471805599453f + logf(sum);
 }
 
+// Scaling of a query row whose largest magnitude has these bits: 2^k brings it into
+// [2^14, 2^15) (subnormals are scaled as if 2^-126), in two factors.
+struct RowScale {
+  float up, up2;
+  bool bad;  // holds an infinity or NaN
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t bits) {
+  RowScale r;
+  r.bad = bits >= 0x7F800000u;
+  const int k = r.bad || bits == 0u ? 0 : 14 - (max((int)(bits >> 23), 1) - 127);
+  r.up = exp2_int(k / 2);
+  r.up2 = exp2_int(k - k / 2);
+  return r;
+}
+// What the row's sums are multiplied by: a row with an infinity or NaN has no finite logit;
+// never 0, so that -inf stays -inf.
+__device__ __forceinline__ float row_factor(const RowScale& r, float scale) {
+  return r.bad ? __uint_as_float(0x7FC00000u)
+               : fmaxf(scale * 1.4426950408889634f / r.up / r.up2, 1.2e-38f);
+}
+__device__ __forceinline__ uint4 row_fragment(const float (&x)[8], const RowScale& r) {
+  uint4 f;
+  f.x = pack_half2(x[0] * r.up * r.up2, x[1] * r.up * r.up2);
+  f.y = pack_half2(x[2] * r.up * r.up2, x[3] * r.up * r.up2);
+  f.z = pack_half2(x[4] * r.up * r.up2, x[5] * r.up * r.up2);
+  f.w = pack_half2(x[6] * r.up * r.up2, x[7] * r.up * r.up2);
+  return f;
+}
+
+// The i-th steps to a piece that is tried: around what fills one pass (`fair`), and what leaves an
+// item to one CTA or one warp.
+__device__ __forceinline__ int steps_choice(int i, int fair, int longest) {
+  if (i == 15) return longest;
+  if (i == 14) return (longest + kWarps - 1) / kWarps;
+  if (fair <= 6) return 1 + i;
+  constexpr uint64_t kLow = 0x1312111008060402ull;  // sixteenths of it, eight at a time
+  constexpr uint64_t kHigh = 0x0000402820181614ull;
+  const int by = (int)((i < 8 ? kLow >> (8 * i) : kHigh >> (8 * (i - 8))) & 0xFF);
+  return max(1, (int)(((long long)fair * by + 15) >> 4));
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
     kv_attention(const KvAttentionArgs a) {
@@ -292,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
   using L = Shape<D, NT>;
   constexpr int CB = G::kBlocks, SB = G::kSlabBlocks, NS = G::kSlabs, NW = (CB + 3) / 4;
   constexpr int kRows = L::kRows, kStages = L::kStages;
-  constexpr bool kQInRegs = NT == 1;
+  constexpr bool kQInRegs = !L::kShared;
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, tq = lane & 3;
@@ -301,103 +327,93 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
   float* merge = reinterpret_cast<float*>(smem + L::kMerge);
   float* m_sh = reinterpret_cast<float*>(smem + L::kStats);
   float* l_sh = m_sh + kWarps * kRows;
+  float* factor_sh =
+      reinterpret_cast<float*>(smem + L::kRowInfo) + (L::kShared ? 0 : warp) * 3 * kRows;
+  int* lo_sh = reinterpret_cast<int*>(factor_sh + kRows);
+  int* hi_sh = lo_sh + kRows;
+  Part* parts_sh = reinterpret_cast<Part*>(smem + L::kParts);
   long long* scan = reinterpret_cast<long long*>(smem + L::kScan);
-  int* scan2 = reinterpret_cast<int*>(scan + kWarps);
+  int* scan2 = reinterpret_cast<int*>(smem + L::kScan2);
   long long* prefix = reinterpret_cast<long long*>(smem + L::kPrefix);
   int2* cached = reinterpret_cast<int2*>(prefix + a.batch.entries + 1);
   uint8_t* ring = smem + L::kRing + warp * kStages * L::kStageBytes;
   const uint32_t bar = smem_u32(smem + L::kBars) + warp * kStages * 8;
-  __shared__ Part parts_sh[2];
   __shared__ int last_sh[2];
 
   if (lane == 0) {
     for (int s = 0; s < kStages; ++s) mbar_init(bar + 8 * s, 1);
     mbar_init_fence();
   }
-  // The division of the work.  Where there are no more items than CTAs, each item gets CTAs of
-  // its own (its steps are padded to a multiple of a CTA's), so that a CTA has one item to do;
-  // else the CTAs' ranges cross the items' bounds and are all of the same length.  A CTA takes at
-  // least kLeast rounds of its warps where an item has as many: fewer would only add parts to
-  // join, and a join through memory costs as much as two rounds.
-  constexpr int kLeast = 3;
-  constexpr int kTries = kWarps;
-  Order order{prefix, cached, 1, group};
+  // ---- the division of the work
   Entry own{-1, 0, 0, 0};
   if ((int)threadIdx.x < a.batch.entries) own = load_entry(a, threadIdx.x);
   long long total = 0;
-  int longest = 0, items = 0;
+  int longest = 1;
   {
     long long steps_here = 0;
     for (int b = threadIdx.x; b < a.batch.entries; b += kThreads) {
       const Entry e = b < kThreads ? own : load_entry(a, b);
       if (b < kCached) cached[b] = make_int2(e.slot, e.len);
-      const int tiles = tiles_of<kRows>(e, group);
-      for (int t = 0; t < tiles; ++t) {
-        const int steps = tile_span<kRows>(e, t, group, a.window).steps;
-        steps_here += steps;
-        longest = max(longest, steps);
-      }
-      items += tiles * heads;
+      const int steps = steps_of<kRows>(e, group, a.window);
+      steps_here += (long long)steps * tiles_of<kRows>(e, group);
+      if (e.n > 0) longest = max(longest, steps);
     }
-    steps_here *= heads;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) steps_here += __shfl_xor_sync(kAll, steps_here, off);
     longest = __reduce_max_sync(kAll, longest);
-    items = __reduce_add_sync(kAll, min(items, 1 << 24));
     if (lane == 0) {
       scan[warp] = steps_here;
-      scan2[8 + 2 * warp] = longest;
-      scan2[9 + 2 * warp] = items;
+      scan2[warp] = longest;
     }
     __syncthreads();
-    items = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       total += scan[w];
-      longest = max(longest, scan2[8 + 2 * w]);
-      items += min(scan2[9 + 2 * w], 1 << 24);
+      longest = max(longest, scan2[w]);
     }
+    total *= heads;
   }
-  const long long rounds = (total + (long long)gridDim.x * kWarps - 1) /
-                           ((long long)gridDim.x * kWarps);
-  int quota = (int)max(rounds, 1ll) * kWarps;
-  if (items <= (int)gridDim.x) {
-    // the shortest of some quotas at which the CTAs suffice
-    const int lowest = max(quota, min(kLeast, (longest + kWarps - 1) / kWarps) * kWarps);
-    const auto try_quota = [&](int i) {  // times 16, 17, 18, 20, 24, 32, 48, 64 sixteenths
-      const int by = i < 3 ? 16 + i : i < 5 ? 12 + 4 * (i - 1) : i < 6 ? 32 : 16 * (i - 3);
-      return (int)((((long long)lowest * by >> 4) + kWarps - 1) >> 3 << 3);
-    };
-    if (longest <= lowest) {  // no item needs two CTAs
-      order.pad = quota = lowest;
-    } else {
-      const unsigned q = try_quota(warp);  // a warp to each
-      int need = 0;
-      for (int b = lane; b < a.batch.entries; b += 32) {
-        const Entry e = load_entry(a, b, cached);
-        const int tiles = tiles_of<kRows>(e, group);
-        for (int t = 0; t < tiles; ++t)
-          need += (int)((unsigned)tile_span<kRows>(e, t, group, a.window).steps + q - 1) / q;
-      }
-      need = __reduce_add_sync(kAll, need);
-      if (lane == 0) scan2[warp] = need;
-      __syncthreads();
+  // Sixteen lengths of a piece, each with the pieces in a row and with every item at the start of
+  // a CTA, are rated in steps: the passes' longest pieces, two steps for what a pass begins and ends with,
+  // three for a join through memory.
+  const long long warps = (long long)gridDim.x * kWarps;
+  const int fair = (int)min((total + warps - 1) / warps, 1ll << 26);
+  __syncthreads();
+  for (int c = warp; c < kChoices; c += kWarps) {
+    const unsigned q = steps_choice(c >> 1, fair, longest);
+    const unsigned align = c & 1 ? kWarps : 1;
+    long long slots = 0;
+    for (int b = lane; b < a.batch.entries; b += 32) {
+      const Entry e = load_entry(a, b, cached);
+      const unsigned pieces = ((unsigned)steps_of<kRows>(e, group, a.window) + q - 1) / q;
+      slots += (long long)tiles_of<kRows>(e, group) * ((pieces + align - 1) / align * align);
+    }
 #pragma unroll
-      for (int i = kTries - 1; i >= 0; --i)
-        if ((long long)scan2[i] * heads <= (long long)gridDim.x) order.pad = quota = try_quota(i);
-    }
+    for (int off = 16; off > 0; off >>= 1) slots += __shfl_xor_sync(kAll, slots, off);
+    slots *= heads;
+    const long long units = (slots + kWarps - 1) / kWarps;
+    const long long passes = (units + gridDim.x - 1) / gridDim.x;
+    const bool across = (unsigned)longest > q * align;
+    const float cost = (passes == 1 ? (float)q : fmaxf((float)q, (float)fair + 0.75f * (float)q)) +
+                       2.f * (float)passes + (across ? 3.f : 0.f);
+    // joins across CTAs have room for so many
+    const bool fits = (!across || units <= kKvMaxUnits / NT) && (!L::kShared || align == kWarps);
+    if (lane == 0) scan2[c] = fits ? (int)fminf(cost * 16.f, 1e9f) : 0x7FFFFFFF;
   }
-  // prefix[b] = steps, with the padding, of the entries before b
+  __syncthreads();
+  const int cheapest = __reduce_min_sync(kAll, scan2[lane]);
+  const int choice = __ffs(__ballot_sync(kAll, scan2[lane] == cheapest)) - 1;
+  const unsigned q_steps = steps_choice(choice >> 1, fair, longest);
+  const unsigned align = choice & 1 ? kWarps : 1;
+  // prefix[b] = places of the entries before b
   total = 0;
   for (int base = 0; base < a.batch.entries; base += kThreads) {
     const int b = base + threadIdx.x;
     long long cost = 0;
     if (b < a.batch.entries) {
       const Entry e = b < kThreads ? own : load_entry(a, b);
-      const int tiles = tiles_of<kRows>(e, group);
-      for (int t = 0; t < tiles; ++t)
-        cost += (tile_span<kRows>(e, t, group, a.window).steps + order.pad - 1) / order.pad * order.pad;
-      cost *= heads;
+      const unsigned pieces = ((unsigned)steps_of<kRows>(e, group, a.window) + q_steps - 1) / q_steps;
+      cost = (long long)tiles_of<kRows>(e, group) * heads * ((pieces + align - 1) / align * align);
     }
     long long incl = cost;
 #pragma unroll
@@ -419,138 +435,161 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
   }
   if (threadIdx.x == 0) prefix[a.batch.entries] = total;
   __syncthreads();
-  const long long begin = (long long)blockIdx.x * quota;
-  if (begin >= total) return;
-  const int mine = (int)min(total - begin, (long long)quota);  // steps of this CTA
-
-  // The warp's steps are warp, warp + kWarps, ... of the CTA's: its k-th step's groups are
-  // worked out by lane k % 32, 32 steps at a time, and copied into stage k % kStages.
-  const uint8_t *src0 = nullptr, *src1 = nullptr;
-  uint32_t bytes0 = 0;
-  const auto plan = [&](int k0) {
-    const int r = warp + kWarps * (k0 + lane);
-    src0 = src1 = nullptr;
-    bytes0 = 0;
-    if (r >= mine) return;
-    Entry e;
-    const Place at = locate<kRows>(a, order, begin + r, e);
-    const int pos = (at.span.first + at.step) * kStep;
-    if (at.step >= at.span.steps || pos >= at.span.end) return;
-    src0 = kv_group(cache, kv_page(cache, e.slot, pos >> cache.page_shift), a.layer, at.head, pos,
-                    G::kBytes);
-    bytes0 = G::kBytes;
-    if (pos + 16 < at.span.end) {
-      if (cache.page_size >= kStep)  // the step lies within a page, its groups side by side
-        bytes0 = 2 * G::kBytes;
-      else
-        src1 = kv_group(cache, kv_page(cache, e.slot, (pos + 16) >> cache.page_shift), a.layer,
-                        at.head, pos + 16, G::kBytes);
-    }
-  };
-  const uint32_t ring_at = smem_u32(ring);
-  const auto issue = [&](int stage) {
-    const uint32_t to = ring_at + stage * L::kStageBytes, full = bar + 8 * stage;
-    mbar_arrive_expect_tx(full, bytes0 + (src1 ? G::kBytes : 0));
-    if (bytes0) bulk_g2s_nohint(to, src0, bytes0, full);
-    if (src1) bulk_g2s_nohint(to + G::kBytes, src1, G::kBytes, full);
-  };
+  const bool no_joins = (unsigned)longest <= q_steps;
 
   const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.q_token % 8 == 0 &&
                    a.q_head % 8 == 0;
-  int r = warp;  // the warp's next step, of the CTA's
-  int k = 0, stage = 0;
+  const uint32_t ring_at = smem_u32(ring);
+  int stage = 0;
   uint32_t phase = 0;
   bool dead = false;  // a wait ran out
-  // refill the stage that the k-th step has used, and go on to the next
-  const auto issue_next = [&]() {
-    __syncwarp();
-    const int next = k + kStages;
-    if ((next & 31) == 0) plan(next);
-    if (lane == (next & 31) && warp + kWarps * next < mine) issue(stage);
-    __syncwarp();
-    if (++stage == kStages) {
-      stage = 0;
-      phase ^= 1u;
-    }
-  };
-  // A tile's queries as fragments: channel 32c + 8t + 4j + 2i + {0,1} of row 8nt + g is register
-  // i of product j in lane 4g + t.  Four lanes to a block of 32 channels.
-  constexpr int kQueryPasses = (kRows * (D / 8) + kThreads - 1) / kThreads;
-  Words<4> query[kQueryPasses];
-  const auto fetch_queries = [&](const Place& at, const Entry& entry) {
-    const int rows = entry.n * group - at.tile * kRows;  // of the tile's, those that are real
-#pragma unroll
-    for (int pass = 0; pass < kQueryPasses; ++pass) {
-      const int i = threadIdx.x + pass * kThreads;
-      const int row = i / (D / 8), e8 = i % (D / 8);
-      const int flat = at.tile * kRows + row;
-      query[pass] = Words<4>{{0u, 0u, 0u, 0u}};
-      if (row < kRows && row < rows)
-        query[pass] = load8(a, (entry.first + flat / group) * a.q_token +
-                                   (at.head * group + flat % group) * a.q_head + 8 * e8, vec);
-    }
-  };
-  const auto put_queries = [&](const Place& at, const Entry& entry, int which) {
-    const int rows = entry.n * group - at.tile * kRows;
-    float* factor_sh = reinterpret_cast<float*>(smem + L::kRowInfo) + which * 3 * kRows;
-    int* lo_sh = reinterpret_cast<int*>(factor_sh + kRows);
-    int* hi_sh = lo_sh + kRows;
-#pragma unroll
-    for (int pass = 0; pass < kQueryPasses; ++pass) {
-      const int i = threadIdx.x + pass * kThreads;
-      const int row = i / (D / 8), e8 = i % (D / 8);
-      if (row >= kRows) break;  // (whole warps)
-      float x[8];
-      widen8(query[pass], a.half, x);
-      uint32_t bits = 0;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) bits = max(bits, __float_as_uint(x[q]) & 0x7FFFFFFFu);
-#pragma unroll
-      for (int off = 1; off < D / 8; off <<= 1)
-        bits = max(bits, __shfl_xor_sync(kAll, bits, off));
-      // 2^k brings the largest magnitude into [2^14, 2^15); subnormals are scaled as if 2^-126
-      const bool bad = bits >= 0x7F800000u;
-      const int k2 = bad || bits == 0u ? 0 : 14 - (max((int)(bits >> 23), 1) - 127);
-      const float up = exp2_int(k2 / 2), up2 = exp2_int(k2 - k2 / 2);
-      uint4 f;
-      f.x = pack_half2(x[0] * up * up2, x[1] * up * up2);
-      f.y = pack_half2(x[2] * up * up2, x[3] * up * up2);
-      f.z = pack_half2(x[4] * up * up2, x[5] * up * up2);
-      f.w = pack_half2(x[6] * up * up2, x[7] * up * up2);
-      *reinterpret_cast<uint4*>(smem + L::kQ + which * L::kQBytes +
-                                (((row >> 3) * CB + (e8 >> 2)) * 32 + (row & 7) * 4 + (e8 & 3)) * 16) = f;
-      if (e8 == 0) {
-        const int pos = entry.len - entry.n + (at.tile * kRows + row) / group;
-        // a row with an infinity or NaN has no finite logit; never 0, so that -inf stays -inf
-        factor_sh[row] = bad ? __uint_as_float(0x7FC00000u)
-                             : fmaxf(a.scale * 1.4426950408889634f / up / up2, 1.2e-38f);
-        const bool real = row < rows;  // no row: nothing to hide, never stored
-        lo_sh[row] = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
-        hi_sh[row] = real ? pos : at.span.end - 1;
+  for (int unit = blockIdx.x; (long long)unit * kWarps < total; unit += gridDim.x) {
+    // ---- the warp's piece
+    const long long slot = (long long)unit * kWarps + warp;
+    Part part;
+    part.pieces = 0;
+    part.slot0 = 0;
+    part.tile = part.head = part.first = part.n = 0;
+    Entry entry{-1, 0, 0, 0};
+    Span span{0, 0};
+    int from = 0, steps = 0;  // the piece: steps [from, from + steps) of the tile
+    if (slot < total) {
+      int lo = 0, hi = a.batch.entries;  // the last entry whose places begin at or before it
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= slot) lo = mid; else hi = mid;
+      }
+      entry = load_entry(a, lo, cached);
+      const int tiles = max(1, tiles_of<kRows>(entry, group));
+      const unsigned pieces =
+          ((unsigned)steps_of<kRows>(entry, group, a.window) + q_steps - 1) / q_steps;
+      const unsigned places = (pieces + align - 1) / align * align;
+      const unsigned long long rest = slot - prefix[lo];
+      unsigned item, piece;
+      if (rest >> 32) {
+        item = (unsigned)(rest / places);
+        piece = (unsigned)(rest % places);
+      } else {
+        item = (unsigned)rest / places;
+        piece = (unsigned)rest % places;
+      }
+      // (within bounds also if someone rewrites the lengths meanwhile)
+      const int turn = min((int)(item / heads), tiles - 1);
+      part.head = item % heads;
+      part.tile = turn & 1 ? tiles - 1 - (turn >> 1) : turn >> 1;
+      part.slot0 = slot - piece;
+      part.first = entry.first;
+      part.n = entry.n;
+      span = tile_span<kRows>(entry, part.tile, group, a.window);
+      if (piece < pieces) {
+        part.pieces = pieces;
+        from = piece * q_steps;
+        steps = min((int)q_steps, (span.end + kStep - 1) / kStep - span.first - from);
+        if (steps < 0 || dead) steps = 0;
       }
     }
-  };
-  Entry entry;
-  Place at = locate<kRows>(a, order, begin, entry);
-  fetch_queries(at, entry);
-  plan(0);
-  if (lane < kStages && warp + kWarps * lane < mine) issue(lane);
-  __syncwarp();
-  put_queries(at, entry, 0);
-  __syncthreads();
-  int pending = 0;  // parts of items that other CTAs have parts of: at most the first and the last
-  for (int r0 = 0, which = 0; r0 < mine; which ^= 1) {
-    const int r1 = min(mine, r0 + at.padded - at.step);  // the segment is [r0, r1)
-    const uint8_t* q_sh = smem + L::kQ + which * L::kQBytes;
-    const float* factor_sh = reinterpret_cast<const float*>(smem + L::kRowInfo) + which * 3 * kRows;
-    const int* lo_sh = reinterpret_cast<const int*>(factor_sh + kRows);
-    const int* hi_sh = lo_sh + kRows;
+    const int rows = entry.n * group - part.tile * kRows;  // of the tile's, those that are real
 
-    uint4 qf[kQInRegs ? CB : 1];
-    if constexpr (kQInRegs) {
+    // the queries are on their way while the pages are looked up
+    constexpr int kFetches = L::kShared ? (kRows * (D / 8) + kThreads - 1) / kThreads : CB;
+    Words<4> query[kFetches];
 #pragma unroll
-      for (int c = 0; c < CB; ++c)
-        qf[c] = *reinterpret_cast<const uint4*>(q_sh + (c * 32 + lane) * 16);
+    for (int i = 0; i < kFetches; ++i) {
+      // shared: 8 channels of any row; else channels 32i + 8tq of row g, the lane's own fragment
+      const int x = threadIdx.x + i * kThreads;
+      const int row = L::kShared ? x / (D / 8) : g;
+      const int ch = L::kShared ? x % (D / 8) * 8 : 32 * i + 8 * tq;
+      const int flat = part.tile * kRows + row;
+      query[i] = Words<4>{{0u, 0u, 0u, 0u}};
+      if (row < kRows && row < rows && (L::kShared || part.pieces > 0))
+        query[i] = load8(a, (entry.first + flat / group) * a.q_token +
+                                (part.head * group + flat % group) * a.q_head + ch, vec);
+    }
+
+    // The i-th step's groups are looked up by lane i % 32, 32 steps at a time, and copied into
+    // the stages in turn.
+    const uint8_t *src0 = nullptr, *src1 = nullptr;
+    uint32_t bytes0 = 0;
+    const auto plan = [&](int i0) {
+      const int pos = (span.first + from + i0 + lane) * kStep;
+      src1 = nullptr;
+      if (i0 + lane >= steps) return;
+      src0 = kv_group(cache, kv_page(cache, entry.slot, pos >> cache.page_shift), a.layer, part.head,
+                      pos, G::kBytes);
+      bytes0 = G::kBytes;
+      if (pos + 16 < span.end) {
+        if (cache.page_size >= kStep)  // the step lies within a page, its groups side by side
+          bytes0 = 2 * G::kBytes;
+        else
+          src1 = kv_group(cache, kv_page(cache, entry.slot, (pos + 16) >> cache.page_shift), a.layer,
+                          part.head, pos + 16, G::kBytes);
+      }
+    };
+    const auto issue = [&](int to_stage) {
+      const uint32_t to = ring_at + to_stage * L::kStageBytes, full = bar + 8 * to_stage;
+      mbar_arrive_expect_tx(full, bytes0 + (src1 ? G::kBytes : 0));
+      bulk_g2s_nohint(to, src0, bytes0, full);
+      if (src1) bulk_g2s_nohint(to + G::kBytes, src1, G::kBytes, full);
+    };
+    plan(0);
+    if (lane < kStages && lane < steps) issue((stage + lane) % kStages);
+    __syncwarp();
+
+    // ---- the queries as fragments: channel 32c + 8t + 4j + 2i + {0,1} of row 8nt + g is
+    // register i of product j in lane 4g + t
+    uint4 qf[kQInRegs ? CB : 1];
+    const uint8_t* q_sh = smem + L::kQ;
+    if constexpr (L::kShared) {
+      __syncthreads();  // the pass before has read its own
+#pragma unroll
+      for (int i = 0; i < kFetches; ++i) {
+        const int x8 = threadIdx.x + i * kThreads;
+        const int row = x8 / (D / 8), e8 = x8 % (D / 8);
+        if (row >= kRows) break;  // (whole warps)
+        float x[8];
+        widen8(query[i], a.half, x);
+        uint32_t bits = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) bits = max(bits, __float_as_uint(x[q]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int off = 1; off < D / 8; off <<= 1)
+          bits = max(bits, __shfl_xor_sync(kAll, bits, off));
+        const RowScale r = row_scale(bits);
+        *reinterpret_cast<uint4*>(smem + L::kQ +
+                                  (((row >> 3) * CB + (e8 >> 2)) * 32 + (row & 7) * 4 + (e8 & 3)) * 16) =
+            row_fragment(x, r);
+        if (e8 == 0) {
+          const int pos = entry.len - entry.n + (part.tile * kRows + row) / group;
+          const bool real = row < rows;  // no row: nothing to hide, never stored
+          factor_sh[row] = row_factor(r, a.scale);
+          lo_sh[row] = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
+          hi_sh[row] = real ? pos : span.end - 1;
+        }
+      }
+      __syncthreads();
+    } else {
+      uint32_t bits = 0;
+      float x[CB][8];
+#pragma unroll
+      for (int c = 0; c < CB; ++c) {
+        widen8(query[c], a.half, x[c]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) bits = max(bits, __float_as_uint(x[c][q]) & 0x7FFFFFFFu);
+      }
+      bits = max(bits, __shfl_xor_sync(kAll, bits, 1));
+      bits = max(bits, __shfl_xor_sync(kAll, bits, 2));
+      const RowScale r = row_scale(bits);
+#pragma unroll
+      for (int c = 0; c < CB; ++c) qf[c] = row_fragment(x[c], r);
+      __syncwarp();
+      if (tq == 0) {
+        const int pos = entry.len - entry.n + (part.tile * kRows + g) / group;
+        const bool real = g < rows;
+        factor_sh[g] = row_factor(r, a.scale);
+        lo_sh[g] = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
+        hi_sh[g] = real ? pos : span.end - 1;
+      }
+      __syncwarp();
     }
     float factor[NT][2];
     int seen_lo = 0, seen_hi = 0x7FFFFFFF;  // keys that every row of the tile sees
@@ -587,40 +626,35 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
 #pragma unroll
     for (int w = 0; w < NW; ++w) ref[w] = 0x10101010u;
 
-    for (; r < r1; r += kWarps, ++k) {
-      const int step = at.step + r - r0;
-      if (step >= at.span.steps) break;  // padding: the CTA has no other item
-      const int j0 = (at.span.first + step) * kStep;
-      if (dead) break;
+    for (int i = 0; i < steps; ++i) {
       const bool landed = mbar_wait(bar + 8 * stage, phase);
-      const uint8_t* buf = ring + stage * L::kStageBytes;
+      const int step_at = (span.first + from + i) * kStep;
+      // (rolled: the two groups' code together outgrows the instruction cache)
+#pragma unroll 1
+      for (int u = 0; u < 2; ++u) {
+      const int j0 = step_at + 16 * u;
+      if (u == 1 && j0 >= span.end) break;  // was not copied
+      uint8_t* buf = ring + stage * L::kStageBytes + u * G::kBytes;
 
       // ---- S^T = K Q^T
-      float s[2][NT][4];
+      float s[NT][4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+      uint32_t kf[2][CB / 2];  // the scales of keys 8h + g, BF16, two blocks to a word
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[u][nt][e] = 0.f;
-      uint32_t kf[2][2][CB / 2];  // the scales of keys 16u + 8h + g, BF16, two blocks to a word
+      for (int h = 0; h < 2; ++h) {
+        const Words<NW> w = lds_scales<CB>(buf + G::kKScale + (8 * h + g) * CB);
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const Words<NW> w = lds_scales<CB>(buf + u * G::kBytes + G::kKScale + (8 * h + g) * CB);
-#pragma unroll
-          for (int c = 0; c < CB / 2; ++c) kf[u][h][c] = e8m0x2(w.v[c / 2] >> (16 * (c & 1)));
-        }
+        for (int c = 0; c < CB / 2; ++c) kf[h][c] = e8m0x2(w.v[c / 2] >> (16 * (c & 1)));
+      }
 #pragma unroll
       for (int sl = 0; sl < NS; ++sl) {
-        Words<SB> kw[2][2];
+        Words<SB> kw[2];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            kw[u][h] = lds<SB>(buf + u * G::kBytes + sl * G::kSlabBytes + (8 * h + g) * 16 * SB +
-                               tq * 4 * SB);
+        for (int h = 0; h < 2; ++h)
+          kw[h] = lds<SB>(buf + sl * G::kSlabBytes + (8 * h + g) * 16 * SB + tq * 4 * SB);
 #pragma unroll
         for (int c = 0; c < SB; ++c) {
           const int cb = sl * SB + c;
@@ -630,31 +664,26 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
             q[nt] = kQInRegs ? qf[kQInRegs ? cb : 0]
                              : *reinterpret_cast<const uint4*>(
                                    q_sh + ((nt * CB + cb) * 32 + lane) * 16);
+          uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+          e2m1x8(kw[0].v[c], a0, a2, b0, b2);
+          e2m1x8(kw[1].v[c], a1, a3, b1, b3);
+          const float s0 = __uint_as_float(cb & 1 ? kf[0][cb / 2] & 0xFFFF0000u : kf[0][cb / 2] << 16);
+          const float s1 = __uint_as_float(cb & 1 ? kf[1][cb / 2] & 0xFFFF0000u : kf[1][cb / 2] << 16);
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
-            e2m1x8(kw[u][0].v[c], a0, a2, b0, b2);
-            e2m1x8(kw[u][1].v[c], a1, a3, b1, b3);
-            const float s0 = __uint_as_float(cb & 1 ? kf[u][0][cb / 2] & 0xFFFF0000u
-                                                    : kf[u][0][cb / 2] << 16);
-            const float s1 = __uint_as_float(cb & 1 ? kf[u][1][cb / 2] & 0xFFFF0000u
-                                                    : kf[u][1][cb / 2] << 16);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              float t[4];
-              mma_f16_zero(t, a0, a1, a2, a3, q[nt].x, q[nt].y);
-              mma_f16_acc(t, b0, b1, b2, b3, q[nt].z, q[nt].w);
-              s[u][nt][0] = fmaf(t[0], s0, s[u][nt][0]);
-              s[u][nt][1] = fmaf(t[1], s0, s[u][nt][1]);
-              s[u][nt][2] = fmaf(t[2], s1, s[u][nt][2]);
-              s[u][nt][3] = fmaf(t[3], s1, s[u][nt][3]);
-            }
+          for (int nt = 0; nt < NT; ++nt) {
+            float t[4];
+            mma_f16_zero(t, a0, a1, a2, a3, q[nt].x, q[nt].y);
+            mma_f16_acc(t, b0, b1, b2, b3, q[nt].z, q[nt].w);
+            s[nt][0] = fmaf(t[0], s0, s[nt][0]);
+            s[nt][1] = fmaf(t[1], s0, s[nt][1]);
+            s[nt][2] = fmaf(t[2], s1, s[nt][2]);
+            s[nt][3] = fmaf(t[3], s1, s[nt][3]);
           }
         }
       }
 
       // ---- does anything change: a larger logit, a V scale out of range, keys behind the end?
-      const bool whole = j0 >= seen_lo && j0 + kStep - 1 <= seen_hi;
+      const bool whole = j0 >= seen_lo && j0 + 15 <= seen_hi;
       float top[NT][2];
       bool odd = !landed;
 #pragma unroll
@@ -663,22 +692,20 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
         for (int e = 0; e < 2; ++e) {
           float t = -INFINITY;
 #pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float& x = s[u][nt][2 * h + e];
-              if (!whole) {
-                const int row = 8 * nt + 2 * tq + e, key = j0 + 16 * u + 8 * h + g;
-                if (key < lo_sh[row] || key > hi_sh[row]) x = -INFINITY;
-              }
-              t = fmaxf(t, x);
+          for (int h = 0; h < 2; ++h) {
+            float& x = s[nt][2 * h + e];
+            if (!whole) {
+              const int row = 8 * nt + 2 * tq + e, key = j0 + 8 * h + g;
+              if (key < lo_sh[row] || key > hi_sh[row]) x = -INFINITY;
             }
+            t = fmaxf(t, x);
+          }
           top[nt][e] = t * factor[nt][e];
           odd |= top[nt][e] > m[nt][e] + kSlack;
         }
-      // the V scales of key j0 + lane: all within [r - 15, r]?
-      const bool inside = j0 + lane < at.span.end;
-      Words<NW> vt = lds_scales<CB>(buf + (lane >> 4) * G::kBytes + G::kVScale + (lane & 15) * CB);
+      // the V scales of key j0 + lane % 16: all within [r - 15, r]?
+      const bool inside = j0 + (lane & 15) < span.end;
+      const Words<NW> vt = lds_scales<CB>(buf + G::kVScale + (lane & 15) * CB);
       const auto out_of_range = [&]() {
         bool bad = false;
 #pragma unroll
@@ -745,10 +772,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
           slow = __any_sync(kAll, bad);
         }
         // keys behind the end get scales in range; their probabilities are zero
-        if (j0 + kStep > at.span.end) {
+        if (j0 + 16 > span.end) {
           if (!inside) {
-            uint8_t* to = ring + stage * L::kStageBytes + (lane >> 4) * G::kBytes + G::kVScale +
-                          (lane & 15) * CB;
+            uint8_t* to = buf + G::kVScale + (lane & 15) * CB;
             if constexpr (CB == 2) {
               *reinterpret_cast<uint16_t*>(to) = (uint16_t)ref[0];
             } else {
@@ -761,21 +787,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
       }
 
       // ---- P = 2^kBias exp2(x - m)
-      uint32_t p[2][2][NT];  // P^T fragments: tokens 16u + 8h + 2tq + {0, 1} of column g
+      uint32_t p[2][NT];  // P^T fragments: tokens 8h + 2tq + {0, 1} of column g
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float z0 = m[nt][0] == -INFINITY ? 0.f : kBias - m[nt][0];
         const float z1 = m[nt][1] == -INFINITY ? 0.f : kBias - m[nt][1];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float p0 = exp2_fast(fmaf(s[u][nt][2 * h], factor[nt][0], z0));
-            const float p1 = exp2_fast(fmaf(s[u][nt][2 * h + 1], factor[nt][1], z1));
-            l[nt][0] += p0;
-            l[nt][1] += p1;
-            p[u][h][nt] = transpose8(pack_half2(p0, p1));
-          }
+        for (int h = 0; h < 2; ++h) {
+          const float p0 = exp2_fast(fmaf(s[nt][2 * h], factor[nt][0], z0));
+          const float p1 = exp2_fast(fmaf(s[nt][2 * h + 1], factor[nt][1], z1));
+          l[nt][0] += p0;
+          l[nt][1] += p1;
+          p[h][nt] = transpose8(pack_half2(p0, p1));
+        }
       }
 
       // ---- O^T += V^T P^T
@@ -783,67 +807,64 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
         uint32_t low[NW];  // 4 * (reference - 16), a byte to a block
 #pragma unroll
         for (int w = 0; w < NW; ++w) low[w] = 4u * (ref[w] - 0x10101010u);
+        // FP16 2^(s - ref + 1) of tokens (2tq, 2tq + 1) of each half: the exponent field is
+        // s - ref + 16, here four times that in the byte it belongs in
+        uint32_t d[2][2][NW];  // [half][pair of blocks' word ...]
+        uint32_t f01[2][NW], f23[2][NW];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          // FP16 2^(s - ref + 1) of tokens (2tq, 2tq + 1) of each half: the exponent field is
-          // s - ref + 16, here four times that in the byte it belongs in
-          uint32_t d[2][2][NW];  // [half][pair of blocks' word ...]
-          uint32_t f01[2][NW], f23[2][NW];
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t* sc = buf + G::kVScale + (8 * h + 2 * tq) * CB;
+          if constexpr (CB == 2) {
+            const uint32_t both = *reinterpret_cast<const uint32_t*>(sc);
+            const uint32_t l2 = 4u * (((ref[0] & 0xFFFFu) | (ref[0] << 16)) - 0x10101010u);
+            f01[h][0] = 4u * both - l2;
+          } else {
+            const Words<NW> w0 = lds<NW>(sc), w1 = lds<NW>(sc + CB);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint8_t* sc = buf + u * G::kBytes + G::kVScale + (8 * h + 2 * tq) * CB;
-            if constexpr (CB == 2) {
-              const uint32_t both = *reinterpret_cast<const uint32_t*>(sc);
-              const uint32_t l2 = 4u * (((ref[0] & 0xFFFFu) | (ref[0] << 16)) - 0x10101010u);
-              f01[h][0] = 4u * both - l2;
-            } else {
-              const Words<NW> w0 = lds<NW>(sc), w1 = lds<NW>(sc + CB);
-#pragma unroll
-              for (int w = 0; w < NW; ++w) {
-                d[h][0][w] = 4u * w0.v[w] - low[w];
-                d[h][1][w] = 4u * w1.v[w] - low[w];
-                f01[h][w] = __byte_perm(d[h][0][w], d[h][1][w], 0x5410);
-                f23[h][w] = __byte_perm(d[h][0][w], d[h][1][w], 0x7632);
-              }
+            for (int w = 0; w < NW; ++w) {
+              d[h][0][w] = 4u * w0.v[w] - low[w];
+              d[h][1][w] = 4u * w1.v[w] - low[w];
+              f01[h][w] = __byte_perm(d[h][0][w], d[h][1][w], 0x5410);
+              f23[h][w] = __byte_perm(d[h][0][w], d[h][1][w], 0x7632);
             }
           }
+        }
 #pragma unroll
-          for (int sl = 0; sl < NS; ++sl) {
-            const uint8_t* vb = buf + u * G::kBytes + G::kCodeBytes + sl * G::kSlabBytes +
-                                g * 16 * SB + tq * 4 * SB;
-            const Words<SB> v0 = lds<SB>(vb), v1 = lds<SB>(vb + 128 * SB);
+        for (int sl = 0; sl < NS; ++sl) {
+          const uint8_t* vb = buf + G::kCodeBytes + sl * G::kSlabBytes +
+                              g * 16 * SB + tq * 4 * SB;
+          const Words<SB> v0 = lds<SB>(vb), v1 = lds<SB>(vb + 128 * SB);
 #pragma unroll
-            for (int cp = 0; cp < SB / 2; ++cp) {  // blocks 2cp, 2cp + 1
-              // codes of two tokens side by side: channels n = 0, 2 (x) and 1, 3 (y)
-              const uint32_t e0 = v0.v[cp], f0 = v0.v[SB / 2 + cp];
-              const uint32_t e1 = v1.v[cp], f1 = v1.v[SB / 2 + cp];
-              const uint32_t x0 = (e0 & 0x0F0F0F0Fu) | ((f0 << 4) & 0xF0F0F0F0u);
-              const uint32_t y0 = ((e0 >> 4) & 0x0F0F0F0Fu) | (f0 & 0xF0F0F0F0u);
-              const uint32_t x1 = (e1 & 0x0F0F0F0Fu) | ((f1 << 4) & 0xF0F0F0F0u);
-              const uint32_t y1 = ((e1 >> 4) & 0x0F0F0F0Fu) | (f1 & 0xF0F0F0F0u);
-              uint32_t a0[4], a1[4], a2[4], a3[4];
-              e2m1x8(x0, a0[0], a0[1], a0[2], a0[3]);
-              e2m1x8(y0, a1[0], a1[1], a1[2], a1[3]);
-              e2m1x8(x1, a2[0], a2[1], a2[2], a2[3]);
-              e2m1x8(y1, a3[0], a3[1], a3[2], a3[3]);
+          for (int cp = 0; cp < SB / 2; ++cp) {  // blocks 2cp, 2cp + 1
+            // codes of two tokens side by side: channels n = 0, 2 (x) and 1, 3 (y)
+            const uint32_t e0 = v0.v[cp], f0 = v0.v[SB / 2 + cp];
+            const uint32_t e1 = v1.v[cp], f1 = v1.v[SB / 2 + cp];
+            const uint32_t x0 = (e0 & 0x0F0F0F0Fu) | ((f0 << 4) & 0xF0F0F0F0u);
+            const uint32_t y0 = ((e0 >> 4) & 0x0F0F0F0Fu) | (f0 & 0xF0F0F0F0u);
+            const uint32_t x1 = (e1 & 0x0F0F0F0Fu) | ((f1 << 4) & 0xF0F0F0F0u);
+            const uint32_t y1 = ((e1 >> 4) & 0x0F0F0F0Fu) | (f1 & 0xF0F0F0F0u);
+            uint32_t a0[4], a1[4], a2[4], a3[4];
+            e2m1x8(x0, a0[0], a0[1], a0[2], a0[3]);
+            e2m1x8(y0, a1[0], a1[1], a1[2], a1[3]);
+            e2m1x8(x1, a2[0], a2[1], a2[2], a2[3]);
+            e2m1x8(y1, a3[0], a3[1], a3[2], a3[3]);
 #pragma unroll
-              for (int cc = 0; cc < 2; ++cc) {
-                const int cb = sl * SB + 2 * cp + cc;
-                uint32_t sc[2];
+            for (int cc = 0; cc < 2; ++cc) {
+              const int cb = sl * SB + 2 * cp + cc;
+              uint32_t sc[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const uint32_t f = (cb % 4) < 2 ? f01[h][cb / 4] : f23[h][cb / 4];
-                  sc[h] = (cb & 1 ? f : f << 8) & 0xFF00FF00u;
-                }
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t f = (cb % 4) < 2 ? f01[h][cb / 4] : f23[h][cb / 4];
+                sc[h] = (cb & 1 ? f : f << 8) & 0xFF00FF00u;
+              }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  const uint32_t b0 = mul_half2(p[u][0][nt], sc[0]);
-                  const uint32_t b1 = mul_half2(p[u][1][nt], sc[1]);
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t b0 = mul_half2(p[0][nt], sc[0]);
+                const uint32_t b1 = mul_half2(p[1][nt], sc[1]);
 #pragma unroll
-                  for (int j = 0; j < 2; ++j)
-                    mma_f16_acc(o[cb][j][nt], a0[2 * cc + j], a1[2 * cc + j], a2[2 * cc + j],
-                                a3[2 * cc + j], b0, b1);
-                }
+                for (int j = 0; j < 2; ++j)
+                  mma_f16_acc(o[cb][j][nt], a0[2 * cc + j], a1[2 * cc + j], a2[2 * cc + j],
+                              a3[2 * cc + j], b0, b1);
               }
             }
           }
@@ -851,19 +872,16 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
       } else {
         // scales that one FP16 exponent range does not hold, or NaN: product by product
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
             for (int t = 0; t < 8; ++t) {
-              const int token = 16 * u + 8 * h + t, key = j0 + token;
-              if (key >= at.span.end) break;
-              const uint8_t* grp = buf + u * G::kBytes;
+              const int key = j0 + 8 * h + t;
+              if (key >= span.end) break;
               float pr[NT][2];
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                  const uint32_t w = __shfl_sync(kAll, p[u][h][nt], (2 * tq + e) * 4 + (t >> 1));
+                  const uint32_t w = __shfl_sync(kAll, p[h][nt], (2 * tq + e) * 4 + (t >> 1));
                   const __half2 both = *reinterpret_cast<const __half2*>(&w);
                   const int row = 8 * nt + 2 * tq + e;
                   const bool seen = key >= lo_sh[row] && key <= hi_sh[row];
@@ -872,12 +890,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
                 }
 #pragma unroll
               for (int c = 0; c < CB; ++c) {
-                const uint32_t sv = grp[G::kVScale + (8 * h + t) * CB + c];
+                const uint32_t sv = buf[G::kVScale + (8 * h + t) * CB + c];
                 const int rc = (int)((ref[c / 4] >> (8 * (c % 4))) & 0xFFu);
                 const float unit = sv == 255u ? __uint_as_float(0x7FC00000u)
                                               : exp2f((float)((int)sv - rc + 1));
                 uint32_t v[4];
-                e2m1x8(*reinterpret_cast<const uint16_t*>(grp + G::v_half(8 * h + t, c, g)), v[0],
+                e2m1x8(*reinterpret_cast<const uint16_t*>(buf + G::v_half(8 * h + t, c, g)), v[0],
                        v[1], v[2], v[3]);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -894,171 +912,188 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
               }
             }
       }
+      }
+      if (dead) {
+        // give up, but not before the copies in flight have landed (or as long again has passed)
+        for (int j = 0; j < kStages && i + j < steps; ++j)
+          mbar_wait(bar + 8 * ((stage + j) % kStages), stage + j < kStages ? phase : phase ^ 1u);
+        break;
+      }
 
-      issue_next();
+      // ---- refill the stage
+      __syncwarp();
+      const int next = i + kStages;
+      if ((next & 31) == 0) plan(next);
+      if (lane == (next & 31) && next < steps) issue(stage);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
 
-    // ---- join the warps
-    if (r0 > 0) __syncthreads();  // the segment before has been read
+    // ---- the piece's result
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float t = l[nt][e];
-        t += __shfl_xor_sync(kAll, t, 4);
-        t += __shfl_xor_sync(kAll, t, 8);
-        t += __shfl_xor_sync(kAll, t, 16);
-        if (g == 0) {
-          m_sh[warp * kRows + 8 * nt + 2 * tq + e] = m[nt][e];
-          l_sh[warp * kRows + 8 * nt + 2 * tq + e] = t;
-        }
+        l[nt][e] += __shfl_xor_sync(kAll, l[nt][e], 4);
+        l[nt][e] += __shfl_xor_sync(kAll, l[nt][e], 8);
+        l[nt][e] += __shfl_xor_sync(kAll, l[nt][e], 16);
       }
-    const auto write_round = [&](int round) {
+    const auto output = [&](int c, int nt, int e) {  // channels 32c + 4g + {0..3} of row 8nt + 2tq + e
+      const float unit = exp2_int((int)((ref[c / 4] >> (8 * (c % 4))) & 0xFFu) - 128);
+      return make_float4(o[c][0][nt][e] * unit, o[c][0][nt][2 + e] * unit, o[c][1][nt][e] * unit,
+                         o[c][1][nt][2 + e] * unit);
+    };
+    if (part.pieces == 1) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int c = 0; c < CB; ++c)
+            store_row<D, kRows>(a, part, 8 * nt + 2 * tq + e, 32 * c + 4 * g, output(c, nt, e),
+                                m[nt][e], l[nt][e]);
+    }
+    if (no_joins) continue;
+
+    // ---- join the pieces of an item that this CTA has
+    if (lane == 0) parts_sh[warp] = part;
+    if (g == 0)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          m_sh[warp * kRows + 8 * nt + 2 * tq + e] = m[nt][e];
+          l_sh[warp * kRows + 8 * nt + 2 * tq + e] = l[nt][e];
+        }
+    int waiting[2], pending = 0;  // warps whose item other CTAs have pieces of
+    waiting[0] = waiting[1] = 0;
+#pragma unroll
+    for (int round = 0; round < L::kRounds; ++round) {
+      if (round > 0) __syncthreads();
 #pragma unroll
       for (int c = 0; c < CB; ++c) {
         const int cr = c - round * L::kRoundBlocks;
         if (cr < 0 || cr >= L::kRoundBlocks) continue;
-        const float unit = exp2_int((int)((ref[c / 4] >> (8 * (c % 4))) & 0xFFu) - 128);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             *reinterpret_cast<float4*>(
                 merge + (warp * kRows + 8 * nt + 2 * tq + e) * L::kMergeRow + 32 * cr + 4 * g) =
-                make_float4(o[c][0][nt][e] * unit, o[c][0][nt][2 + e] * unit,
-                            o[c][1][nt][e] * unit, o[c][1][nt][2 + e] * unit);
-      }
-    };
-    write_round(0);
-    Part part;
-    part.item = begin + r0 - at.step;
-    part.first_cta = (int)(part.item / quota);
-    part.last_cta = (int)((part.item + at.padded - 1) / quota);
-    part.tile = at.tile;
-    part.head = at.head;
-    part.first = entry.first;
-    part.n = entry.n;
-    const bool alone = at.step == 0 && r1 - r0 == at.padded;
-    float* to = part_at(a, part, blockIdx.x, quota);
-    if (!alone) {
-      if (threadIdx.x == 0) parts_sh[pending] = part;
-      ++pending;
-    }
-    // what comes next, while the slower warps finish
-    if (r1 < mine) {
-      at = locate<kRows>(a, order, begin + r1, entry);
-      fetch_queries(at, entry);
-      put_queries(at, entry, which ^ 1);
-    }
-#pragma unroll
-    for (int round = 0; round < L::kRounds; ++round) {
-      if (round > 0) {
-        __syncthreads();
-        write_round(round);
+                output(c, nt, e);
       }
       __syncthreads();
-      constexpr int kQuads = 8 * L::kRoundBlocks;  // four channels each, of a row
-      for (int i = threadIdx.x; i < kRows * kQuads; i += kThreads) {
-        const int row = i / kQuads, ch = 4 * (i % kQuads);
-        float mw[kWarps], top = -INFINITY, sum = 0.f;
+      pending = 0;
+      for (int w0 = 0, w1; w0 < kWarps; w0 = w1) {
+        const Part p = parts_sh[w0];
+        w1 = w0 + 1;
+        if (p.pieces <= 1) continue;
+        while (w1 < kWarps && parts_sh[w1].pieces > 0 && parts_sh[w1].slot0 == p.slot0) ++w1;
+        const bool whole = p.slot0 >= (long long)unit * kWarps &&
+                           p.slot0 + p.pieces <= (long long)(unit + 1) * kWarps;
+        float* to = part_at<kRows>(a, p, unit);
+        if (!whole) waiting[pending++ & 1] = w0;
+        constexpr int kQuads = 8 * L::kRoundBlocks;  // four channels each, of a row
+        for (int i = threadIdx.x; i < kRows * kQuads; i += kThreads) {
+          const int row = i / kQuads, ch = 4 * (i % kQuads);
+          float top = -INFINITY, sum = 0.f;
+          for (int w = w0; w < w1; ++w) top = fmaxf(top, m_sh[w * kRows + row]);
+          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          mw[w] = m_sh[w * kRows + row];
-          top = fmaxf(top, mw[w]);
-        }
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = top == -INFINITY ? 0.f : exp2_fast(mw[w] - top);
-          const float lw = l_sh[w * kRows + row];
-          // a warp whose keys were all NaN has no maximum, but a NaN sum
-          sum += lw != lw ? lw : lw * f;
-          const float4 v = *reinterpret_cast<const float4*>(merge + (w * kRows + row) * L::kMergeRow + ch);
-          y.x = fmaf(v.x, f, y.x);
-          y.y = fmaf(v.y, f, y.y);
-          y.z = fmaf(v.z, f, y.z);
-          y.w = fmaf(v.w, f, y.w);
-        }
-        const int at_ch = 32 * round * L::kRoundBlocks + ch;
-        if (alone) {
-          store_row<D, kRows>(a, part, row, at_ch, y, top, sum);
-        } else {
-          __stcg(reinterpret_cast<float4*>(to + row * D + at_ch), y);
-          if (at_ch == 0) {
-            __stcg(to + kRows * D + row, top);
-            __stcg(to + kRows * D + kRows + row, sum);
+          for (int w = 0; w < kWarps; ++w) {
+            if (w < w0 || w >= w1) continue;
+            const float f = top == -INFINITY ? 0.f : exp2_fast(m_sh[w * kRows + row] - top);
+            const float lw = l_sh[w * kRows + row];
+            // a warp whose keys were all NaN has no maximum, but a NaN sum
+            sum += lw != lw ? lw : lw * f;
+            const float4 v =
+                *reinterpret_cast<const float4*>(merge + (w * kRows + row) * L::kMergeRow + ch);
+            y.x = fmaf(v.x, f, y.x);
+            y.y = fmaf(v.y, f, y.y);
+            y.z = fmaf(v.z, f, y.z);
+            y.w = fmaf(v.w, f, y.w);
           }
-        }
-      }
-    }
-    r0 = r1;
-  }
-  if (pending > 0) {
-    // the CTA that arrives last at an item joins its parts, in their order
-    __syncthreads();
-    if (threadIdx.x < pending) {
-      __threadfence();
-      const Part part = parts_sh[threadIdx.x];
-      const uint32_t others = (uint32_t)(part.last_cta - part.first_cta);
-      const bool last = atomicAdd(a.counters + part.first_cta, 1u) == others;
-      if (last) a.counters[part.first_cta] = 0;
-      __threadfence();
-      last_sh[threadIdx.x] = last;
-    }
-    __syncthreads();
-    for (int which = 0; which < pending; ++which) {
-      if (!last_sh[which]) continue;
-      const Part part = parts_sh[which];
-      const int parts = part.last_cta - part.first_cta + 1;
-      for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
-        const int row = i / (D / 4), ch = 4 * (i % (D / 4));
-        float top = -INFINITY, sum = 0.f;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int kBatch = 8;  // parts on their way at a time
-        for (int x0 = 0; x0 < parts; x0 += kBatch) {
-          float mx[kBatch], lx[kBatch];
-          float4 v[kBatch];
-#pragma unroll
-          for (int x = 0; x < kBatch; ++x) {
-            mx[x] = -INFINITY;
-            lx[x] = 0.f;
-            v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (x0 + x < parts) {
-              const float* from = part_at(a, part, part.first_cta + x0 + x, quota);
-              mx[x] = __ldcg(from + kRows * D + row);
-              lx[x] = __ldcg(from + kRows * D + kRows + row);
-              v[x] = __ldcg(reinterpret_cast<const float4*>(from + row * D + ch));
+          const int at_ch = 32 * round * L::kRoundBlocks + ch;
+          if (whole) {
+            store_row<D, kRows>(a, p, row, at_ch, y, top, sum);
+          } else {
+            __stcg(reinterpret_cast<float4*>(to + row * D + at_ch), y);
+            if (at_ch == 0) {
+              __stcg(to + kRows * D + row, top);
+              __stcg(to + kRows * D + kRows + row, sum);
             }
           }
-          float next = top;
-#pragma unroll
-          for (int x = 0; x < kBatch; ++x) next = fmaxf(next, mx[x]);
-          const float keep = top == -INFINITY ? 0.f : exp2_fast(top - next);
-          if (x0 > 0) {
-            sum = sum != sum ? sum : sum * keep;
-            y.x *= keep;
-            y.y *= keep;
-            y.z *= keep;
-            y.w *= keep;
-          }
-          top = next;
-#pragma unroll
-          for (int x = 0; x < kBatch; ++x) {
-            const float f = top == -INFINITY ? 0.f : exp2_fast(mx[x] - top);
-            sum += lx[x] != lx[x] ? lx[x] : lx[x] * f;
-            y.x = fmaf(v[x].x, f, y.x);
-            y.y = fmaf(v[x].y, f, y.y);
-            y.z = fmaf(v[x].z, f, y.z);
-            y.w = fmaf(v[x].w, f, y.w);
-          }
         }
-        store_row<D, kRows>(a, part, row, ch, y, top, sum);
       }
     }
-  }
-  if (dead) {
-    // give up, but not before the copies in flight have landed (or as long again has passed)
-    for (int s = 0; s < kStages; ++s) mbar_wait(bar + 8 * s, s >= stage ? phase : phase ^ 1u);
+    __syncthreads();
+    // ---- the CTA that arrives last at an item joins its parts, in their order
+    if (pending > 0) {
+      if ((int)threadIdx.x < pending) {
+        __threadfence();
+        const Part p = parts_sh[waiting[threadIdx.x & 1]];
+        const int first_unit = (int)(p.slot0 / kWarps);
+        const uint32_t others = (uint32_t)((p.slot0 + p.pieces - 1) / kWarps - first_unit);
+        const bool last = atomicAdd(a.counters + first_unit, 1u) == others;
+        if (last) a.counters[first_unit] = 0;
+        __threadfence();
+        last_sh[threadIdx.x] = last;
+      }
+      __syncthreads();
+      for (int which = 0; which < pending; ++which) {
+        if (!last_sh[which]) continue;
+        const Part part = parts_sh[waiting[which]];
+        const int first_unit = (int)(part.slot0 / kWarps);
+        const int parts = (int)((part.slot0 + part.pieces - 1) / kWarps) - first_unit + 1;
+        for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
+          const int row = i / (D / 4), ch = 4 * (i % (D / 4));
+          float top = -INFINITY, sum = 0.f;
+          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+          constexpr int kBatch = 8;  // parts on their way at a time
+          for (int x0 = 0; x0 < parts; x0 += kBatch) {
+            float mx[kBatch], lx[kBatch];
+            float4 v[kBatch];
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+              mx[x] = -INFINITY;
+              lx[x] = 0.f;
+              v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (x0 + x < parts) {
+                const float* from = part_at<kRows>(a, part, first_unit + x0 + x);
+                mx[x] = __ldcg(from + kRows * D + row);
+                lx[x] = __ldcg(from + kRows * D + kRows + row);
+                v[x] = __ldcg(reinterpret_cast<const float4*>(from + row * D + ch));
+              }
+            }
+            float next = top;
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) next = fmaxf(next, mx[x]);
+            const float keep = top == -INFINITY ? 0.f : exp2_fast(top - next);
+            if (x0 > 0) {
+              sum = sum != sum ? sum : sum * keep;
+              y.x *= keep;
+              y.y *= keep;
+              y.z *= keep;
+              y.w *= keep;
+            }
+            top = next;
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+              const float f = top == -INFINITY ? 0.f : exp2_fast(mx[x] - top);
+              sum += lx[x] != lx[x] ? lx[x] : lx[x] * f;
+              y.x = fmaf(v[x].x, f, y.x);
+              y.y = fmaf(v[x].y, f, y.y);
+              y.z = fmaf(v[x].z, f, y.z);
+              y.w = fmaf(v[x].w, f, y.w);
+            }
+          }
+        store_row<D, kRows>(a, part, row, ch, y, top, sum);
+        }
+      }
+      __syncthreads();
+    }
   }
 }
 
@@ -1069,8 +1104,7 @@ cudaError_t run(const KvAttentionArgs& a, cudaStream_t s) {
   const void* fn = reinterpret_cast<const void*>(kv_attention<D, NT>);
   cudaError_t e = ensure_dynamic_smem(fn, bytes);
   if (e != cudaSuccess) return e;
-  const int sms = kKvMaxCtas / 2;
-  kv_attention<D, NT><<<sms * L::kCtasPerSm, kThreads, bytes, s>>>(a);
+  kv_attention<D, NT><<<kKvSms * L::kCtasPerSm, kThreads, bytes, s>>>(a);
   return cudaGetLastError();
 }
 

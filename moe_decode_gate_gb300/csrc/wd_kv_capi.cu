@@ -66,9 +66,9 @@ KvScratch kv_scratch(const wd_kv_cache& c) {
   };
   KvScratch w;
   const size_t pages = c.num_pages, slots = c.slots;
-  w.counters = reinterpret_cast<uint32_t*>(take(4 * (size_t)kKvMaxCtas));
+  w.counters = reinterpret_cast<uint32_t*>(take(4 * (size_t)kKvMaxUnits));
   w.partial = reinterpret_cast<float*>(
-      take(4 * 2 * (size_t)kKvMaxCtas * kKvMaxRows * ((size_t)c.head_dim + 2)));
+      take(4 * 2 * (size_t)kKvMaxUnits * 8 * ((size_t)c.head_dim + 2)));
   w.list_a = reinterpret_cast<int32_t*>(take(4 * pages));
   w.list_b = reinterpret_cast<int32_t*>(take(4 * pages));
   w.list_c = reinterpret_cast<int32_t*>(take(4 * pages));
@@ -122,7 +122,7 @@ wd_status wd_kv_workspace_init(const wd_kv_cache* cache, wd_stream_t stream) {
   const wd_status st = check_cache(cache);
   if (st != WD_OK) return st;
   // the flag's slot and the counters behind it
-  return cuda_status(cudaMemsetAsync(cache->workspace, 0, kFlagBytes + 4 * kKvMaxCtas,
+  return cuda_status(cudaMemsetAsync(cache->workspace, 0, kFlagBytes + 4 * kKvMaxUnits,
                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 
