@@ -70,14 +70,18 @@ struct Shape {
   static constexpr int kStats = kMerge + kWarps * kRows * kMergeRow * 4;  // float m, l [kWarps][kRows]
   static constexpr int kRowInfo = kStats + 2 * kWarps * kRows * 4;  // factor, lo, hi [kRows], of each warp or all
   static constexpr int kParts = kRowInfo + (kShared ? 1 : kWarps) * 3 * kRows * 4;  // Part [kWarps]
-  static constexpr int kBars = kParts + kWarps * (int)sizeof(Part);  // uint64 [kWarps][kStages]
+  // a step's scales as the products want them, per warp: float of each key and block,
+  // FP16 factor of each pair of keys and block
+  static constexpr int kScaleBytes = 32 * G::kBlocks * 4 + 16 * G::kBlocks * 4;
+  static constexpr int kScales = kParts + kWarps * (int)sizeof(Part);
+  static constexpr int kBars = kScales + kWarps * kScaleBytes;  // uint64 [kWarps][kStages]
   static constexpr int kScan = kBars + kWarps * kStages * 8;         // long long [kWarps]
   static constexpr int kScan2 = kScan + kWarps * 8;                  // int [kChoices]
   static constexpr int kPrefix = kScan2 + kChoices * 4;              // long long [entries + 1]
   static constexpr int shared_bytes(int entries) {  // ... and int2 [min(entries, kCached)]
     return kPrefix + 8 * (entries + 1) + 8 * (entries < kCached ? entries : kCached);
   }
-  static_assert(kBars % 8 == 0 && kParts % 8 == 0, "alignment");
+  static_assert(kScales % 16 == 0 && kBars % 8 == 0, "alignment");
   static_assert(kPrefix + 8 * (WD_KV_MAX_ENTRIES + 1) + 8 * kCached <= 227 * 1024, "shared memory");
 };
 
@@ -337,6 +341,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
   long long* prefix = reinterpret_cast<long long*>(smem + L::kPrefix);
   int2* cached = reinterpret_cast<int2*>(prefix + a.batch.entries + 1);
   uint8_t* ring = smem + L::kRing + warp * kStages * L::kStageBytes;
+  uint8_t* k_scales = smem + L::kScales + warp * L::kScaleBytes;  // float [32 keys][CB]
+  uint8_t* v_scales = k_scales + 32 * CB * 4;                    // f16x2 [16 pairs of keys][CB]
   const uint32_t bar = smem_u32(smem + L::kBars) + warp * kStages * 8;
   __shared__ int last_sh[2];
 
@@ -379,26 +385,29 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
   const long long warps = (long long)gridDim.x * kWarps;
   const int fair = (int)min((total + warps - 1) / warps, 1ll << 26);
   __syncthreads();
-  for (int c = warp; c < kChoices; c += kWarps) {
-    const unsigned q = steps_choice(c >> 1, fair, longest);
-    const unsigned align = c & 1 ? kWarps : 1;
-    long long slots = 0;
+  for (int c = warp; c < kChoices / 2; c += kWarps) {
+    const unsigned q = steps_choice(c, fair, longest);
+    float loose = 0.f, aligned = 0.f;  // units (exact where it matters, below 2^24)
     for (int b = lane; b < a.batch.entries; b += 32) {
       const Entry e = load_entry(a, b, cached);
       const unsigned pieces = ((unsigned)steps_of<kRows>(e, group, a.window) + q - 1) / q;
-      slots += (long long)tiles_of<kRows>(e, group) * ((pieces + align - 1) / align * align);
+      const float tiles = (float)tiles_of<kRows>(e, group);
+      loose += tiles * (float)pieces;
+      aligned += tiles * (float)((pieces + kWarps - 1) / kWarps);
     }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) slots += __shfl_xor_sync(kAll, slots, off);
-    slots *= heads;
-    const long long units = (slots + kWarps - 1) / kWarps;
-    const long long passes = (units + gridDim.x - 1) / gridDim.x;
-    const bool across = (unsigned)longest > q * align;
-    const float cost = (passes == 1 ? (float)q : fmaxf((float)q, (float)fair + 0.75f * (float)q)) +
-                       2.f * (float)passes + (across ? 3.f : 0.f);
+    for (int off = 16; off > 0; off >>= 1) {
+      loose += __shfl_xor_sync(kAll, loose, off);
+      aligned += __shfl_xor_sync(kAll, aligned, off);
+    }
+    const float units = (float)heads * (lane == 0 ? loose * (1.f / kWarps) : aligned);
+    const float passes = ceilf(units / (float)gridDim.x);
+    const bool across = (float)longest > (float)q * (lane == 0 ? 1.f : (float)kWarps);
+    const float cost = (passes <= 1.f ? (float)q : fmaxf((float)q, (float)fair + 0.75f * (float)q)) +
+                       2.f * passes + (across ? 3.f : 0.f);
     // joins across CTAs have room for so many
-    const bool fits = (!across || units <= kKvMaxUnits / NT) && (!L::kShared || align == kWarps);
-    if (lane == 0) scan2[c] = fits ? (int)fminf(cost * 16.f, 1e9f) : 0x7FFFFFFF;
+    const bool fits = (!across || units <= (float)(kKvMaxUnits / NT)) && (!L::kShared || lane == 1);
+    if (lane < 2) scan2[2 * c + lane] = fits ? (int)fminf(cost * 16.f, 1e9f) : 0x7FFFFFFF;
   }
   __syncthreads();
   const int cheapest = __reduce_min_sync(kAll, scan2[lane]);
@@ -629,12 +638,66 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
     for (int i = 0; i < steps; ++i) {
       const bool landed = mbar_wait(bar + 8 * stage, phase);
       const int step_at = (span.first + from + i) * kStep;
-      // (rolled: the two groups' code together outgrows the instruction cache)
+
+      // ---- the scales of key step_at + lane, for the lanes whose products want them
+      const bool inside = step_at + lane < span.end;
+      const uint8_t* scale_at = ring + stage * L::kStageBytes + (lane >> 4) * G::kBytes + (lane & 15) * CB;
+      const Words<NW> kt = lds_scales<CB>(scale_at + G::kKScale);
+      Words<NW> vt = lds_scales<CB>(scale_at + G::kVScale);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        float4 f;
+        const uint32_t lo = e8m0x2(kt.v[w]);
+        f.x = __uint_as_float(lo << 16);
+        f.y = __uint_as_float(lo & 0xFFFF0000u);
+        if constexpr (CB == 2) {
+          *reinterpret_cast<float2*>(k_scales + lane * 8) = make_float2(f.x, f.y);
+        } else {
+          const uint32_t hi = e8m0x2(kt.v[w] >> 16);
+          f.z = __uint_as_float(hi << 16);
+          f.w = __uint_as_float(hi & 0xFFFF0000u);
+          *reinterpret_cast<float4*>(k_scales + lane * 4 * CB + 16 * w) = f;
+        }
+      }
+      // 2^(s - ref + 1) of V: the exponent field is s - ref + 16, here first four times that in
+      // the byte it belongs in.  Keys behind the end take the reference itself; their
+      // probabilities are zero.
+      const auto put_v_scales = [&]() {
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const uint32_t d = 4u * (inside ? vt.v[w] : ref[w]) - 4u * (ref[w] - 0x10101010u);
+          const uint32_t other = __shfl_xor_sync(kAll, d, 1);
+          const bool second = lane & 1;
+          if constexpr (CB == 2) {
+            const uint32_t both = second ? __byte_perm(other, d, 0x5410) << 0
+                                         : __byte_perm(d, other, 0x5410) << 8;
+            *reinterpret_cast<uint32_t*>(v_scales + (lane >> 1) * 8 + (lane & 1) * 4) =
+                both & 0xFF00FF00u;
+          } else {
+            const uint32_t both = second ? __byte_perm(other, d, 0x7632) : __byte_perm(d, other, 0x5410);
+            *reinterpret_cast<uint2*>(v_scales + (lane >> 1) * 4 * CB + 16 * w + (lane & 1) * 8) =
+                make_uint2((both << 8) & 0xFF00FF00u, both & 0xFF00FF00u);
+          }
+        }
+        __syncwarp();
+      };
+      bool odd = !landed;  // are all V scales within [ref - 15, ref]?
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const uint32_t v = CB == 2 ? vt.v[w] | (ref[w] & 0xFFFF0000u) : vt.v[w];
+        const uint32_t t0 = ((ref[w] & 0x00FF00FFu) | 0x80008000u) - (v & 0x00FF00FFu);
+        const uint32_t t1 = (((ref[w] >> 8) & 0x00FF00FFu) | 0x80008000u) - ((v >> 8) & 0x00FF00FFu);
+        odd |= inside && ((t0 | t1) & 0x7FF07FF0u) != 0u;
+      }
+      put_v_scales();
+      bool slow = false;
+
+      // (rolled: nothing is gained by the two groups side by side, and the code is half as long)
 #pragma unroll 1
       for (int u = 0; u < 2; ++u) {
-      const int j0 = step_at + 16 * u;
-      if (u == 1 && j0 >= span.end) break;  // was not copied
-      uint8_t* buf = ring + stage * L::kStageBytes + u * G::kBytes;
+        const int j0 = step_at + 16 * u;
+        if (u == 1 && j0 >= span.end) break;  // was not copied
+        const uint8_t* buf = ring + stage * L::kStageBytes + u * G::kBytes;
 
       // ---- S^T = K Q^T
       float s[NT][4];
@@ -642,13 +705,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-      uint32_t kf[2][CB / 2];  // the scales of keys 8h + g, BF16, two blocks to a word
+      Words<SB> kf[2][NS];  // the scales of keys 8h + g
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const Words<NW> w = lds_scales<CB>(buf + G::kKScale + (8 * h + g) * CB);
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int c = 0; c < CB / 2; ++c) kf[h][c] = e8m0x2(w.v[c / 2] >> (16 * (c & 1)));
-      }
+        for (int sl = 0; sl < NS; ++sl)
+          kf[h][sl] = lds<SB>(k_scales + ((16 * u + 8 * h + g) * CB + sl * SB) * 4);
 #pragma unroll
       for (int sl = 0; sl < NS; ++sl) {
         Words<SB> kw[2];
@@ -667,8 +729,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
           uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
           e2m1x8(kw[0].v[c], a0, a2, b0, b2);
           e2m1x8(kw[1].v[c], a1, a3, b1, b3);
-          const float s0 = __uint_as_float(cb & 1 ? kf[0][cb / 2] & 0xFFFF0000u : kf[0][cb / 2] << 16);
-          const float s1 = __uint_as_float(cb & 1 ? kf[1][cb / 2] & 0xFFFF0000u : kf[1][cb / 2] << 16);
+          const float s0 = __uint_as_float(kf[0][sl].v[c]), s1 = __uint_as_float(kf[1][sl].v[c]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float t[4];
@@ -682,10 +743,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
         }
       }
 
-      // ---- does anything change: a larger logit, a V scale out of range, keys behind the end?
+      // ---- does anything change: a larger logit, a V scale out of range?
       const bool whole = j0 >= seen_lo && j0 + 15 <= seen_hi;
       float top[NT][2];
-      bool odd = !landed;
+      bool grow = odd;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -701,25 +762,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
             t = fmaxf(t, x);
           }
           top[nt][e] = t * factor[nt][e];
-          odd |= top[nt][e] > m[nt][e] + kSlack;
+          grow |= top[nt][e] > m[nt][e] + kSlack;
         }
-      // the V scales of key j0 + lane % 16: all within [r - 15, r]?
-      const bool inside = j0 + (lane & 15) < span.end;
-      const Words<NW> vt = lds_scales<CB>(buf + G::kVScale + (lane & 15) * CB);
-      const auto out_of_range = [&]() {
-        bool bad = false;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const uint32_t v = CB == 2 ? vt.v[w] | (ref[w] & 0xFFFF0000u) : vt.v[w];
-          const uint32_t t0 = ((ref[w] & 0x00FF00FFu) | 0x80008000u) - (v & 0x00FF00FFu);
-          const uint32_t t1 = (((ref[w] >> 8) & 0x00FF00FFu) | 0x80008000u) - ((v >> 8) & 0x00FF00FFu);
-          bad |= ((t0 | t1) & 0x7FF07FF0u) != 0u;
-        }
-        return bad;
-      };
-      odd |= inside ? out_of_range() : true;
-      bool slow = false;
-      if (__any_sync(kAll, odd)) {
+      if (__any_sync(kAll, grow)) {
         if (__any_sync(kAll, !landed)) {
           dead = true;
           if (lane == 0) atomicOr(cache.flag, WD_KV_FLAG_TIMEOUT);
@@ -749,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
               }
           }
         // the largest V scales, and what stands on them
-        if (__any_sync(kAll, inside && out_of_range())) {
+        if (__any_sync(kAll, odd)) {
           bool bad = false;
 #pragma unroll
           for (int c = 0; c < CB; ++c) {
@@ -770,19 +815,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
             bad |= inside && (mine_c > most || mine_c + 15u < most);
           }
           slow = __any_sync(kAll, bad);
-        }
-        // keys behind the end get scales in range; their probabilities are zero
-        if (j0 + 16 > span.end) {
-          if (!inside) {
-            uint8_t* to = buf + G::kVScale + (lane & 15) * CB;
-            if constexpr (CB == 2) {
-              *reinterpret_cast<uint16_t*>(to) = (uint16_t)ref[0];
-            } else {
-#pragma unroll
-              for (int w = 0; w < NW; ++w) reinterpret_cast<uint32_t*>(to)[w] = ref[w];
-            }
-          }
           __syncwarp();
+          put_v_scales();
+          odd = false;
         }
       }
 
@@ -804,31 +839,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
 
       // ---- O^T += V^T P^T
       if (!slow) {
-        uint32_t low[NW];  // 4 * (reference - 16), a byte to a block
+        Words<SB> vf[2][NS];  // the factors of keys 8h + 2tq + {0, 1}
 #pragma unroll
-        for (int w = 0; w < NW; ++w) low[w] = 4u * (ref[w] - 0x10101010u);
-        // FP16 2^(s - ref + 1) of tokens (2tq, 2tq + 1) of each half: the exponent field is
-        // s - ref + 16, here four times that in the byte it belongs in
-        uint32_t d[2][2][NW];  // [half][pair of blocks' word ...]
-        uint32_t f01[2][NW], f23[2][NW];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint8_t* sc = buf + G::kVScale + (8 * h + 2 * tq) * CB;
-          if constexpr (CB == 2) {
-            const uint32_t both = *reinterpret_cast<const uint32_t*>(sc);
-            const uint32_t l2 = 4u * (((ref[0] & 0xFFFFu) | (ref[0] << 16)) - 0x10101010u);
-            f01[h][0] = 4u * both - l2;
-          } else {
-            const Words<NW> w0 = lds<NW>(sc), w1 = lds<NW>(sc + CB);
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-              d[h][0][w] = 4u * w0.v[w] - low[w];
-              d[h][1][w] = 4u * w1.v[w] - low[w];
-              f01[h][w] = __byte_perm(d[h][0][w], d[h][1][w], 0x5410);
-              f23[h][w] = __byte_perm(d[h][0][w], d[h][1][w], 0x7632);
-            }
-          }
-        }
+          for (int sl = 0; sl < NS; ++sl)
+            vf[h][sl] = lds<SB>(v_scales + ((8 * u + 4 * h + tq) * CB + sl * SB) * 4);
 #pragma unroll
         for (int sl = 0; sl < NS; ++sl) {
           const uint8_t* vb = buf + G::kCodeBytes + sl * G::kSlabBytes +
@@ -851,16 +867,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
               const int cb = sl * SB + 2 * cp + cc;
-              uint32_t sc[2];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t f = (cb % 4) < 2 ? f01[h][cb / 4] : f23[h][cb / 4];
-                sc[h] = (cb & 1 ? f : f << 8) & 0xFF00FF00u;
-              }
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                const uint32_t b0 = mul_half2(p[0][nt], sc[0]);
-                const uint32_t b1 = mul_half2(p[1][nt], sc[1]);
+                const uint32_t b0 = mul_half2(p[0][nt], vf[0][sl].v[2 * cp + cc]);
+                const uint32_t b1 = mul_half2(p[1][nt], vf[1][sl].v[2 * cp + cc]);
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                   mma_f16_acc(o[cb][j][nt], a0[2 * cc + j], a1[2 * cc + j], a2[2 * cc + j],
