@@ -33,11 +33,8 @@
 namespace wd {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kStep = 32;      // keys of a step: two groups
 constexpr int kCached = 256;   // entries whose slot and length are kept in shared memory
-constexpr int kChoices = 32;   // divisions of the work that are compared
 constexpr float kBias = 8.f;   // P = 2^kBias at the reference m ...
 constexpr float kSlack = 6.f;  // ... which may fall this far behind the maximum (log2)
 constexpr uint32_t kAll = 0xFFFFFFFFu;
@@ -55,7 +52,9 @@ struct Shape {
   static constexpr int kRows = 8 * NT;
   static constexpr int kStageBytes = 2 * G::kBytes;
   static constexpr int kStages = D == 64 ? 4 : 2;
-  static constexpr int kCtasPerSm = D <= 128 && NT == 1 ? 2 : 1;
+  static constexpr int kWarps = D <= 128 && NT == 1 ? 12 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kCtasPerSm = 1;
   // One tile of queries fits the registers; more are shared by the CTA's warps, whose
   // pieces are then always of one item.
   static constexpr bool kShared = NT > 1;
@@ -76,8 +75,8 @@ struct Shape {
   static constexpr int kScales = kParts + kWarps * (int)sizeof(Part);
   static constexpr int kBars = kScales + kWarps * kScaleBytes;  // uint64 [kWarps][kStages]
   static constexpr int kScan = kBars + kWarps * kStages * 8;         // long long [kWarps]
-  static constexpr int kScan2 = kScan + kWarps * 8;                  // int [kChoices]
-  static constexpr int kPrefix = kScan2 + kChoices * 4;              // long long [entries + 1]
+  static constexpr int kScan2 = kScan + kWarps * 8;                  // int [2 * kWarps]
+  static constexpr int kPrefix = kScan2 + 2 * kWarps * 4;              // long long [entries + 1]
   static constexpr int shared_bytes(int entries) {  // ... and int2 [min(entries, kCached)]
     return kPrefix + 8 * (entries + 1) + 8 * (entries < kCached ? entries : kCached);
   }
@@ -245,10 +244,11 @@ __device__ __forceinline__ void widen8(const Words<4>& w, bool half, float (&x)[
 
 // Where CTA `unit` leaves its part of an item: it has at most two, that of an item that began
 // before it and that of one that goes on behind it.
-template <int kRows>
+template <int D, int NT>
 __device__ __forceinline__ float* part_at(const KvAttentionArgs& a, const Part& p, int unit) {
-  const long long slot = 2 * (long long)unit + (p.slot0 >= (long long)unit * kWarps ? 1 : 0);
-  return a.partial + slot * kRows * (a.cache.head_dim + 2);
+  using L = Shape<D, NT>;
+  const long long slot = 2 * (long long)unit + (p.slot0 >= (long long)unit * L::kWarps ? 1 : 0);
+  return a.partial + slot * L::kRows * (D + 2);
 }
 
 // Four channels of a finished row: y / sum, and with the first of them the row's lse.
@@ -303,25 +303,25 @@ __device__ __forceinline__ uint4 row_fragment(const float (&x)[8], const RowScal
   return f;
 }
 
-// The i-th steps to a piece that is tried: around what fills one pass (`fair`), and what leaves an
-// item to one CTA or one warp.
+// The i-th of the lengths of a piece that are tried, a warp to each: around what fills one pass
+// (`fair`), and at last what leaves an item to one CTA and to one warp.
+template <int kWarps>
 __device__ __forceinline__ int steps_choice(int i, int fair, int longest) {
-  if (i == 15) return longest;
-  if (i == 14) return (longest + kWarps - 1) / kWarps;
-  if (fair <= 6) return 1 + i;
-  constexpr uint64_t kLow = 0x1312111008060402ull;  // sixteenths of it, eight at a time
-  constexpr uint64_t kHigh = 0x0000402820181614ull;
-  const int by = (int)((i < 8 ? kLow >> (8 * i) : kHigh >> (8 * (i - 8))) & 0xFF);
+  if (i == kWarps - 1) return longest;
+  if (i == kWarps - 2) return (longest + kWarps - 1) / kWarps;
+  if (fair < kWarps - 3) return 1 + i;
+  constexpr uint64_t kBy = kWarps == 12 ? 0x2820181614131110ull : 0x0000282018141210ull;  // sixteenths
+  const int by = i < 8 ? (int)(kBy >> (8 * i)) & 0xFF : i == 8 ? 8 : 12;
   return max(1, (int)(((long long)fair * by + 15) >> 4));
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPerSm)
     kv_attention(const KvAttentionArgs a) {
   using G = KvGroup<D>;
   using L = Shape<D, NT>;
   constexpr int CB = G::kBlocks, SB = G::kSlabBlocks, NS = G::kSlabs, NW = (CB + 3) / 4;
-  constexpr int kRows = L::kRows, kStages = L::kStages;
+  constexpr int kRows = L::kRows, kStages = L::kStages, kWarps = L::kWarps, kThreads = L::kThreads;
   constexpr bool kQInRegs = !L::kShared;
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -379,14 +379,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
     }
     total *= heads;
   }
-  // Sixteen lengths of a piece, each with the pieces in a row and with every item at the start of
+  // Some lengths of a piece, each with the pieces in a row and with every item at the start of
   // a CTA, are rated in steps: the passes' longest pieces, two steps for what a pass begins and ends with,
   // three for a join through memory.
   const long long warps = (long long)gridDim.x * kWarps;
   const int fair = (int)min((total + warps - 1) / warps, 1ll << 26);
   __syncthreads();
-  for (int c = warp; c < kChoices / 2; c += kWarps) {
-    const unsigned q = steps_choice(c, fair, longest);
+  {
+    const unsigned q = steps_choice<kWarps>(warp, fair, longest);
     float loose = 0.f, aligned = 0.f;  // units (exact where it matters, below 2^24)
     for (int b = lane; b < a.batch.entries; b += 32) {
       const Entry e = load_entry(a, b, cached);
@@ -407,12 +407,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
                        2.f * passes + (across ? 3.f : 0.f);
     // joins across CTAs have room for so many
     const bool fits = (!across || units <= (float)(kKvMaxUnits / NT)) && (!L::kShared || lane == 1);
-    if (lane < 2) scan2[2 * c + lane] = fits ? (int)fminf(cost * 16.f, 1e9f) : 0x7FFFFFFF;
+    if (lane < 2) scan2[2 * warp + lane] = fits ? (int)fminf(cost * 16.f, 1e9f) : 0x7FFFFFFF;
   }
   __syncthreads();
-  const int cheapest = __reduce_min_sync(kAll, scan2[lane]);
-  const int choice = __ffs(__ballot_sync(kAll, scan2[lane] == cheapest)) - 1;
-  const unsigned q_steps = steps_choice(choice >> 1, fair, longest);
+  const int rated = lane < 2 * kWarps ? scan2[lane] : 0x7FFFFFFF;
+  const int cheapest = __reduce_min_sync(kAll, rated);
+  const int choice = __ffs(__ballot_sync(kAll, rated == cheapest)) - 1;
+  const unsigned q_steps = steps_choice<kWarps>(choice >> 1, fair, longest);
   const unsigned align = choice & 1 ? kWarps : 1;
   // prefix[b] = places of the entries before b
   total = 0;
@@ -463,10 +464,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
     Span span{0, 0};
     int from = 0, steps = 0;  // the piece: steps [from, from + steps) of the tile
     if (slot < total) {
-      int lo = 0, hi = a.batch.entries;  // the last entry whose places begin at or before it
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= slot) lo = mid; else hi = mid;
+      // the last entry whose places begin at or before it
+      int lo = -1;
+      if (a.batch.entries <= 256) {
+        for (int b = 0; b < a.batch.entries; b += 32)
+          lo += __popc(__ballot_sync(kAll, b + lane < a.batch.entries && prefix[b + lane] <= slot));
+      } else {
+        int hi = a.batch.entries;
+        lo = 0;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (prefix[mid] <= slot) lo = mid; else hi = mid;
+        }
       }
       entry = load_entry(a, lo, cached);
       const int tiles = max(1, tiles_of<kRows>(entry, group));
@@ -483,8 +492,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
         piece = (unsigned)rest % places;
       }
       // (within bounds also if someone rewrites the lengths meanwhile)
-      const int turn = min((int)(item / heads), tiles - 1);
-      part.head = item % heads;
+      int turn = 0;
+      part.head = item;
+      if (item >= (unsigned)heads) {
+        turn = min((int)(item / heads), tiles - 1);
+        part.head = item % heads;
+      }
       part.tile = turn & 1 ? tiles - 1 - (turn >> 1) : turn >> 1;
       part.slot0 = slot - piece;
       part.first = entry.first;
@@ -692,8 +705,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
       put_v_scales();
       bool slow = false;
 
-      // (rolled: nothing is gained by the two groups side by side, and the code is half as long)
-#pragma unroll 1
+      // (unrolled for the instructions that one group's dependences leave room for: 64.1 -> 60.4 us)
+#pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int j0 = step_at + 16 * u;
         if (u == 1 && j0 >= span.end) break;  // was not copied
@@ -1003,7 +1016,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
         while (w1 < kWarps && parts_sh[w1].pieces > 0 && parts_sh[w1].slot0 == p.slot0) ++w1;
         const bool whole = p.slot0 >= (long long)unit * kWarps &&
                            p.slot0 + p.pieces <= (long long)(unit + 1) * kWarps;
-        float* to = part_at<kRows>(a, p, unit);
+        float* to = part_at<D, NT>(a, p, unit);
         if (!whole) waiting[pending++ & 1] = w0;
         constexpr int kQuads = 8 * L::kRoundBlocks;  // four channels each, of a row
         for (int i = threadIdx.x; i < kRows * kQuads; i += kThreads) {
@@ -1071,7 +1084,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtasPerSm)
               lx[x] = 0.f;
               v[x] = make_float4(0.f, 0.f, 0.f, 0.f);
               if (x0 + x < parts) {
-                const float* from = part_at<kRows>(a, part, first_unit + x0 + x);
+                const float* from = part_at<D, NT>(a, part, first_unit + x0 + x);
                 mx[x] = __ldcg(from + kRows * D + row);
                 lx[x] = __ldcg(from + kRows * D + kRows + row);
                 v[x] = __ldcg(reinterpret_cast<const float4*>(from + row * D + ch));
@@ -1114,7 +1127,7 @@ cudaError_t run(const KvAttentionArgs& a, cudaStream_t s) {
   const void* fn = reinterpret_cast<const void*>(kv_attention<D, NT>);
   cudaError_t e = ensure_dynamic_smem(fn, bytes);
   if (e != cudaSuccess) return e;
-  kv_attention<D, NT><<<kKvSms * L::kCtasPerSm, kThreads, bytes, s>>>(a);
+  kv_attention<D, NT><<<kKvSms * L::kCtasPerSm, L::kThreads, bytes, s>>>(a);
   return cudaGetLastError();
 }
 
