@@ -98,13 +98,16 @@ __device__ __forceinline__ void kv_tokens(const KvView& v, const KvBatch& q, int
   n = (int)end - first;
 }
 
-// Page in column j of slot s; page 0 (and the flag) if the id is out of range,
+// A page id of the table, in column j of slot s; page 0 (and the flag) if the id is out of range,
 // so that what follows stays inside the pool.
-__device__ __forceinline__ int kv_page(const KvView& v, int s, int j) {
-  const int p = v.table[(long long)s * v.columns + j];
+__device__ __forceinline__ int kv_page_checked(const KvView& v, int p) {
   if ((unsigned)p < (unsigned)v.num_pages) return p;
   atomicOr(v.flag, WD_KV_FLAG_BAD_INDEX);
   return 0;
+}
+
+__device__ __forceinline__ int kv_page(const KvView& v, int s, int j) {
+  return kv_page_checked(v, v.table[(long long)s * v.columns + j]);
 }
 
 // Address of the 16-token group that holds position `pos` of a head.
@@ -133,6 +136,25 @@ struct KvScratch {
   int32_t* owner;      // [slots]
   size_t bytes;        // all of it, the flag's 256 bytes included
 };
+// Launch as a programmatic dependent: the kernel may start while the one before it
+// on the stream drains.  Each of them waits for the results of that one before its first
+// read of memory.
+template <typename... Params, typename... Args>
+cudaError_t kv_launch(void (*kernel)(Params...), int grid, int block, int shared, cudaStream_t s,
+                      const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = (size_t)shared;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 KvScratch kv_scratch(const wd_kv_cache& c);
 KvView kv_view(const wd_kv_cache& c);
 

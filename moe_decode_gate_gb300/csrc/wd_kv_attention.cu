@@ -27,6 +27,7 @@
 //     columns is multiplied by 2^(s - r + 1) for every block, with r the largest scale that the warp
 //     has met for that block of channels: exact while s >= r - 15. A step that holds other
 //     scales (or NaN) adds its products one by one in FP32 instead.
+#include "wd_device.cuh"
 #include "wd_kv.cuh"
 #include "wd_mma.cuh"
 
@@ -76,12 +77,12 @@ struct Shape {
   static constexpr int kBars = kScales + kWarps * kScaleBytes;  // uint64 [kWarps][kStages]
   static constexpr int kScan = kBars + kWarps * kStages * 8;         // long long [kWarps]
   static constexpr int kScan2 = kScan + kWarps * 8;                  // int [2 * kWarps]
-  static constexpr int kPrefix = kScan2 + 2 * kWarps * 4;              // long long [entries + 1]
+  static constexpr int kPrefix = kScan2 + 2 * kWarps * 4;              // long long [entries]
   static constexpr int shared_bytes(int entries) {  // ... and int2 [min(entries, kCached)]
-    return kPrefix + 8 * (entries + 1) + 8 * (entries < kCached ? entries : kCached);
+    return kPrefix + 8 * entries + 8 * (entries < kCached ? entries : kCached);
   }
   static_assert(kScales % 16 == 0 && kBars % 8 == 0, "alignment");
-  static_assert(kPrefix + 8 * (WD_KV_MAX_ENTRIES + 1) + 8 * kCached <= 227 * 1024, "shared memory");
+  static_assert(kPrefix + 8 * WD_KV_MAX_ENTRIES + 8 * kCached <= 227 * 1024, "shared memory");
 };
 
 // Four E2M1 pairs (the bytes of w, low half first) -> four f16x2, exactly.
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
   long long* scan = reinterpret_cast<long long*>(smem + L::kScan);
   int* scan2 = reinterpret_cast<int*>(smem + L::kScan2);
   long long* prefix = reinterpret_cast<long long*>(smem + L::kPrefix);
-  int2* cached = reinterpret_cast<int2*>(prefix + a.batch.entries + 1);
+  int2* cached = reinterpret_cast<int2*>(prefix + a.batch.entries);
   uint8_t* ring = smem + L::kRing + warp * kStages * L::kStageBytes;
   uint8_t* k_scales = smem + L::kScales + warp * L::kScaleBytes;  // float [32 keys][CB]
   uint8_t* v_scales = k_scales + 32 * CB * 4;                    // f16x2 [16 pairs of keys][CB]
@@ -350,101 +351,144 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
     for (int s = 0; s < kStages; ++s) mbar_init(bar + 8 * s, 1);
     mbar_init_fence();
   }
+  grid_dependency_wait();  // nothing above reads what an earlier kernel may write
+  grid_launch_dependents();
+
   // ---- the division of the work
   Entry own{-1, 0, 0, 0};
   if ((int)threadIdx.x < a.batch.entries) own = load_entry(a, threadIdx.x);
   long long total = 0;
   int longest = 1;
+  float items = 0.f;
   {
     long long steps_here = 0;
     for (int b = threadIdx.x; b < a.batch.entries; b += kThreads) {
       const Entry e = b < kThreads ? own : load_entry(a, b);
       if (b < kCached) cached[b] = make_int2(e.slot, e.len);
-      const int steps = steps_of<kRows>(e, group, a.window);
-      steps_here += (long long)steps * tiles_of<kRows>(e, group);
+      const int steps = steps_of<kRows>(e, group, a.window), tiles = tiles_of<kRows>(e, group);
+      steps_here += (long long)steps * tiles;
+      items += (float)tiles;
       if (e.n > 0) longest = max(longest, steps);
     }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) steps_here += __shfl_xor_sync(kAll, steps_here, off);
+    for (int off = 16; off > 0; off >>= 1) {
+      steps_here += __shfl_xor_sync(kAll, steps_here, off);
+      items += __shfl_xor_sync(kAll, items, off);
+    }
     longest = __reduce_max_sync(kAll, longest);
     if (lane == 0) {
       scan[warp] = steps_here;
       scan2[warp] = longest;
+      scan2[kWarps + warp] = __float_as_int(items);
     }
     __syncthreads();
+    items = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       total += scan[w];
       longest = max(longest, scan2[w]);
+      items += __int_as_float(scan2[kWarps + w]);
     }
     total *= heads;
+    items *= (float)heads;
   }
-  // Some lengths of a piece, each with the pieces in a row and with every item at the start of
-  // a CTA, are rated in steps: the passes' longest pieces, two steps for what a pass begins and ends with,
-  // three for a join through memory.
-  const long long warps = (long long)gridDim.x * kWarps;
-  const int fair = (int)min((total + warps - 1) / warps, 1ll << 26);
-  __syncthreads();
-  {
-    const unsigned q = steps_choice<kWarps>(warp, fair, longest);
-    float loose = 0.f, aligned = 0.f;  // units (exact where it matters, below 2^24)
+  const float warps = (float)(gridDim.x * kWarps);
+  unsigned q_steps, align;
+  if (!L::kShared && 2.f * items <= warps) {
+    // Few items: q for which one pass does, whatever the lengths are (an item wastes less than a
+    // piece).  Rather than that, whole items to a CTA, if that costs less than a join through memory
+    // does, which is about three steps.
+    const float loose = ceilf((float)total / (warps - items));
+    const float aligned = (float)kWarps * items < warps
+                              ? fmaxf(ceilf((float)total / (warps - (float)kWarps * items)),
+                                      (float)((longest + kWarps - 1) / kWarps))
+                              : 1e30f;
+    align = aligned <= loose + ((float)longest > loose ? 3.f : 0.f) ? kWarps : 1;
+    q_steps = (unsigned)fmaxf(1.f, fminf(align > 1 ? aligned : loose, 1e9f));
+  } else {
+    // Some lengths of a piece, each with the pieces in a row and with every item at the start of
+    // a CTA, are rated in steps: the passes' longest pieces, two steps for what a pass begins and
+    // ends with, three for a join through memory.
+    const int fair = (int)fminf(ceilf((float)total / warps), 6e7f);
+    __syncthreads();
+    {
+      const unsigned q = steps_choice<kWarps>(warp, fair, longest);
+      float loose = 0.f, aligned = 0.f;  // units (exact where it matters, below 2^24)
+      for (int b = lane; b < a.batch.entries; b += 32) {
+        const Entry e = load_entry(a, b, cached);
+        const unsigned pieces = ((unsigned)steps_of<kRows>(e, group, a.window) + q - 1) / q;
+        const float tiles = (float)tiles_of<kRows>(e, group);
+        loose += tiles * (float)pieces;
+        aligned += tiles * (float)((pieces + kWarps - 1) / kWarps);
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) {
+        loose += __shfl_xor_sync(kAll, loose, off);
+        aligned += __shfl_xor_sync(kAll, aligned, off);
+      }
+      const float units = (float)heads * (lane == 0 ? loose * (1.f / kWarps) : aligned);
+      const float passes = ceilf(units / (float)gridDim.x);
+      const bool across = (float)longest > (float)q * (lane == 0 ? 1.f : (float)kWarps);
+      const float cost =
+          (passes <= 1.f ? (float)q : fmaxf((float)q, (float)fair + 0.75f * (float)q)) +
+          2.f * passes + (across ? 3.f : 0.f);
+      // joins across CTAs have room for so many
+      const bool fits =
+          (!across || units <= (float)(kKvMaxUnits / NT)) && (!L::kShared || lane == 1);
+      if (lane < 2) scan2[2 * warp + lane] = fits ? (int)fminf(cost * 16.f, 1e9f) : 0x7FFFFFFF;
+    }
+    __syncthreads();
+    const int rated = lane < 2 * kWarps ? scan2[lane] : 0x7FFFFFFF;
+    const int cheapest = __reduce_min_sync(kAll, rated);
+    const int choice = __ffs(__ballot_sync(kAll, rated == cheapest)) - 1;
+    q_steps = steps_choice<kWarps>(choice >> 1, fair, longest);
+    align = choice & 1 ? kWarps : 1;
+  }
+  const auto places_of = [&](const Entry& e, unsigned& pieces) {  // of one item
+    pieces = ((unsigned)steps_of<kRows>(e, group, a.window) + q_steps - 1) / q_steps;
+    return (pieces + align - 1) / align * align;
+  };
+  // Places of the entries before each entry.  A small batch is gone through by every warp for
+  // itself whenever it looks for a place; else prefix[] holds them.
+  const bool small = a.batch.entries <= 128 && (float)total + items * (float)kWarps < 2e9f;
+  total = 0;
+  if (small) {
+    unsigned all = 0;
     for (int b = lane; b < a.batch.entries; b += 32) {
       const Entry e = load_entry(a, b, cached);
-      const unsigned pieces = ((unsigned)steps_of<kRows>(e, group, a.window) + q - 1) / q;
-      const float tiles = (float)tiles_of<kRows>(e, group);
-      loose += tiles * (float)pieces;
-      aligned += tiles * (float)((pieces + kWarps - 1) / kWarps);
+      unsigned pieces;
+      all += tiles_of<kRows>(e, group) * heads * places_of(e, pieces);
     }
+    total = __reduce_add_sync(kAll, all);
+  } else {
+    for (int base = 0; base < a.batch.entries; base += kThreads) {
+      const int b = base + threadIdx.x;
+      long long cost = 0;
+      if (b < a.batch.entries) {
+        const Entry e = b < kThreads ? own : load_entry(a, b);
+        unsigned pieces;
+        cost = (long long)tiles_of<kRows>(e, group) * heads * places_of(e, pieces);
+      }
+      long long incl = cost;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      loose += __shfl_xor_sync(kAll, loose, off);
-      aligned += __shfl_xor_sync(kAll, aligned, off);
-    }
-    const float units = (float)heads * (lane == 0 ? loose * (1.f / kWarps) : aligned);
-    const float passes = ceilf(units / (float)gridDim.x);
-    const bool across = (float)longest > (float)q * (lane == 0 ? 1.f : (float)kWarps);
-    const float cost = (passes <= 1.f ? (float)q : fmaxf((float)q, (float)fair + 0.75f * (float)q)) +
-                       2.f * passes + (across ? 3.f : 0.f);
-    // joins across CTAs have room for so many
-    const bool fits = (!across || units <= (float)(kKvMaxUnits / NT)) && (!L::kShared || lane == 1);
-    if (lane < 2) scan2[2 * warp + lane] = fits ? (int)fminf(cost * 16.f, 1e9f) : 0x7FFFFFFF;
-  }
-  __syncthreads();
-  const int rated = lane < 2 * kWarps ? scan2[lane] : 0x7FFFFFFF;
-  const int cheapest = __reduce_min_sync(kAll, rated);
-  const int choice = __ffs(__ballot_sync(kAll, rated == cheapest)) - 1;
-  const unsigned q_steps = steps_choice<kWarps>(choice >> 1, fair, longest);
-  const unsigned align = choice & 1 ? kWarps : 1;
-  // prefix[b] = places of the entries before b
-  total = 0;
-  for (int base = 0; base < a.batch.entries; base += kThreads) {
-    const int b = base + threadIdx.x;
-    long long cost = 0;
-    if (b < a.batch.entries) {
-      const Entry e = b < kThreads ? own : load_entry(a, b);
-      const unsigned pieces = ((unsigned)steps_of<kRows>(e, group, a.window) + q_steps - 1) / q_steps;
-      cost = (long long)tiles_of<kRows>(e, group) * heads * ((pieces + align - 1) / align * align);
-    }
-    long long incl = cost;
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long t = __shfl_up_sync(kAll, incl, off);
+        if (lane >= off) incl += t;
+      }
+      __syncthreads();
+      if (lane == 31) scan[warp] = incl;
+      __syncthreads();
+      long long below = total, all = 0;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long long t = __shfl_up_sync(kAll, incl, off);
-      if (lane >= off) incl += t;
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) below += scan[w];
+        all += scan[w];
+      }
+      if (b < a.batch.entries) prefix[b] = below + incl - cost;
+      total += all;
     }
     __syncthreads();
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    long long below = total, all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) below += scan[w];
-      all += scan[w];
-    }
-    if (b < a.batch.entries) prefix[b] = below + incl - cost;
-    total += all;
   }
-  if (threadIdx.x == 0) prefix[a.batch.entries] = total;
-  __syncthreads();
   const bool no_joins = (unsigned)longest <= q_steps;
 
   const bool vec = (reinterpret_cast<uintptr_t>(a.q) & 15u) == 0 && a.q_token % 8 == 0 &&
@@ -464,25 +508,45 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
     Span span{0, 0};
     int from = 0, steps = 0;  // the piece: steps [from, from + steps) of the tile
     if (slot < total) {
-      // the last entry whose places begin at or before it
-      int lo = -1;
-      if (a.batch.entries <= 256) {
-        for (int b = 0; b < a.batch.entries; b += 32)
-          lo += __popc(__ballot_sync(kAll, b + lane < a.batch.entries && prefix[b + lane] <= slot));
+      // the entry that it belongs to, and its place among that entry's
+      unsigned long long rest = 0;
+      int lo = 0;
+      if (small) {
+        unsigned before = 0;
+        for (int b0 = 0; b0 < a.batch.entries; b0 += 32) {
+          const int b = b0 + lane;
+          unsigned cost = 0, pieces;
+          if (b < a.batch.entries) {
+            const Entry e = load_entry(a, b, cached);
+            cost = tiles_of<kRows>(e, group) * heads * places_of(e, pieces);
+          }
+          unsigned incl = cost;
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) {
+            const unsigned t = __shfl_up_sync(kAll, incl, off);
+            if (lane >= off) incl += t;
+          }
+          const unsigned hit = __ballot_sync(kAll, before + incl > (unsigned)slot);
+          if (hit) {
+            lo = __ffs(hit) - 1;
+            rest = (unsigned)slot - before - __shfl_sync(kAll, incl - cost, lo);
+            lo += b0;
+            break;
+          }
+          before += __shfl_sync(kAll, incl, 31);
+        }
       } else {
         int hi = a.batch.entries;
-        lo = 0;
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
           if (prefix[mid] <= slot) lo = mid; else hi = mid;
         }
+        rest = slot - prefix[lo];
       }
       entry = load_entry(a, lo, cached);
       const int tiles = max(1, tiles_of<kRows>(entry, group));
-      const unsigned pieces =
-          ((unsigned)steps_of<kRows>(entry, group, a.window) + q_steps - 1) / q_steps;
-      const unsigned places = (pieces + align - 1) / align * align;
-      const unsigned long long rest = slot - prefix[lo];
+      unsigned pieces;
+      const unsigned places = places_of(entry, pieces);
       unsigned item, piece;
       if (rest >> 32) {
         item = (unsigned)(rest / places);
@@ -512,7 +576,34 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
     }
     const int rows = entry.n * group - part.tile * kRows;  // of the tile's, those that are real
 
-    // the queries are on their way while the pages are looked up
+    // The i-th step's groups are looked up by lane i % 32, 32 steps at a time, and copied into
+    // the stages in turn.
+    const uint8_t *src0 = nullptr, *src1 = nullptr;
+    uint32_t bytes0 = 0;
+    int page0 = 0, page1 = 0;
+    const auto look_up = [&](int i0) {
+      const int pos = (span.first + from + i0 + lane) * kStep;
+      if (i0 + lane >= steps) return;
+      const int32_t* row = cache.table + (long long)entry.slot * cache.columns;
+      page0 = row[pos >> cache.page_shift];
+      page1 = cache.page_size < kStep && pos + 16 < span.end ? row[(pos + 16) >> cache.page_shift] : 0;
+    };
+    const auto plan = [&](int i0) {
+      const int pos = (span.first + from + i0 + lane) * kStep;
+      src1 = nullptr;
+      if (i0 + lane >= steps) return;
+      src0 = kv_group(cache, kv_page_checked(cache, page0), a.layer, part.head, pos, G::kBytes);
+      bytes0 = G::kBytes;
+      if (pos + 16 < span.end) {
+        if (cache.page_size >= kStep)  // the step lies within a page, its groups side by side
+          bytes0 = 2 * G::kBytes;
+        else
+          src1 = kv_group(cache, kv_page_checked(cache, page1), a.layer, part.head, pos + 16, G::kBytes);
+      }
+    };
+    look_up(0);
+
+    // the queries, on their way while the first groups are asked for
     constexpr int kFetches = L::kShared ? (kRows * (D / 8) + kThreads - 1) / kThreads : CB;
     Words<4> query[kFetches];
 #pragma unroll
@@ -528,25 +619,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
                                 (part.head * group + flat % group) * a.q_head + ch, vec);
     }
 
-    // The i-th step's groups are looked up by lane i % 32, 32 steps at a time, and copied into
-    // the stages in turn.
-    const uint8_t *src0 = nullptr, *src1 = nullptr;
-    uint32_t bytes0 = 0;
-    const auto plan = [&](int i0) {
-      const int pos = (span.first + from + i0 + lane) * kStep;
-      src1 = nullptr;
-      if (i0 + lane >= steps) return;
-      src0 = kv_group(cache, kv_page(cache, entry.slot, pos >> cache.page_shift), a.layer, part.head,
-                      pos, G::kBytes);
-      bytes0 = G::kBytes;
-      if (pos + 16 < span.end) {
-        if (cache.page_size >= kStep)  // the step lies within a page, its groups side by side
-          bytes0 = 2 * G::kBytes;
-        else
-          src1 = kv_group(cache, kv_page(cache, entry.slot, (pos + 16) >> cache.page_shift), a.layer,
-                          part.head, pos + 16, G::kBytes);
-      }
-    };
     const auto issue = [&](int to_stage) {
       const uint32_t to = ring_at + to_stage * L::kStageBytes, full = bar + 8 * to_stage;
       mbar_arrive_expect_tx(full, bytes0 + (src1 ? G::kBytes : 0));
@@ -946,7 +1018,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
       // ---- refill the stage
       __syncwarp();
       const int next = i + kStages;
-      if ((next & 31) == 0) plan(next);
+      if ((next & 31) == 0) {
+        look_up(next);
+        plan(next);
+      }
       if (lane == (next & 31) && next < steps) issue(stage);
       if (++stage == kStages) {
         stage = 0;
@@ -990,8 +1065,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
           m_sh[warp * kRows + 8 * nt + 2 * tq + e] = m[nt][e];
           l_sh[warp * kRows + 8 * nt + 2 * tq + e] = l[nt][e];
         }
-    int waiting[2], pending = 0;  // warps whose item other CTAs have pieces of
-    waiting[0] = waiting[1] = 0;
+    uint32_t leads = 0, follows = 0, partial = 0;  // warps: first of an item here, further ones, of items that go on elsewhere
 #pragma unroll
     for (int round = 0; round < L::kRounds; ++round) {
       if (round > 0) __syncthreads();
@@ -1008,55 +1082,67 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
                 output(c, nt, e);
       }
       __syncthreads();
-      pending = 0;
-      for (int w0 = 0, w1; w0 < kWarps; w0 = w1) {
+      if (round == 0) {
+        long long slot0 = 0;
+        int pieces = 0;
+        if (lane < kWarps) {
+          slot0 = parts_sh[lane].slot0;
+          pieces = parts_sh[lane].pieces;
+        }
+        const long long slot0_before = __shfl_up_sync(kAll, slot0, 1);
+        const int pieces_before = __shfl_up_sync(kAll, pieces, 1);
+        const bool follow = lane > 0 && pieces > 1 && pieces_before > 1 && slot0 == slot0_before;
+        const bool whole = slot0 >= (long long)unit * kWarps &&
+                           slot0 + pieces <= (long long)(unit + 1) * kWarps;
+        follows = __ballot_sync(kAll, follow);
+        leads = __ballot_sync(kAll, pieces > 1 && !follow);
+        partial = __ballot_sync(kAll, pieces > 1 && !follow && !whole);
+      }
+      constexpr int kQuads = 8 * L::kRoundBlocks;  // four channels each, of a row
+      for (int i = threadIdx.x; i < __popc(leads) * kRows * kQuads; i += kThreads) {
+        uint32_t rest = leads;
+        for (int skip = i / (kRows * kQuads); skip > 0; --skip) rest &= rest - 1;
+        const int w0 = __ffs(rest) - 1;
+        const int w1 = w0 + __ffs(~(follows >> (w0 + 1)));
+        const int row = i % (kRows * kQuads) / kQuads, ch = 4 * (i % kQuads);
+        float top = -INFINITY, sum = 0.f;
+        for (int w = w0; w < w1; ++w) top = fmaxf(top, m_sh[w * kRows + row]);
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int w = w0; w < w1; ++w) {
+          const float f = top == -INFINITY ? 0.f : exp2_fast(m_sh[w * kRows + row] - top);
+          const float lw = l_sh[w * kRows + row];
+          // a warp whose keys were all NaN has no maximum, but a NaN sum
+          sum += lw != lw ? lw : lw * f;
+          const float4 v =
+              *reinterpret_cast<const float4*>(merge + (w * kRows + row) * L::kMergeRow + ch);
+          y.x = fmaf(v.x, f, y.x);
+          y.y = fmaf(v.y, f, y.y);
+          y.z = fmaf(v.z, f, y.z);
+          y.w = fmaf(v.w, f, y.w);
+        }
         const Part p = parts_sh[w0];
-        w1 = w0 + 1;
-        if (p.pieces <= 1) continue;
-        while (w1 < kWarps && parts_sh[w1].pieces > 0 && parts_sh[w1].slot0 == p.slot0) ++w1;
-        const bool whole = p.slot0 >= (long long)unit * kWarps &&
-                           p.slot0 + p.pieces <= (long long)(unit + 1) * kWarps;
-        float* to = part_at<D, NT>(a, p, unit);
-        if (!whole) waiting[pending++ & 1] = w0;
-        constexpr int kQuads = 8 * L::kRoundBlocks;  // four channels each, of a row
-        for (int i = threadIdx.x; i < kRows * kQuads; i += kThreads) {
-          const int row = i / kQuads, ch = 4 * (i % kQuads);
-          float top = -INFINITY, sum = 0.f;
-          for (int w = w0; w < w1; ++w) top = fmaxf(top, m_sh[w * kRows + row]);
-          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            if (w < w0 || w >= w1) continue;
-            const float f = top == -INFINITY ? 0.f : exp2_fast(m_sh[w * kRows + row] - top);
-            const float lw = l_sh[w * kRows + row];
-            // a warp whose keys were all NaN has no maximum, but a NaN sum
-            sum += lw != lw ? lw : lw * f;
-            const float4 v =
-                *reinterpret_cast<const float4*>(merge + (w * kRows + row) * L::kMergeRow + ch);
-            y.x = fmaf(v.x, f, y.x);
-            y.y = fmaf(v.y, f, y.y);
-            y.z = fmaf(v.z, f, y.z);
-            y.w = fmaf(v.w, f, y.w);
-          }
-          const int at_ch = 32 * round * L::kRoundBlocks + ch;
-          if (whole) {
-            store_row<D, kRows>(a, p, row, at_ch, y, top, sum);
-          } else {
-            __stcg(reinterpret_cast<float4*>(to + row * D + at_ch), y);
-            if (at_ch == 0) {
-              __stcg(to + kRows * D + row, top);
-              __stcg(to + kRows * D + kRows + row, sum);
-            }
+        const int at_ch = 32 * round * L::kRoundBlocks + ch;
+        if (!(partial >> w0 & 1u)) {
+          store_row<D, kRows>(a, p, row, at_ch, y, top, sum);
+        } else {
+          float* to = part_at<D, NT>(a, p, unit);
+          __stcg(reinterpret_cast<float4*>(to + row * D + at_ch), y);
+          if (at_ch == 0) {
+            __stcg(to + kRows * D + row, top);
+            __stcg(to + kRows * D + kRows + row, sum);
           }
         }
       }
     }
     __syncthreads();
     // ---- the CTA that arrives last at an item joins its parts, in their order
+    const int pending = __popc(partial);  // the first warps' item, the last warps', or both
     if (pending > 0) {
+      const int waiting[2] = {__ffs(partial) - 1, 31 - __clz(partial)};
       if ((int)threadIdx.x < pending) {
         __threadfence();
-        const Part p = parts_sh[waiting[threadIdx.x & 1]];
+        const Part p = parts_sh[threadIdx.x == 0 ? waiting[0] : waiting[1]];
         const int first_unit = (int)(p.slot0 / kWarps);
         const uint32_t others = (uint32_t)((p.slot0 + p.pieces - 1) / kWarps - first_unit);
         const bool last = atomicAdd(a.counters + first_unit, 1u) == others;
@@ -1067,7 +1153,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
       __syncthreads();
       for (int which = 0; which < pending; ++which) {
         if (!last_sh[which]) continue;
-        const Part part = parts_sh[waiting[which]];
+        const Part part = parts_sh[which == 0 ? waiting[0] : waiting[1]];
         const int first_unit = (int)(part.slot0 / kWarps);
         const int parts = (int)((part.slot0 + part.pieces - 1) / kWarps) - first_unit + 1;
         for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
@@ -1127,8 +1213,7 @@ cudaError_t run(const KvAttentionArgs& a, cudaStream_t s) {
   const void* fn = reinterpret_cast<const void*>(kv_attention<D, NT>);
   cudaError_t e = ensure_dynamic_smem(fn, bytes);
   if (e != cudaSuccess) return e;
-  kv_attention<D, NT><<<kKvSms * L::kCtasPerSm, L::kThreads, bytes, s>>>(a);
-  return cudaGetLastError();
+  return kv_launch(kv_attention<D, NT>, kKvSms * L::kCtasPerSm, L::kThreads, bytes, s, a);
 }
 
 }  // namespace
