@@ -4,56 +4,129 @@
 // A thread takes 8 consecutive channels of one token, head and side (K or V):
 // one 16-byte load of 16-bit inputs.  Four neighbouring lanes hold a block of 32
 // channels, so its largest magnitude is two shuffles away.  The 8 codes are one
-// 32-bit word of the K layout or two 16-bit halves of the V layout.
+// 32-bit word of the K layout; in the V layout they are two 16-bit halves in
+// different places, and a third shuffle pairs them with those of the neighbouring block to
+// one 32-bit word per lane.
 //
 // Bound by memory: 2 * 2 * head_dim bytes in and head_dim + head_dim / 16 out
 // per token and head (BF16), the values back (if asked for) as much as the input.
+#include "wd_device.cuh"
 #include "wd_kv.cuh"
 
 namespace wd {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTokens = 16;  // tokens whose places a CTA looks up at a time
-
-template <typename T>
-__device__ __forceinline__ float to_float(T v);
-template <>
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <>
-__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
-template <>
-__device__ __forceinline__ float to_float(float v) { return v; }
-template <typename T>
-__device__ __forceinline__ T from_float(float v);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
-template <>
-__device__ __forceinline__ float from_float(float v) { return v; }
+constexpr int kMaxTokens = 16;  // tokens of a CTA
 
 template <typename T>
 struct alignas(16) Eight {
   T v[8];
 };
 
-// Two values -> two E2M1 codes (round to nearest even, saturating), x in the
-// low half of the byte.
-__device__ __forceinline__ uint32_t e2m1x2(float x, float y) {
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+
+// Eight inputs as floats, and the bits of the largest magnitude as a float (NaN above Inf).
+template <typename T>
+struct Widen;
+template <>
+struct Widen<float> {
+  static __device__ __forceinline__ uint32_t run(const Eight<float>& x, float (&f)[8]) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      f[k] = x.v[k];
+      top = max(top, __float_as_uint(f[k]) & 0x7FFFFFFFu);
+    }
+    return top;
+  }
+};
+template <typename T>
+__device__ __forceinline__ uint32_t top_half(const Eight<T>& x) {
+  const uint4 w = *reinterpret_cast<const uint4*>(&x);
+  const uint32_t m = max_u16x2(max_u16x2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                               max_u16x2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+  return max(m & 0xFFFFu, m >> 16);
+}
+template <>
+struct Widen<__nv_bfloat16> {
+  static __device__ __forceinline__ uint32_t run(const Eight<__nv_bfloat16>& x, float (&f)[8]) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[2 * k] = __uint_as_float(w[k] << 16);
+      f[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+    }
+    return top_half(x) << 16;
+  }
+};
+template <>
+struct Widen<__half> {
+  static __device__ __forceinline__ uint32_t run(const Eight<__half>& x, float (&f)[8]) {
+    const __half2* h = reinterpret_cast<const __half2*>(&x);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 p = __half22float2(h[k]);
+      f[2 * k] = p.x;
+      f[2 * k + 1] = p.y;
+    }
+    const uint32_t top = top_half(x);
+    return __float_as_uint(__half2float(__ushort_as_half((unsigned short)top))) & 0x7FFFFFFFu;
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ Eight<T> narrow(const float (&f)[8]);
+template <>
+__device__ __forceinline__ Eight<float> narrow(const float (&f)[8]) {
+  Eight<float> y;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) y.v[k] = f[k];
+  return y;
+}
+template <>
+__device__ __forceinline__ Eight<__nv_bfloat16> narrow(const float (&f)[8]) {
+  Eight<__nv_bfloat16> y;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    reinterpret_cast<__nv_bfloat162*>(&y)[k] = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+  return y;
+}
+template <>
+__device__ __forceinline__ Eight<__half> narrow(const float (&f)[8]) {
+  Eight<__half> y;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    reinterpret_cast<__half2*>(&y)[k] = __floats2half2_rn(f[2 * k], f[2 * k + 1]);
+  return y;
+}
+
+// Eight values -> eight E2M1 codes (round to nearest even, saturating), the first in the low bits.
+__device__ __forceinline__ uint32_t e2m1x8_of(const float (&f)[8]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(x), "f"(y));
+      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
   return r;
 }
 
-// E2M1 code -> value
-__device__ __forceinline__ float e2m1_value(uint32_t code) {
-  const uint32_t m = code & 7u;
-  const float a = m < 2u ? 0.5f * (float)m
-                         : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
-  return (code & 8u) ? -a : a;
+// ... and back.
+__device__ __forceinline__ void e2m1x8_values(uint32_t w, float (&f)[8]) {
+  uint32_t r[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&r[k]));
+    f[2 * k] = p.x;
+    f[2 * k + 1] = p.y;
+  }
 }
 
 // 2^e for e in [-127, 127], the lowest a subnormal.
@@ -66,120 +139,138 @@ struct Place {
   int t;           // token within the group
 };
 
-template <typename T, int D, bool kVec>
-__global__ void __launch_bounds__(kThreads) kv_append(const KvAppendArgs a) {
-  using G = KvGroup<D>;
-  __shared__ Place place[kTokens];
+// Where a token of the batch goes.
+template <int D>
+__device__ __forceinline__ Place find_place(const KvAppendArgs& a, int token) {
   const KvView& c = a.cache;
-  const int per_head = D / 8;  // threads to a token, head and side
-  const int per_token = 2 * c.kv_heads * per_head;
-  for (long long base = (long long)blockIdx.x * kTokens; base < a.batch.tokens;
-       base += (long long)gridDim.x * kTokens) {
-    if (threadIdx.x < kTokens) {
-      const long long token = base + threadIdx.x;
-      Place p{nullptr, 0};
-      if (token < a.batch.tokens) {
-        // the last entry that starts at or before this token
-        int b = (int)token;
-        if (a.batch.q_start) {
-          int lo = 0, hi = a.batch.entries;
-          while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (a.batch.q_start[mid] <= token) lo = mid + 1; else hi = mid;
-          }
-          b = lo - 1;
-        }
-        if (b >= 0 && b < a.batch.entries) {
-          int first, n;
-          kv_tokens(c, a.batch, b, first, n);
-          const int s = kv_slot(c, a.batch, b);
-          if (s >= 0 && token < (long long)first + n) {
-            const int pos = kv_length(c, s) - n + (int)(token - first);
-            if (pos < 0) {
-              atomicOr(c.flag, WD_KV_FLAG_BAD_INDEX);
-            } else {
-              const int id = c.table[(long long)s * c.columns + (pos >> c.page_shift)];
-              if ((unsigned)id < (unsigned)c.num_pages) {
-                p.group = kv_group(c, id, a.layer, 0, pos, G::kBytes);
-                p.t = pos & 15;
-              } else {
-                atomicOr(c.flag, WD_KV_FLAG_BAD_INDEX);
-              }
-            }
-          }
-        }
-      }
-      place[threadIdx.x] = p;
+  Place p{nullptr, 0};
+  int b = token;  // the last entry that starts at or before this token
+  if (a.batch.q_start) {
+    int lo = 0, hi = a.batch.entries;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (a.batch.q_start[mid] <= token) lo = mid + 1; else hi = mid;
     }
-    __syncthreads();
-    const int here = (int)min((long long)kTokens, a.batch.tokens - base);
-    for (int i = threadIdx.x; i < here * per_token; i += kThreads) {
-      const int token = i / per_token, r = i % per_token;
-      const int head = r / (2 * per_head);
-      const int side = (r / per_head) & 1;  // 0: K, 1: V
-      const int e = r % per_head;           // channels 8e .. 8e + 7
-      const T* src = static_cast<const T*>(side ? a.v : a.k) +
-                     (base + token) * (side ? a.v_token : a.k_token) +
-                     head * (side ? a.v_head : a.k_head) + 8 * e;
-      Eight<T> x;
+    b = lo - 1;
+  }
+  if (b < 0 || b >= a.batch.entries) return p;
+  int first, n;
+  kv_tokens(c, a.batch, b, first, n);
+  const int s = kv_slot(c, a.batch, b);
+  if (s < 0 || token >= first + n) return p;
+  const int pos = kv_length(c, s) - n + token - first;
+  if (pos < 0) {
+    atomicOr(c.flag, WD_KV_FLAG_BAD_INDEX);
+    return p;
+  }
+  const int id = c.table[(long long)s * c.columns + (pos >> c.page_shift)];
+  if ((unsigned)id >= (unsigned)c.num_pages) {
+    atomicOr(c.flag, WD_KV_FLAG_BAD_INDEX);
+    return p;
+  }
+  p.group = kv_group(c, id, a.layer, 0, pos, KvGroup<D>::kBytes);
+  p.t = pos & 15;
+  return p;
+}
+
+// per_cta: tokens of a CTA; magic: ceil(2^32 / (2 * kv_heads)), for a division of numbers below
+// 2^16 by it.
+template <typename T, int D, bool kVec>
+__global__ void __launch_bounds__(kThreads)
+    kv_append(const KvAppendArgs a, int per_cta, uint32_t magic) {
+  using G = KvGroup<D>;
+  constexpr int kPerRow = D / 8;  // threads to a token, head and side
+  __shared__ Place place[kMaxTokens];
+  const KvView& c = a.cache;
+  const int rows = 2 * c.kv_heads;  // of a token: the heads' K, then the heads' V
+  const int base = blockIdx.x * per_cta;
+  const int items = min(per_cta, a.batch.tokens - base) * rows * kPerRow;
+  const int e = threadIdx.x % kPerRow;  // channels 8e .. 8e + 7
+  const int block = e >> 2, t8 = e & 3;
+  grid_dependency_wait();  // nothing above reads what an earlier kernel may write
+  grid_launch_dependents();
+  const auto fetch = [&](int i) {
+    const int row = i / kPerRow, token = __umulhi(row, magic), hs = row - token * rows;
+    const bool v = hs >= c.kv_heads;
+    const int head = v ? hs - c.kv_heads : hs;
+    const T* src = static_cast<const T*>(v ? a.v : a.k) +
+                   (base + token) * (v ? a.v_token : a.k_token) +
+                   head * (v ? a.v_head : a.k_head) + 8 * e;
+    Eight<T> x;
+    if (kVec) {
+      x = *reinterpret_cast<const Eight<T>*>(src);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x.v[k] = src[k];
+    }
+    return x;
+  };
+  Eight<T> next;
+  if ((int)threadIdx.x < items) next = fetch(threadIdx.x);  // on its way while the places are found
+  if ((int)threadIdx.x < per_cta && base + (int)threadIdx.x < a.batch.tokens)
+    place[threadIdx.x] = find_place<D>(a, base + threadIdx.x);
+  __syncthreads();
+  for (int i = threadIdx.x; i < items; i += kThreads) {
+    const int row = i / kPerRow, token = __umulhi(row, magic), hs = row - token * rows;
+    const bool v = hs >= c.kv_heads;
+    const int head = v ? hs - c.kv_heads : hs;
+    const Eight<T> x = next;
+    if (i + kThreads < items) next = fetch(i + kThreads);
+    float f[8];
+    uint32_t top = Widen<T>::run(x, f);
+    // a row's lanes are all here, or none: kPerRow divides the warp or is a warp
+    const unsigned lanes = kPerRow >= 32 ? 0xFFFFFFFFu
+                                         : ((1u << (kPerRow % 32)) - 1u) << (threadIdx.x & 31 & ~(kPerRow - 1));
+    top = max(top, __shfl_xor_sync(lanes, top, 1));
+    top = max(top, __shfl_xor_sync(lanes, top, 2));
+    const bool bad = top >= 0x7F800000u;
+    // floor(log2(top)) - 2, at least -127; a subnormal's floor(log2) is below -126
+    const int ex = (int)(top >> 23);
+    const int exp2 = top == 0 || bad ? 0 : (ex <= 2 ? -127 : ex - 129);
+    const float inv = power_of_two(-exp2);
+    float y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = f[k] * inv;
+    const uint32_t word = bad ? 0u : e2m1x8_of(y);
+    // the scales of the row's blocks side by side
+    uint32_t scales = (bad ? 255u : (uint32_t)(exp2 + 127)) << (8 * (block & 3));
+    scales |= __shfl_xor_sync(lanes, scales, 4);
+    if (G::kBlocks >= 4) scales |= __shfl_xor_sync(lanes, scales, 8);
+    // V: blocks c and c ^ 1 swap halves, so that the even one has channels 4g .. of both for
+    // g = 2 t8 and the odd one for g = 2 t8 + 1
+    const uint32_t other = __shfl_xor_sync(lanes, word, 4);
+    const Place p = place[token];
+    if (!p.group) continue;
+    uint8_t* g = p.group + (long long)head * c.head_bytes;
+    if (!v) {
+      *reinterpret_cast<uint32_t*>(g + G::k_word(p.t, block, t8)) = word;
+    } else {
+      const uint32_t both = block & 1 ? __byte_perm(other, word, 0x7632)
+                                      : __byte_perm(word, other, 0x5410);
+      *reinterpret_cast<uint32_t*>(g + G::v_half(p.t, block & ~1, 2 * t8 + (block & 1))) = both;
+    }
+    if ((e & 15) == 0) {
+      uint8_t* to = g + (v ? G::kVScale : G::kKScale) + p.t * G::kBlocks + block;
+      if (G::kBlocks == 2)
+        *reinterpret_cast<uint16_t*>(to) = (uint16_t)scales;
+      else
+        *reinterpret_cast<uint32_t*>(to) = scales;
+    }
+    if (a.k_out) {
+      const float unit = bad ? __uint_as_float(0x7FC00000u) : power_of_two(exp2);
+      e2m1x8_values(word, y);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] *= unit;
+      const Eight<T> z = narrow<T>(y);
+      T* out = static_cast<T*>(v ? a.v_out : a.k_out) +
+               ((long long)(base + token) * c.kv_heads + head) * D + 8 * e;
       if (kVec) {
-        x = *reinterpret_cast<const Eight<T>*>(src);
+        *reinterpret_cast<Eight<T>*>(out) = z;
       } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x.v[k] = src[k];
-      }
-      float f[8];
-      uint32_t top = 0;  // largest magnitude's bits: order as the values do, NaN above Inf
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        f[k] = to_float(x.v[k]);
-        top = max(top, __float_as_uint(f[k]) & 0x7FFFFFFFu);
-      }
-      // per_token is a multiple of 4, so the four lanes of a block are active together
-      const unsigned quad = 0xFu << (threadIdx.x & 28);
-      top = max(top, __shfl_xor_sync(quad, top, 1));
-      top = max(top, __shfl_xor_sync(quad, top, 2));
-      const bool bad = top >= 0x7F800000u;
-      // floor(log2(top)) - 2, at least -127; a subnormal's floor(log2) is below -126
-      const int ex = (int)(top >> 23);
-      const int exp2 = top == 0 ? 0 : (ex <= 2 ? -127 : ex - 129);
-      const uint32_t scale = bad ? 255u : (uint32_t)(exp2 + 127);
-      const float inv = power_of_two(-exp2);
-      uint32_t word = 0;
-      if (!bad) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) word |= e2m1x2(f[2 * k] * inv, f[2 * k + 1] * inv) << (8 * k);
-      }
-      const Place p = place[token];
-      if (p.group) {
-        uint8_t* g = p.group + (long long)head * c.head_bytes;
-        const int block = e >> 2, t8 = e & 3;
-        if (side == 0) {
-          *reinterpret_cast<uint32_t*>(g + G::k_word(p.t, block, t8)) = word;
-        } else {
-          *reinterpret_cast<uint16_t*>(g + G::v_half(p.t, block, 2 * t8)) = (uint16_t)word;
-          *reinterpret_cast<uint16_t*>(g + G::v_half(p.t, block, 2 * t8 + 1)) =
-              (uint16_t)(word >> 16);
-        }
-        if (t8 == 0)
-          g[(side ? G::kVScale : G::kKScale) + p.t * G::kBlocks + block] = (uint8_t)scale;
-      }
-      if (a.k_out && p.group) {
-        const float unit = bad ? __uint_as_float(0x7FC00000u) : power_of_two(exp2);
-        Eight<T> y;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y.v[k] = from_float<T>(e2m1_value(word >> (4 * k)) * unit);
-        T* out = static_cast<T*>(side ? a.v_out : a.k_out) +
-                 ((base + token) * c.kv_heads + head) * D + 8 * e;
-        if (kVec) {
-          *reinterpret_cast<Eight<T>*>(out) = y;
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) out[k] = y.v[k];
-        }
+        for (int k = 0; k < 8; ++k) out[k] = z.v[k];
       }
     }
-    __syncthreads();
   }
 }
 
@@ -187,16 +278,21 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 template <typename T, int D>
 cudaError_t run(const KvAppendArgs& a, cudaStream_t s) {
-  const int ctas = (a.batch.tokens + kTokens - 1) / kTokens;
+  // Few tokens are spread over the SMs, a pass of the threads to each CTA at least; many get CTAs of
+  // kMaxTokens.
+  const int rows = 2 * a.cache.kv_heads;
+  const int one_pass = (kThreads / (D / 8) + rows - 1) / rows;
+  int per_cta = (a.batch.tokens + 8 * kKvSms - 1) / (8 * kKvSms);
+  per_cta = per_cta < one_pass ? one_pass : per_cta;
+  per_cta = per_cta > kMaxTokens ? kMaxTokens : per_cta;
+  const uint32_t magic = (uint32_t)(((1ull << 32) + rows - 1) / rows);
+  const int ctas = (a.batch.tokens + per_cta - 1) / per_cta;
   constexpr long long u = 16 / sizeof(T);  // elements to 16 bytes
   const bool vec = aligned16(a.k) && aligned16(a.v) && aligned16(a.k_out) && aligned16(a.v_out) &&
                    a.k_token % u == 0 && a.k_head % u == 0 && a.v_token % u == 0 &&
                    a.v_head % u == 0;
-  if (vec)
-    kv_append<T, D, true><<<ctas, kThreads, 0, s>>>(a);
-  else
-    kv_append<T, D, false><<<ctas, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return kv_launch(vec ? kv_append<T, D, true> : kv_append<T, D, false>, ctas, kThreads, 0, s, a,
+                   per_cta, magic);
 }
 
 template <typename T>

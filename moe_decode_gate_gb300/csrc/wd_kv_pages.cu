@@ -7,6 +7,7 @@
 // over the requests) and the work that it describes (table rows, counts, and the
 // pages' bytes, which are what it costs: a page of 48 layers is over a megabyte).
 // Counts change by integer atomics, whose order does not show.
+#include "wd_device.cuh"
 #include "wd_kv.cuh"
 
 namespace wd {
@@ -49,13 +50,23 @@ __device__ __forceinline__ int block_scan(int v, int& total, int* warp_sums) {
 template <typename F>
 __device__ __forceinline__ int find_free(const KvView& v, int wanted, int* warp_sums, F take) {
   constexpr int kEach = 16;
+  const bool vec = (reinterpret_cast<uintptr_t>(v.refs) & 15u) == 0;
   int found = 0;
   for (int base = 0; base < v.num_pages && found < wanted; base += kPlan * kEach) {
     const int at = base + threadIdx.x * kEach;
     uint32_t free_bits = 0;
+    if (vec && at + kEach <= v.num_pages) {
 #pragma unroll
-    for (int k = 0; k < kEach; ++k)
-      if (at + k < v.num_pages && v.refs[at + k] == 0) free_bits |= 1u << k;
+      for (int k = 0; k < kEach; k += 4) {
+        const int4 r = *reinterpret_cast<const int4*>(v.refs + at + k);
+        free_bits |= (r.x == 0 ? 1u : 0u) << k | (r.y == 0 ? 2u : 0u) << k |
+                     (r.z == 0 ? 4u : 0u) << k | (r.w == 0 ? 8u : 0u) << k;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kEach; ++k)
+        if (at + k < v.num_pages && v.refs[at + k] == 0) free_bits |= 1u << k;
+    }
     int total;
     int rank = found + block_scan(__popc(free_bits), total, warp_sums);
     while (free_bits) {
@@ -89,6 +100,8 @@ __device__ __forceinline__ void mark_owners(const KvView& v, const int32_t* slot
 __global__ void __launch_bounds__(kPlan)
     kv_reserve(const KvView v, const KvScratch w, const int32_t* seqs, const int32_t* counts,
                int n, int32_t* ok) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   __shared__ int warp_sums[33];
   __shared__ int wanted_sh;
   int32_t* begin = w.plan;              // pages that the requests before i ask for
@@ -166,6 +179,8 @@ __device__ __host__ __forceinline__ ForkPlan fork_plan(const KvScratch& w, int s
 __global__ void __launch_bounds__(kPlan)
     kv_fork_plan(const KvView v, const KvScratch w, const int32_t* src, const int32_t* dst, int n,
                  int32_t* ok) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   __shared__ int warp_sums[33];
   const ForkPlan p = fork_plan(w, v.slots);
   mark_owners(v, dst, n, w.owner);
@@ -241,6 +256,8 @@ constexpr int kPiece = 4 * kCopy * 16;  // bytes that a CTA copies at a time
 __global__ void __launch_bounds__(kCopy) kv_fork_work(const KvView v, const KvScratch w,
                                                       const int32_t* src, const int32_t* dst,
                                                       int n) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   const ForkPlan p = fork_plan(w, v.slots);
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
     const int whole = p.whole[i];
@@ -282,6 +299,8 @@ __global__ void __launch_bounds__(kCopy) kv_fork_work(const KvView v, const KvSc
 // The rows and lengths, now that nothing reads the old ones any more.
 __global__ void __launch_bounds__(kCopy) kv_fork_rows(const KvView v, const KvScratch w,
                                                       const int32_t* dst, int n) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   const ForkPlan p = fork_plan(w, v.slots);
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
     const int whole = p.whole[i];
@@ -298,6 +317,8 @@ __global__ void __launch_bounds__(kCopy) kv_fork_rows(const KvView v, const KvSc
 
 // Live pages of each chunk of kKvChunkPages pages.
 __global__ void __launch_bounds__(kPlan) kv_compact_count(const KvView v, const KvScratch w) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   __shared__ int sums[32];
   const int base = blockIdx.x * kKvChunkPages;
   int live = 0;
@@ -322,6 +343,8 @@ __global__ void __launch_bounds__(kPlan) kv_compact_count(const KvView v, const 
 // live pages, chunk[chunks + 1] = movers.
 __global__ void __launch_bounds__(kPlan)
     kv_compact_plan(const KvView v, const KvScratch w, int chunks) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   __shared__ int warp_sums[33];
   int live_total = 0, live_before = 0, live_to_split = 0, total;
   for (int base = 0; base < chunks; base += kPlan) {
@@ -382,6 +405,8 @@ __global__ void __launch_bounds__(kPlan)
 __global__ void __launch_bounds__(kCopy)
     kv_compact_work(const KvView v, const KvScratch w, int chunks, int32_t* table_out,
                     int32_t* refs_out, int32_t* page_map) {
+  grid_dependency_wait();
+  grid_launch_dependents();
   const int movers = w.chunk[chunks + 1];
   const long long threads = (long long)gridDim.x * kCopy;
   const long long me = (long long)blockIdx.x * kCopy + threadIdx.x;
@@ -426,25 +451,26 @@ constexpr int kWorkCtas = 152 * 8;
 
 cudaError_t launch_kv_reserve(const KvView& v, const KvScratch& w, const int32_t* seqs,
                               const int32_t* counts, int n, int32_t* ok, cudaStream_t s) {
-  kv_reserve<<<1, kPlan, 0, s>>>(v, w, seqs, counts, n, ok);
-  return cudaGetLastError();
+  return kv_launch(kv_reserve, 1, kPlan, 0, s, v, w, seqs, counts, n, ok);
 }
 
 cudaError_t launch_kv_fork(const KvView& v, const KvScratch& w, const int32_t* src,
                            const int32_t* dst, int n, int32_t* ok, cudaStream_t s) {
-  kv_fork_plan<<<1, kPlan, 0, s>>>(v, w, src, dst, n, ok);
-  kv_fork_work<<<kWorkCtas, kCopy, 0, s>>>(v, w, src, dst, n);
-  kv_fork_rows<<<n < 1024 ? n : 1024, kCopy, 0, s>>>(v, w, dst, n);
-  return cudaGetLastError();
+  cudaError_t e = kv_launch(kv_fork_plan, 1, kPlan, 0, s, v, w, src, dst, n, ok);
+  if (e == cudaSuccess) e = kv_launch(kv_fork_work, kWorkCtas, kCopy, 0, s, v, w, src, dst, n);
+  if (e == cudaSuccess) e = kv_launch(kv_fork_rows, n < 1024 ? n : 1024, kCopy, 0, s, v, w, dst, n);
+  return e;
 }
 
 cudaError_t launch_kv_compact(const KvView& v, const KvScratch& w, int32_t* table_out,
                               int32_t* refs_out, int32_t* page_map, cudaStream_t s) {
   const int chunks = (v.num_pages + kKvChunkPages - 1) / kKvChunkPages;
-  kv_compact_count<<<chunks, kPlan, 0, s>>>(v, w);
-  kv_compact_plan<<<chunks, kPlan, 0, s>>>(v, w, chunks);
-  kv_compact_work<<<kWorkCtas, kCopy, 0, s>>>(v, w, chunks, table_out, refs_out, page_map);
-  return cudaGetLastError();
+  cudaError_t e = kv_launch(kv_compact_count, chunks, kPlan, 0, s, v, w);
+  if (e == cudaSuccess) e = kv_launch(kv_compact_plan, chunks, kPlan, 0, s, v, w, chunks);
+  if (e == cudaSuccess)
+    e = kv_launch(kv_compact_work, kWorkCtas, kCopy, 0, s, v, w, chunks, table_out, refs_out,
+                  page_map);
+  return e;
 }
 
 }  // namespace wd
