@@ -52,10 +52,10 @@ struct Shape {
   using G = KvGroup<D>;
   static constexpr int kRows = 8 * NT;
   static constexpr int kStageBytes = 2 * G::kBytes;
-  static constexpr int kStages = D == 64 ? 4 : 2;
+  static constexpr int kStages = 2;
   static constexpr int kWarps = D <= 128 && NT == 1 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kCtasPerSm = 1;
+  static constexpr int kCtasPerSm = D == 64 && NT == 2 ? 2 : 1;
   // One tile of queries fits the registers; more are shared by the CTA's warps, whose
   // pieces are then always of one item.
   static constexpr bool kShared = NT > 1;
