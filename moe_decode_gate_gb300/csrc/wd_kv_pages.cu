@@ -7,6 +7,12 @@
 // over the requests) and the work that it describes (table rows, counts, and the
 // pages' bytes, which are what it costs: a page of 48 layers is over a megabyte).
 // Counts change by integer atomics, whose order does not show.
+//
+// Calls whose plan is short run as one kernel: every CTA makes the whole plan for
+// itself, copies its share of the pages, and the last one to finish writes the
+// bookkeeping, which nobody reads any more.  Where the plan is long it is made once,
+// and the operation takes three kernels.  (Measured, GB300: four beams, 48 layers 10.0
+// us in three kernels, 7.4 in one; 4096 small pages compacted 10.0 and 7.3.)
 #include "wd_device.cuh"
 #include "wd_kv.cuh"
 
@@ -14,7 +20,10 @@ namespace wd {
 namespace {
 
 constexpr int kPlan = 1024;  // threads of the planning CTA
-constexpr int kCopy = 256;   // threads of a copying CTA
+constexpr int kCopy = 256;   // threads that copy a piece of a page
+// What is done in one kernel: the pool's scan takes one look of kPlan threads, the tables one CTA.
+constexpr int kOnePages = 16 * kPlan;
+constexpr int kOneCells = 1 << 16;
 
 // Exclusive scan of one int per thread of a kPlan-thread CTA; `total` is the sum.
 __device__ __forceinline__ int block_scan(int v, int& total, int* warp_sums) {
@@ -232,24 +241,56 @@ __global__ void __launch_bounds__(kPlan)
   }
 }
 
-// `bytes` (a multiple of 16) from src to dst by the threads of a CTA, four
-// 16-byte loads in flight each.
-__device__ __forceinline__ void copy_bytes(uint8_t* dst, const uint8_t* src, int bytes) {
+// `bytes` (a multiple of 16) from src to dst by kThreads threads, this one being `me` of them,
+// four 16-byte loads in flight each.
+template <int kThreads>
+__device__ __forceinline__ void copy_bytes(uint8_t* dst, const uint8_t* src, int bytes, int me) {
   const uint4* in = reinterpret_cast<const uint4*>(src);
   uint4* out = reinterpret_cast<uint4*>(dst);
   const int n = bytes >> 4;
-  int i = threadIdx.x;
-  for (; i + 3 * kCopy < n; i += 4 * kCopy) {
-    const uint4 a = in[i], b = in[i + kCopy], c = in[i + 2 * kCopy], d = in[i + 3 * kCopy];
+  int i = me;
+  for (; i + 3 * kThreads < n; i += 4 * kThreads) {
+    const uint4 a = in[i], b = in[i + kThreads], c = in[i + 2 * kThreads], d = in[i + 3 * kThreads];
     out[i] = a;
-    out[i + kCopy] = b;
-    out[i + 2 * kCopy] = c;
-    out[i + 3 * kCopy] = d;
+    out[i + kThreads] = b;
+    out[i + 2 * kThreads] = c;
+    out[i + 3 * kThreads] = d;
   }
-  for (; i < n; i += kCopy) out[i] = in[i];
+  for (; i < n; i += kThreads) out[i] = in[i];
 }
 
-constexpr int kPiece = 4 * kCopy * 16;  // bytes that a CTA copies at a time
+constexpr int kPiece = 4 * kCopy * 16;  // bytes that kCopy threads copy at a time
+
+// The t-th piece of a page, page after page: the pages' pieces are dealt out to teams of kCopy
+// threads over the whole grid.  page_of(k) gives the k-th copy's source and destination, -1 for none.
+template <typename F>
+__device__ __forceinline__ void copy_pages(const KvView& v, int count, F page_of) {
+  const int pieces = (int)((v.page_bytes + kPiece - 1) / kPiece);
+  const int teams = gridDim.x * (blockDim.x / kCopy);
+  // (neighbouring teams to different CTAs, so that few pieces occupy many SMs)
+  const int team = threadIdx.x / kCopy * gridDim.x + blockIdx.x;
+  for (long long t = team; t < (long long)count * pieces; t += teams) {
+    const int2 pair = page_of((int)(t / pieces));
+    if (pair.y < 0) continue;
+    const long long off = t % pieces * kPiece;
+    copy_bytes<kCopy>(v.pool + pair.y * v.page_bytes + off, v.pool + pair.x * v.page_bytes + off,
+                      (int)min((long long)kPiece, v.page_bytes - off), threadIdx.x % kCopy);
+  }
+}
+
+// True in all threads of the CTA of the grid that gets here last, with what the others wrote visible.
+__device__ __forceinline__ bool last_cta(uint32_t* counter) {
+  __shared__ int last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = atomicAdd(counter, 1u) == gridDim.x - 1;
+    if (last) *counter = 0;
+    __threadfence();
+  }
+  __syncthreads();
+  return last != 0;
+}
 
 // Stage the new table rows (the table itself is still being read), change the
 // counts, and copy the partly filled pages.
@@ -286,14 +327,9 @@ __global__ void __launch_bounds__(kCopy) kv_fork_work(const KvView v, const KvSc
       w.rows[(long long)i * v.columns + j] = next;
     }
   }
-  const int pieces = (int)((v.page_bytes + kPiece - 1) / kPiece);
-  for (long long t = blockIdx.x; t < (long long)n * pieces; t += gridDim.x) {
-    const int i = (int)(t / pieces), piece = (int)(t % pieces);
-    if (p.whole[i] < 0 || p.page[i] < 0) continue;
-    const long long off = (long long)piece * kPiece;
-    copy_bytes(v.pool + p.page[i] * v.page_bytes + off, v.pool + p.from[i] * v.page_bytes + off,
-               (int)min((long long)kPiece, v.page_bytes - off));
-  }
+  copy_pages(v, n, [&](int i) {
+    return p.whole[i] < 0 ? make_int2(-1, -1) : make_int2(p.from[i], p.page[i]);
+  });
 }
 
 // The rows and lengths, now that nothing reads the old ones any more.
@@ -310,6 +346,111 @@ __global__ void __launch_bounds__(kCopy) kv_fork_rows(const KvView v, const KvSc
     for (int j = threadIdx.x; j < most; j += kCopy)
       v.table[(long long)d * v.columns + j] = w.rows[(long long)i * v.columns + j];
     if (threadIdx.x == 0) v.lengths[d] = p.length[i];
+  }
+}
+
+// The whole operation for up to kOneRequests requests, a pool of up to kOnePages pages and rows of up to
+// kOneCells cells in all.
+constexpr int kOneRequests = 256;
+
+__global__ void __launch_bounds__(kPlan)
+    kv_fork_one(const KvView v, const KvScratch w, const int32_t* src, const int32_t* dst, int n,
+                int32_t* ok) {
+  __shared__ int warp_sums[33], dst_sh[kOneRequests], src_sh[kOneRequests], whole_sh[kOneRequests],
+      from_sh[kOneRequests], page_sh[kOneRequests], found_sh[kOneRequests];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int i = threadIdx.x;
+  int d = -1, s = -1;
+  if (i < n) {
+    d = dst[i];
+    s = src ? src[i] : -1;
+    dst_sh[i] = d;
+    src_sh[i] = s;
+  }
+  __syncthreads();
+  bool copy = false;
+  int whole = -1, from = -1, old = 0, len = 0;
+  if (i < n) {
+    bool good = (unsigned)d < (unsigned)v.slots && s >= -1 && s < v.slots;
+    for (int k = 0; k < i; ++k) good &= dst_sh[k] != d;
+    if (good) {
+      old = (kv_length(v, d) + v.page_size - 1) >> v.page_shift;
+      len = s < 0 ? 0 : kv_length(v, s);
+      if (s == d) {
+        whole = -2;  // stays, but not refused
+      } else {
+        whole = len >> v.page_shift;
+        copy = (len & (v.page_size - 1)) != 0;
+        if (copy) from = kv_page(v, s, whole);
+      }
+    } else {
+      atomicOr(v.flag, WD_KV_FLAG_BAD_INDEX);
+    }
+  }
+  int wanted;
+  const int rank = block_scan(copy ? 1 : 0, wanted, warp_sums);
+  const int found = find_free(v, wanted, warp_sums, [&](int r, int page) { found_sh[r] = page; });
+  __syncthreads();
+  int page = -1;
+  if (copy) {
+    if (rank < found) {
+      page = found_sh[rank];
+    } else {
+      whole = -1;
+      atomicOr(v.flag, WD_KV_FLAG_NO_PAGES);
+    }
+  }
+  if (i < n) {
+    whole_sh[i] = whole;
+    from_sh[i] = from;
+    page_sh[i] = page;
+  }
+  __syncthreads();
+  copy_pages(v, n, [&](int k) { return make_int2(from_sh[k], page_sh[k]); });
+  if (!last_cta(w.counters)) return;
+  // the rows, staged first: a slot may be source and destination
+  __shared__ int old_sh[kOneRequests];
+  if (i < n) old_sh[i] = old;
+  __syncthreads();
+  const int lane = i & 31;
+  for (int k = i >> 5; k < n; k += kPlan / 32) {
+    const int wh = whole_sh[k];
+    if (wh < 0) continue;
+    const int most = min(v.columns, max(old_sh[k], wh + 1));
+    for (int j = lane; j < most; j += 32) {
+      int next = -1;
+      if (j < wh) {
+        next = v.table[(long long)src_sh[k] * v.columns + j];
+        if ((unsigned)next < (unsigned)v.num_pages)
+          atomicAdd(v.refs + next, 1);
+        else
+          atomicOr(v.flag, WD_KV_FLAG_BAD_INDEX);
+      } else if (j == wh && page_sh[k] >= 0) {
+        next = page_sh[k];
+        atomicAdd(v.refs + next, 1);
+      }
+      if (j < old_sh[k]) {
+        const int gone = v.table[(long long)dst_sh[k] * v.columns + j];
+        if ((unsigned)gone < (unsigned)v.num_pages)
+          atomicSub(v.refs + gone, 1);
+        else
+          atomicOr(v.flag, WD_KV_FLAG_BAD_INDEX);
+      }
+      w.rows[(long long)k * v.columns + j] = next;
+    }
+  }
+  __syncthreads();
+  for (int k = i >> 5; k < n; k += kPlan / 32) {
+    const int wh = whole_sh[k];
+    if (wh < 0) continue;
+    const int most = min(v.columns, max(old_sh[k], wh + 1));
+    for (int j = lane; j < most; j += 32)
+      v.table[(long long)dst_sh[k] * v.columns + j] = w.rows[(long long)k * v.columns + j];
+  }
+  if (i < n) {
+    if (whole >= 0) v.lengths[d] = len;
+    if (ok) ok[i] = whole != -1 ? 1 : 0;
   }
 }
 
@@ -436,16 +577,128 @@ __global__ void __launch_bounds__(kCopy)
     }
     if (page_map) page_map[page] = to <= -2 ? w.list_c[-2 - to] : to;
   }
-  const int pieces = (int)((v.page_bytes + kPiece - 1) / kPiece);
-  for (long long t = blockIdx.x; t < (long long)movers * pieces; t += gridDim.x) {
-    const int k = (int)(t / pieces), piece = (int)(t % pieces);
-    const long long off = (long long)piece * kPiece;
-    copy_bytes(v.pool + w.list_c[k] * v.page_bytes + off, v.pool + w.list_b[k] * v.page_bytes + off,
-               (int)min((long long)kPiece, v.page_bytes - off));
+  copy_pages(v, movers, [&](int k) { return make_int2(w.list_b[k], w.list_c[k]); });
+}
+
+// The whole operation for a pool of up to kOnePages pages and tables of up to kOneCells cells.
+// kEach: pages to a thread of the plan.
+template <int kEach>
+__global__ void __launch_bounds__(kPlan)
+    kv_compact_one(const KvView v, uint32_t* counter, int32_t* table_out, int32_t* refs_out,
+                   int32_t* page_map) {
+  constexpr int kPages = kEach * kPlan;
+  constexpr uint16_t kNowhere = 0xFFFF;
+  extern __shared__ __align__(16) uint16_t lists[];
+  __shared__ int warp_sums[33];
+  uint16_t* mover = lists;              // [kPages / 2]
+  uint16_t* hole = lists + kPages / 2;  // [kPages / 2]
+  uint16_t* to = lists + kPages;        // [kPages] where a page goes, kNowhere for a free one
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int at = threadIdx.x * kEach;
+  uint32_t live = 0;
+  if ((reinterpret_cast<uintptr_t>(v.refs) & 15u) == 0 && at + kEach <= v.num_pages) {
+#pragma unroll
+    for (int k = 0; k < kEach; k += 4) {
+      const int4 r = *reinterpret_cast<const int4*>(v.refs + at + k);
+      live |= ((r.x > 0 ? 1u : 0u) | (r.y > 0 ? 2u : 0u) | (r.z > 0 ? 4u : 0u) | (r.w > 0 ? 8u : 0u)) << k;
+    }
+  } else {
+    for (int k = 0; k < kEach; ++k)
+      if (at + k < v.num_pages && v.refs[at + k] > 0) live |= 1u << k;
+  }
+  int total, below;
+  int rank = block_scan(__popc(live), total, warp_sums);  // live pages before `at`
+  const int under = min(max(total - at, 0), kEach);       // of the thread's pages, those below `total`
+  block_scan(__popc(live & ((1u << under) - 1u)), below, warp_sums);
+  uint32_t goes[kEach / 2];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int page = at + k;
+    const bool is_live = live >> k & 1u;
+    const uint32_t stays = is_live ? (uint32_t)page : kNowhere;
+    goes[k / 2] = k & 1 ? goes[k / 2] | stays << 16 : stays;
+    if (is_live) {
+      if (page >= total) mover[rank - below] = (uint16_t)page;
+      ++rank;
+    } else if (page < total) {
+      hole[page - rank] = (uint16_t)page;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kEach / 4; ++k)
+    reinterpret_cast<uint2*>(to + at)[k] = make_uint2(goes[2 * k], goes[2 * k + 1]);
+  __syncthreads();
+  const int movers = total - below;
+  for (int k = threadIdx.x; k < movers; k += kPlan) to[mover[k]] = hole[k];
+  __syncthreads();
+  // Bookkeeping of its own is written by all CTAs, each its share; the cache's own by the
+  // last one to finish, when nobody reads it any more.
+  const bool apart = table_out != v.table && refs_out != v.refs;
+  const int first = apart ? blockIdx.x * kPlan + threadIdx.x : threadIdx.x;
+  const int step = apart ? gridDim.x * kPlan : kPlan;
+  const auto write_tables = [&]() {
+    for (int e = first; e < v.slots * v.columns; e += step) {
+      const int page = v.table[e];
+      if (page >= v.num_pages) atomicOr(v.flag, WD_KV_FLAG_BAD_INDEX);
+      const int now = (unsigned)page < (unsigned)v.num_pages ? to[page] : kNowhere;
+      table_out[e] = now == kNowhere ? -1 : now;
+    }
+  };
+  const auto map_page = [&](int page) {
+    if (page_map) page_map[page] = to[page] == kNowhere ? -1 : to[page];
+  };
+  if (apart) {
+    write_tables();
+    for (int page = first; page < v.num_pages; page += step) {
+      map_page(page);
+      if (to[page] != kNowhere) refs_out[to[page]] = v.refs[page];
+      if (page >= total) refs_out[page] = 0;
+    }
+  }
+  copy_pages(v, movers, [&](int k) { return make_int2(mover[k], hole[k]); });
+  if (apart || !last_cta(counter)) return;
+  write_tables();
+  int count[kEach];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int page = k * kPlan + threadIdx.x;
+    if (page >= v.num_pages) break;
+    count[k] = v.refs[page];
+    map_page(page);
+  }
+  __syncthreads();  // refs_out may be refs
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int page = k * kPlan + threadIdx.x;
+    if (page >= v.num_pages) break;
+    if (to[page] != kNowhere) refs_out[to[page]] = count[k];
+    if (page >= total) refs_out[page] = 0;
   }
 }
 
-constexpr int kWorkCtas = 152 * 8;
+constexpr int kWorkCtas = kKvSms * 8;
+
+// Whether up to `copies` page copies are few enough for the one-kernel forms.  Their CTAs are large, and
+// copy less well than the many small ones of the other form: 107 MB take 38.0 us against 37.0,
+// 411 MB 138 against 133.
+bool few_bytes(const KvView& v, long long copies) { return copies * v.page_bytes <= (64ll << 20); }
+// CTAs of kPlan threads for them.
+int copying_ctas(const KvView& v, int copies) {
+  const long long pieces = (v.page_bytes + kPiece - 1) / kPiece * copies;
+  return (int)(pieces < 1 ? 1 : pieces < kKvSms ? pieces : kKvSms);
+}
+
+template <int kEach>
+cudaError_t compact_one(const KvView& v, const KvScratch& w, int32_t* table_out, int32_t* refs_out,
+                        int32_t* page_map, cudaStream_t s) {
+  constexpr int kBytes = 2 * 2 * kEach * kPlan;
+  const cudaError_t e =
+      ensure_dynamic_smem(reinterpret_cast<const void*>(kv_compact_one<kEach>), kBytes);
+  if (e != cudaSuccess) return e;
+  return kv_launch(kv_compact_one<kEach>, copying_ctas(v, v.num_pages / 2), kPlan, kBytes, s, v,
+                   w.counters, table_out, refs_out, page_map);
+}
 
 }  // namespace
 
@@ -456,6 +709,9 @@ cudaError_t launch_kv_reserve(const KvView& v, const KvScratch& w, const int32_t
 
 cudaError_t launch_kv_fork(const KvView& v, const KvScratch& w, const int32_t* src,
                            const int32_t* dst, int n, int32_t* ok, cudaStream_t s) {
+  if (n <= kOneRequests && v.num_pages <= kOnePages && (long long)n * v.columns <= kOneCells &&
+      few_bytes(v, n))
+    return kv_launch(kv_fork_one, copying_ctas(v, n), kPlan, 0, s, v, w, src, dst, n, ok);
   cudaError_t e = kv_launch(kv_fork_plan, 1, kPlan, 0, s, v, w, src, dst, n, ok);
   if (e == cudaSuccess) e = kv_launch(kv_fork_work, kWorkCtas, kCopy, 0, s, v, w, src, dst, n);
   if (e == cudaSuccess) e = kv_launch(kv_fork_rows, n < 1024 ? n : 1024, kCopy, 0, s, v, w, dst, n);
@@ -464,6 +720,10 @@ cudaError_t launch_kv_fork(const KvView& v, const KvScratch& w, const int32_t* s
 
 cudaError_t launch_kv_compact(const KvView& v, const KvScratch& w, int32_t* table_out,
                               int32_t* refs_out, int32_t* page_map, cudaStream_t s) {
+  if (v.num_pages <= kOnePages && (long long)v.slots * v.columns <= kOneCells &&
+      few_bytes(v, v.num_pages / 2))
+    return v.num_pages <= 4 * kPlan ? compact_one<4>(v, w, table_out, refs_out, page_map, s)
+                                    : compact_one<16>(v, w, table_out, refs_out, page_map, s);
   const int chunks = (v.num_pages + kKvChunkPages - 1) / kKvChunkPages;
   cudaError_t e = kv_launch(kv_compact_count, chunks, kPlan, 0, s, v, w);
   if (e == cudaSuccess) e = kv_launch(kv_compact_plan, chunks, kPlan, 0, s, v, w, chunks);

@@ -12,7 +12,8 @@ KV_FLAG_BAD_INDEX = 1
 KV_FLAG_TIMEOUT = 2
 KV_FLAG_NO_PAGES = 4
 
-_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_Q_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+_DTYPES = {**_Q_DTYPES, torch.float32: 2}
 
 
 class _Cache(ctypes.Structure):
@@ -95,6 +96,7 @@ class KVCache:
         self._ref = ctypes.byref(c)
         self._lib = lib()
         self._index = self.device.index
+        self._scale = 1.0 / math.sqrt(head_dim)
         size = int(self._lib.wd_kv_workspace_size(self._ref))
         if not size:
             raise ValueError(f"unsupported cache: num_pages={num_pages}, slots={slots}, "
@@ -112,37 +114,45 @@ class KVCache:
             return torch._C._cuda_getCurrentRawStream(self._index)
         return stream.cuda_stream
 
+    # Each call checks its tensors with as few attribute look-ups as it can (a call costs the host
+    # about ten microseconds, half of it the launch) and says what is wrong in the slow path.
+
     def _ints(self, name, t, n=None):
         """Pointer of an int32 vector on the cache's device (None stays None)."""
         if t is None:
             return None
-        if t.dtype != torch.int32 or t.dim() != 1 or t.device != self.device or \
+        if t.dtype is not torch.int32 or t.dim() != 1 or t.device != self.device or \
                 not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous int32 vector on {self.device}")
-        if n is not None and t.numel() != n:
-            raise ValueError(f"{name} must have {n} elements, not {t.numel()}")
+        if n is not None and t.shape[0] != n:
+            raise ValueError(f"{name} must have {n} elements, not {t.shape[0]}")
         return t.data_ptr()
 
-    def _rows(self, name, t, heads=None):
-        """Checks a [tokens, heads, head_dim] tensor with contiguous channels."""
+    def _refuse(self, name, t, heads, types):
+        """Says what is wrong with a tensor that should be [tokens, heads, head_dim]."""
         if t.dim() != 3 or t.shape[2] != self.head_dim or (heads and t.shape[1] != heads):
             raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {self.head_dim}], "
                              f"not {list(t.shape)}")
         if t.device != self.device:
             raise ValueError(f"{name} must be on {self.device}")
+        if t.dtype not in types:
+            raise ValueError(f"{name} must be one of {', '.join(str(d) for d in types)}")
         if t.stride(2) != 1:
             raise ValueError(f"{name} must have contiguous channels")
+        raise ValueError(f"{t.shape[1]} query heads over {self.kv_heads} key heads")
 
     def _entries(self, seqs, q_start, tokens):
         if q_start is not None:
-            if q_start.numel() < 1:
+            n = q_start.shape[0] - 1
+            if n < 0:
                 raise ValueError("q_start must have one element more than there are entries")
-            n = q_start.numel() - 1
-        else:
-            n = seqs.numel() if seqs is not None else tokens
-            if tokens > n:
-                raise ValueError(f"{tokens} tokens for {n} entries: q_start is needed")
-        return self._ints("seqs", seqs, n), self._ints("q_start", q_start), n
+            return self._ints("seqs", seqs, n), self._ints("q_start", q_start), n
+        if seqs is None:
+            return None, None, tokens
+        n = seqs.shape[0]
+        if tokens > n:
+            raise ValueError(f"{tokens} tokens for {n} entries: q_start is needed")
+        return self._ints("seqs", seqs), None, n
 
     # ------------------------------------------------------------------ the calls ---
 
@@ -166,21 +176,31 @@ class KVCache:
         q_start[b + 1] (token b without q_start), the last ones of its sequence.  With
         ``return_values`` returns what the cache now holds for them, (k, v) in their type; tokens
         of no entry are then undefined."""
-        self._rows("k", k, self.kv_heads)
-        self._rows("v", v, self.kv_heads)
-        if k.dtype not in _DTYPES or v.dtype != k.dtype or v.shape != k.shape:
-            raise ValueError("k and v must have the same shape and the same type of BF16, FP16, FP32")
-        tokens = k.shape[0]
+        dtype, shape = k.dtype, k.shape
+        code = _DTYPES.get(dtype)
+        if code is None or len(shape) != 3 or shape[1] != self.kv_heads or \
+                shape[2] != self.head_dim or k.device != self.device:
+            self._refuse("k", k, self.kv_heads, _DTYPES)
+        if v.dtype is not dtype or v.shape != shape or v.device != self.device:
+            raise ValueError("v must have k's shape and type, on its device")
+        k_token, k_head, k_channel = k.stride()
+        v_token, v_head, v_channel = v.stride()
+        if k_channel != 1 or v_channel != 1:
+            raise ValueError("k and v must have contiguous channels")
+        tokens = shape[0]
         s, qs, n = self._entries(seqs, q_start, tokens)
-        k_out = v_out = None
         if return_values:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=self.device)
-            v_out = torch.empty(k.shape, dtype=k.dtype, device=self.device)
-        _check("wd_kv_append", self._lib.wd_kv_append(
-            self._ref, layer, k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], k.stride(0),
-            k.stride(1), v.stride(0), v.stride(1), k_out.data_ptr() if return_values else None,
-            v_out.data_ptr() if return_values else None, s, qs, n, tokens, self._stream(stream)))
-        return (k_out, v_out) if return_values else None
+            values = torch.empty((2, *shape), dtype=dtype, device=self.device)
+            k_to = values.data_ptr()
+            v_to = k_to + values.nbytes // 2
+        else:
+            k_to = v_to = None
+        st = self._lib.wd_kv_append(self._ref, layer, k.data_ptr(), v.data_ptr(), code, k_token,
+                                    k_head, v_token, v_head, k_to, v_to, s, qs, n, tokens,
+                                    self._stream(stream))
+        if st:
+            _check("wd_kv_append", st)
+        return values.unbind(0) if return_values else None
 
     def attention(self, layer, q, seqs=None, q_start=None, max_q=0, scale=None, window=0, out=None,
                   return_lse=False, stream=None):
@@ -191,25 +211,32 @@ class KVCache:
         defaults to 1 / sqrt(head_dim); ``max_q`` is the most tokens an entry has, if known.
         Returns ``out`` [tokens, q_heads, head_dim], and lse FP32 [tokens, q_heads] with
         ``return_lse``; zeros and -inf where nothing is seen."""
-        self._rows("q", q)
-        tokens, heads = q.shape[:2]
-        if q.dtype not in (torch.bfloat16, torch.float16):
-            raise ValueError("q must be BF16 or FP16")
-        if heads == 0 or heads % self.kv_heads:
-            raise ValueError(f"{heads} query heads over {self.kv_heads} key heads")
+        dtype, shape = q.dtype, q.shape
+        code = _Q_DTYPES.get(dtype)
+        if code is None or len(shape) != 3 or shape[2] != self.head_dim or \
+                q.device != self.device or shape[1] % self.kv_heads or not shape[1]:
+            self._refuse("q", q, None, _Q_DTYPES)
+        q_token, q_head, q_channel = q.stride()
+        if q_channel != 1:
+            self._refuse("q", q, None, _Q_DTYPES)
+        tokens, heads = shape[0], shape[1]
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or \
+            out = torch.empty(shape, dtype=dtype, device=self.device)
+        elif out.shape != shape or out.dtype is not dtype or not out.is_contiguous() or \
                 out.device != self.device:
             raise ValueError("out must be contiguous, of q's shape and type")
-        lse = None
         if return_lse:
-            lse = torch.empty(tokens, heads, dtype=torch.float32, device=self.device)
+            lse = torch.empty((tokens, heads), dtype=torch.float32, device=self.device)
+            lse_to = lse.data_ptr()
+        else:
+            lse_to = None
         s, qs, n = self._entries(seqs, q_start, tokens)
-        _check("wd_kv_attention", self._lib.wd_kv_attention(
-            self._ref, layer, q.data_ptr(), _DTYPES[q.dtype], q.stride(0), q.stride(1), heads,
-            out.data_ptr(), lse.data_ptr() if return_lse else None, s, qs, n, tokens, max_q,
-            1.0 / math.sqrt(self.head_dim) if scale is None else scale, window, self._stream(stream)))
+        st = self._lib.wd_kv_attention(self._ref, layer, q.data_ptr(), code, q_token, q_head, heads,
+                                       out.data_ptr(), lse_to, s, qs, n, tokens, max_q,
+                                       self._scale if scale is None else scale, window,
+                                       self._stream(stream))
+        if st:
+            _check("wd_kv_attention", st)
         return (out, lse) if return_lse else out
 
     def fork(self, src, dst, ok=None, stream=None):
