@@ -12,7 +12,7 @@
 // itself, copies its share of the pages, and the last one to finish writes the
 // bookkeeping, which nobody reads any more.  Where the plan is long it is made once,
 // and the operation takes three kernels.  (Measured, GB300: four beams, 48 layers 10.0
-// us in three kernels, 7.4 in one; 4096 small pages compacted 10.0 and 7.3.)
+// us in three kernels, 8.3 in one; 4096 small pages compacted 10.0 and 5.4.)
 #include "wd_device.cuh"
 #include "wd_kv.cuh"
 
@@ -241,25 +241,25 @@ __global__ void __launch_bounds__(kPlan)
   }
 }
 
-// `bytes` (a multiple of 16) from src to dst by kThreads threads, this one being `me` of them,
-// four 16-byte loads in flight each.
-template <int kThreads>
-__device__ __forceinline__ void copy_bytes(uint8_t* dst, const uint8_t* src, int bytes, int me) {
+// Bytes that kCopy threads copy at a time, each with eight 16-byte loads in flight.  (With
+// streaming loads and stores and 32 CTAs to an SM: a compaction that moves 411 MB 124.7 us, 97 % of
+// the copy bandwidth; four loads, 8 CTAs and the caches' own ways took 141.)
+constexpr int kLoads = 8;
+constexpr int kPiece = kLoads * kCopy * 16;
+
+// Up to kPiece bytes (a multiple of 16) from src to dst by kCopy threads, this one `me` of them.
+__device__ __forceinline__ void copy_piece(uint8_t* dst, const uint8_t* src, int bytes, int me) {
   const uint4* in = reinterpret_cast<const uint4*>(src);
   uint4* out = reinterpret_cast<uint4*>(dst);
   const int n = bytes >> 4;
-  int i = me;
-  for (; i + 3 * kThreads < n; i += 4 * kThreads) {
-    const uint4 a = in[i], b = in[i + kThreads], c = in[i + 2 * kThreads], d = in[i + 3 * kThreads];
-    out[i] = a;
-    out[i + kThreads] = b;
-    out[i + 2 * kThreads] = c;
-    out[i + 3 * kThreads] = d;
-  }
-  for (; i < n; i += kThreads) out[i] = in[i];
+  uint4 x[kLoads];
+#pragma unroll
+  for (int q = 0; q < kLoads; ++q)
+    if (me + q * kCopy < n) x[q] = __ldcs(in + me + q * kCopy);
+#pragma unroll
+  for (int q = 0; q < kLoads; ++q)
+    if (me + q * kCopy < n) __stcs(out + me + q * kCopy, x[q]);
 }
-
-constexpr int kPiece = 4 * kCopy * 16;  // bytes that kCopy threads copy at a time
 
 // The t-th piece of a page, page after page: the pages' pieces are dealt out to teams of kCopy
 // threads over the whole grid.  page_of(k) gives the k-th copy's source and destination, -1 for none.
@@ -273,8 +273,8 @@ __device__ __forceinline__ void copy_pages(const KvView& v, int count, F page_of
     const int2 pair = page_of((int)(t / pieces));
     if (pair.y < 0) continue;
     const long long off = t % pieces * kPiece;
-    copy_bytes<kCopy>(v.pool + pair.y * v.page_bytes + off, v.pool + pair.x * v.page_bytes + off,
-                      (int)min((long long)kPiece, v.page_bytes - off), threadIdx.x % kCopy);
+    copy_piece(v.pool + pair.y * v.page_bytes + off, v.pool + pair.x * v.page_bytes + off,
+               (int)min((long long)kPiece, v.page_bytes - off), threadIdx.x % kCopy);
   }
 }
 
@@ -677,11 +677,10 @@ __global__ void __launch_bounds__(kPlan)
   }
 }
 
-constexpr int kWorkCtas = kKvSms * 8;
+constexpr int kWorkCtas = kKvSms * 32;
 
 // Whether up to `copies` page copies are few enough for the one-kernel forms.  Their CTAs are large, and
-// copy less well than the many small ones of the other form: 107 MB take 38.0 us against 37.0,
-// 411 MB 138 against 133.
+// copy less well than the many small ones of the other form: 97 MB take 38.0 us against 33.7.
 bool few_bytes(const KvView& v, long long copies) { return copies * v.page_bytes <= (64ll << 20); }
 // CTAs of kPlan threads for them.
 int copying_ctas(const KvView& v, int copies) {
