@@ -596,3 +596,34 @@ def test_reserve_many_pages_at_once(cuda_device):
     b.reserve([2, 0], [300000, 1000])
     b.reserve([1, 2], [17, 16])
     assert b.cache.read_error_flag() == 0
+
+
+@pytest.mark.parametrize("seed", range(2))
+def test_random_page_operations_in_a_large_pool(cuda_device, seed):
+    """A pool whose plans are made once for all CTAs, by kernels of their own."""
+    r = np.random.RandomState(100 + seed)
+    slots = 300
+    b = Both(cuda_device, 16385 + 5000 * seed, slots, 30, layers=1)
+    b.reserve(list(range(0, slots, 2)), r.randint(0, 450, slots // 2).tolist())
+    for _ in range(6):
+        n = int(r.choice([5, 100, 290]))
+        which = r.permutation(slots)[:n]
+        op = r.randint(3)
+        if op == 0:
+            b.reserve(which.tolist(), r.randint(0, 40, n).tolist())
+            b.write()
+        elif op == 1:
+            b.fork(r.randint(-1, slots, n).tolist(), which.tolist())
+        else:
+            b.compact()
+
+
+def test_more_requests_than_one_kernel_takes(cuda_device):
+    r = np.random.RandomState(5)
+    b = Both(cuda_device, 3000, 400, 8)
+    b.reserve(list(range(400)), r.randint(0, 100, 400).tolist())
+    b.write()
+    b.fork(r.randint(-1, 400, 400).tolist(), r.permutation(400).tolist())
+    b.fork([3] * 300 + [900], list(range(100, 400)) + [1])  # too few pages for all, one bad slot
+    b.compact()
+    assert b.cache.read_error_flag() & wd.KV_FLAG_BAD_INDEX
