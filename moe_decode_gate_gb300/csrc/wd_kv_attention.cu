@@ -160,6 +160,22 @@ __device__ __forceinline__ Words<(CB + 3) / 4> lds_scales(const uint8_t* p) {
   }
 }
 
+// x / d with inv = 1.f / d: the quotient in FP32 is at most one off where x is small, and put right; the
+// compiler's own division takes three times as long, and a piece is found by several in a row.
+struct Divisor {
+  unsigned d;
+  float inv;
+  __device__ __forceinline__ explicit Divisor(unsigned by) : d(by), inv(1.f / (float)by) {}
+  __device__ __forceinline__ unsigned of(unsigned x) const {
+    if (x >= 1u << 22) return x / d;
+    unsigned q = (unsigned)((float)x * inv);
+    const int r = (int)(x - q * d);
+    q += r >= (int)d ? 1u : 0u;
+    q -= r < 0 ? 1u : 0u;
+    return q;
+  }
+};
+
 // What of the sequence one entry of the batch works on.
 struct Entry {
   int slot, len, first, n;
@@ -259,8 +275,9 @@ __device__ __forceinline__ void store_row(const KvAttentionArgs& a, const Part& 
   const int group = a.q_heads / a.cache.kv_heads;
   const int flat = p.tile * kRows + row;
   if (flat >= p.n * group) return;
+  const int token = p.n > 1 ? flat / group : 0;
   const long long at =
-      (long long)(p.first + flat / group) * a.q_heads + p.head * group + flat % group;
+      (long long)(p.first + token) * a.q_heads + p.head * group + flat - token * group;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const float v[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
   uint16_t* to = static_cast<uint16_t*>(a.out) + at * D + ch;
@@ -444,9 +461,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
     q_steps = steps_choice<kWarps>(choice >> 1, fair, longest);
     align = choice & 1 ? kWarps : 1;
   }
+  const Divisor by_q(q_steps);
   const auto places_of = [&](const Entry& e, unsigned& pieces) {  // of one item
-    pieces = ((unsigned)steps_of<kRows>(e, group, a.window) + q_steps - 1) / q_steps;
-    return (pieces + align - 1) / align * align;
+    pieces = by_q.of((unsigned)steps_of<kRows>(e, group, a.window) + q_steps - 1);
+    return align > 1 ? (pieces + kWarps - 1) / kWarps * kWarps : pieces;
   };
   // Places of the entries before each entry.  A small batch is gone through by every warp for
   // itself whenever it looks for a place; else prefix[] holds them.
@@ -511,14 +529,17 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
       // the entry that it belongs to, and its place among that entry's
       unsigned long long rest = 0;
       int lo = 0;
+      unsigned pieces, places;
       if (small) {
         unsigned before = 0;
         for (int b0 = 0; b0 < a.batch.entries; b0 += 32) {
           const int b = b0 + lane;
-          unsigned cost = 0, pieces;
+          unsigned cost = 0, lane_pieces = 0, lane_places = 0;
+          Entry e{-1, 0, 0, 0};
           if (b < a.batch.entries) {
-            const Entry e = load_entry(a, b, cached);
-            cost = tiles_of<kRows>(e, group) * heads * places_of(e, pieces);
+            e = load_entry(a, b, cached);
+            lane_places = places_of(e, lane_pieces);
+            cost = tiles_of<kRows>(e, group) * heads * lane_places;
           }
           unsigned incl = cost;
 #pragma unroll
@@ -530,7 +551,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
           if (hit) {
             lo = __ffs(hit) - 1;
             rest = (unsigned)slot - before - __shfl_sync(kAll, incl - cost, lo);
-            lo += b0;
+            pieces = __shfl_sync(kAll, lane_pieces, lo);
+            places = __shfl_sync(kAll, lane_places, lo);
+            entry.slot = __shfl_sync(kAll, e.slot, lo);
+            entry.len = __shfl_sync(kAll, e.len, lo);
+            entry.first = __shfl_sync(kAll, e.first, lo);
+            entry.n = __shfl_sync(kAll, e.n, lo);
             break;
           }
           before += __shfl_sync(kAll, incl, 31);
@@ -542,25 +568,18 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
           if (prefix[mid] <= slot) lo = mid; else hi = mid;
         }
         rest = slot - prefix[lo];
+        entry = load_entry(a, lo, cached);
+        places = places_of(entry, pieces);
       }
-      entry = load_entry(a, lo, cached);
       const int tiles = max(1, tiles_of<kRows>(entry, group));
-      unsigned pieces;
-      const unsigned places = places_of(entry, pieces);
-      unsigned item, piece;
-      if (rest >> 32) {
-        item = (unsigned)(rest / places);
-        piece = (unsigned)(rest % places);
-      } else {
-        item = (unsigned)rest / places;
-        piece = (unsigned)rest % places;
-      }
+      const unsigned item = rest >> 32 ? (unsigned)(rest / places) : Divisor(places).of((unsigned)rest);
+      const unsigned piece = (unsigned)(rest - (unsigned long long)item * places);
       // (within bounds also if someone rewrites the lengths meanwhile)
       int turn = 0;
       part.head = item;
       if (item >= (unsigned)heads) {
         turn = min((int)(item / heads), tiles - 1);
-        part.head = item % heads;
+        part.head = item - (item / heads) * heads;
       }
       part.tile = turn & 1 ? tiles - 1 - (turn >> 1) : turn >> 1;
       part.slot0 = slot - piece;
@@ -613,10 +632,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
       const int row = L::kShared ? x / (D / 8) : g;
       const int ch = L::kShared ? x % (D / 8) * 8 : 32 * i + 8 * tq;
       const int flat = part.tile * kRows + row;
+      const int token = entry.n > 1 ? flat / group : 0;
       query[i] = Words<4>{{0u, 0u, 0u, 0u}};
       if (row < kRows && row < rows && (L::kShared || part.pieces > 0))
-        query[i] = load8(a, (entry.first + flat / group) * a.q_token +
-                                (part.head * group + flat % group) * a.q_head + ch, vec);
+        query[i] = load8(a, (entry.first + token) * a.q_token +
+                                (part.head * group + flat - token * group) * a.q_head + ch, vec);
     }
 
     const auto issue = [&](int to_stage) {
@@ -653,7 +673,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
                                   (((row >> 3) * CB + (e8 >> 2)) * 32 + (row & 7) * 4 + (e8 & 3)) * 16) =
             row_fragment(x, r);
         if (e8 == 0) {
-          const int pos = entry.len - entry.n + (part.tile * kRows + row) / group;
+          const int pos = entry.len - entry.n + (entry.n > 1 ? (part.tile * kRows + row) / group : 0);
           const bool real = row < rows;  // no row: nothing to hide, never stored
           factor_sh[row] = row_factor(r, a.scale);
           lo_sh[row] = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
@@ -677,7 +697,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
       for (int c = 0; c < CB; ++c) qf[c] = row_fragment(x[c], r);
       __syncwarp();
       if (tq == 0) {
-        const int pos = entry.len - entry.n + (part.tile * kRows + g) / group;
+        const int pos = entry.len - entry.n + (entry.n > 1 ? (part.tile * kRows + g) / group : 0);
         const bool real = g < rows;
         factor_sh[g] = row_factor(r, a.scale);
         lo_sh[g] = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
@@ -1141,13 +1161,17 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
     if (pending > 0) {
       const int waiting[2] = {__ffs(partial) - 1, 31 - __clz(partial)};
       if ((int)threadIdx.x < pending) {
-        __threadfence();
         const Part p = parts_sh[threadIdx.x == 0 ? waiting[0] : waiting[1]];
         const int first_unit = (int)(p.slot0 / kWarps);
         const uint32_t others = (uint32_t)((p.slot0 + p.pieces - 1) / kWarps - first_unit);
-        const bool last = atomicAdd(a.counters + first_unit, 1u) == others;
+        // releases what the CTA wrote before its barrier, and acquires what the others released
+        uint32_t before;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;"
+                     : "=r"(before)
+                     : "l"(a.counters + first_unit)
+                     : "memory");
+        const bool last = before == others;
         if (last) a.counters[first_unit] = 0;
-        __threadfence();
         last_sh[threadIdx.x] = last;
       }
       __syncthreads();
