@@ -59,6 +59,8 @@ struct Shape {
   // One tile of queries fits the registers; more are shared by the CTA's warps, whose
   // pieces are then always of one item.
   static constexpr bool kShared = NT > 1;
+  // groups of a step whose products run side by side, as far as the registers go
+  static constexpr int kTogether = NT == 1 || (NT == 2 && D <= 128) ? 2 : 1;
   // the warps' outputs are joined through shared memory, in one round where it has room for all
   static constexpr int kRounds = D == 256 ? 2 * NT : D == 128 && NT == 4 ? 2 : 1;
   static constexpr int kRoundBlocks = G::kBlocks / kRounds;
@@ -333,14 +335,157 @@ __device__ __forceinline__ int steps_choice(int i, int fair, int longest) {
   return max(1, (int)(((long long)fair * by + 15) >> 4));
 }
 
+// S^T of one group of 16 keys: s[nt] has keys g (0, 1) and 8 + g (2, 3) of columns 2tq, 2tq + 1.
+// `scales`: the group's keys' block scales as floats.
+template <int D, int NT>
+__device__ __forceinline__ void scores(const uint8_t* buf, const uint8_t* scales, const uint4* qf,
+                                       const uint8_t* q_sh, int lane, float (&s)[NT][4]) {
+  using G = KvGroup<D>;
+  constexpr int CB = G::kBlocks, SB = G::kSlabBlocks, NS = G::kSlabs;
+  const int g = lane >> 2, tq = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+#pragma unroll
+  for (int sl = 0; sl < NS; ++sl) {
+    Words<SB> kw[2], kf[2];  // codes and scales of keys 8h + g
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      kw[h] = lds<SB>(buf + sl * G::kSlabBytes + (8 * h + g) * 16 * SB + tq * 4 * SB);
+      kf[h] = lds<SB>(scales + ((8 * h + g) * CB + sl * SB) * 4);
+    }
+#pragma unroll
+    for (int c = 0; c < SB; ++c) {
+      const int cb = sl * SB + c;
+      uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+      e2m1x8(kw[0].v[c], a0, a2, b0, b2);
+      e2m1x8(kw[1].v[c], a1, a3, b1, b3);
+      const float s0 = __uint_as_float(kf[0].v[c]), s1 = __uint_as_float(kf[1].v[c]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4 q = Shape<D, NT>::kShared ? *reinterpret_cast<const uint4*>(
+                                                    q_sh + ((nt * CB + cb) * 32 + lane) * 16)
+                                              : qf[Shape<D, NT>::kShared ? 0 : cb];
+        float t[4];
+        mma_f16_zero(t, a0, a1, a2, a3, q.x, q.y);
+        mma_f16_acc(t, b0, b1, b2, b3, q.z, q.w);
+        s[nt][0] = fmaf(t[0], s0, s[nt][0]);
+        s[nt][1] = fmaf(t[1], s0, s[nt][1]);
+        s[nt][2] = fmaf(t[2], s1, s[nt][2]);
+        s[nt][3] = fmaf(t[3], s1, s[nt][3]);
+      }
+    }
+  }
+}
+
+// O^T += V^T P^T of one group: p[h] has tokens 8h + 2tq + {0, 1} of column g; `factors`: the group's
+// pairs of tokens' block factors, FP16.
+template <int D, int NT>
+__device__ __forceinline__ void values(const uint8_t* buf, const uint8_t* factors,
+                                       const uint32_t (&p)[2][NT], int lane,
+                                       float (&o)[KvGroup<D>::kBlocks][2][NT][4]) {
+  using G = KvGroup<D>;
+  constexpr int CB = G::kBlocks, SB = G::kSlabBlocks, NS = G::kSlabs;
+  const int g = lane >> 2, tq = lane & 3;
+#pragma unroll
+  for (int sl = 0; sl < NS; ++sl) {
+    const uint8_t* vb = buf + G::kCodeBytes + sl * G::kSlabBytes + g * 16 * SB + tq * 4 * SB;
+    const Words<SB> v0 = lds<SB>(vb), v1 = lds<SB>(vb + 128 * SB);
+    const Words<SB> f0 = lds<SB>(factors + (tq * CB + sl * SB) * 4);
+    const Words<SB> f1 = lds<SB>(factors + ((4 + tq) * CB + sl * SB) * 4);
+#pragma unroll
+    for (int cp = 0; cp < SB / 2; ++cp) {  // blocks 2cp, 2cp + 1
+      // codes of two tokens side by side: channels n = 0, 2 (x) and 1, 3 (y)
+      const uint32_t l0 = v0.v[cp], h0 = v0.v[SB / 2 + cp];
+      const uint32_t l1 = v1.v[cp], h1 = v1.v[SB / 2 + cp];
+      const uint32_t x0 = (l0 & 0x0F0F0F0Fu) | ((h0 << 4) & 0xF0F0F0F0u);
+      const uint32_t y0 = ((l0 >> 4) & 0x0F0F0F0Fu) | (h0 & 0xF0F0F0F0u);
+      const uint32_t x1 = (l1 & 0x0F0F0F0Fu) | ((h1 << 4) & 0xF0F0F0F0u);
+      const uint32_t y1 = ((l1 >> 4) & 0x0F0F0F0Fu) | (h1 & 0xF0F0F0F0u);
+      uint32_t a0[4], a1[4], a2[4], a3[4];
+      e2m1x8(x0, a0[0], a0[1], a0[2], a0[3]);
+      e2m1x8(y0, a1[0], a1[1], a1[2], a1[3]);
+      e2m1x8(x1, a2[0], a2[1], a2[2], a2[3]);
+      e2m1x8(y1, a3[0], a3[1], a3[2], a3[3]);
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        const int cb = sl * SB + 2 * cp + cc;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t b0 = mul_half2(p[0][nt], f0.v[2 * cp + cc]);
+          const uint32_t b1 = mul_half2(p[1][nt], f1.v[2 * cp + cc]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            mma_f16_acc(o[cb][j][nt], a0[2 * cc + j], a1[2 * cc + j], a2[2 * cc + j],
+                        a3[2 * cc + j], b0, b1);
+        }
+      }
+    }
+  }
+}
+
+// The same, product by product in FP32, for scales that one FP16 exponent range does not hold, or
+// NaN.  `key0`: the group's first key, `end`: the first that no row sees.
+template <int D, int NT>
+__device__ __forceinline__ void values_singly(const uint8_t* buf, const uint32_t (&p)[2][NT],
+                                              const uint32_t (&ref)[(KvGroup<D>::kBlocks + 3) / 4],
+                                              int key0, int end, const int* lo, const int* hi, int lane,
+                                              float (&o)[KvGroup<D>::kBlocks][2][NT][4]) {
+  using G = KvGroup<D>;
+  constexpr int CB = G::kBlocks;
+  const int g = lane >> 2, tq = lane & 3;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    for (int t = 0; t < 8; ++t) {
+      const int key = key0 + 8 * h + t;
+      if (key >= end) break;
+      float pr[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t w = __shfl_sync(kAll, p[h][nt], (2 * tq + e) * 4 + (t >> 1));
+          const __half2 both = *reinterpret_cast<const __half2*>(&w);
+          const int row = 8 * nt + 2 * tq + e;
+          const bool seen = key >= lo[row] && key <= hi[row];
+          // what is not seen adds nothing, not even 0 * NaN
+          pr[nt][e] = !seen ? -1.f : (t & 1 ? __high2float(both) : __low2float(both));
+        }
+#pragma unroll
+      for (int c = 0; c < CB; ++c) {
+        const uint32_t sv = buf[G::kVScale + (8 * h + t) * CB + c];
+        const int rc = (int)((ref[c / 4] >> (8 * (c % 4))) & 0xFFu);
+        const float unit =
+            sv == 255u ? __uint_as_float(0x7FC00000u) : exp2f((float)((int)sv - rc + 1));
+        uint32_t v[4];
+        e2m1x8(*reinterpret_cast<const uint16_t*>(buf + G::v_half(8 * h + t, c, g)), v[0], v[1], v[2],
+               v[3]);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v[j]));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (pr[nt][e] >= 0.f || pr[nt][e] != pr[nt][e]) {
+                o[c][j][nt][e] += pr[nt][e] * (x.x * unit);
+                o[c][j][nt][2 + e] += pr[nt][e] * (x.y * unit);
+              }
+        }
+      }
+    }
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPerSm)
     kv_attention(const KvAttentionArgs a) {
   using G = KvGroup<D>;
   using L = Shape<D, NT>;
-  constexpr int CB = G::kBlocks, SB = G::kSlabBlocks, NS = G::kSlabs, NW = (CB + 3) / 4;
+  constexpr int CB = G::kBlocks, NW = (CB + 3) / 4;
   constexpr int kRows = L::kRows, kStages = L::kStages, kWarps = L::kWarps, kThreads = L::kThreads;
   constexpr bool kQInRegs = !L::kShared;
+  constexpr int kU = L::kTogether;
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, tq = lane & 3;
@@ -797,236 +942,125 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
       put_v_scales();
       bool slow = false;
 
-      // (unrolled for the instructions that one group's dependences leave room for: 64.1 -> 60.4 us)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int j0 = step_at + 16 * u;
-        if (u == 1 && j0 >= span.end) break;  // was not copied
-        const uint8_t* buf = ring + stage * L::kStageBytes + u * G::kBytes;
+      for (int u0 = 0; u0 < 2; u0 += kU) {
+        const int j0 = step_at + 16 * u0;
+        if (u0 > 0 && j0 >= span.end) break;  // was not copied
+        const uint8_t* buf = ring + stage * L::kStageBytes + u0 * G::kBytes;
 
-      // ---- S^T = K Q^T
-      float s[NT][4];
+        // ---- S^T = K Q^T
+        float s[kU][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-      Words<SB> kf[2][NS];  // the scales of keys 8h + g
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int sl = 0; sl < NS; ++sl)
-          kf[h][sl] = lds<SB>(k_scales + ((16 * u + 8 * h + g) * CB + sl * SB) * 4);
-#pragma unroll
-      for (int sl = 0; sl < NS; ++sl) {
-        Words<SB> kw[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          kw[h] = lds<SB>(buf + sl * G::kSlabBytes + (8 * h + g) * 16 * SB + tq * 4 * SB);
-#pragma unroll
-        for (int c = 0; c < SB; ++c) {
-          const int cb = sl * SB + c;
-          uint4 q[NT];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            q[nt] = kQInRegs ? qf[kQInRegs ? cb : 0]
-                             : *reinterpret_cast<const uint4*>(
-                                   q_sh + ((nt * CB + cb) * 32 + lane) * 16);
-          uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
-          e2m1x8(kw[0].v[c], a0, a2, b0, b2);
-          e2m1x8(kw[1].v[c], a1, a3, b1, b3);
-          const float s0 = __uint_as_float(kf[0][sl].v[c]), s1 = __uint_as_float(kf[1][sl].v[c]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float t[4];
-            mma_f16_zero(t, a0, a1, a2, a3, q[nt].x, q[nt].y);
-            mma_f16_acc(t, b0, b1, b2, b3, q[nt].z, q[nt].w);
-            s[nt][0] = fmaf(t[0], s0, s[nt][0]);
-            s[nt][1] = fmaf(t[1], s0, s[nt][1]);
-            s[nt][2] = fmaf(t[2], s1, s[nt][2]);
-            s[nt][3] = fmaf(t[3], s1, s[nt][3]);
-          }
-        }
-      }
+        for (int u = 0; u < kU; ++u)
+          scores<D, NT>(buf + u * G::kBytes, k_scales + (u0 + u) * 16 * CB * 4, qf, q_sh, lane, s[u]);
 
-      // ---- does anything change: a larger logit, a V scale out of range?
-      const bool whole = j0 >= seen_lo && j0 + 15 <= seen_hi;
-      float top[NT][2];
-      bool grow = odd;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float t = -INFINITY;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float& x = s[nt][2 * h + e];
-            if (!whole) {
-              const int row = 8 * nt + 2 * tq + e, key = j0 + 8 * h + g;
-              if (key < lo_sh[row] || key > hi_sh[row]) x = -INFINITY;
-            }
-            t = fmaxf(t, x);
-          }
-          top[nt][e] = t * factor[nt][e];
-          grow |= top[nt][e] > m[nt][e] + kSlack;
-        }
-      if (__any_sync(kAll, grow)) {
-        if (__any_sync(kAll, !landed)) {
-          dead = true;
-          if (lane == 0) atomicOr(cache.flag, WD_KV_FLAG_TIMEOUT);
-          break;
-        }
-        // the maxima, and what stands on them
+        // ---- does anything change: a larger logit, a V scale out of range?
+        const bool whole = j0 >= seen_lo && j0 + 16 * kU - 1 <= seen_hi;
+        float top[NT][2];
+        bool grow = odd;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float t = fmaxf(m[nt][e], top[nt][e]);
-            t = fmaxf(t, __shfl_xor_sync(kAll, t, 4));
-            t = fmaxf(t, __shfl_xor_sync(kAll, t, 8));
-            t = fmaxf(t, __shfl_xor_sync(kAll, t, 16));
-            if (t <= m[nt][e] + kSlack) t = m[nt][e];
-            // both -inf: nothing stands yet
-            const float keep = m[nt][e] == -INFINITY ? 0.f : exp2_fast(m[nt][e] - t);
-            // (a NaN that stands there stays: a sum of NaN is not forgotten)
-            l[nt][e] = m[nt][e] == -INFINITY ? l[nt][e] : l[nt][e] * keep;
-            m[nt][e] = t;
+            float t = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < CB; ++c)
+            for (int u = 0; u < kU; ++u)
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                o[c][j][nt][e] *= keep;
-                o[c][j][nt][2 + e] *= keep;
-              }
-          }
-        // the largest V scales, and what stands on them
-        if (__any_sync(kAll, odd)) {
-          bool bad = false;
-#pragma unroll
-          for (int c = 0; c < CB; ++c) {
-            const uint32_t sh = 8 * (c % 4), mine_c = (vt.v[c / 4] >> sh) & 0xFFu;
-            const uint32_t old = (ref[c / 4] >> sh) & 0xFFu;
-            const uint32_t most =
-                max(old, __reduce_max_sync(kAll, inside && mine_c != 255u ? mine_c : 0u));
-            if (most != old) {
-              const float down = exp2_fast((float)(int)old - (float)(int)most);
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) o[c][j][nt][e] *= down;
-              ref[c / 4] = (ref[c / 4] & ~(0xFFu << sh)) | (most << sh);
-            }
-            bad |= inside && (mine_c > most || mine_c + 15u < most);
-          }
-          slow = __any_sync(kAll, bad);
-          __syncwarp();
-          put_v_scales();
-          odd = false;
-        }
-      }
-
-      // ---- P = 2^kBias exp2(x - m)
-      uint32_t p[2][NT];  // P^T fragments: tokens 8h + 2tq + {0, 1} of column g
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float z0 = m[nt][0] == -INFINITY ? 0.f : kBias - m[nt][0];
-        const float z1 = m[nt][1] == -INFINITY ? 0.f : kBias - m[nt][1];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float p0 = exp2_fast(fmaf(s[nt][2 * h], factor[nt][0], z0));
-          const float p1 = exp2_fast(fmaf(s[nt][2 * h + 1], factor[nt][1], z1));
-          l[nt][0] += p0;
-          l[nt][1] += p1;
-          p[h][nt] = transpose8(pack_half2(p0, p1));
-        }
-      }
-
-      // ---- O^T += V^T P^T
-      if (!slow) {
-        Words<SB> vf[2][NS];  // the factors of keys 8h + 2tq + {0, 1}
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int sl = 0; sl < NS; ++sl)
-            vf[h][sl] = lds<SB>(v_scales + ((8 * u + 4 * h + tq) * CB + sl * SB) * 4);
-#pragma unroll
-        for (int sl = 0; sl < NS; ++sl) {
-          const uint8_t* vb = buf + G::kCodeBytes + sl * G::kSlabBytes +
-                              g * 16 * SB + tq * 4 * SB;
-          const Words<SB> v0 = lds<SB>(vb), v1 = lds<SB>(vb + 128 * SB);
-#pragma unroll
-          for (int cp = 0; cp < SB / 2; ++cp) {  // blocks 2cp, 2cp + 1
-            // codes of two tokens side by side: channels n = 0, 2 (x) and 1, 3 (y)
-            const uint32_t e0 = v0.v[cp], f0 = v0.v[SB / 2 + cp];
-            const uint32_t e1 = v1.v[cp], f1 = v1.v[SB / 2 + cp];
-            const uint32_t x0 = (e0 & 0x0F0F0F0Fu) | ((f0 << 4) & 0xF0F0F0F0u);
-            const uint32_t y0 = ((e0 >> 4) & 0x0F0F0F0Fu) | (f0 & 0xF0F0F0F0u);
-            const uint32_t x1 = (e1 & 0x0F0F0F0Fu) | ((f1 << 4) & 0xF0F0F0F0u);
-            const uint32_t y1 = ((e1 >> 4) & 0x0F0F0F0Fu) | (f1 & 0xF0F0F0F0u);
-            uint32_t a0[4], a1[4], a2[4], a3[4];
-            e2m1x8(x0, a0[0], a0[1], a0[2], a0[3]);
-            e2m1x8(y0, a1[0], a1[1], a1[2], a1[3]);
-            e2m1x8(x1, a2[0], a2[1], a2[2], a2[3]);
-            e2m1x8(y1, a3[0], a3[1], a3[2], a3[3]);
-#pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-              const int cb = sl * SB + 2 * cp + cc;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const uint32_t b0 = mul_half2(p[0][nt], vf[0][sl].v[2 * cp + cc]);
-                const uint32_t b1 = mul_half2(p[1][nt], vf[1][sl].v[2 * cp + cc]);
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                  mma_f16_acc(o[cb][j][nt], a0[2 * cc + j], a1[2 * cc + j], a2[2 * cc + j],
-                              a3[2 * cc + j], b0, b1);
-              }
-            }
-          }
-        }
-      } else {
-        // scales that one FP16 exponent range does not hold, or NaN: product by product
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            for (int t = 0; t < 8; ++t) {
-              const int key = j0 + 8 * h + t;
-              if (key >= span.end) break;
-              float pr[NT][2];
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const uint32_t w = __shfl_sync(kAll, p[h][nt], (2 * tq + e) * 4 + (t >> 1));
-                  const __half2 both = *reinterpret_cast<const __half2*>(&w);
-                  const int row = 8 * nt + 2 * tq + e;
-                  const bool seen = key >= lo_sh[row] && key <= hi_sh[row];
-                  // what is not seen adds nothing, not even 0 * NaN
-                  pr[nt][e] = !seen ? -1.f : (t & 1 ? __high2float(both) : __low2float(both));
+              for (int h = 0; h < 2; ++h) {
+                float& x = s[u][nt][2 * h + e];
+                if (!whole) {
+                  const int row = 8 * nt + 2 * tq + e, key = j0 + 16 * u + 8 * h + g;
+                  if (key < lo_sh[row] || key > hi_sh[row]) x = -INFINITY;
                 }
+                t = fmaxf(t, x);
+              }
+            top[nt][e] = t * factor[nt][e];
+            grow |= top[nt][e] > m[nt][e] + kSlack;
+          }
+        if (__any_sync(kAll, grow)) {
+          if (__any_sync(kAll, !landed)) {
+            dead = true;
+            if (lane == 0) atomicOr(cache.flag, WD_KV_FLAG_TIMEOUT);
+            break;
+          }
+          // the maxima, and what stands on them
 #pragma unroll
-              for (int c = 0; c < CB; ++c) {
-                const uint32_t sv = buf[G::kVScale + (8 * h + t) * CB + c];
-                const int rc = (int)((ref[c / 4] >> (8 * (c % 4))) & 0xFFu);
-                const float unit = sv == 255u ? __uint_as_float(0x7FC00000u)
-                                              : exp2f((float)((int)sv - rc + 1));
-                uint32_t v[4];
-                e2m1x8(*reinterpret_cast<const uint16_t*>(buf + G::v_half(8 * h + t, c, g)), v[0],
-                       v[1], v[2], v[3]);
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float t = fmaxf(m[nt][e], top[nt][e]);
+              t = fmaxf(t, __shfl_xor_sync(kAll, t, 4));
+              t = fmaxf(t, __shfl_xor_sync(kAll, t, 8));
+              t = fmaxf(t, __shfl_xor_sync(kAll, t, 16));
+              if (t <= m[nt][e] + kSlack) t = m[nt][e];
+              // both -inf: nothing stands yet
+              const float keep = m[nt][e] == -INFINITY ? 0.f : exp2_fast(m[nt][e] - t);
+              // (a NaN that stands there stays: a sum of NaN is not forgotten)
+              l[nt][e] = m[nt][e] == -INFINITY ? l[nt][e] : l[nt][e] * keep;
+              m[nt][e] = t;
+#pragma unroll
+              for (int c = 0; c < CB; ++c)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v[j]));
+                  o[c][j][nt][e] *= keep;
+                  o[c][j][nt][2 + e] *= keep;
+                }
+            }
+          // the largest V scales, and what stands on them
+          if (__any_sync(kAll, odd)) {
+            bool bad = false;
+#pragma unroll
+            for (int c = 0; c < CB; ++c) {
+              const uint32_t sh = 8 * (c % 4), mine_c = (vt.v[c / 4] >> sh) & 0xFFu;
+              const uint32_t old = (ref[c / 4] >> sh) & 0xFFu;
+              const uint32_t most =
+                  max(old, __reduce_max_sync(kAll, inside && mine_c != 255u ? mine_c : 0u));
+              if (most != old) {
+                const float down = exp2_fast((float)(int)old - (float)(int)most);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
                   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                      if (pr[nt][e] >= 0.f || pr[nt][e] != pr[nt][e]) {
-                        o[c][j][nt][e] += pr[nt][e] * (x.x * unit);
-                        o[c][j][nt][2 + e] += pr[nt][e] * (x.y * unit);
-                      }
-                }
+                    for (int e = 0; e < 4; ++e) o[c][j][nt][e] *= down;
+                ref[c / 4] = (ref[c / 4] & ~(0xFFu << sh)) | (most << sh);
               }
+              bad |= inside && (mine_c > most || mine_c + 15u < most);
             }
-      }
+            slow = __any_sync(kAll, bad);
+            __syncwarp();
+            put_v_scales();
+            odd = false;
+          }
+        }
+
+        // ---- P = 2^kBias exp2(x - m)
+        uint32_t p[kU][2][NT];  // P^T fragments: tokens 16u + 8h + 2tq + {0, 1} of column g
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float z0 = m[nt][0] == -INFINITY ? 0.f : kBias - m[nt][0];
+          const float z1 = m[nt][1] == -INFINITY ? 0.f : kBias - m[nt][1];
+#pragma unroll
+          for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float p0 = exp2_fast(fmaf(s[u][nt][2 * h], factor[nt][0], z0));
+              const float p1 = exp2_fast(fmaf(s[u][nt][2 * h + 1], factor[nt][1], z1));
+              l[nt][0] += p0;
+              l[nt][1] += p1;
+              p[u][h][nt] = transpose8(pack_half2(p0, p1));
+            }
+        }
+
+        // ---- O^T += V^T P^T
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          if (!slow)
+            values<D, NT>(buf + u * G::kBytes, v_scales + (u0 + u) * 8 * CB * 4, p[u], lane, o);
+          else
+            values_singly<D, NT>(buf + u * G::kBytes, p[u], ref, j0 + 16 * u, span.end, lo_sh, hi_sh,
+                                 lane, o);
+        }
       }
       if (dead) {
         // give up, but not before the copies in flight have landed (or as long again has passed)
