@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kPlan)
       begin[i] = before + excl;
       need[i] = pages;
     }
-    before += total;
+    before = min(before + total, 1 << 30);  // (a call may ask for more than an int counts)
   }
   if (threadIdx.x == 0) wanted_sh = before;
   __syncthreads();
