@@ -122,11 +122,12 @@ __device__ __forceinline__ uint8_t* kv_group(const KvView& v, int page, int laye
 // counts, staged table rows and per-slot owners.
 constexpr int kKvSms = 152;           // what the attention's grid is made for
 constexpr int kKvMaxUnits = 8 * kKvSms;  // units of 8 query rows that there is room for
+constexpr int kKvMaxRowUnits = 2 * kKvSms;  // of 256 query rows
 constexpr int kKvChunkPages = 4096;   // pages that one CTA counts in wd_kv_compact
 
 struct KvScratch {
   uint32_t* counters;  // [kKvMaxUnits], zero between calls
-  float* partial;      // [2 * kKvMaxUnits][8][head_dim + 2]
+  float* partial;      // [2 * kKvMaxUnits][8][head_dim + 2] or [kKvMaxRowUnits][256][head_dim + 2]
   int32_t* list_a;     // [num_pages]
   int32_t* list_b;     // [num_pages]
   int32_t* list_c;     // [num_pages]

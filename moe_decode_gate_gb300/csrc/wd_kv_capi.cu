@@ -68,7 +68,8 @@ KvScratch kv_scratch(const wd_kv_cache& c) {
   const size_t pages = c.num_pages, slots = c.slots;
   w.counters = reinterpret_cast<uint32_t*>(take(4 * (size_t)kKvMaxUnits));
   w.partial = reinterpret_cast<float*>(
-      take(4 * 2 * (size_t)kKvMaxUnits * 8 * ((size_t)c.head_dim + 2)));
+      take(4 * ((size_t)c.head_dim + 2) *
+           (c.head_dim <= 128 ? (size_t)kKvMaxRowUnits * 256 : 2 * (size_t)kKvMaxUnits * 8)));
   w.list_a = reinterpret_cast<int32_t*>(take(4 * pages));
   w.list_b = reinterpret_cast<int32_t*>(take(4 * pages));
   w.list_c = reinterpret_cast<int32_t*>(take(4 * pages));
