@@ -117,9 +117,10 @@ __device__ __forceinline__ uint8_t* kv_group(const KvView& v, int page, int laye
          ((pos & (v.page_size - 1)) >> 4) * group_bytes;
 }
 
-// Scratch inside a cache's workspace.  Attention: an arrival counter and two
-// partial results per unit (what a CTA does in one pass).  Pages: lists of page ids, chunk
-// counts, staged table rows and per-slot owners.
+// Scratch inside a cache's workspace.  Attention: arrival counters and partial results of the
+// units (what a CTA does in one pass) of items that several CTAs share: two to a unit of
+// 8 rows, one to a unit of 256.  Pages: lists of page ids, chunk counts, staged table rows and
+// per-slot owners.
 constexpr int kKvSms = 152;           // what the attention's grid is made for
 constexpr int kKvMaxUnits = 8 * kKvSms;  // units of 8 query rows that there is room for
 constexpr int kKvMaxRowUnits = 2 * kKvSms;  // of 256 query rows

@@ -8,8 +8,12 @@
 // different places, and a third shuffle pairs them with those of the neighbouring block to
 // one 32-bit word per lane.
 //
-// Bound by memory: 2 * 2 * head_dim bytes in and head_dim + head_dim / 16 out
+// To read and write: 2 * 2 * head_dim bytes in and head_dim + head_dim / 16 out
 // per token and head (BF16), the values back (if asked for) as much as the input.
+// Measured: 147 MB of prompts (BF16, head_dim 128, values back) 36.8 us, 4.0 TB/s, 0.59
+// of the copy rate: the pipe that compares, permutes and converts is 57 % busy and the
+// issue slots 64 %, the loads of a thread's few blocks do not hide the rest.  One token of
+// 32 sequences: 2.6 us.  Tried: loads ahead, other numbers of tokens to a CTA (37 to 41 us).
 #include "wd_device.cuh"
 #include "wd_kv.cuh"
 
