@@ -25,14 +25,14 @@
 // enough items for the GPU; the CTA that finishes last joins them in their order.
 //
 // Measured (bfloat16, head_dim 128, 8 query heads to a key head).  2432 tokens after 30,336, 4 key
-// heads: 1325 us, 949 TFLOP/s, 0.54 of the cuBLAS rate; the products alone would take 1300
+// heads: 1328 us, 947 TFLOP/s, 0.50 of the cuBLAS rate; the products alone would take 1300
 // cycles a tile of 64 keys, the softmax takes 2400 (64 exponentials a thread at a quarter of the
 // rate, and instructions that two warps to a scheduler do not hide).  Chunks of 200 to
-// 256 tokens in two sequences of 4100 to 6001, 4 key heads: 95 us, where wd_kv_attention.cu
-// takes 233; 19 tiles to a piece cost 45 us, the rest is the start (7 us), Q and the joins of pieces.
-// Tried: m16n8k16 products over ldmatrix fragments (354 us); one S to a half (2 % slower at
-// long lengths); the issuing thread without uniform registers (119 us); every tile's V
-// converted by two warps (130 us).
+// 256 tokens in two sequences of 4100 to 6001, 4 key heads: 83 us, where wd_kv_attention.cu
+// takes 233; the 48 tiles of a piece cost 60 us, the rest is the start (7 us), Q and the joins.
+// Tried: m16n8k16 products over ldmatrix fragments (354 us); two warps for V (130 us); products
+// issued without uniform registers (2432 tokens: 1651 us); 160 registers for the softmax warps and 88
+// for the others by setmaxnreg, which leaves no spills (2432 tokens: 1392 us).
 #include "wd_kv_attention.cuh"
 
 namespace wd {
@@ -257,8 +257,8 @@ struct Planned {
   int before, pieces;
 };
 
-// Not inlined: every role looks up its pieces, and code that is run once a piece is
-// fetched slowly.
+// Not inlined: every role looks up its pieces, and with as much more code the roles' loops are
+// fetched more slowly (57 items in 2 pieces: 83 us, inlined 89).
 __device__ __noinline__ Piece find_piece(const Planned* plan, int entries, int heads, int group,
                                          int window, unsigned q, int unit) {
   int lo = 0, hi = entries;
@@ -369,10 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
   }
   items *= (float)heads;
   // Into how many pieces is the longest item cut?  Each lane rates a number: passes of the CTAs over
-  // all pieces, each as long as its tiles and what a piece costs besides (about four tiles), and
+  // all pieces, each as long as its tiles and what a piece costs besides (about twelve tiles), and
   // the parts that an item's last CTA reads (about 2/3 of a tile each).  One piece needs no
-  // parts; else there is room for kKvMaxRowUnits.  16 entries of 16 tokens over 6000 keys, 64 items:
-  // 2 pieces 88 us, 4 pieces 97; 8 tiles of rows over 5000 keys, 57 items: 5 pieces 95 us.
+  // parts; else there is room for kKvMaxRowUnits.  Measured: 64 items of up to 126 tiles 86 us in 2
+  // pieces each, 97 in 4; 57 items of up to 94 tiles 83 us in 2 pieces, 95 in 5.
   unsigned q = longest;
   bool cut = false;
   if (items < 1.5f * (float)gridDim.x) {
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
 #pragma unroll 1
     for (int b = 0; b < a.batch.entries; ++b)
       units += plan[b].row_tiles * heads * (int)((plan[b].seen + tiles - 1) / tiles);
-    float cost = (float)((units + gridDim.x - 1) / gridDim.x) * (float)(tiles + 4) +
+    float cost = (float)((units + gridDim.x - 1) / gridDim.x) * (float)(tiles + 12) +
                  (pieces > 1 ? 0.7f * (float)pieces + 2.f : 0.f);
     if (pieces > 1 && (units > kKvMaxRowUnits || tiles < 2)) cost = INFINITY;
     const uint32_t best = __reduce_min_sync(kAll, __float_as_uint(cost));
