@@ -1052,7 +1052,12 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t s) {
   // have those in tiles of 256 rows): the other kernel.  16 entries, 4000 to 8000 keys, 4 key
   // heads, head_dim 128: 40 rows 91 us against 103 here, 64 rows 85 against 104, 128 rows 87 against 201;
   // head_dim 64: 62 against 70, 59 against 71, 60 against 136.  32 rows take 52 us here.
-  const bool many = rows > 32 && (long long)a.batch.tokens * group > 32ll * a.batch.entries;
+  // Up to 64 rows of few entries and heads stay, as their long sequences are cut finer here: 64 rows of one
+  // head over 131,072 keys 62 us against 121, 40 rows of 4 heads over 4000 23 against 28 (but 64
+  // rows over 100 keys 14 against 11); 32 heads of 100 to 200 keys 16 against 14, 128 heads 27 against 16.
+  const long long items = (long long)a.batch.entries * a.cache.kv_heads;
+  const bool many = rows > (items < 64 ? 64 : 32) &&
+                    (long long)a.batch.tokens * group > 32ll * a.batch.entries;
   if (many && kv_attention_rows_supported(a)) return launch_kv_attention_rows(a, s);
   switch (a.cache.head_dim) {
     case 64: return rows <= 8 ? run<64, 1>(a, s) : rows <= 16 ? run<64, 2>(a, s) : run<64, 4>(a, s);
