@@ -38,7 +38,9 @@ class KVCache:
     [slots, columns] (the pages of each slot's sequence, -1 beyond), ``lengths`` int32 [slots] and
     ``refs`` int32 [num_pages] are the cache, on the device; include/wd_kv.h has their layout.
     Every call is asynchronous on the current stream (or ``stream``); calls on different streams
-    must be ordered by the caller, as they share the workspace.
+    must be ordered by the caller, as they share the workspace.  A call on ``stream`` keeps the memory of what
+    it reads and writes until it is done; that the inputs are there when it starts, and that it is done
+    before its results are read elsewhere, is the caller's to see to, as with any two streams.
 
     A decode step::
 
@@ -114,6 +116,26 @@ class KVCache:
             return torch._C._cuda_getCurrentRawStream(self._index)
         return stream.cuda_stream
 
+    def _output(self, shape, dtype, stream):
+        """A result of a call on ``stream``: that stream's memory, so that nothing that still runs on
+        another one uses it, and not given away before the current stream too, on which the caller may
+        read it, has done what it was asked until then."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(torch.cuda.current_stream(self.device))
+        return t
+
+    def _keep(self, stream, *tensors):
+        """After a call on ``stream`` that uses these tensors, and the cache's own: their memory is not
+        given away before the call is done, even if the caller drops them at once."""
+        if stream is None:
+            return
+        for t in (*tensors, self.pool, self.table, self.lengths, self.refs, self.workspace):
+            if t is not None:
+                t.record_stream(stream)
+
     # Each call checks its tensors with as few attribute look-ups as it can (a call costs the host
     # about ten microseconds, half of it the launch) and says what is wrong in the slow path.
 
@@ -162,10 +184,11 @@ class KVCache:
         Returns ``ok`` int32 [n]: 0 where a request was refused (see include/wd_kv.h)."""
         n = counts.numel()
         if ok is None:
-            ok = torch.empty(n, dtype=torch.int32, device=self.device)
+            ok = self._output(n, torch.int32, stream)
         _check("wd_kv_reserve", self._lib.wd_kv_reserve(
             self._ref, self._ints("seqs", seqs, n), self._ints("counts", counts), n,
             self._ints("ok", ok, n), self._stream(stream)))
+        self._keep(stream, counts, seqs, ok)
         return ok
 
     def append(self, layer, k, v, seqs=None, q_start=None, return_values=False, stream=None):
@@ -190,16 +213,17 @@ class KVCache:
         tokens = shape[0]
         s, qs, n = self._entries(seqs, q_start, tokens)
         if return_values:
-            values = torch.empty((2, *shape), dtype=dtype, device=self.device)
+            values = self._output((2, *shape), dtype, stream)
             k_to = values.data_ptr()
             v_to = k_to + values.nbytes // 2
         else:
-            k_to = v_to = None
+            values = k_to = v_to = None
         st = self._lib.wd_kv_append(self._ref, layer, k.data_ptr(), v.data_ptr(), code, k_token,
                                     k_head, v_token, v_head, k_to, v_to, s, qs, n, tokens,
                                     self._stream(stream))
         if st:
             _check("wd_kv_append", st)
+        self._keep(stream, k, v, seqs, q_start, values)
         return values.unbind(0) if return_values else None
 
     def attention(self, layer, q, seqs=None, q_start=None, max_q=0, scale=None, window=0, out=None,
@@ -221,15 +245,15 @@ class KVCache:
             self._refuse("q", q, None, _Q_DTYPES)
         tokens, heads = shape[0], shape[1]
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=self.device)
+            out = self._output(shape, dtype, stream)
         elif out.shape != shape or out.dtype is not dtype or not out.is_contiguous() or \
                 out.device != self.device:
             raise ValueError("out must be contiguous, of q's shape and type")
         if return_lse:
-            lse = torch.empty((tokens, heads), dtype=torch.float32, device=self.device)
+            lse = self._output((tokens, heads), torch.float32, stream)
             lse_to = lse.data_ptr()
         else:
-            lse_to = None
+            lse = lse_to = None
         s, qs, n = self._entries(seqs, q_start, tokens)
         st = self._lib.wd_kv_attention(self._ref, layer, q.data_ptr(), code, q_token, q_head, heads,
                                        out.data_ptr(), lse_to, s, qs, n, tokens, max_q,
@@ -237,6 +261,7 @@ class KVCache:
                                        self._stream(stream))
         if st:
             _check("wd_kv_attention", st)
+        self._keep(stream, q, seqs, q_start, out, lse)
         return (out, lse) if return_lse else out
 
     def fork(self, src, dst, ok=None, stream=None):
@@ -244,21 +269,23 @@ class KVCache:
         src[i] = -1 frees it.  Returns ``ok`` int32 [n]: 0 where a request was refused."""
         n = dst.numel()
         if ok is None:
-            ok = torch.empty(n, dtype=torch.int32, device=self.device)
+            ok = self._output(n, torch.int32, stream)
         _check("wd_kv_fork", self._lib.wd_kv_fork(
             self._ref, self._ints("src", src, n), self._ints("dst", dst), n,
             self._ints("ok", ok, n), self._stream(stream)))
+        self._keep(stream, src, dst, ok)
         return ok
 
     def free(self, seqs, stream=None):
         """Release the sequences in these slots."""
         _check("wd_kv_free", self._lib.wd_kv_free(self._ref, self._ints("seqs", seqs),
                                                   seqs.numel(), self._stream(stream)))
+        self._keep(stream, seqs)
 
     def compact(self, table_out=None, refs_out=None, stream=None):
         """Move the live pages to the front of the pool.  The bookkeeping is rewritten in place, or
         into table_out and refs_out.  Returns int32 [num_pages]: where each page went, -1 if free."""
-        page_map = torch.empty(self.num_pages, dtype=torch.int32, device=self.device)
+        page_map = self._output(self.num_pages, torch.int32, stream)
         for name, t, like in (("table_out", table_out, self.table),
                               ("refs_out", refs_out, self.refs)):
             if t is not None and (t.shape != like.shape or t.dtype != torch.int32 or
@@ -268,6 +295,7 @@ class KVCache:
             self._ref, None if table_out is None else table_out.data_ptr(),
             None if refs_out is None else refs_out.data_ptr(), page_map.data_ptr(),
             self._stream(stream)))
+        self._keep(stream, table_out, refs_out, page_map)
         return page_map
 
     def read_error_flag(self, stream=None):
