@@ -100,7 +100,9 @@ WD_API wd_status wd_kv_workspace_init(const wd_kv_cache* cache, wd_stream_t stre
 
 /* Copy the error flag to `*flag` and clear it; SYNCHRONISES `stream`.  Returns
  * WD_ERR_PIPELINE_TIMEOUT, WD_ERR_OUT_OF_PAGES or WD_ERR_BAD_INDEX for the
- * first of these bits that is set, else WD_OK. */
+ * first of these bits that is set, else WD_OK.  A timeout makes the output of the call that ran into it
+ * invalid and leaves the calls behind it, and the cache, as they are; this call then also
+ * sets the workspace's counters to zero again. */
 WD_API wd_status wd_kv_read_error_flag(const wd_kv_cache* cache, wd_stream_t stream, int* flag);
 
 /* Make room for counts[i] >= 0 more tokens at the end of the sequence in slot

@@ -71,7 +71,7 @@ struct Rows {
                        kFree = kFull + kStages, kScore = kFree + kStages, kProb = kScore + 4,
                        kOut = kProb + 4, kQuery = kOut + 2, kJoinIn = kQuery + 2,
                        kJoinOut = kJoinIn + 1, kDrain = kJoinOut + 1, kBarriers = kDrain + 1;
-  static constexpr int kWords = kBars + 8 * kBarriers;  // int [4]: tensor memory, last
+  static constexpr int kWords = kBars + 8 * kBarriers;  // int [4]: tensor memory, last, next to arrive at
   static constexpr int kScan = (kWords + 31) / 16 * 16;  // int [16], float [16], int [16]
   static constexpr int kEntries = kScan + 192;           // Planned [entries]
   static constexpr int shared_bytes(int entries) { return kEntries + 32 * entries + 1024; }
@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
     mbar_init(bar(L::kJoinOut), 1);
     mbar_init(bar(L::kDrain), 1);
     mbar_init_fence();
+    words[2] = blockIdx.x;
   }
   if (warp == kIssueWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -959,7 +960,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
         }
       }
       __syncwarp();
-      if (p.part.pieces == 1) continue;
+      if (p.part.pieces == 1) {
+        if (threadIdx.x == 0) words[2] = unit + gridDim.x;
+        continue;
+      }
       mbar_arrive(bar(L::kJoinIn));
       if (warp == 0) {
         if (!wait(L::kJoinIn, joins & 1)) return;
@@ -972,6 +976,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
           const bool last = before == p.part.pieces - 1u;
           if (last) a.counters[p.part.slot0] = 0;
           words[1] = last;
+          words[2] = unit + gridDim.x;
           mbar_arrive(bar(L::kJoinOut));
         }
         __syncwarp();
@@ -1047,6 +1052,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
   }
   tmem_fence_before();
   __syncthreads();
+  // Where a wait ran out, the pieces that were not got to arrive all the same: an item's counter is zero
+  // again when its last piece has, and the calls behind this one find it so.
+  if (cut && threadIdx.x == 0) {
+#pragma unroll 1
+    for (int unit = words[2]; unit < total; unit += gridDim.x) {
+      const Piece p = find(unit);
+      if (p.part.pieces > 1 && atomicAdd(a.counters + p.part.slot0, 1u) == p.part.pieces - 1u)
+        a.counters[p.part.slot0] = 0;
+    }
+  }
   if (warp == kIssueWarp) {
     tmem_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),

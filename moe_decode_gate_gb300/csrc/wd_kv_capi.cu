@@ -136,6 +136,9 @@ wd_status wd_kv_read_error_flag(const wd_kv_cache* cache, wd_stream_t stream, in
   cudaError_t e = cudaMemcpyAsync(&v, cache->workspace, sizeof(v), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaMemsetAsync(cache->workspace, 0, sizeof(v), s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  // A call that gave up leaves its counters at zero; whatever the reason was, the next one starts from that.
+  if (e == cudaSuccess && (v & WD_KV_FLAG_TIMEOUT))
+    e = cudaMemsetAsync(kv_scratch(*cache).counters, 0, 4 * kKvMaxUnits, s);
   if (e != cudaSuccess) return cuda_status(e);
   *flag = (int)(v & (WD_KV_FLAG_BAD_INDEX | WD_KV_FLAG_TIMEOUT | WD_KV_FLAG_NO_PAGES));
   if (v & WD_KV_FLAG_TIMEOUT) return WD_ERR_PIPELINE_TIMEOUT;
