@@ -861,6 +861,27 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
         l[nt][e] += __shfl_xor_sync(kAll, l[nt][e], 8);
         l[nt][e] += __shfl_xor_sync(kAll, l[nt][e], 16);
       }
+    // A sum of values beyond 2^73, each up to 2^14 times, may be more than FP32 holds where their mean
+    // is not: then sums and outputs stand on a maximum 2^64 times as large.
+    bool far = false;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) far |= __vcmpgeu4(ref[w], 0xC8C8C8C8u) != 0u;
+    if (far) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          m[nt][e] += 64.f;
+          l[nt][e] *= 0x1p-64f;
+#pragma unroll
+          for (int c = 0; c < CB; ++c)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              o[c][j][nt][e] *= 0x1p-64f;
+              o[c][j][nt][2 + e] *= 0x1p-64f;
+            }
+        }
+    }
     const auto output = [&](int c, int nt, int e) {  // channels 32c + 4g + {0..3} of row 8nt + 2tq + e
       const float unit = exp2_int((int)((ref[c / 4] >> (8 * (c % 4))) & 0xFFu) - 128);
       return make_float4(o[c][0][nt][e] * unit, o[c][0][nt][2 + e] * unit, o[c][1][nt][e] * unit,

@@ -1,0 +1,100 @@
+"""Attention over the 4-bit cache at the edges of what its types hold, on the GPU, against the definition
+in 64 bits: scales far apart, values and logits near the ends of FP32, rows that see nothing, keys
+that are there and not seen, pages that do not exist.
+
+Tolerances as in test_gpu_kv.py, but from what each row sees: |error| <= u_out |want| + (2^-11 + 2^-15)
+sum_j p_j |v_j| + 2^-20 max_j |v_j| over the keys j that the row sees.  lse: 1e-5 + 2^-20 max_j scale
+sum_c |q_c| |k_jc| over these keys, which FP32 sums of the products stay within.
+"""
+import numpy as np
+import pytest
+import torch
+
+import kv_reference as ref
+import moe_decode_gate_gb300 as wd
+from test_gpu_kv import ROUNDOFF, Case, device, quantised_pool
+
+pytestmark = pytest.mark.gpu
+
+# few new tokens, and so many that they take the kernel for chunks (8 query heads to a key head)
+FEW, MANY = [1, 3], [40, 64]
+
+
+def definition(c, window=0, scale=None, gone=()):
+    """out, lse, and per row sum p |v|, max |v| and max_j sum |q||k| over what it sees; tokens of the pages
+    `gone` are seen by nobody."""
+    scale = 1 / np.sqrt(c.D) if scale is None else scale
+    T, hq, D = c.q_values.shape
+    hkv = c.pool.shape[2]
+    out, lse = np.zeros((T, hq, D)), np.full((T, hq), -np.inf)
+    mag, top, reach = np.zeros((T, hq, D)), np.zeros((T, hq, 1)), np.zeros((T, hq))
+    for b, s in enumerate(c.slots):
+        L, first, n = int(c.lengths[s]), c.q_start[b], c.q_start[b + 1] - c.q_start[b]
+        row = c.table[s][:-(-L // c.P)]
+        there = np.repeat([p not in gone for p in row], c.P)[:L]
+        for h in range(hkv):
+            if not L:
+                continue
+            k, v = ref.sequence(c.pool, np.where([p in gone for p in row], 0, row), L, c.layer, h, D,
+                                c.P)
+            for i in range(n):
+                p = L - n + i
+                lo = max(0, p - window + 1) if window else 0
+                at = np.flatnonzero(there[:p + 1][lo:]) + lo if p >= 0 else []
+                if not len(at):
+                    continue
+                for qh in range(h * hq // hkv, (h + 1) * hq // hkv):
+                    q = c.q_values[first + i, qh]
+                    x = scale * (k[at] @ q)
+                    e = np.exp(x - x.max())
+                    out[first + i, qh] = e @ v[at] / e.sum()
+                    mag[first + i, qh] = e @ np.abs(v[at]) / e.sum()
+                    lse[first + i, qh] = x.max() + np.log(e.sum())
+                    top[first + i, qh] = np.abs(v[at]).max()
+                    reach[first + i, qh] = scale * (np.abs(k[at]) @ np.abs(q)).max()
+    return out, lse, mag, top, reach
+
+
+def check(c, got, window=0, flag=0, gone=()):
+    out, lse = (x.double().cpu().numpy() for x in got)
+    want, want_lse, mag, top, reach = definition(c, window, gone=gone)
+    tol = ROUNDOFF[c.dtype] * np.abs(want) + (2.0 ** -11 + 2.0 ** -15) * mag + 2.0 ** -20 * top
+    assert (np.abs(out - want) <= tol).all(), np.argwhere(~(np.abs(out - want) <= tol))[:4]
+    nothing = np.isneginf(want_lse)
+    assert np.array_equal(np.isneginf(lse), nothing)
+    assert (np.abs(lse - want_lse) <= 1e-5 + 2.0 ** -20 * reach)[~nothing].all()
+    assert c.cache.read_error_flag() == flag
+
+
+def shift_scales(side, by):
+    """A pool whose keys' (or values') blocks are 2^by times as large."""
+    def make(r, pages, layers, hkv, P, D):
+        pool = quantised_pool(r, pages, layers, hkv, P, D)
+        at = 16 * D + (D // 2 if side == "v" else 0)
+        s = pool[..., at:at + D // 2].astype(int)
+        pool[..., at:at + D // 2] = np.clip(s + by, 0, 254)
+        return pool
+    return make
+
+
+def set_scales(c, side, b, positions, byte, blocks=slice(None)):
+    """The scale byte of these tokens of entry b, of all heads, on the host and the GPU."""
+    n = c.D // 32
+    at = 16 * c.D + (16 * n if side == "v" else 0)
+    for pos in positions:
+        page = c.table[c.slots[b], pos // c.P]
+        g = c.pool[page, :, :, pos % c.P // 16]
+        g[..., at + (pos % 16) * n:at + (pos % 16 + 1) * n][..., blocks] = byte
+    c.cache.pool.copy_(device(c.pool, c.dev))
+
+
+# ------------------------------------------------------------ large values ---
+
+@pytest.mark.parametrize("D,lens,news", [
+    (64, [1, 40, 300, 3000], [1, 1, 1, 1]), (128, [1, 40, 300, 20000], [1, 1, 1, 1]),
+    (256, [50, 4000], [1, 1]), (128, [300, 2000], [3, 2]), (64, [300, 5000], MANY),
+    (128, [300, 5000], MANY)])
+def test_values_near_the_largest(cuda_device, D, lens, news):
+    # values of up to 6 x 2^119: a mean of them is finite, the sum of a few hundred, weighted, is not
+    c = Case(cuda_device, lens, news, 8, 1, D, 32, seed=D, pool=shift_scales("v", 118))
+    check(c, c.run())
