@@ -25,7 +25,9 @@
 //     down to 2^-22 of 2^m (2^-16 of the largest at worst) and an error of 2^-33 of 2^m below.
 //   - V: the scales lie along the channels that are the product's rows, so each of P's
 //     columns is multiplied by 2^(s - r + 1) for every block, with r the largest scale that the warp
-//     has met for that block of channels: exact while s >= r - 15. A step that holds other
+//     has met for that block of channels (keys that some rows do not see raise it to 2^23 at most, and
+//     what no row sees does not): 2^(s - r + 1) is a normal FP16 number while s >= r - 15, and a product that
+//     is not one, of P below 1 (2^-8 of the reference), is off by 2^-25 at most.  A step that holds other
 //     scales (or NaN) adds its products one by one in FP32 instead.
 //
 // What bounds it.  A key head's 32 keys cost 4352 bytes and, in each warp, about 620 instructions,
@@ -659,7 +661,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
       const int step_at = (span.first + from + i) * kStep;
 
       // ---- the scales of key step_at + lane, for the lanes whose products want them
-      const bool inside = step_at + lane < span.end;
+      bool inside = step_at + lane < span.end;
       const uint8_t* scale_at = ring + stage * L::kStageBytes + (lane >> 4) * G::kBytes + (lane & 15) * CB;
       const Words<NW> kt = lds_scales<CB>(scale_at + G::kKScale);
       Words<NW> vt = lds_scales<CB>(scale_at + G::kVScale);
@@ -679,7 +681,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
         }
       }
       // 2^(s - ref + 1) of V: the exponent field is s - ref + 16, here first four times that in
-      // the byte it belongs in.  Keys behind the end take the reference itself; their
+      // the byte it belongs in.  Keys that no row sees take the reference itself; their
       // probabilities are zero.
       const auto put_v_scales = [&]() {
 #pragma unroll
@@ -778,12 +780,17 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
           // the largest V scales, and what stands on them
           if (__any_sync(kAll, odd)) {
             bool bad = false;
+            // what lies before the window of all rows (the first row's) takes part in nothing, and a key
+            // that not every row sees must not push what the others see out of FP32
+            const int key = step_at + lane;
+            inside = inside && key >= lo_sh[0];
+            const uint32_t limit = !inside ? 0u : key >= seen_lo && key <= seen_hi ? 254u : kSharedMost;
 #pragma unroll
             for (int c = 0; c < CB; ++c) {
               const uint32_t sh = 8 * (c % 4), mine_c = (vt.v[c / 4] >> sh) & 0xFFu;
               const uint32_t old = (ref[c / 4] >> sh) & 0xFFu;
               const uint32_t most =
-                  max(old, __reduce_max_sync(kAll, inside && mine_c != 255u ? mine_c : 0u));
+                  max(old, __reduce_max_sync(kAll, mine_c != 255u ? min(mine_c, limit) : 0u));
               if (most != old) {
                 const float down = exp2_fast((float)(int)old - (float)(int)most);
 #pragma unroll
@@ -861,16 +868,29 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
         l[nt][e] += __shfl_xor_sync(kAll, l[nt][e], 8);
         l[nt][e] += __shfl_xor_sync(kAll, l[nt][e], 16);
       }
-    // A sum of values beyond 2^73, each up to 2^14 times, may be more than FP32 holds where their mean
-    // is not: then sums and outputs stand on a maximum 2^64 times as large.
-    bool far = false;
+    const auto unit_of = [&](int c) {
+      return exp2_int((int)((ref[c / 4] >> (8 * (c % 4))) & 0xFFu) - 128);
+    };
+    // Values beyond 2^23 (which raise the reference that far, whoever sees them) may be so large that their sum,
+    // each up to 2^14 times, is more than FP32 holds where their mean is not: a row's sums and
+    // outputs then stand on a maximum 2^64 times as large.
+    bool large = false;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) far |= __vcmpgeu4(ref[w], 0xC8C8C8C8u) != 0u;
-    if (far) {
+    for (int w = 0; w < NW; ++w) large |= __vcmpgeu4(ref[w], 0x01010101u * kSharedMost) != 0u;
+    if (large) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          float most = 0.f;
+#pragma unroll
+          for (int c = 0; c < CB; ++c)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              most = fmaxf(most, fmaxf(fabsf(o[c][j][nt][e]), fabsf(o[c][j][nt][2 + e])) * unit_of(c));
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) most = fmaxf(most, __shfl_xor_sync(kAll, most, off));
+          if (!(most > 0x1p100f)) continue;
           m[nt][e] += 64.f;
           l[nt][e] *= 0x1p-64f;
 #pragma unroll
@@ -883,7 +903,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
         }
     }
     const auto output = [&](int c, int nt, int e) {  // channels 32c + 4g + {0..3} of row 8nt + 2tq + e
-      const float unit = exp2_int((int)((ref[c / 4] >> (8 * (c % 4))) & 0xFFu) - 128);
+      const float unit = unit_of(c);
       return make_float4(o[c][0][nt][e] * unit, o[c][0][nt][2 + e] * unit, o[c][1][nt][e] * unit,
                          o[c][1][nt][2 + e] * unit);
     };

@@ -13,6 +13,9 @@ constexpr int kCached = 256;   // entries whose slot and length are kept in shar
 constexpr float kBias = 8.f;   // P = 2^kBias at the reference m ...
 constexpr float kSlack = 6.f;  // ... which may fall this far behind the maximum (log2)
 constexpr uint32_t kAll = 0xFFFFFFFFu;
+// How far the values of a key that some rows of a tile do not see may raise V's reference: what those rows see
+// stays within FP32 beside it (2^-134 of it at worst), and so does what lies above (up to 2^104, added one by one).
+constexpr uint32_t kSharedMost = 150;
 
 // A piece of an item, and where the item's output goes.
 struct Part {

@@ -19,7 +19,8 @@
 //     where that block counts), and 2^(r - 127) multiplies the logit in FP32.
 //   - V: blocks are scaled by 2^(s - R), exactly down to 2^-22, with R at least the largest scale
 //     met for the block of channels (16 times it where it was set, so that it is seldom
-//     set again).  What is smaller, or NaN, is 0 in the tile, and added to O in FP32 one by one.
+//     set again; keys that some of the rows do not see raise it to 2^23 at most).  What is smaller or
+//     larger, or NaN, is 0 in the tile, and added to O in FP32 one by one.
 //   - Queries, P and the lazy maximum as in wd_kv_attention.cu.
 // An item (entry, tile of rows, key head) is cut into pieces along the keys where there are not
 // enough items for the GPU; the CTA that finishes last joins them in their order.
@@ -219,6 +220,9 @@ __device__ __forceinline__ uint32_t half_power(int d) {
   return d < 15 ? (uint32_t)(15 - d) << 10 : d < 25 ? 1u << (24 - d) : 0u;
 }
 
+// Whether V that is 2^-d of the reference is in the tile: else it is added on its own.
+__device__ __forceinline__ bool in_tile(int d) { return (unsigned)d <= 22u; }
+
 // Two FP32 values in one register pair: one instruction for both.
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
   uint64_t r;
@@ -247,6 +251,8 @@ __device__ __forceinline__ int byte_of(uint32_t w, int c) { return (int)(w >> (8
 struct Piece {
   Part part;
   int slot, len, key0, tiles, end, rows;
+  int lo;                  // no row sees keys before it,
+  int shared_lo, shared;   // and every row sees those from shared_lo up to `shared`
 };
 
 // An entry and its share of the work: each of its tiles of rows, for each key head, is cut into pieces;
@@ -286,6 +292,10 @@ __device__ __noinline__ Piece find_piece(const Planned* plan, int entries, int h
                     (long long)(span.end + kKeys - 1) / kKeys * kKeys);
   p.tiles = max(0, min((int)q, (span.end - p.key0 + kKeys - 1) / kKeys));
   p.rows = min(kRows, e.entry.n * group - p.part.tile * kRows);
+  const int pos0 = p.len - p.part.n + (p.part.n > 1 ? p.part.tile * kRows / group : 0);  // first row's
+  p.lo = window > 0 ? max(0, pos0 - window + 1) : 0;
+  p.shared_lo = window > 0 ? max(0, p.end - window) : 0;
+  p.shared = pos0 + 1;
   return p;
 }
 
@@ -481,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
         if (!wait(L::kRawFull + r, (count / kRaws) & 1)) return;
         const uint8_t* raw = smem + L::kRaw + r * L::kRawBytes;
         const int left = p.end - (p.key0 + i * kKeys);  // keys of the tile
+        const int before = p.lo - (p.key0 + i * kKeys);   // of which no row sees these
         // the scales of all keys, 32h + lane, of which every warp makes the same
         uint32_t sc[2];
 #pragma unroll
@@ -548,13 +559,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
             *reinterpret_cast<float*>(smem + L::kInfo + 16 * st + 8) =
                 alike ? exp2f((float)(high - 127)) : 0.f;
         } else {
+          // A key that not every row sees must not push what the others see out of FP32: it raises the
+          // reference to kSharedMost at most.
           bool above = false, other = false;
+          int most[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int t = 32 * h + lane, key = p.key0 + i * kKeys + t;
+            most[h] = t < before || t >= left ? -1
+                      : key >= p.shared_lo && key < p.shared ? 254 : (int)kSharedMost - kRoom;
+          }
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int c = 0; c < CB; ++c) {
               const int s = byte_of(sc[h], c);
-              above |= 32 * h + lane < left && s != 255 && s > byte_of(ref, c);
+              above |= s != 255 && min(s, most[h]) > byte_of(ref, c);
             }
           if (__any_sync(kAll, above)) {
 #pragma unroll
@@ -563,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const int x = byte_of(sc[h], c);
-                if (32 * h + lane < left && x != 255) s = max(s, x);
+                if (x != 255) s = max(s, min(x, most[h]));
               }
               s = __reduce_max_sync(kAll, s);
               if (s > byte_of(ref, c))
@@ -575,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
 #pragma unroll
             for (int c = 0; c < CB; ++c) {
               const int s = byte_of(sc[h], c);
-              other |= 32 * h + lane < left && (s == 255 || byte_of(ref, c) - s > 22);
+              other |= most[h] >= 0 && (s == 255 || !in_tile(byte_of(ref, c) - s));
             }
           other = __any_sync(kAll, other);
           // the factors of the warp's 16 keys, a lane to half of a key's
@@ -588,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
 #pragma unroll
             for (int c = 0; c < CB / 2; ++c) {
               const int s = byte_of(mine, c), d = byte_of(ref, c0 + c) - s;
-              if (t < left && s != 255 && d <= 22) f |= half_power(d) << (16 * c);
+              if (t < left && s != 255 && in_tile(d)) f |= half_power(d) << (16 * c);
             }
             if constexpr (CB == 4)
               *reinterpret_cast<uint32_t*>(factors + 8 * (lane & 15) + 2 * c0) = f;
@@ -869,9 +889,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
 #pragma unroll 1
               for (int c = 0; c < CB; ++c) {
                 const int s = grp[G::kVScale + (key & 15) * CB + c], d = byte_of(ref, c) - s;
-                if (s != 255 && d <= 22) continue;
-                const float by = s == 255 ? (seen ? __uint_as_float(0x7FC00000u) : 0.f)
-                                          : weight * exp2f((float)-d);
+                if (s != 255 && in_tile(d)) continue;
+                const float by = !seen ? 0.f
+                                 : s == 255 ? __uint_as_float(0x7FC00000u) : weight * exp2f((float)-d);
                 uint32_t o[32];
                 tmem_ld32(o_at + 32 * c, o);
 #pragma unroll

@@ -98,3 +98,41 @@ def test_values_near_the_largest(cuda_device, D, lens, news):
     # values of up to 6 x 2^119: a mean of them is finite, the sum of a few hundred, weighted, is not
     c = Case(cuda_device, lens, news, 8, 1, D, 32, seed=D, pool=shift_scales("v", 118))
     check(c, c.run())
+
+
+# ---------------------------------------------- values that a row does not see ---
+
+def small_values(r, pages, layers, hkv, P, D):
+    pool = quantised_pool(r, pages, layers, hkv, P, D)
+    at = 16 * D + D // 2
+    pool[..., at:at + D // 2] = r.randint(90, 111, pool[..., at:at + D // 2].shape)
+    return pool
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_values_before_the_window_do_not_count(cuda_device, D):
+    # the window starts inside a step of 32 keys: the keys before it there are copied, and far larger
+    c = Case(cuda_device, [100, 300], [1, 1], 8, 2, D, 32, seed=D, pool=small_values)
+    set_scales(c, "v", 0, range(0, 80), 254)
+    set_scales(c, "v", 1, range(256, 280), 254)
+    check(c, c.run(window=20), window=20)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_before_the_window_of_a_chunk_do_not_count(cuda_device, D):
+    # tiles of 32 tokens: the first one's rows see from 97 on, and its first tile of keys starts at 64
+    c = Case(cuda_device, [200], [64], 8, 1, D, 32, seed=D, pool=small_values)
+    set_scales(c, "v", 0, range(64, 97), 254)
+    check(c, c.run(window=40), window=40)
+
+
+@pytest.mark.parametrize("news", [[3, 2], [32, 64]])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("window", [0, 20])
+def test_values_that_some_rows_see(cuda_device, news, D, window):
+    # the last token's values, which the others of the chunk do not see, and those at the start of the
+    # first row's window, which the later rows do not see
+    c = Case(cuda_device, [100, 300], news, 8, 1, D, 32, seed=D + window, pool=small_values)
+    set_scales(c, "v", 0, [99], 250)
+    set_scales(c, "v", 1, [299, 300 - news[1] - (window or 300) + 1] if window else [299], 247)
+    check(c, c.run(window=window), window=window)
