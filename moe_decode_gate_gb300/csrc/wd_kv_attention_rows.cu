@@ -15,8 +15,8 @@
 //   - K: where the scales of a tile are within 2^22 of each other, its blocks are scaled by
 //     2^(s - R), exactly, and 2^(R - 127) goes into the rows' softmax factor.  Else each token has its
 //     own r, the largest scale of its blocks that are not all zero, 2^(s - r) is exact down to
-//     2^-23 (below, to 2^-24 of the token's largest block: what FP32 keeps of the logit's sum
-//     where that block counts), and 2^(r - 127) multiplies the logit in FP32.
+//     2^-23, and 2^(r - 127) multiplies the logit in FP32.  Smaller blocks are 0 in the tile, and the
+//     softmax adds their part of the logits in FP32 (a query may be zero where the large ones are).
 //   - V: blocks are scaled by 2^(s - R), exactly down to 2^-22, with R at least the largest scale
 //     met for the block of channels (16 times it where it was set, so that it is seldom
 //     set again; keys that some of the rows do not see raise it to 2^23 at most).  What is smaller or
@@ -64,7 +64,8 @@ struct Rows {
   static constexpr int kRaw = kV + kStages * kTileBytes;
   static constexpr int kCol = kRaw + kRaws * kRawBytes;    // float [stages][kKeys]: 2^(r - 127)
   static constexpr int kFactor = kCol + kStages * kKeys * 4;  // FP16 [kKeys][4]: of V
-  // uint32 [stages][4]: V's references, whether there is more of it; K's 2^(R - 127), or 0
+  // uint32 [stages][4]: V's references, whether there is more of it; K's 2^(R - 127), or 0; whether there
+  // is more of K, a byte for each warp that writes it
   static constexpr int kInfo = kFactor + kKeys * 8;
   static constexpr int kBars = kInfo + kStages * 16;
   // uint64, one after the other:
@@ -157,6 +158,9 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t addr) {
       : "memory");
   return r;
 }
+__device__ __forceinline__ void tmem_st1(uint32_t addr, uint32_t r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr), "r"(r) : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -222,6 +226,46 @@ __device__ __forceinline__ uint32_t half_power(int d) {
 
 // Whether V that is 2^-d of the reference is in the tile: else it is added on its own.
 __device__ __forceinline__ bool in_tile(int d) { return (unsigned)d <= 22u; }
+
+// Whether a block of K that is 2^-d of its token's largest is in the tile: E2M1's 0.5 x 2^-d is an FP16 number.
+__device__ __forceinline__ bool key_in_tile(int d) { return d <= 23; }
+
+// What of a key's sum with a query row is not in its tile.  grp: the key's group, of which it is token t; q: the
+// tile of the row's half, in shared memory.
+template <int D>
+__device__ __noinline__ float key_rest(const uint8_t* grp, int t, const uint8_t* q, int row) {
+  using G = KvGroup<D>;
+  int top = 0;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass)
+#pragma unroll 1
+    for (int c = 0; c < G::kBlocks; ++c) {
+      const int s = grp[G::kKScale + t * G::kBlocks + c];
+      if (pass == 1 && (s == 255 || key_in_tile(top - s))) continue;
+      uint32_t any = 0;
+      float part = 0.f;
+#pragma unroll 1
+      for (int t8 = 0; t8 < 4; ++t8) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(grp + G::k_word(t, c, t8));
+        any |= w & 0x77777777u;
+        if (pass == 0) continue;
+        uint32_t k[4];
+        e2m1x8(w, k[0], k[1], k[2], k[3]);
+        const uint4 x = *reinterpret_cast<const uint4*>(q + tile_at(128, row, 4 * c + t8));
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&k[e]));
+          const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&xs[e]));
+          part = fmaf(a.y, b.y, fmaf(a.x, b.x, part));
+        }
+      }
+      if (pass == 0 && (s == 255 || any != 0u)) top = max(top, s);
+      if (pass == 1 && any != 0u) sum += part * exp2f((float)(s - 127));
+    }
+  return sum;
+}
 
 // Two FP32 values in one register pair: one instruction for both.
 __device__ __forceinline__ uint64_t pair(uint32_t lo, uint32_t hi) {
@@ -520,6 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
           const uint32_t mine = own ? sc[1] : sc[0];
           const uint8_t* codes = raw + (t >> 4) * G::kBytes + (t & 15) * 16 * CB;
           int top = high;
+          bool rest = false;  // the token has blocks that are not in the tile
           if (!alike) {
             uint32_t any[CB] = {};
             for (int j = 0; j < 4; ++j) {
@@ -533,10 +578,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
               const int s = byte_of(mine, c);
               if (s == 255 || (any[c] & 0x77777777u)) top = max(top, s);
             }
+#pragma unroll
+            for (int c = 0; c < CB; ++c)
+              rest |= t < left && (any[c] & 0x77777777u) && !key_in_tile(top - byte_of(mine, c));
+            rest = __any_sync(kAll, rest);
           }
           uint32_t f[CB];
 #pragma unroll
-          for (int c = 0; c < CB; ++c) f[c] = half_power(max(0, top - byte_of(mine, c))) * 0x10001u;
+          for (int c = 0; c < CB; ++c) {
+            const int d = max(0, top - byte_of(mine, c));
+            f[c] = key_in_tile(d) ? half_power(d) * 0x10001u : 0u;
+          }
           if (count >= kStages && !wait(L::kFree + st, (count / kStages - 1) & 1)) return;
           uint8_t* to = smem + L::kK + st * L::kTileBytes;
 #pragma unroll 1
@@ -558,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
           if (own == 0 && lane == 0)
             *reinterpret_cast<float*>(smem + L::kInfo + 16 * st + 8) =
                 alike ? exp2f((float)(high - 127)) : 0.f;
+          if (lane == 0) smem[L::kInfo + 16 * st + 12 + own] = rest;
         } else {
           // A key that not every row sees must not push what the others see out of FP32: it raises the
           // reference to kSharedMost at most.
@@ -820,9 +873,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
             if (f == 0.f) f = 1.2e-38f;  // (-inf stays -inf)
           } else {
             const float* col = reinterpret_cast<const float*>(smem + L::kCol) + st * kKeys;
+            if ((info.w & 0xFFFFu) == 0u) {
 #pragma unroll
-            for (int n = 0; n < kKeys; ++n)
-              sr[n] = __float_as_uint(__uint_as_float(sr[n]) * col[n]);
+              for (int n = 0; n < kKeys; ++n)
+                sr[n] = __float_as_uint(__uint_as_float(sr[n]) * col[n]);
+            } else {
+              // ---- what of the tile's K is not in it
+#pragma unroll 1
+              for (int t = 0; t < kKeys && j0 + t < p.end; ++t) {
+                const int key = j0 + t;
+                const uint8_t* grp =
+                    kv_group(cache, kv_page(cache, p.slot, key >> cache.page_shift), a.layer,
+                             p.part.head, key, G::kBytes);
+                const float rest =
+                    key_rest<D>(grp, key & 15, smem + L::kQ + x * L::kHalfBytes, row & 127);
+                const float sum = __uint_as_float(tmem_ld1(s_at + t));
+                tmem_st1(s_at + t, __float_as_uint(fmaf(sum, col[t], rest)));
+              }
+              tmem_st_wait();
+              tmem_ld64(s_at, sr);
+            }
           }
           if (!whole) {
 #pragma unroll

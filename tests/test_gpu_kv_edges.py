@@ -136,3 +136,34 @@ def test_values_that_some_rows_see(cuda_device, news, D, window):
     set_scales(c, "v", 0, [99], 250)
     set_scales(c, "v", 1, [299, 300 - news[1] - (window or 300) + 1] if window else [299], 247)
     check(c, c.run(window=window), window=window)
+
+
+# --------------------------------------------------- key blocks of unlike size ---
+
+@pytest.mark.parametrize("news", [FEW, MANY])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("apart", [22, 23, 24, 25, 40, 60])
+def test_small_key_blocks_count_where_the_query_is_zero_in_the_large_one(cuda_device, news, D, apart):
+    c = Case(cuda_device, [100, 300], news, 8, 1, D, 32, seed=D + apart)
+    q = c.q_values.copy()
+    q[..., :32] = 0.0
+    c.q = torch.from_numpy(q).to(c.dtype)
+    c.q_values = c.q.double().numpy()
+    for b, L in enumerate((100, 300)):  # block 0 of every other key
+        set_scales(c, "k", b, range(0, L, 2), 126 + apart, slice(0, 1))
+    check(c, c.run())
+
+
+@pytest.mark.parametrize("news", [FEW, MANY])
+@pytest.mark.parametrize("D", [64, 128])
+def test_key_blocks_apart_of_which_both_count(cuda_device, news, D):
+    # the query is as much smaller in the large block as that is larger (and holds it exactly in FP16
+    # beside its other channels)
+    c = Case(cuda_device, [100, 300], news, 8, 1, D, 32, seed=D)
+    q = c.q_values.copy()
+    q[..., 32:64] = np.where(q[..., 32:64] < 0, -(2.0 ** -28), 2.0 ** -28)
+    c.q = torch.from_numpy(q).to(c.dtype)
+    c.q_values = c.q.double().numpy()
+    for b, L in enumerate((100, 300)):
+        set_scales(c, "k", b, range(L), 126 + 28, slice(1, 2))
+    check(c, c.run())
