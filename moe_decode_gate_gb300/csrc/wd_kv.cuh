@@ -181,6 +181,7 @@ struct KvAttentionArgs {
   void* out;
   float* lse;
   float scale;
+  float key_scale, row_scale;  // of launch_kv_attention's own: scale log2 e = key_scale 2^kKeyShift row_scale
   int window, max_q;
   bool half;  // FP16 (else BF16)
   uint32_t* counters;

@@ -16,7 +16,10 @@
 // so eight query heads fill a tile, where a 16-row query tile would be half empty.  The groups are
 // stored in fragment order: one 16-byte shared-memory read per lane brings 32 codes, which the
 // hardware conversion turns into FP16 (exactly) in place.
-//   - K: the sums over a block of 32 channels are scaled by the block's 2^(s-127) in FP32.
+//   - K: the sums over a block of 32 channels are scaled by the block's 2^(s-127) in FP32, with it by what the
+//     softmax scale x log2 e is of a power of two, and by 2^-26, so that no finite keys leave FP32
+//     here.  The rows' own factors are then powers of two: a logit and the maximum are exact products, and
+//     their difference is right however large they are.
 //   - Queries are FP16 x 2^k with k per row (exact for BF16 and FP16 within 2^31 of the row's
 //     largest magnitude), 2^-k folded into the softmax scale.
 //   - P = 2^8 exp2(x - m) is rounded to FP16 once; the row sums are of the unrounded values, in
@@ -107,7 +110,7 @@ __device__ __forceinline__ int steps_choice(int i, int fair, int longest) {
 }
 
 // S^T of one group of 16 keys: s[nt] has keys g (0, 1) and 8 + g (2, 3) of columns 2tq, 2tq + 1.
-// `scales`: the group's keys' block scales as floats.
+// `scales`: the group's keys' block scales, times a.key_scale.
 template <int D, int NT>
 __device__ __forceinline__ void scores(const uint8_t* buf, const uint8_t* scales, const uint4* qf,
                                        const uint8_t* q_sh, int lane, float (&s)[NT][4]) {
@@ -591,7 +594,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
         if (e8 == 0) {
           const int pos = entry.len - entry.n + (entry.n > 1 ? (part.tile * kRows + row) / group : 0);
           const bool real = row < rows;  // no row: nothing to hide, never stored
-          factor_sh[row] = row_factor(r, a.scale);
+          factor_sh[row] = power_factor(r, a.row_scale);
           lo_sh[row] = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
           hi_sh[row] = real ? pos : span.end - 1;
         }
@@ -615,7 +618,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
       if (tq == 0) {
         const int pos = entry.len - entry.n + (entry.n > 1 ? (part.tile * kRows + g) / group : 0);
         const bool real = g < rows;
-        factor_sh[g] = row_factor(r, a.scale);
+        factor_sh[g] = power_factor(r, a.row_scale);
         lo_sh[g] = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
         hi_sh[g] = real ? pos : span.end - 1;
       }
@@ -669,14 +672,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
       for (int w = 0; w < NW; ++w) {
         float4 f;
         const uint32_t lo = e8m0x2(kt.v[w]);
-        f.x = __uint_as_float(lo << 16);
-        f.y = __uint_as_float(lo & 0xFFFF0000u);
+        f.x = __uint_as_float(lo << 16) * a.key_scale;
+        f.y = __uint_as_float(lo & 0xFFFF0000u) * a.key_scale;
         if constexpr (CB == 2) {
           *reinterpret_cast<float2*>(k_scales + lane * 8) = make_float2(f.x, f.y);
         } else {
           const uint32_t hi = e8m0x2(kt.v[w] >> 16);
-          f.z = __uint_as_float(hi << 16);
-          f.w = __uint_as_float(hi & 0xFFFF0000u);
+          f.z = __uint_as_float(hi << 16) * a.key_scale;
+          f.w = __uint_as_float(hi & 0xFFFF0000u) * a.key_scale;
           *reinterpret_cast<float4*>(k_scales + lane * 4 * CB + 16 * w) = f;
         }
       }
@@ -1086,7 +1089,12 @@ cudaError_t run(const KvAttentionArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t s) {
+cudaError_t launch_kv_attention(const KvAttentionArgs& args, cudaStream_t s) {
+  KvAttentionArgs a = args;
+  int exponent;
+  const float fraction = frexpf(fminf(fmaxf(a.scale * 1.4426950408889634f, FLT_MIN), FLT_MAX), &exponent);
+  a.key_scale = ldexpf(fraction, -kKeyShift);
+  a.row_scale = ldexpf(1.f, exponent > 127 ? 127 : exponent);
   const int group = a.q_heads / a.cache.kv_heads;
   const long long rows = (long long)a.max_q * group;
   // More rows than one tile here holds, and so on average too (a chunk among many single tokens would

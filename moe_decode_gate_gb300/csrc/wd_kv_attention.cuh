@@ -2,6 +2,8 @@
 // batch's entries, the keys that a tile of query rows sees, and the store of a finished row.
 #pragma once
 
+#include <float.h>
+
 #include "wd_device.cuh"
 #include "wd_kv.cuh"
 #include "wd_mma.cuh"
@@ -12,6 +14,9 @@ constexpr int kStep = 32;      // keys of a step: two groups
 constexpr int kCached = 256;   // entries whose slot and length are kept in shared memory
 constexpr float kBias = 8.f;   // P = 2^kBias at the reference m ...
 constexpr float kSlack = 6.f;  // ... which may fall this far behind the maximum (log2)
+// Sums of K with queries of up to 2^15, each scaled by its block's 2^(s - 127), are kept 2^26 times smaller: 256
+// products of up to 6 x 2^15 then stay within FP32 for any s.
+constexpr int kKeyShift = 26;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 // How far the values of a key that some rows of a tile do not see may raise V's reference: what those rows see
 // stays within FP32 beside it (2^-134 of it at worst), and so does what lies above (up to 2^104, added one by one).
@@ -236,11 +241,25 @@ __device__ __forceinline__ RowScale row_scale(uint32_t bits) {
   r.up2 = exp2_int(k - k / 2);
   return r;
 }
-// What the row's sums are multiplied by: a row with an infinity or NaN has no finite logit;
-// never 0, so that -inf stays -inf.
+// 2^kFactorShift times what the row's sums are multiplied by, a number that FP32 holds for all queries (scale up
+// to 1): a row with an infinity or NaN has no finite logit; never 0, so that -inf stays -inf.
+constexpr int kFactorShift = kKeyShift / 2;
 __device__ __forceinline__ float row_factor(const RowScale& r, float scale) {
+  constexpr float kUp = (float)(1 << kFactorShift);
   return r.bad ? __uint_as_float(0x7FC00000u)
-               : fmaxf(scale * 1.4426950408889634f / r.up / r.up2, 1.2e-38f);
+               : fminf(fmaxf(scale * 1.4426950408889634f / r.up * kUp / r.up2, 1.2e-38f), FLT_MAX);
+}
+// Of a row whose sums are 2^kKeyShift times smaller and have all of `scale` but a power of two, `unit`, in them.
+// (|q| unit beyond 2^114 has to do with 2^127.)
+__device__ __forceinline__ float power_factor(const RowScale& r, float unit) {
+  constexpr float kUp = (float)(1 << (kKeyShift / 2));
+  return r.bad ? __uint_as_float(0x7FC00000u)
+               : fminf(fmaxf(unit / r.up * kUp / r.up2 * kUp, 0x1p-126f), 0x1p127f);
+}
+// ... for sums that are 2^kKeyShift times smaller (where |q| scale is beyond 2^114 FP32's largest has to do).
+__device__ __forceinline__ float shifted_factor(float factor) {
+  const float f = factor * (float)(1 << (kKeyShift - kFactorShift));
+  return f > FLT_MAX ? FLT_MAX : f;
 }
 __device__ __forceinline__ uint4 row_fragment(const float (&x)[8], const RowScale& r) {
   uint4 f;

@@ -15,7 +15,7 @@
 //   - K: where the scales of a tile are within 2^22 of each other, its blocks are scaled by
 //     2^(s - R), exactly, and 2^(R - 127) goes into the rows' softmax factor.  Else each token has its
 //     own r, the largest scale of its blocks that are not all zero, 2^(s - r) is exact down to
-//     2^-23, and 2^(r - 127) multiplies the logit in FP32.  Smaller blocks are 0 in the tile, and the
+//     2^-23, and 2^(r - 127) multiplies the logit in FP32 (as 2^(r - 153), the rest in the row's factor).  Smaller blocks are 0 in the tile, and the
 //     softmax adds their part of the logits in FP32 (a query may be zero where the large ones are).
 //   - V: blocks are scaled by 2^(s - R), exactly down to 2^-22, with R at least the largest scale
 //     met for the block of channels (16 times it where it was set, so that it is seldom
@@ -49,6 +49,9 @@ constexpr int kKeyWarp = 8, kValueWarp = 10, kIssueWarp = 14, kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxEntries = 1024;  // of a batch: they are kept in shared memory
 constexpr int kAlike = 30;  // octaves around 1 in which a tile's R may be part of a row's factor
+// Logits whose reference is beyond this are rounded before the reference is taken off: in one fused step the
+// rounding of the reference alone, 2^-24 of it, would be an exponent.
+constexpr float kSteep = 16384.f;
 constexpr int kRoom = 4;  // octaves that a V reference is set above the largest scale
 constexpr uint32_t kTmemColumns = 512;
 
@@ -62,9 +65,9 @@ struct Rows {
   static constexpr int kK = kQ + 2 * kHalfBytes;
   static constexpr int kV = kK + kStages * kTileBytes;
   static constexpr int kRaw = kV + kStages * kTileBytes;
-  static constexpr int kCol = kRaw + kRaws * kRawBytes;    // float [stages][kKeys]: 2^(r - 127)
+  static constexpr int kCol = kRaw + kRaws * kRawBytes;    // float [stages][kKeys]: 2^(r - 127 - kKeyShift)
   static constexpr int kFactor = kCol + kStages * kKeys * 4;  // FP16 [kKeys][4]: of V
-  // uint32 [stages][4]: V's references, whether there is more of it; K's 2^(R - 127), or 0; whether there
+  // uint32 [stages][4]: V's references, whether there is more of it; K's 2^(R - 127 - kFactorShift), or 0; whether there
   // is more of K, a byte for each warp that writes it
   static constexpr int kInfo = kFactor + kKeys * 8;
   static constexpr int kBars = kInfo + kStages * 16;
@@ -230,7 +233,7 @@ __device__ __forceinline__ bool in_tile(int d) { return (unsigned)d <= 22u; }
 // Whether a block of K that is 2^-d of its token's largest is in the tile: E2M1's 0.5 x 2^-d is an FP16 number.
 __device__ __forceinline__ bool key_in_tile(int d) { return d <= 23; }
 
-// What of a key's sum with a query row is not in its tile.  grp: the key's group, of which it is token t; q: the
+// What of a key's sum with a query row is not in its tile, times 2^-kKeyShift.  grp: the key's group, of which it is token t; q: the
 // tile of the row's half, in shared memory.
 template <int D>
 __device__ __noinline__ float key_rest(const uint8_t* grp, int t, const uint8_t* q, int row) {
@@ -262,7 +265,7 @@ __device__ __noinline__ float key_rest(const uint8_t* grp, int t, const uint8_t*
         }
       }
       if (pass == 0 && (s == 255 || any != 0u)) top = max(top, s);
-      if (pass == 1 && any != 0u) sum += part * exp2f((float)(s - 127));
+      if (pass == 1 && any != 0u) sum += part * exp2f((float)(s - 127 - kKeyShift));
     }
   return sum;
 }
@@ -606,10 +609,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
           }
           reinterpret_cast<float*>(smem + L::kCol)[st * kKeys + t] =
               t >= left ? 0.f : top == 255 ? __uint_as_float(0x7FC00000u)
-                                           : exp2f((float)(top - 127));
+                                           : exp2f((float)(top - 127 - kKeyShift));
           if (own == 0 && lane == 0)
             *reinterpret_cast<float*>(smem + L::kInfo + 16 * st + 8) =
-                alike ? exp2f((float)(high - 127)) : 0.f;
+                alike ? exp2f((float)(high - 127 - kFactorShift)) : 0.f;
           if (lane == 0) smem[L::kInfo + 16 * st + 12 + own] = rest;
         } else {
           // A key that not every row sees must not push what the others see out of FP32: it raises the
@@ -811,6 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
       const bool active = x == 0 || p.rows > 128;
       float m = -INFINITY, l = 0.f, factor = 0.f;
       uint32_t ref = 0;
+      bool steep = false;  // a reference of one of the warp's rows is beyond kSteep
       if (active && p.tiles > 0) {
         // ---- the row's query
         const long long q_at = (p.part.first + token) * a.q_token + head * a.q_head;
@@ -867,12 +871,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
           tmem_ld64(s_at, sr);
           const uint4 info = *reinterpret_cast<const uint4*>(smem + L::kInfo + 16 * st);
           const bool whole = __all_sync(kAll, j0 >= row_lo && j0 + kKeys - 1 <= row_hi);
+          const float* col = reinterpret_cast<const float*>(smem + L::kCol) + st * kKeys;
           float f = factor;
           if (info.z) {
             f *= __uint_as_float(info.z);
             if (f == 0.f) f = 1.2e-38f;  // (-inf stays -inf)
           } else {
-            const float* col = reinterpret_cast<const float*>(smem + L::kCol) + st * kKeys;
+            f = shifted_factor(f);
             if ((info.w & 0xFFFFu) == 0u) {
 #pragma unroll
               for (int n = 0; n < kKeys; ++n)
@@ -911,6 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
             const float keep = m == -INFINITY ? (t == m ? 1.f : 0.f) : exp2_fast(m - t);
             l = m == -INFINITY ? l : l * keep;  // (a sum of NaN is not forgotten)
             m = t;
+            steep = __any_sync(kAll, fabsf(m) >= kSteep && m != -INFINITY);
             if (i > 0) {
               if (!wait_outs(mine)) return;
 #pragma unroll 1
@@ -925,7 +931,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
             }
           }
           ref = info.x;
-          const float z = m == -INFINITY ? 0.f : kBias - m;
+          float z = m == -INFINITY ? 0.f : kBias - m;
+          if (steep) {
+            const float from = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+            for (int n = 0; n < kKeys; ++n) {
+              float v = __uint_as_float(tmem_ld1(s_at + n));
+              if (!info.z && (info.w & 0xFFFFu) == 0u) v *= col[n];
+              v = j0 + n < row_lo || j0 + n > row_hi ? -INFINITY : __fsub_rn(__fmul_rn(v, f), from);
+              tmem_st1(s_at + n, __float_as_uint(v));
+            }
+            tmem_st_wait();
+            tmem_ld64(s_at, sr);
+            f = 1.f;
+            z = kBias;
+          }
           uint64_t sums[2] = {0, 0};
           const uint64_t f2 = pair(__float_as_uint(f), __float_as_uint(f)),
                          z2 = pair(__float_as_uint(z), __float_as_uint(z));

@@ -167,3 +167,33 @@ def test_key_blocks_apart_of_which_both_count(cuda_device, news, D):
     for b, L in enumerate((100, 300)):
         set_scales(c, "k", b, range(L), 126 + 28, slice(1, 2))
     check(c, c.run())
+
+
+# ------------------------------------------------------------ logits near the ends ---
+
+@pytest.mark.parametrize("news", [FEW, MANY])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("by", [90, 105, 122, -100])
+def test_large_keys_and_small_queries(cuda_device, news, D, by):
+    # (and the other way round): the logits are those of a plain case
+    c = Case(cuda_device, [100, 300], news, 8, 1, D, 32, seed=D, q_scale=2.0 ** -by,
+             pool=shift_scales("k", by))
+    check(c, c.run())
+
+
+@pytest.mark.parametrize("news", [FEW, MANY])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("byte", [150, 170, 200, 235])
+def test_a_few_far_larger_keys(cuda_device, news, D, byte):
+    # logits of up to 2^110: a row's softmax is one of these keys, or none of them
+    c = Case(cuda_device, [100, 300], news, 8, 1, D, 32, seed=D + byte)
+    for b, L in enumerate((100, 300)):
+        set_scales(c, "k", b, [3, 17, 61, L - 2], byte)
+    check(c, c.run())
+
+
+@pytest.mark.parametrize("news", [FEW, MANY])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_all_logits_far_from_zero(cuda_device, news, D):
+    c = Case(cuda_device, [100, 300], news, 8, 1, D, 32, seed=D, q_scale=2.0 ** 40)
+    check(c, c.run())
