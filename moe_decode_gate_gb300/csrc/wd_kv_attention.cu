@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
         if (e8 == 0) {
           const int pos = entry.len - entry.n + (entry.n > 1 ? (part.tile * kRows + row) / group : 0);
           const bool real = row < rows;  // no row: nothing to hide, never stored
-          factor_sh[row] = power_factor(r, a.row_scale);
+          factor_sh[row] = pos < 0 ? 1.f : power_factor(r, a.row_scale);  // (sees nothing: no NaN)
           lo_sh[row] = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
           hi_sh[row] = real ? pos : span.end - 1;
         }
@@ -618,7 +618,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
       if (tq == 0) {
         const int pos = entry.len - entry.n + (entry.n > 1 ? (part.tile * kRows + g) / group : 0);
         const bool real = g < rows;
-        factor_sh[g] = power_factor(r, a.row_scale);
+        factor_sh[g] = pos < 0 ? 1.f : power_factor(r, a.row_scale);  // (sees nothing: no NaN)
         lo_sh[g] = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
         hi_sh[g] = real ? pos : span.end - 1;
       }

@@ -812,6 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
       const int head = p.part.head * group + flat - token * group;
       const long long at = (long long)(p.part.first + token) * a.q_heads + head;
       const bool active = x == 0 || p.rows > 128;
+      const int pos = p.len - p.part.n + token;
       float m = -INFINITY, l = 0.f, factor = 0.f;
       uint32_t ref = 0;
       bool steep = false;  // a reference of one of the warp's rows is beyond kSteep
@@ -837,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
         bits = a.half ? __float_as_uint(__half2float(__ushort_as_half((unsigned short)bits)))
                       : bits << 16;
         const RowScale scale = row_scale(bits);
-        factor = row_factor(scale, a.scale);
+        factor = pos < 0 ? 1.f : row_factor(scale, a.scale);  // (sees nothing: no NaN)
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {
           float v[8];
@@ -854,7 +855,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
         tmem_fence_before();
         mbar_arrive(bar(L::kQuery + x));
       }
-      const int pos = p.len - p.part.n + token;
       const int row_lo = real && a.window > 0 ? max(0, pos - a.window + 1) : 0;
       const int row_hi = real ? pos : 0x7FFFFFFF;  // no row: nothing to hide, never stored
       if (!active) {

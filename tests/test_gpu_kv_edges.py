@@ -197,3 +197,17 @@ def test_a_few_far_larger_keys(cuda_device, news, D, byte):
 def test_all_logits_far_from_zero(cuda_device, news, D):
     c = Case(cuda_device, [100, 300], news, 8, 1, D, 32, seed=D, q_scale=2.0 ** 40)
     check(c, c.run())
+
+
+# ------------------------------------------------------------- rows that see nothing ---
+
+@pytest.mark.parametrize("lens,news", [([2], [4]), ([20], [40])])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_query_of_nan_that_sees_nothing(cuda_device, lens, news, bad):
+    c = Case(cuda_device, lens, news, 8, 1, 128, 32, seed=1)
+    want, want_lse = c.run()
+    q = c.q.clone()
+    q[0, 3, 7] = q[1] = bad
+    got, lse = c.run(q=q.to(cuda_device))
+    assert torch.equal(got, want) and torch.equal(lse, want_lse)
+    assert not got[:2].any() and torch.isneginf(lse[:2]).all()
