@@ -98,16 +98,17 @@ __device__ __forceinline__ void kv_tokens(const KvView& v, const KvBatch& q, int
   n = (int)end - first;
 }
 
-// A page id of the table, in column j of slot s; page 0 (and the flag) if the id is out of range,
-// so that what follows stays inside the pool.
-__device__ __forceinline__ int kv_page_checked(const KvView& v, int p) {
-  if ((unsigned)p < (unsigned)v.num_pages) return p;
-  atomicOr(v.flag, WD_KV_FLAG_BAD_INDEX);
-  return 0;
+// Whether the pool has this page.
+__device__ __forceinline__ bool kv_page_there(const KvView& v, int p) {
+  return (unsigned)p < (unsigned)v.num_pages;
 }
 
+// The page in column j of slot s; -1 (and the flag) if the id is out of range.
 __device__ __forceinline__ int kv_page(const KvView& v, int s, int j) {
-  return kv_page_checked(v, v.table[(long long)s * v.columns + j]);
+  const int p = v.table[(long long)s * v.columns + j];
+  if (kv_page_there(v, p)) return p;
+  atomicOr(v.flag, WD_KV_FLAG_BAD_INDEX);
+  return -1;
 }
 
 // Address of the 16-token group that holds position `pos` of a head.

@@ -526,18 +526,25 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
       page0 = row[pos >> cache.page_shift];
       page1 = cache.page_size < kStep && pos + 16 < span.end ? row[(pos + 16) >> cache.page_shift] : 0;
     };
+    // (false, and the flag, if a page is out of range: its groups are not copied)
     const auto plan = [&](int i0) {
       const int pos = (span.first + from + i0 + lane) * kStep;
+      bool there = true;
       src1 = nullptr;
-      if (i0 + lane >= steps) return;
-      src0 = kv_group(cache, kv_page_checked(cache, page0), a.layer, part.head, pos, G::kBytes);
-      bytes0 = G::kBytes;
-      if (pos + 16 < span.end) {
-        if (cache.page_size >= kStep)  // the step lies within a page, its groups side by side
-          bytes0 = 2 * G::kBytes;
-        else
-          src1 = kv_group(cache, kv_page_checked(cache, page1), a.layer, part.head, pos + 16, G::kBytes);
+      if (i0 + lane < steps) {
+        there = kv_page_there(cache, page0) && kv_page_there(cache, page1);
+        bytes0 = 0;
+        if (kv_page_there(cache, page0)) {
+          src0 = kv_group(cache, page0, a.layer, part.head, pos, G::kBytes);
+          // the step lies within a page, its groups side by side, or its groups lie in two pages
+          bytes0 = cache.page_size >= kStep && pos + 16 < span.end ? 2 * G::kBytes : G::kBytes;
+        }
+        if (cache.page_size < kStep && pos + 16 < span.end && kv_page_there(cache, page1))
+          src1 = kv_group(cache, page1, a.layer, part.head, pos + 16, G::kBytes);
       }
+      if (__all_sync(kAll, there)) return true;
+      if (lane == 0) atomicOr(cache.flag, WD_KV_FLAG_BAD_INDEX);
+      return false;
     };
     look_up(0);
 
@@ -561,10 +568,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
     const auto issue = [&](int to_stage) {
       const uint32_t to = ring_at + to_stage * L::kStageBytes, full = bar + 8 * to_stage;
       mbar_arrive_expect_tx(full, bytes0 + (src1 ? G::kBytes : 0));
-      bulk_g2s_nohint(to, src0, bytes0, full);
+      if (bytes0) bulk_g2s_nohint(to, src0, bytes0, full);
       if (src1) bulk_g2s_nohint(to + G::kBytes, src1, G::kBytes, full);
     };
-    plan(0);
+    const bool pages_there = plan(0);
     if (lane < kStages && lane < steps) issue((stage + lane) % kStages);
     __syncwarp();
 
@@ -640,6 +647,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
     seen_hi = min(seen_hi, __shfl_xor_sync(kAll, seen_hi, 1));
     seen_hi = min(seen_hi, __shfl_xor_sync(kAll, seen_hi, 2));
 
+    // Once a page out of range has been looked up, no key counts as seen by all any more, and seen_hi has
+    // the groups of the step that are not there (bits 0 and 16).
+    constexpr int kNone = 0x7FFFFFFF;
+    if (!pages_there) seen_lo = kNone;
+
     float o[CB][2][NT][4];
     float m[NT][2], l[NT][2];
     uint32_t ref[NW];  // the largest V scale met, a byte to a block, at least 16
@@ -665,6 +677,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
 
       // ---- the scales of key step_at + lane, for the lanes whose products want them
       bool inside = step_at + lane < span.end;
+      if (seen_lo == kNone) {
+        inside = inside && kv_page_there(cache, cache.table[(long long)entry.slot * cache.columns +
+                                                            ((step_at + lane) >> cache.page_shift)]);
+        seen_hi = (int)(~__ballot_sync(kAll, inside) & 0x10001u);
+      }
       const uint8_t* scale_at = ring + stage * L::kStageBytes + (lane >> 4) * G::kBytes + (lane & 15) * CB;
       const Words<NW> kt = lds_scales<CB>(scale_at + G::kKScale);
       Words<NW> vt = lds_scales<CB>(scale_at + G::kVScale);
@@ -730,6 +747,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
 
         // ---- does anything change: a larger logit, a V scale out of range?
         const bool whole = j0 >= seen_lo && j0 + 16 * kU - 1 <= seen_hi;
+        const auto there = [&](int u) {
+          return seen_lo != kNone || ((unsigned)seen_hi >> (16 * (u0 + u)) & 1u) == 0u;
+        };
         float top[NT][2];
         bool grow = odd;
 #pragma unroll
@@ -744,7 +764,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
                 float& x = s[u][nt][2 * h + e];
                 if (!whole) {
                   const int row = 8 * nt + 2 * tq + e, key = j0 + 16 * u + 8 * h + g;
-                  if (key < lo_sh[row] || key > hi_sh[row]) x = -INFINITY;
+                  if (key < lo_sh[row] || key > hi_sh[row] || !there(u)) x = -INFINITY;
                 }
                 t = fmaxf(t, x);
               }
@@ -836,7 +856,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
         for (int u = 0; u < kU; ++u) {
           if (!slow)
             values<D, NT>(buf + u * G::kBytes, v_scales + (u0 + u) * 8 * CB * 4, p[u], lane, o);
-          else
+          else if (there(u))
             values_singly<D, NT>(buf + u * G::kBytes, p[u], ref, j0 + 16 * u, span.end, lo_sh, hi_sh,
                                  lane, o);
         }
@@ -853,7 +873,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
       const int next = i + kStages;
       if ((next & 31) == 0) {
         look_up(next);
-        plan(next);
+        if (!plan(next)) seen_lo = kNone;
       }
       if (lane == (next & 31) && next < steps) issue(stage);
       if (++stage == kStages) {

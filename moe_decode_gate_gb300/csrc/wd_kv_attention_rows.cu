@@ -68,7 +68,7 @@ struct Rows {
   static constexpr int kCol = kRaw + kRaws * kRawBytes;    // float [stages][kKeys]: 2^(r - 127 - kKeyShift)
   static constexpr int kFactor = kCol + kStages * kKeys * 4;  // FP16 [kKeys][4]: of V
   // uint32 [stages][4]: V's references, whether there is more of it; K's 2^(R - 127 - kFactorShift), or 0; whether there
-  // is more of K, a byte for each warp that writes it
+  // is more of K, a byte for each warp that writes it, and the groups that are not there
   static constexpr int kInfo = kFactor + kKeys * 8;
   static constexpr int kBars = kInfo + kStages * 16;
   // uint64, one after the other:
@@ -76,7 +76,8 @@ struct Rows {
                        kFree = kFull + kStages, kScore = kFree + kStages, kProb = kScore + 4,
                        kOut = kProb + 4, kQuery = kOut + 2, kJoinIn = kQuery + 2,
                        kJoinOut = kJoinIn + 1, kDrain = kJoinOut + 1, kBarriers = kDrain + 1;
-  static constexpr int kWords = kBars + 8 * kBarriers;  // int [4]: tensor memory, last, next to arrive at
+  // int [4]: tensor memory, last, next to arrive at; groups of the raw tiles that are not there, a byte each
+  static constexpr int kWords = kBars + 8 * kBarriers;
   static constexpr int kScan = (kWords + 31) / 16 * 16;  // int [16], float [16], int [16]
   static constexpr int kEntries = kScan + 192;           // Planned [entries]
   static constexpr int shared_bytes(int entries) { return kEntries + 32 * entries + 1024; }
@@ -493,6 +494,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
     return ok;
   };
 
+  // The page of a key that was there when the tile was loaded (within the pool whatever the table says by now).
+  const auto page_of = [&](const Piece& p, int key) {
+    return max(kv_page(cache, p.slot, key >> cache.page_shift), 0);
+  };
+
   const auto load_role = [&]() {
     uint32_t count = 0;  // tiles so far
     bool ok = true;
@@ -507,16 +513,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
           break;
         }
         const int pos = p.key0 + i * kKeys + 16 * lane;
-        const bool mine = lane < 4 && pos < p.end;
-        const uint32_t groups = __popc(__ballot_sync(kAll, mine));
-        if (lane == 0) mbar_arrive_expect_tx(bar(L::kRawFull + r), groups * G::kBytes);
+        const bool asked = lane < 4 && pos < p.end;
+        const int page = asked ? kv_page(cache, p.slot, pos >> cache.page_shift) : 0;
+        const bool mine = asked && page >= 0;
+        const uint32_t groups = __ballot_sync(kAll, mine);
+        const uint32_t gone = __ballot_sync(kAll, asked && page < 0);
+        if (lane == 0) {
+          smem[L::kWords + 12 + r] = (uint8_t)gone;
+          mbar_arrive_expect_tx(bar(L::kRawFull + r), __popc(groups) * G::kBytes);
+        }
         __syncwarp();
         if (mine)
-          bulk_g2s_nohint(
-              smem_u32(smem + L::kRaw) + r * L::kRawBytes + lane * G::kBytes,
-              kv_group(cache, kv_page(cache, p.slot, pos >> cache.page_shift), a.layer,
-                       p.part.head, pos, G::kBytes),
-              G::kBytes, bar(L::kRawFull + r));
+          bulk_g2s_nohint(smem_u32(smem + L::kRaw) + r * L::kRawBytes + lane * G::kBytes,
+                          kv_group(cache, page, a.layer, p.part.head, pos, G::kBytes), G::kBytes,
+                          bar(L::kRawFull + r));
       }
     }
     // nothing in flight at the end, whatever the others did
@@ -539,6 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
         const uint8_t* raw = smem + L::kRaw + r * L::kRawBytes;
         const int left = p.end - (p.key0 + i * kKeys);  // keys of the tile
         const int before = p.lo - (p.key0 + i * kKeys);   // of which no row sees these
+        const uint32_t gone = smem[L::kWords + 12 + r];   // (groups)
+        const auto there = [&](int t) { return t < left && (gone >> (t >> 4) & 1u) == 0u; };
         // the scales of all keys, 32h + lane, of which every warp makes the same
         uint32_t sc[2];
 #pragma unroll
@@ -552,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
           int high = 0, low = 255;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (32 * h + lane >= left) continue;
+            if (!there(32 * h + lane)) continue;
 #pragma unroll
             for (int c = 0; c < CB; ++c) {
               high = max(high, byte_of(sc[h], c));
@@ -614,6 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
             *reinterpret_cast<float*>(smem + L::kInfo + 16 * st + 8) =
                 alike ? exp2f((float)(high - 127 - kFactorShift)) : 0.f;
           if (lane == 0) smem[L::kInfo + 16 * st + 12 + own] = rest;
+          if (lane == 0 && own == 0) smem[L::kInfo + 16 * st + 14] = (uint8_t)gone;
         } else {
           // A key that not every row sees must not push what the others see out of FP32: it raises the
           // reference to kSharedMost at most.
@@ -622,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int t = 32 * h + lane, key = p.key0 + i * kKeys + t;
-            most[h] = t < before || t >= left ? -1
+            most[h] = t < before || !there(t) ? -1
                       : key >= p.shared_lo && key < p.shared ? 254 : (int)kSharedMost - kRoom;
           }
 #pragma unroll
@@ -870,6 +883,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
           uint32_t sr[64];
           tmem_ld64(s_at, sr);
           const uint4 info = *reinterpret_cast<const uint4*>(smem + L::kInfo + 16 * st);
+          const uint32_t gone = info.w >> 16 & 0xFu;  // groups that nobody sees
+          const bool rare = (info.w & 0xFFFFFFu) != 0u;
           const bool whole = __all_sync(kAll, j0 >= row_lo && j0 + kKeys - 1 <= row_hi);
           const float* col = reinterpret_cast<const float*>(smem + L::kCol) + st * kKeys;
           float f = factor;
@@ -878,26 +893,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
             if (f == 0.f) f = 1.2e-38f;  // (-inf stays -inf)
           } else {
             f = shifted_factor(f);
-            if ((info.w & 0xFFFFu) == 0u) {
+            if (!rare) {
 #pragma unroll
               for (int n = 0; n < kKeys; ++n)
                 sr[n] = __float_as_uint(__uint_as_float(sr[n]) * col[n]);
-            } else {
-              // ---- what of the tile's K is not in it
-#pragma unroll 1
-              for (int t = 0; t < kKeys && j0 + t < p.end; ++t) {
-                const int key = j0 + t;
-                const uint8_t* grp =
-                    kv_group(cache, kv_page(cache, p.slot, key >> cache.page_shift), a.layer,
-                             p.part.head, key, G::kBytes);
-                const float rest =
-                    key_rest<D>(grp, key & 15, smem + L::kQ + x * L::kHalfBytes, row & 127);
-                const float sum = __uint_as_float(tmem_ld1(s_at + t));
-                tmem_st1(s_at + t, __float_as_uint(fmaf(sum, col[t], rest)));
-              }
-              tmem_st_wait();
-              tmem_ld64(s_at, sr);
             }
+          }
+          if (rare) {
+            // ---- what of the tile's K is not in it, key by key
+#pragma unroll 1
+            for (int t = 0; t < kKeys; ++t) {
+              const int key = j0 + t;
+              if (gone >> (t >> 4) & 1u) {
+                tmem_st1(s_at + t, 0xFF800000u);
+              } else if (!info.z && key < p.end) {
+                float sum = __uint_as_float(tmem_ld1(s_at + t)) * col[t];
+                if (info.w & 0xFFFFu)
+                  sum += key_rest<D>(kv_group(cache, page_of(p, key), a.layer, p.part.head, key, G::kBytes),
+                                     key & 15, smem + L::kQ + x * L::kHalfBytes, row & 127);
+                tmem_st1(s_at + t, __float_as_uint(sum));
+              }
+            }
+            tmem_st_wait();
+            tmem_ld64(s_at, sr);
           }
           if (!whole) {
 #pragma unroll
@@ -937,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
 #pragma unroll 1
             for (int n = 0; n < kKeys; ++n) {
               float v = __uint_as_float(tmem_ld1(s_at + n));
-              if (!info.z && (info.w & 0xFFFFu) == 0u) v *= col[n];
+              if (!info.z && !rare) v *= col[n];
               v = j0 + n < row_lo || j0 + n > row_hi ? -INFINITY : __fsub_rn(__fmul_rn(v, f), from);
               tmem_st1(s_at + n, __float_as_uint(v));
             }
@@ -968,9 +986,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
             if (!wait_outs(mine)) return;
 #pragma unroll 1
             for (int t = 0; t < kKeys && j0 + t < p.end; ++t) {
+              if (gone >> (t >> 4) & 1u) continue;
               const int key = j0 + t;
               const uint8_t* grp =
-                  kv_group(cache, kv_page(cache, p.slot, key >> cache.page_shift), a.layer,
+                  kv_group(cache, page_of(p, key), a.layer,
                            p.part.head, key, G::kBytes);
               const uint32_t weights = tmem_ld1(s_at + t / 2);
               const __half2 two = *reinterpret_cast<const __half2*>(&weights);

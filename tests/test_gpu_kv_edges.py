@@ -62,7 +62,7 @@ def check(c, got, window=0, flag=0, gone=()):
     assert (np.abs(out - want) <= tol).all(), np.argwhere(~(np.abs(out - want) <= tol))[:4]
     nothing = np.isneginf(want_lse)
     assert np.array_equal(np.isneginf(lse), nothing)
-    assert (np.abs(lse - want_lse) <= 1e-5 + 2.0 ** -20 * reach)[~nothing].all()
+    assert (np.abs(lse[~nothing] - want_lse[~nothing]) <= 1e-5 + 2.0 ** -20 * reach[~nothing]).all()
     assert c.cache.read_error_flag() == flag
 
 
@@ -211,3 +211,18 @@ def test_a_query_of_nan_that_sees_nothing(cuda_device, lens, news, bad):
     got, lse = c.run(q=q.to(cuda_device))
     assert torch.equal(got, want) and torch.equal(lse, want_lse)
     assert not got[:2].any() and torch.isneginf(lse[:2]).all()
+
+
+# ------------------------------------------------------------- pages that do not exist ---
+
+@pytest.mark.parametrize("news", [FEW, MANY])
+@pytest.mark.parametrize("D,P", [(64, 16), (64, 64), (128, 16), (128, 32), (256, 16), (256, 64)])
+@pytest.mark.parametrize("window", [0, 50])
+def test_keys_of_a_page_out_of_range_are_skipped(cuda_device, news, D, P, window):
+    c = Case(cuda_device, [200, 2500], news, 8, 2, D, P, seed=D + P)
+    for b, column, page in ((0, 160 // P, -1), (0, 64 // P, 1 << 20), (1, 2400 // P, len(c.pool)),
+                            (1, 32 // P, -5)):
+        c.table[c.slots[b], column] = page
+    c.cache.table.copy_(device(c.table, cuda_device))
+    gone = {-1, 1 << 20, len(c.pool), -5}
+    check(c, c.run(window=window), window=window, flag=wd.KV_FLAG_BAD_INDEX, gone=gone)
