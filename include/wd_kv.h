@@ -150,8 +150,8 @@ WD_API wd_status wd_kv_attention(const wd_kv_cache* cache, int layer, const void
  * what dst[i] held before is released.  src[i] = -1 (or src NULL) frees dst[i];
  * src[i] = dst[i] leaves it as it is.  New pages come from those free before the
  * call, lowest first, in order of i; a request that they do not suffice for, a
- * slot out of range or a dst that appears earlier in the call is refused
- * (ok[i] = 0, dst[i] unchanged).  `ok` int32 [n] (may be NULL); n <= slots. */
+ * slot out of range, a last page to copy that is out of range, or a dst that appears
+ * earlier in the call is refused (ok[i] = 0, dst[i] unchanged).  `ok` int32 [n] (may be NULL); n <= slots. */
 WD_API wd_status wd_kv_fork(const wd_kv_cache* cache, const int32_t* src, const int32_t* dst,
                             int n, int32_t* ok, wd_stream_t stream);
 

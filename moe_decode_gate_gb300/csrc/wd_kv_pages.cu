@@ -208,7 +208,11 @@ __global__ void __launch_bounds__(kPlan)
         } else {
           whole = len >> v.page_shift;
           copy = (len & (v.page_size - 1)) != 0;
-          if (copy) from = max(kv_page(v, s, whole), 0);
+          if (copy) from = kv_page(v, s, whole);
+          if (copy && from < 0) {  // refused: there is nothing to copy
+            copy = false;
+            whole = -1;
+          }
         }
       } else {
         atomicOr(v.flag, WD_KV_FLAG_BAD_INDEX);
@@ -382,7 +386,11 @@ __global__ void __launch_bounds__(kPlan)
       } else {
         whole = len >> v.page_shift;
         copy = (len & (v.page_size - 1)) != 0;
-        if (copy) from = max(kv_page(v, s, whole), 0);
+        if (copy) from = kv_page(v, s, whole);
+        if (copy && from < 0) {  // refused: there is nothing to copy
+          copy = false;
+          whole = -1;
+        }
       }
     } else {
       atomicOr(v.flag, WD_KV_FLAG_BAD_INDEX);

@@ -226,3 +226,25 @@ def test_keys_of_a_page_out_of_range_are_skipped(cuda_device, news, D, P, window
     c.cache.table.copy_(device(c.table, cuda_device))
     gone = {-1, 1 << 20, len(c.pool), -5}
     check(c, c.run(window=window), window=window, flag=wd.KV_FLAG_BAD_INDEX, gone=gone)
+
+
+@pytest.mark.parametrize("pages", [50, 20000])
+def test_a_fork_whose_last_page_is_out_of_range_is_refused(cuda_device, pages):
+    cache = wd.KVCache(pages, 6, 8, 1, 1, 64, 16, device=cuda_device)
+
+    def ints(*v):
+        return torch.tensor(v, dtype=torch.int32, device=cuda_device)
+
+    assert cache.reserve(ints(20, 40, 33), ints(0, 1, 2)).tolist() == [1, 1, 1]
+    cache.pool.copy_(torch.randint(0, 256, cache.pool.shape, device=cuda_device).to(torch.uint8))
+    cache.table[1, 2] = pages + 7
+    table, refs, lengths = cache.table.clone(), cache.refs.clone(), cache.lengths.clone()
+    assert cache.fork(ints(1), ints(2)).tolist() == [0]
+    assert cache.read_error_flag() == wd.KV_FLAG_BAD_INDEX
+    for now, before in ((cache.table, table), (cache.refs, refs), (cache.lengths, lengths)):
+        assert torch.equal(now, before)
+    # the others of the call are served, and the refused one takes no page
+    assert cache.fork(ints(1, 0, 2), ints(3, 4, 5)).tolist() == [0, 1, 1]
+    assert cache.read_error_flag() == wd.KV_FLAG_BAD_INDEX
+    assert cache.table[4].tolist() == [0, 8] + [-1] * 6 and cache.table[5, :3].tolist() == [5, 6, 9]
+    assert cache.lengths.tolist() == [20, 40, 33, 0, 20, 33]
