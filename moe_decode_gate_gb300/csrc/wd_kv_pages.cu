@@ -139,7 +139,9 @@ __global__ void __launch_bounds__(kPlan)
       begin[i] = before + excl;
       need[i] = pages;
     }
-    before = min(before + total, 1 << 30);  // (a call may ask for more than an int counts)
+    // A call may ask for more than an int counts: kPlan requests of 2^20 pages are 2^30, and from there on
+    // none is served any more.
+    before = total > (1 << 30) - before ? 1 << 30 : before + total;
   }
   if (threadIdx.x == 0) wanted_sh = before;
   __syncthreads();
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(kPlan)
     const int lane = threadIdx.x & 31;
     const int s = seqs ? seqs[i] : i;
     const int pages = need[i];
-    const bool served = pages == 0 || (pages > 0 && begin[i] + pages <= found);
+    const bool served = pages == 0 || (pages > 0 && begin[i] <= found - pages);
     if (served) {
       const int len = kv_length(v, s);
       const int have = (len + v.page_size - 1) >> v.page_shift;
