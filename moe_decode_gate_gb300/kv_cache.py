@@ -37,6 +37,7 @@ class KVCache:
     ``pool`` uint8 [num_pages, layers, kv_heads, page_size / 16, group bytes], ``table`` int32
     [slots, columns] (the pages of each slot's sequence, -1 beyond), ``lengths`` int32 [slots] and
     ``refs`` int32 [num_pages] are the cache, on the device; include/wd_kv.h has their layout.
+    The cache's device has to be the current one.
     Every call is asynchronous on the current stream (or ``stream``); calls on different streams
     must be ordered by the caller, as they share the workspace.  A call on ``stream`` keeps the memory of what
     it reads and writes until it is done; that the inputs are there when it starts, and that it is done
@@ -111,9 +112,14 @@ class KVCache:
 
     def _stream(self, stream):
         """The raw handle of ``stream``, or of the current stream of the cache's device (looked up
-        without the Stream object that torch.cuda.current_stream() makes: 0.1 against 3 us)."""
+        without the Stream object that torch.cuda.current_stream() makes: 0.1 against 3 us).  The kernels
+        are launched on the current device, which has to be the cache's."""
+        if torch._C._cuda_getDevice() != self._index:
+            raise ValueError(f"the current device must be the cache's, {self.device}")
         if stream is None:
             return torch._C._cuda_getCurrentRawStream(self._index)
+        if stream.device != self.device:
+            raise ValueError(f"stream must be one of {self.device}")
         return stream.cuda_stream
 
     def _output(self, shape, dtype, stream):

@@ -64,15 +64,17 @@ def cache(monkeypatch):
     fake = types.SimpleNamespace(
         empty=empty, int32=torch.int32, float32=torch.float32,
         cuda=types.SimpleNamespace(stream=on, current_stream=lambda device=None: now[-1]),
-        _C=types.SimpleNamespace(_cuda_getCurrentRawStream=lambda index: 3))
+        _C=types.SimpleNamespace(_cuda_getCurrentRawStream=lambda index: 3,
+                                 _cuda_getDevice=lambda: 0))
     monkeypatch.setattr(kv_cache, "torch", fake)
     c = wd.KVCache.__new__(wd.KVCache)
     c.device, c._index, c._ref, c._scale = "gpu", 0, None, 0.1
     c.kv_heads, c.head_dim, c.num_pages, c.slots = 2, 64, 8, 4
     for name in ("pool", "table", "lengths", "refs", "workspace"):
         setattr(c, name, Note())
+    c.launched = []
     c._lib = types.SimpleNamespace(**{
-        "wd_kv_" + name: lambda *a: 0
+        "wd_kv_" + name: lambda *a: c.launched.append(a) or 0
         for name in ("reserve", "append", "attention", "fork", "free", "compact")})
     c.made = made
     return c
@@ -118,6 +120,29 @@ def test_nothing_is_noted_on_the_current_stream(cache):
     cache.compact()
     assert [x.made_on for x in cache.made] == ["current", "current"]
     assert not any(x.used_on for x in (t, cache.pool, *cache.made))
+
+
+@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("wrong", ["current device", "stream"])
+def test_another_device_is_refused(cache, call, wrong):
+    # the library launches on the current device, with pointers of the cache's
+    side = Side()
+    if wrong == "stream":
+        side.device = "another gpu"
+    else:
+        kv_cache.torch._C._cuda_getDevice = lambda: 1
+
+    def tensor(kind):
+        shape, dtype = {"i": ((4,), torch.int32), "start": ((5,), torch.int32),
+                        "kv": ((4, 2, 64), torch.bfloat16), "q": ((4, 6, 64), torch.bfloat16)}[kind]
+        return Note(shape, dtype)
+
+    with pytest.raises(ValueError):
+        call(cache, tensor, side)
+    if wrong != "stream":
+        with pytest.raises(ValueError):
+            call(cache, tensor, None)
+    assert not cache.launched
 
 
 @pytest.mark.gpu
