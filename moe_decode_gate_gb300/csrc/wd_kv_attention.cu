@@ -3,8 +3,8 @@
 // Work.  An item is (entry, tile of 8 * NT query rows, key head); the rows of a tile are the
 // heads that share the key head and, behind them, further new tokens.  An item is cut into pieces
 // of q steps of 32 keys, a warp to a piece, and the pieces of the call, in order, are dealt out
-// to the warps of as many CTAs as fit the GPU (eight pieces to a CTA, in several passes if they
-// are many).  The lengths are known to the device alone, so every CTA derives q and the whole
+// to the warps of as many CTAs as fit the GPU (twelve or eight pieces to a CTA, in several passes if
+// they are many).  The lengths are known to the device alone, so every CTA derives q and the whole
 // division from them; a captured graph can be replayed while the sequences grow.  A warp that
 // has all of an item writes its output; the pieces of one CTA meet in shared memory; and where an
 // item has pieces in several CTAs, each leaves a partial result (maximum, sum, output) in
