@@ -40,11 +40,22 @@ class MoEDecodeLayer:
         return sum(t.numel() for t in (self.gate_up, self.gate_up_scale, self.down, self.down_scale))
 
     def __call__(self, x, topk_ids, topk_w, out=None, stream=None):
-        """x bf16 [B, H], topk_ids int32 [B, K], topk_w fp32 [B, K] -> out bf16 [B, H]."""
+        """x bf16 [B, H], topk_ids int32 [B, K], topk_w fp32 [B, K] -> out bf16 [B, H].
+
+        A call on ``stream`` keeps the memory of what it reads and writes until it is done; an ``out`` of
+        its own is that stream's memory."""
         if x.shape[0] > self.max_batch:
             raise ValueError(f"batch {x.shape[0]} exceeds max_batch {self.max_batch}")
-        if out is None:
+        if out is None and stream is None:
             out = torch.empty_like(x)
+        elif out is None:
+            with torch.cuda.stream(stream):
+                out = torch.empty_like(x)
         wd_moe_decode(x, topk_ids, topk_w, self.gate_up, self.gate_up_scale, self.down,
                       self.down_scale, out, self.workspace, stream=stream)
+        if stream is not None:
+            for t in (x, topk_ids, topk_w, out, self.gate_up, self.gate_up_scale, self.down,
+                      self.down_scale, self.workspace):
+                t.record_stream(stream)
+            out.record_stream(torch.cuda.current_stream(self.device))
         return out
