@@ -94,8 +94,8 @@ WD_API size_t wd_kv_page_bytes(int layers, int kv_heads, int head_dim, int page_
  * the other pointers are not looked at); 0 for invalid dimensions. */
 WD_API size_t wd_kv_workspace_size(const wd_kv_cache* cache);
 
-/* Zero the error flag and the counters of the workspace.  Call once after
- * allocating it. */
+/* Set up the error flag, the counters and the constants of the workspace.  Call once
+ * after allocating it. */
 WD_API wd_status wd_kv_workspace_init(const wd_kv_cache* cache, wd_stream_t stream);
 
 /* Copy the error flag to `*flag` and clear it; SYNCHRONISES `stream`.  Returns

@@ -125,10 +125,12 @@ __device__ __forceinline__ uint8_t* kv_group(const KvView& v, int page, int laye
 constexpr int kKvSms = 152;           // what the attention's grid is made for
 constexpr int kKvMaxUnits = 8 * kKvSms;  // units of 8 query rows that there is room for
 constexpr int kKvMaxRowUnits = 2 * kKvSms;  // of 256 query rows
+constexpr int kKvNoneBytes = 2 * KvGroup<256>::kBytes;
 constexpr int kKvChunkPages = 4096;   // pages that one CTA counts in wd_kv_compact
 
 struct KvScratch {
   uint32_t* counters;  // [kKvMaxUnits], zero between calls
+  uint8_t* none;       // [kKvNoneBytes], 0xFF: the groups of a page that is not there
   float* partial;      // [2 * kKvMaxUnits][8][head_dim + 2] or [kKvMaxRowUnits][256][head_dim + 2]
   int32_t* list_a;     // [num_pages]
   int32_t* list_b;     // [num_pages]
@@ -186,6 +188,7 @@ struct KvAttentionArgs {
   int window, max_q;
   bool half;  // FP16 (else BF16)
   uint32_t* counters;
+  const uint8_t* none;
   float* partial;
 };
 cudaError_t launch_kv_attention(const KvAttentionArgs& a, cudaStream_t s);

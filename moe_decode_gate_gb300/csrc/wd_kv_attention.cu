@@ -526,25 +526,29 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
       page0 = row[pos >> cache.page_shift];
       page1 = cache.page_size < kStep && pos + 16 < span.end ? row[(pos + 16) >> cache.page_shift] : 0;
     };
-    // (false, and the flag, if a page is out of range: its groups are not copied)
+    // (a page out of range: the flag, and NaN from the workspace in its place)
+    const auto group_at = [&](int page, int pos) -> const uint8_t* {
+      if (kv_page_there(cache, page)) return kv_group(cache, page, a.layer, part.head, pos, G::kBytes);
+      atomicOr(cache.flag, WD_KV_FLAG_BAD_INDEX);
+      return a.none;
+    };
     const auto plan = [&](int i0) {
       const int pos = (span.first + from + i0 + lane) * kStep;
-      bool there = true;
       src1 = nullptr;
-      if (i0 + lane < steps) {
-        there = kv_page_there(cache, page0) && kv_page_there(cache, page1);
-        bytes0 = 0;
-        if (kv_page_there(cache, page0)) {
-          src0 = kv_group(cache, page0, a.layer, part.head, pos, G::kBytes);
-          // the step lies within a page, its groups side by side, or its groups lie in two pages
-          bytes0 = cache.page_size >= kStep && pos + 16 < span.end ? 2 * G::kBytes : G::kBytes;
-        }
-        if (cache.page_size < kStep && pos + 16 < span.end && kv_page_there(cache, page1))
-          src1 = kv_group(cache, page1, a.layer, part.head, pos + 16, G::kBytes);
+      if (i0 + lane >= steps) return;
+      src0 = group_at(page0, pos);
+      bytes0 = G::kBytes;
+      if (pos + 16 < span.end) {
+        if (cache.page_size >= kStep)  // the step lies within a page, its groups side by side
+          bytes0 = 2 * G::kBytes;
+        else
+          src1 = group_at(page1, pos + 16);
       }
-      if (__all_sync(kAll, there)) return true;
-      if (lane == 0) atomicOr(cache.flag, WD_KV_FLAG_BAD_INDEX);
-      return false;
+    };
+    const auto gone = [&](int key) {  // is the page of a key out of range?
+      return key < span.end &&
+             !kv_page_there(cache, cache.table[(long long)entry.slot * cache.columns +
+                                               (key >> cache.page_shift)]);
     };
     look_up(0);
 
@@ -568,10 +572,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
     const auto issue = [&](int to_stage) {
       const uint32_t to = ring_at + to_stage * L::kStageBytes, full = bar + 8 * to_stage;
       mbar_arrive_expect_tx(full, bytes0 + (src1 ? G::kBytes : 0));
-      if (bytes0) bulk_g2s_nohint(to, src0, bytes0, full);
+      bulk_g2s_nohint(to, src0, bytes0, full);
       if (src1) bulk_g2s_nohint(to + G::kBytes, src1, G::kBytes, full);
     };
-    const bool pages_there = plan(0);
+    plan(0);
     if (lane < kStages && lane < steps) issue((stage + lane) % kStages);
     __syncwarp();
 
@@ -647,11 +651,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
     seen_hi = min(seen_hi, __shfl_xor_sync(kAll, seen_hi, 1));
     seen_hi = min(seen_hi, __shfl_xor_sync(kAll, seen_hi, 2));
 
-    // Once a page out of range has been looked up, no key counts as seen by all any more, and seen_hi has
-    // the groups of the step that are not there (bits 0 and 16).
-    constexpr int kNone = 0x7FFFFFFF;
-    if (!pages_there) seen_lo = kNone;
-
     float o[CB][2][NT][4];
     float m[NT][2], l[NT][2];
     uint32_t ref[NW];  // the largest V scale met, a byte to a block, at least 16
@@ -677,11 +676,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
 
       // ---- the scales of key step_at + lane, for the lanes whose products want them
       bool inside = step_at + lane < span.end;
-      if (seen_lo == kNone) {
-        inside = inside && kv_page_there(cache, cache.table[(long long)entry.slot * cache.columns +
-                                                            ((step_at + lane) >> cache.page_shift)]);
-        seen_hi = (int)(~__ballot_sync(kAll, inside) & 0x10001u);
-      }
       const uint8_t* scale_at = ring + stage * L::kStageBytes + (lane >> 4) * G::kBytes + (lane & 15) * CB;
       const Words<NW> kt = lds_scales<CB>(scale_at + G::kKScale);
       Words<NW> vt = lds_scales<CB>(scale_at + G::kVScale);
@@ -747,9 +741,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
 
         // ---- does anything change: a larger logit, a V scale out of range?
         const bool whole = j0 >= seen_lo && j0 + 16 * kU - 1 <= seen_hi;
-        const auto there = [&](int u) {
-          return seen_lo != kNone || ((unsigned)seen_hi >> (16 * (u0 + u)) & 1u) == 0u;
-        };
         float top[NT][2];
         bool grow = odd;
 #pragma unroll
@@ -764,13 +755,20 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
                 float& x = s[u][nt][2 * h + e];
                 if (!whole) {
                   const int row = 8 * nt + 2 * tq + e, key = j0 + 16 * u + 8 * h + g;
-                  if (key < lo_sh[row] || key > hi_sh[row] || !there(u)) x = -INFINITY;
+                  if (key < lo_sh[row] || key > hi_sh[row]) x = -INFINITY;
                 }
                 t = fmaxf(t, x);
               }
             top[nt][e] = t * factor[nt][e];
             grow |= top[nt][e] > m[nt][e] + kSlack;
           }
+        const auto hide = [&](int u) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[u][nt][e] = -INFINITY;
+        };
+        if (kU == 1 && u0 > 0 && slow && gone(j0)) hide(0);
         if (__any_sync(kAll, grow)) {
           if (__any_sync(kAll, !landed)) {
             dead = true;
@@ -807,6 +805,18 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
             // that not every row sees must not push what the others see out of FP32
             const int key = step_at + lane;
             inside = inside && key >= lo_sh[0];
+            // Scales that are all NaN may be those of a page that is not there: nobody sees its keys.
+            uint32_t nan = CB == 2 ? vt.v[0] | 0xFFFF0000u : vt.v[0];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) nan &= vt.v[w];
+            bool hidden = false;
+            if (__any_sync(kAll, nan == kAll)) {
+              inside = inside && !gone(key);
+#pragma unroll
+              for (int u = 0; u < kU; ++u)
+                if (gone(j0 + 16 * u)) hide(u);
+              hidden = kU == 1 && gone(step_at + 16);  // (its turn comes)
+            }
             const uint32_t limit = !inside ? 0u : key >= seen_lo && key <= seen_hi ? 254u : kSharedMost;
 #pragma unroll
             for (int c = 0; c < CB; ++c) {
@@ -826,7 +836,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
               }
               bad |= inside && (mine_c > most || mine_c + 15u < most);
             }
-            slow = __any_sync(kAll, bad);
+            slow = __any_sync(kAll, bad) || hidden;
             __syncwarp();
             put_v_scales();
             odd = false;
@@ -856,7 +866,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
         for (int u = 0; u < kU; ++u) {
           if (!slow)
             values<D, NT>(buf + u * G::kBytes, v_scales + (u0 + u) * 8 * CB * 4, p[u], lane, o);
-          else if (there(u))
+          else if (!gone(j0 + 16 * u))
             values_singly<D, NT>(buf + u * G::kBytes, p[u], ref, j0 + 16 * u, span.end, lo_sh, hi_sh,
                                  lane, o);
         }
@@ -873,7 +883,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
       const int next = i + kStages;
       if ((next & 31) == 0) {
         look_up(next);
-        if (!plan(next)) seen_lo = kNone;
+        plan(next);
       }
       if (lane == (next & 31) && next < steps) issue(stage);
       if (++stage == kStages) {
@@ -900,7 +910,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtasPer
     bool large = false;
 #pragma unroll
     for (int w = 0; w < NW; ++w) large |= __vcmpgeu4(ref[w], 0x01010101u * kSharedMost) != 0u;
-    if (large) {
+    if (__builtin_expect(large, 0)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -65,10 +65,11 @@ struct Rows {
   static constexpr int kK = kQ + 2 * kHalfBytes;
   static constexpr int kV = kK + kStages * kTileBytes;
   static constexpr int kRaw = kV + kStages * kTileBytes;
-  static constexpr int kCol = kRaw + kRaws * kRawBytes;    // float [stages][kKeys]: 2^(r - 127 - kKeyShift)
+  // float [stages][kKeys]: 2^(r - 127 - kKeyShift) of K, negative if there is more of the key than the tile
+  // has, -inf if it is not there
+  static constexpr int kCol = kRaw + kRaws * kRawBytes;
   static constexpr int kFactor = kCol + kStages * kKeys * 4;  // FP16 [kKeys][4]: of V
-  // uint32 [stages][4]: V's references, whether there is more of it; K's 2^(R - 127 - kFactorShift), or 0; whether there
-  // is more of K, a byte for each warp that writes it, and the groups that are not there
+  // uint32 [stages][4]: V's references, whether there is more of it; K's 2^(R - 127 - kFactorShift), or 0
   static constexpr int kInfo = kFactor + kKeys * 8;
   static constexpr int kBars = kInfo + kStages * 16;
   // uint64, one after the other:
@@ -223,21 +224,41 @@ __device__ __forceinline__ int tile_at(int rows, int row, int chunk) {
   return (chunk >> 3) * rows * 128 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
-// FP16 2^-d, 0 from 25 on (a subnormal from 15 on, exact); d >= 0.
+// FP16 2^-d (a subnormal from 15 on, exact), 0 from 24 on, where 0.5 x 2^-d, of E2M1, is no FP16 number; d >= 0.
 __device__ __forceinline__ uint32_t half_power(int d) {
-  return d < 15 ? (uint32_t)(15 - d) << 10 : d < 25 ? 1u << (24 - d) : 0u;
+  return d < 15 ? (uint32_t)(15 - d) << 10 : d < 24 ? 1u << (24 - d) : 0u;
 }
 
 // Whether V that is 2^-d of the reference is in the tile: else it is added on its own.
 __device__ __forceinline__ bool in_tile(int d) { return (unsigned)d <= 22u; }
 
-// Whether a block of K that is 2^-d of its token's largest is in the tile: E2M1's 0.5 x 2^-d is an FP16 number.
+// Whether a block of K that is 2^-d of its token's largest is in the tile (as half_power has it).
 __device__ __forceinline__ bool key_in_tile(int d) { return d <= 23; }
 
-// What of a key's sum with a query row is not in its tile, times 2^-kKeyShift.  grp: the key's group, of which it is token t; q: the
-// tile of the row's half, in shared memory.
+// Where the keys of one head and layer of a sequence lie.
+struct Keys {
+  const int32_t* row;   // of the table
+  const uint8_t* base;  // the head in page 0
+  long long page_bytes;
+  int page_shift, num_pages;
+};
+__device__ __forceinline__ Keys keys_of(const KvView& c, int slot, int layer, int head) {
+  return Keys{c.table + (long long)slot * c.columns,
+              c.pool + layer * c.layer_bytes + (long long)head * c.head_bytes, c.page_bytes,
+              c.page_shift, c.num_pages};
+}
+// The group of a key whose page is there (within the pool whatever the table says by now).
 template <int D>
-__device__ __noinline__ float key_rest(const uint8_t* grp, int t, const uint8_t* q, int row) {
+__device__ __forceinline__ const uint8_t* group_of(const Keys& k, int key) {
+  const int page = k.row[key >> k.page_shift];
+  return k.base + (page >= 0 && page < k.num_pages ? page : 0) * k.page_bytes +
+         ((key & ((1 << k.page_shift) - 1)) >> 4) * KvGroup<D>::kBytes;
+}
+
+// What of a key's sum with a query row is not in its tile, times 2^-kKeyShift.  grp: the key's group, of which it
+// is token t; q: the tile of the row's half, in shared memory.
+template <int D>
+__device__ __forceinline__ float key_rest(const uint8_t* grp, int t, const uint8_t* q, int row) {
   using G = KvGroup<D>;
   int top = 0;
   float sum = 0.f;
@@ -269,6 +290,39 @@ __device__ __noinline__ float key_rest(const uint8_t* grp, int t, const uint8_t*
       if (pass == 1 && any != 0u) sum += part * exp2f((float)(s - 127 - kKeyShift));
     }
   return sum;
+}
+
+// Whether a tile has keys of which there is more, or that are not there.
+__device__ __forceinline__ bool rare_tile(const float* col, int lane) {
+  return __any_sync(kAll, signbit(col[lane]) || signbit(col[32 + lane]));
+}
+// The scores of such a tile times `col`, in place, key by key.
+template <int D>
+__device__ __noinline__ void rare_scores(const Keys k, uint32_t s_at, const float* col, int j0, int end,
+                                         const uint8_t* q, int row) {
+#pragma unroll 1
+  for (int t = 0; t < kKeys && j0 + t < end; ++t) {
+    const float by = col[t];
+    float sum = -INFINITY;
+    if (by != -INFINITY) {
+      sum = __uint_as_float(tmem_ld1(s_at + t)) * fabsf(by);
+      if (by < 0.f) sum += key_rest<D>(group_of<D>(k, j0 + t), (j0 + t) & 15, q, row);
+    }
+    tmem_st1(s_at + t, __float_as_uint(sum));
+  }
+  tmem_st_wait();
+}
+// The tile's logits, in place, less the reference `from`: -inf but for keys lo to hi of the tile.
+__device__ __noinline__ void steep_scores(uint32_t s_at, const float* col, float factor, float from, int lo,
+                                          int hi) {
+#pragma unroll 1
+  for (int t = 0; t < kKeys; ++t) {
+    float v = __uint_as_float(tmem_ld1(s_at + t));
+    if (col) v *= col[t];
+    v = t < lo || t > hi ? -INFINITY : __fsub_rn(__fmul_rn(v, factor), from);
+    tmem_st1(s_at + t, __float_as_uint(v));
+  }
+  tmem_st_wait();
 }
 
 // Two FP32 values in one register pair: one instruction for both.
@@ -494,11 +548,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
     return ok;
   };
 
-  // The page of a key that was there when the tile was loaded (within the pool whatever the table says by now).
-  const auto page_of = [&](const Piece& p, int key) {
-    return max(kv_page(cache, p.slot, key >> cache.page_shift), 0);
-  };
-
   const auto load_role = [&]() {
     uint32_t count = 0;  // tiles so far
     bool ok = true;
@@ -548,9 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
         if (!wait(L::kRawFull + r, (count / kRaws) & 1)) return;
         const uint8_t* raw = smem + L::kRaw + r * L::kRawBytes;
         const int left = p.end - (p.key0 + i * kKeys);  // keys of the tile
-        const int before = p.lo - (p.key0 + i * kKeys);   // of which no row sees these
-        const uint32_t gone = smem[L::kWords + 12 + r];   // (groups)
-        const auto there = [&](int t) { return t < left && (gone >> (t >> 4) & 1u) == 0u; };
+        const uint32_t gone = smem[L::kWords + 12 + r];  // groups that are not there
         // the scales of all keys, 32h + lane, of which every warp makes the same
         uint32_t sc[2];
 #pragma unroll
@@ -558,13 +605,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
           const int t = 32 * h + lane;
           sc[h] = lds_scales<CB>(raw + (t >> 4) * G::kBytes +
                                  (values ? G::kVScale : G::kKScale) + (t & 15) * CB).v[0];
+          // (nobody sees these: any number of the others' size)
+          if (gone != 0u && (gone >> (t >> 4) & 1u)) sc[h] = values ? ref : 0x7F7F7F7Fu;
         }
         if (!values) {
           // scales that are alike in all of the tile become one factor of its logits
           int high = 0, low = 255;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (!there(32 * h + lane)) continue;
+            if (32 * h + lane >= left) continue;
 #pragma unroll
             for (int c = 0; c < CB; ++c) {
               high = max(high, byte_of(sc[h], c));
@@ -573,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
           }
           high = __reduce_max_sync(kAll, high);
           low = __reduce_min_sync(kAll, low);
-          const bool alike =
+          const bool alike = gone == 0u &&
               high - low <= 22 && high >= 127 - kAlike && high <= 127 + kAlike;
           const int t = 32 * own + lane;
           const uint32_t mine = own ? sc[1] : sc[0];
@@ -596,14 +645,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
 #pragma unroll
             for (int c = 0; c < CB; ++c)
               rest |= t < left && (any[c] & 0x77777777u) && !key_in_tile(top - byte_of(mine, c));
-            rest = __any_sync(kAll, rest);
           }
           uint32_t f[CB];
 #pragma unroll
-          for (int c = 0; c < CB; ++c) {
-            const int d = max(0, top - byte_of(mine, c));
-            f[c] = key_in_tile(d) ? half_power(d) * 0x10001u : 0u;
-          }
+          for (int c = 0; c < CB; ++c) f[c] = half_power(max(0, top - byte_of(mine, c))) * 0x10001u;
           if (count >= kStages && !wait(L::kFree + st, (count / kStages - 1) & 1)) return;
           uint8_t* to = smem + L::kK + st * L::kTileBytes;
 #pragma unroll 1
@@ -619,33 +664,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
               *reinterpret_cast<uint4*>(to + tile_at(kKeys, t, 4 * c + c4)) = v;
             }
           }
-          reinterpret_cast<float*>(smem + L::kCol)[st * kKeys + t] =
-              t >= left ? 0.f : top == 255 ? __uint_as_float(0x7FC00000u)
-                                           : exp2f((float)(top - 127 - kKeyShift));
+          float col = t >= left ? 0.f : top == 255 ? __uint_as_float(0x7FC00000u)
+                                                   : exp2f((float)(top - 127 - kKeyShift));
+          if (rest) col = -col;
+          if (gone != 0u && (gone >> (t >> 4) & 1u)) col = -INFINITY;
+          reinterpret_cast<float*>(smem + L::kCol)[st * kKeys + t] = col;
           if (own == 0 && lane == 0)
             *reinterpret_cast<float*>(smem + L::kInfo + 16 * st + 8) =
                 alike ? exp2f((float)(high - 127 - kFactorShift)) : 0.f;
-          if (lane == 0) smem[L::kInfo + 16 * st + 12 + own] = rest;
-          if (lane == 0 && own == 0) smem[L::kInfo + 16 * st + 14] = (uint8_t)gone;
         } else {
-          // A key that not every row sees must not push what the others see out of FP32: it raises the
-          // reference to kSharedMost at most.
-          bool above = false, other = false;
-          int most[2];
+          // Mostly all scales are within 2^15 below the references.
+          bool odd = false, other = false;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int t = 32 * h + lane, key = p.key0 + i * kKeys + t;
-            most[h] = t < before || !there(t) ? -1
-                      : key >= p.shared_lo && key < p.shared ? 254 : (int)kSharedMost - kRoom;
+            const uint32_t d0 = ((ref & 0x00FF00FFu) | 0x80008000u) - (sc[h] & 0x00FF00FFu);
+            const uint32_t d1 = ((ref >> 8 & 0x00FF00FFu) | 0x80008000u) - (sc[h] >> 8 & 0x00FF00FFu);
+            odd |= 32 * h + lane < left && ((d0 | d1) & 0x7FF07FF0u) != 0u;
           }
+          if (__any_sync(kAll, odd)) {
+            // What no row sees takes part in nothing, and a key that not every row sees must not push what the
+            // others see out of FP32: it raises the reference to kSharedMost at most.
+            int most[2];
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int c = 0; c < CB; ++c) {
-              const int s = byte_of(sc[h], c);
-              above |= s != 255 && min(s, most[h]) > byte_of(ref, c);
+            for (int h = 0; h < 2; ++h) {
+              const int t = 32 * h + lane, key = p.key0 + i * kKeys + t;
+              most[h] = key < p.lo || t >= left ? -1
+                        : key >= p.shared_lo && key < p.shared ? 254 : (int)kSharedMost - kRoom;
             }
-          if (__any_sync(kAll, above)) {
 #pragma unroll
             for (int c = 0; c < CB; ++c) {
               int s = 0;
@@ -658,15 +703,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
               if (s > byte_of(ref, c))
                 ref = (ref & ~(0xFFu << (8 * c))) | (uint32_t)min(s + kRoom, 254) << (8 * c);
             }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int c = 0; c < CB; ++c) {
+                const int s = byte_of(sc[h], c);
+                other |= most[h] >= 0 && (s == 255 || !in_tile(byte_of(ref, c) - s));
+              }
+            other = __any_sync(kAll, other);
           }
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int c = 0; c < CB; ++c) {
-              const int s = byte_of(sc[h], c);
-              other |= most[h] >= 0 && (s == 255 || !in_tile(byte_of(ref, c) - s));
-            }
-          other = __any_sync(kAll, other);
           // the factors of the warp's 16 keys, a lane to half of a key's
           uint8_t* factors = smem + L::kFactor + own * 16 * 8;
           {
@@ -883,8 +928,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
           uint32_t sr[64];
           tmem_ld64(s_at, sr);
           const uint4 info = *reinterpret_cast<const uint4*>(smem + L::kInfo + 16 * st);
-          const uint32_t gone = info.w >> 16 & 0xFu;  // groups that nobody sees
-          const bool rare = (info.w & 0xFFFFFFu) != 0u;
           const bool whole = __all_sync(kAll, j0 >= row_lo && j0 + kKeys - 1 <= row_hi);
           const float* col = reinterpret_cast<const float*>(smem + L::kCol) + st * kKeys;
           float f = factor;
@@ -893,29 +936,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
             if (f == 0.f) f = 1.2e-38f;  // (-inf stays -inf)
           } else {
             f = shifted_factor(f);
-            if (!rare) {
+            if (rare_tile(col, lane)) {
+              rare_scores<D>(keys_of(cache, p.slot, a.layer, p.part.head), s_at, col, j0, p.end,
+                             smem + L::kQ + x * L::kHalfBytes, row & 127);
+              tmem_ld64(s_at, sr);
+            } else {
 #pragma unroll
               for (int n = 0; n < kKeys; ++n)
                 sr[n] = __float_as_uint(__uint_as_float(sr[n]) * col[n]);
             }
-          }
-          if (rare) {
-            // ---- what of the tile's K is not in it, key by key
-#pragma unroll 1
-            for (int t = 0; t < kKeys; ++t) {
-              const int key = j0 + t;
-              if (gone >> (t >> 4) & 1u) {
-                tmem_st1(s_at + t, 0xFF800000u);
-              } else if (!info.z && key < p.end) {
-                float sum = __uint_as_float(tmem_ld1(s_at + t)) * col[t];
-                if (info.w & 0xFFFFu)
-                  sum += key_rest<D>(kv_group(cache, page_of(p, key), a.layer, p.part.head, key, G::kBytes),
-                                     key & 15, smem + L::kQ + x * L::kHalfBytes, row & 127);
-                tmem_st1(s_at + t, __float_as_uint(sum));
-              }
-            }
-            tmem_st_wait();
-            tmem_ld64(s_at, sr);
           }
           if (!whole) {
 #pragma unroll
@@ -951,15 +980,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
           ref = info.x;
           float z = m == -INFINITY ? 0.f : kBias - m;
           if (steep) {
-            const float from = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
-            for (int n = 0; n < kKeys; ++n) {
-              float v = __uint_as_float(tmem_ld1(s_at + n));
-              if (!info.z && !rare) v *= col[n];
-              v = j0 + n < row_lo || j0 + n > row_hi ? -INFINITY : __fsub_rn(__fmul_rn(v, f), from);
-              tmem_st1(s_at + n, __float_as_uint(v));
-            }
-            tmem_st_wait();
+            steep_scores(s_at, info.z || rare_tile(col, lane) ? nullptr : col, f, m == -INFINITY ? 0.f : m,
+                         row_lo - j0, row_hi - j0);
             tmem_ld64(s_at, sr);
             f = 1.f;
             z = kBias;
@@ -984,13 +1006,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows(const KvAttenti
           if (info.y) {
             // ---- what of the tile's V is not in it
             if (!wait_outs(mine)) return;
+            const Keys keys = keys_of(cache, p.slot, a.layer, p.part.head);
 #pragma unroll 1
             for (int t = 0; t < kKeys && j0 + t < p.end; ++t) {
-              if (gone >> (t >> 4) & 1u) continue;
+              if (col[t] == -INFINITY) continue;  // (not there)
               const int key = j0 + t;
-              const uint8_t* grp =
-                  kv_group(cache, page_of(p, key), a.layer,
-                           p.part.head, key, G::kBytes);
+              const uint8_t* grp = group_of<D>(keys, key);
               const uint32_t weights = tmem_ld1(s_at + t / 2);
               const __half2 two = *reinterpret_cast<const __half2*>(&weights);
               const float weight = t & 1 ? __high2float(two) : __low2float(two);

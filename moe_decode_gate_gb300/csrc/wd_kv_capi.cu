@@ -67,6 +67,7 @@ KvScratch kv_scratch(const wd_kv_cache& c) {
   KvScratch w;
   const size_t pages = c.num_pages, slots = c.slots;
   w.counters = reinterpret_cast<uint32_t*>(take(4 * (size_t)kKvMaxUnits));
+  w.none = take(kKvNoneBytes);
   w.partial = reinterpret_cast<float*>(
       take(4 * ((size_t)c.head_dim + 2) *
            (c.head_dim <= 128 ? (size_t)kKvMaxRowUnits * 256 : 2 * (size_t)kKvMaxUnits * 8)));
@@ -122,9 +123,11 @@ size_t wd_kv_workspace_size(const wd_kv_cache* cache) {
 wd_status wd_kv_workspace_init(const wd_kv_cache* cache, wd_stream_t stream) {
   const wd_status st = check_cache(cache);
   if (st != WD_OK) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // the flag's slot and the counters behind it
-  return cuda_status(cudaMemsetAsync(cache->workspace, 0, kFlagBytes + 4 * kKvMaxUnits,
-                                     reinterpret_cast<cudaStream_t>(stream)));
+  cudaError_t e = cudaMemsetAsync(cache->workspace, 0, kFlagBytes + 4 * kKvMaxUnits, s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(kv_scratch(*cache).none, 0xFF, kKvNoneBytes, s);
+  return cuda_status(e);
 }
 
 wd_status wd_kv_read_error_flag(const wd_kv_cache* cache, wd_stream_t stream, int* flag) {
@@ -221,6 +224,7 @@ wd_status wd_kv_attention(const wd_kv_cache* cache, int layer, const void* q, wd
   a.max_q = q_start ? (max_q > 0 && max_q < tokens ? max_q : tokens) : 1;
   a.half = dtype == WD_KV_FP16;
   a.counters = w.counters;
+  a.none = w.none;
   a.partial = w.partial;
   return cuda_status(launch_kv_attention(a, reinterpret_cast<cudaStream_t>(stream)));
 }
