@@ -46,7 +46,9 @@
  * checks its arguments on the host before any launch, and finds its scratch in a
  * workspace that calls on different streams must not share.  What only the
  * device can see is range-checked there: a slot, page id or position out of
- * range is skipped and raises a bit of the workspace's error flag.
+ * range is skipped and raises a bit of the workspace's error flag.  Lengths grow by wd_kv_reserve and
+ * change by wd_kv_fork alone: a caller who lowers one keeps the pages behind the new end taken, and may write into a
+ * page that another sequence shares.
  */
 #ifndef WD_KV_H_
 #define WD_KV_H_
@@ -135,9 +137,14 @@ WD_API wd_status wd_kv_append(const wd_kv_cache* cache, int layer, const void* k
  *
  * out: [tokens, q_heads, head_dim] contiguous, q's type; lse: FP32 [tokens,
  * q_heads] or NULL.  A query that sees nothing gets zeros and -inf.  What is
- * not seen never enters the result, whatever its bytes.  max_q: the most
- * tokens an entry has, a hint for the tile (0: not known).  Tokens of no entry
- * are not written. */
+ * not seen never enters the result, whatever its bytes; keys of a page id out of range are not
+ * seen.  max_q: the most tokens an entry has, a hint for the tile (0: not known: `tokens` is
+ * taken for it).  scale > 0.  Tokens of no entry are not written.
+ *
+ * Numbers: sums are FP32, probabilities are rounded to FP16 once, and any finite keys and values of the
+ * cache give a finite result while the logits are FP32 numbers and |q| scale is below 2^114.  A query's
+ * channels below 2^-31 of its largest lose bits; so do values 2^126 times smaller than another one that a row
+ * sees in the same 32 channels. */
 WD_API wd_status wd_kv_attention(const wd_kv_cache* cache, int layer, const void* q,
                                  wd_kv_dtype dtype, int64_t q_stride_token, int64_t q_stride_head,
                                  int q_heads, void* out, float* lse, const int32_t* seqs,

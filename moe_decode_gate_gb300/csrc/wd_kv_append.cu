@@ -12,8 +12,9 @@
 // per token and head (BF16), the values back (if asked for) as much as the input.
 // Measured: 147 MB of prompts (BF16, head_dim 128, values back) 36.8 us, 4.0 TB/s, 0.59
 // of the copy rate: the pipe that compares, permutes and converts is 57 % busy and the
-// issue slots 64 %, the loads of a thread's few blocks do not hide the rest.  One token of
-// 32 sequences: 2.6 us.  Tried: loads ahead, other numbers of tokens to a CTA (37 to 41 us).
+// issue slots 64 %, the loads of a thread's few blocks do not hide the rest, and 8 CTAs to an SM
+// leave 32 registers, which every instance spills beyond (28 bytes of stores and 40 of loads here,
+// 68 and 88 for FP32).  One token of 32 sequences: 2.9 us.  Tried: loads ahead, other numbers of tokens to a CTA (37 to 41 us).
 #include "wd_device.cuh"
 #include "wd_kv.cuh"
 

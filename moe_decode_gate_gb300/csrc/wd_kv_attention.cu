@@ -34,11 +34,11 @@
 //     scales (or NaN) adds its products one by one in FP32 instead.
 //
 // What bounds it.  A key head's 32 keys cost 4352 bytes and, in each warp, about 620 instructions,
-// half of them on the pipe that converts codes, permutes and compares; so neither the memory (52 %
-// busy) nor that pipe (54 %) nor the tensor cores (23 %) is full, and twelve warps to an SM do
+// half of them on the pipe that converts codes, permutes and compares; so neither the memory (50 %
+// busy) nor that pipe (53 %) nor the tensor cores (23 %) is full, and twelve warps to an SM do
 // not hide each other's latencies.  Measured (BF16, head_dim 128, 8 query heads to a key
-// head): 4 sequences of up to 131,072 keys, 4 key heads 56.1 us, 4.46 TB/s, 0.66 of the copy rate;
-// 32 sequences of up to 8192 21.0 us; one of 517 9.2 us, of which 5 us find the work
+// head): 4 sequences of up to 131,072 keys, 4 key heads 57.6 us, 4.35 TB/s, 0.64 of the copy rate;
+// 32 sequences of up to 8192 21.4 us; one of 517 9.4 us, of which 5 us find the work
 // and read the first page, 1.5 us are the launch and the rest is one step and the join.
 #include "wd_kv_attention.cuh"
 
@@ -1129,11 +1129,11 @@ cudaError_t launch_kv_attention(const KvAttentionArgs& args, cudaStream_t s) {
   const long long rows = (long long)a.max_q * group;
   // More rows than one tile here holds, and so on average too (a chunk among many single tokens would
   // have those in tiles of 256 rows): the other kernel.  16 entries, 4000 to 8000 keys, 4 key
-  // heads, head_dim 128: 40 rows 91 us against 103 here, 64 rows 85 against 104, 128 rows 87 against 201;
-  // head_dim 64: 62 against 70, 59 against 71, 60 against 136.  32 rows take 52 us here.
+  // heads, head_dim 128: 40 rows 89 us against 105 here, 64 rows 82 against 106, 128 rows 84 against 207;
+  // head_dim 64: 62 against 72, 60 against 73, 61 against 141.  32 rows take 52 us here, 81 there.
   // Up to 64 rows of few entries and heads stay, as their long sequences are cut finer here: 64 rows of one
-  // head over 131,072 keys 62 us against 121, 40 rows of 4 heads over 4000 23 against 28 (but 64
-  // rows over 100 keys 14 against 11); 32 heads of 100 to 200 keys 16 against 14, 128 heads 27 against 16.
+  // head over 131,072 keys 62 us against 105, 40 rows of 4 heads over 4000 23 against 28 (but 64
+  // rows over 100 keys 14 against 11); 32 heads of 100 to 200 keys 16 against 14, 128 heads 28 against 16.
   const long long items = (long long)a.batch.entries * a.cache.kv_heads;
   const bool many = rows > (items < 64 ? 64 : 32) &&
                     (long long)a.batch.tokens * group > 32ll * a.batch.entries;

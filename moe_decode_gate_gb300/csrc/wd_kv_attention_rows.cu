@@ -26,14 +26,16 @@
 // enough items for the GPU; the CTA that finishes last joins them in their order.
 //
 // Measured (bfloat16, head_dim 128, 8 query heads to a key head).  2432 tokens after 30,336, 4 key
-// heads: 1328 us, 947 TFLOP/s, 0.50 of the cuBLAS rate; the products alone would take 1300
-// cycles a tile of 64 keys, the softmax takes 2400 (64 exponentials a thread at a quarter of the
+// heads: 1275 us, 986 TFLOP/s, 0.52 of the cuBLAS rate; the products alone would take 1300
+// cycles a tile of 64 keys, the softmax takes about 2300 (64 exponentials a thread at a quarter of the
 // rate, and instructions that two warps to a scheduler do not hide).  Chunks of 200 to
-// 256 tokens in two sequences of 4100 to 6001, 4 key heads: 83 us, where wd_kv_attention.cu
-// takes 233; the 48 tiles of a piece cost 60 us, the rest is the start (7 us), Q and the joins.
+// 256 tokens in two sequences of 4100 to 6001, 4 key heads: 81 us, where wd_kv_attention.cu
+// takes 233; the 48 tiles of a piece cost 58 us, the rest is the start (7 us), Q and the joins.
 // Tried: m16n8k16 products over ldmatrix fragments (354 us); two warps for V (130 us); products
-// issued without uniform registers (2432 tokens: 1651 us); 160 registers for the softmax warps and 88
-// for the others by setmaxnreg, which leaves no spills (2432 tokens: 1392 us).
+// issued without uniform registers (2432 tokens: 1651 us, then 1328); 160 registers for the softmax
+// warps and 88 for the others by setmaxnreg, which leaves no spills (1392; with 128 each, 32 bytes
+// of stores and about 130 of loads are spilled); the rare keys noted in a word that two of the
+// conversion warps write (1306 to 1345, head_dim 64 1043 against 1005).
 #include "wd_kv_attention.cuh"
 
 namespace wd {
