@@ -36,7 +36,7 @@
  * is the same from run to run.
  *
  * A decode step: wd_kv_reserve adds the new tokens' places to the sequences,
- * then for each layer wd_kv_append writes their keys and values and
+ * then for each layer wd_kv_append (or wd_kv_append_rotated) writes their keys and values and
  * wd_kv_attention reads.  Both take the new tokens as a batch of `entries`
  * sequences: entry b is slot seqs[b] (NULL: slot b) and owns tokens
  * [q_start[b], q_start[b+1]) of the tensors (NULL: token b alone); its n new
@@ -126,6 +126,26 @@ WD_API wd_status wd_kv_append(const wd_kv_cache* cache, int layer, const void* k
                               int64_t v_stride_token, int64_t v_stride_head, void* k_out,
                               void* v_out, const int32_t* seqs, const int32_t* q_start,
                               int entries, int tokens, wd_stream_t stream);
+
+/* The same, with the rotation of queries and keys by their positions: channels x1, x2 of a pair i of the
+ * token at position p become
+ *
+ *   x1 c - x2 s,   x2 c + x1 s,   c = cos_sin[p][i],  s = cos_sin[p][rot / 2 + i]
+ *
+ * for the pairs of the first `rot` channels of each head: channels i and i + rot / 2, or 2i and 2i + 1 if
+ * `paired`; the others stay.  cos_sin: FP32 [positions, rot], 16-byte aligned, rot a multiple of 16 up to head_dim.
+ * Products and sums are rounded to FP32 one by one, keys are quantised from that, queries rounded
+ * once to their type.  q: [tokens, q_heads, head_dim] of `dtype` with the given strides (NULL, with q_out:
+ * keys and values alone; q_heads up to 4096); q_out: contiguous, and may be q where that is.  Tokens at positions that cos_sin does not
+ * have are skipped and raise WD_KV_FLAG_BAD_INDEX. */
+WD_API wd_status wd_kv_append_rotated(const wd_kv_cache* cache, int layer, const void* q, const void* k,
+                                      const void* v, wd_kv_dtype dtype, int64_t q_stride_token,
+                                      int64_t q_stride_head, int q_heads, int64_t k_stride_token,
+                                      int64_t k_stride_head, int64_t v_stride_token,
+                                      int64_t v_stride_head, void* q_out, void* k_out, void* v_out,
+                                      const float* cos_sin, int positions, int rot, int paired,
+                                      const int32_t* seqs, const int32_t* q_start, int entries,
+                                      int tokens, wd_stream_t stream);
 
 /* Attention of the new tokens' queries over one layer of the cache.
  * q: [tokens, q_heads, head_dim] BF16 or FP16 with the given strides in

@@ -11,7 +11,9 @@ each routed row is read and dequantised once for all of its tokens:
 every routed expert); ``wd_moe_describe_plan`` names the kernels a shape gets.
 Next to the layer, ``KVCache`` (include/wd_kv.h) is the attention half of a
 decode step: a paged cache of keys and values in MXFP4, the attention that reads
-it, and forking, freeing and compacting its pages.
+it, and forking, freeing and compacting its pages.  Around the two stand the small
+operators of a step (include/wd_step.h): ``rms_norm`` with the residual's addition,
+the rotation in ``KVCache.append_rotated``, ``route`` and ``adjust_logits``.
 This package is the thin Python binding over that library; PyTorch only
 supplies device memory and streams.
 
@@ -54,6 +56,8 @@ from .kv_cache import (  # noqa: F401
     KV_FLAG_NO_PAGES,
     KV_FLAG_TIMEOUT,
     KVCache,
+    rotation_table,
     wd_kv_page_bytes,
 )
 from .layer import MoEDecodeLayer  # noqa: F401
+from .step import adjust_logits, rms_norm, route  # noqa: F401

@@ -1,5 +1,5 @@
-"""ctypes binding of the C-ABI in include/wd_moe.h, include/wd_kv.h and include/wd_bench.h
-(the calls of wd_kv.h are wrapped by kv_cache.py).
+"""ctypes binding of the C-ABI in include/wd_moe.h, include/wd_kv.h, include/wd_step.h and
+include/wd_bench.h (the calls of wd_kv.h are wrapped by kv_cache.py, those of wd_step.h by step.py).
 
 Argument marshalling only: shapes are read off the tensors, pointers and the
 current CUDA stream are passed through, and a non-OK status raises WdError.
@@ -52,11 +52,18 @@ SIGNATURES = {
     "wd_kv_read_error_flag": (_I, [_P, _P, ctypes.POINTER(_I)]),
     "wd_kv_reserve": (_I, [_P, _P, _P, _I, _P, _P]),
     "wd_kv_append": (_I, [_P, _I, _P, _P, _I, _I64, _I64, _I64, _I64, _P, _P, _P, _P, _I, _I, _P]),
+    "wd_kv_append_rotated": (_I, [_P, _I, _P, _P, _P, _I, _I64, _I64, _I, _I64, _I64, _I64, _I64, _P, _P, _P, _P,
+                                  _I, _I, _I, _P, _P, _I, _I, _P]),
     "wd_kv_attention": (_I, [_P, _I, _P, _I, _I64, _I64, _I, _P, _P, _P, _P, _I, _I, _I,
                              ctypes.c_float, _I, _P]),
     "wd_kv_fork": (_I, [_P, _P, _P, _I, _P, _P]),
     "wd_kv_free": (_I, [_P, _P, _I, _P]),
     "wd_kv_compact": (_I, [_P, _P, _P, _P, _P]),
+    "wd_rms_norm": (_I, [_P, _I, _I64, _I64, _I64, _I, _I, _P, _I, _P, _I64, _I64, _P, ctypes.c_float, _P, _P, _P,
+                         _P]),
+    "wd_route": (_I, [_P, _I, _I64, _I64, _I, _I, _I, _P, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P]),
+    "wd_adjust_logits": (_I, [_P, _I, _I64, _I, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _I64, _P, _I, _I64,
+                              _P]),
     "wd_bench_copy": (_I, [_P, _P, _SZ, _I, _P]),
     "wd_bench_read": (_I, [_P, _SZ, _P, _I, _P]),
     "wd_bench_fill": (_I, [_P, _SZ, _U32, _I, _P]),

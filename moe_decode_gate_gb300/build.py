@@ -1,7 +1,7 @@
 """Build the native library ``libwd_moe.so`` in-tree with nvcc for sm_103a.
 
 Each .cu file compiles to an object in parallel, then one shared link.  The
-library is plain C-ABI (include/wd_moe.h, include/wd_kv.h,
+library is plain C-ABI (include/wd_moe.h, include/wd_kv.h, include/wd_step.h,
 include/wd_bench.h); no PyTorch headers are involved.
 """
 from __future__ import annotations
@@ -18,7 +18,8 @@ BUILD = os.path.join(HERE, "_build")
 SOURCES = ["wd_gate_up.cu", "wd_gate_up_rowshare.cu", "wd_gate_up_persist.cu", "wd_gate_up_mma.cu",
            "wd_down.cu", "wd_down_dimblock.cu", "wd_capi.cu", "wd_bench.cu", "wd_no_alloc.cu",
            "wd_expert_centric.cu", "wd_kv_append.cu", "wd_kv_attention.cu",
-           "wd_kv_attention_rows.cu", "wd_kv_pages.cu", "wd_kv_capi.cu"]
+           "wd_kv_attention_rows.cu", "wd_kv_pages.cu", "wd_kv_capi.cu", "wd_kv_append_rotated.cu",
+           "wd_norm.cu", "wd_route.cu", "wd_logits.cu", "wd_step_capi.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-Xcompiler", "-Wall", "-I", os.path.join(ROOT, "include")]

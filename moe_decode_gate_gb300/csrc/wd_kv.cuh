@@ -141,24 +141,6 @@ struct KvScratch {
   int32_t* owner;      // [slots]
   size_t bytes;        // all of it, the flag's 256 bytes included
 };
-// Launch as a programmatic dependent: the kernel may start while the one before it
-// on the stream drains.  Each of them waits for the results of that one before its first
-// read of memory.
-template <typename... Params, typename... Args>
-cudaError_t kv_launch(void (*kernel)(Params...), int grid, int block, int shared, cudaStream_t s,
-                      const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3((unsigned)block);
-  cfg.dynamicSmemBytes = (size_t)shared;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
 
 KvScratch kv_scratch(const wd_kv_cache& c);
 KvView kv_view(const wd_kv_cache& c);
@@ -173,6 +155,18 @@ struct KvAppendArgs {
   wd_kv_dtype dtype;
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t s);
+
+struct KvRotateArgs {
+  KvAppendArgs kv;
+  const void* q;  // null: keys and values alone
+  long long q_token, q_head;
+  int q_heads;
+  void* q_out;
+  const float* cos_sin;  // [positions][rot]
+  int positions, rot;
+  bool paired;
+};
+cudaError_t launch_kv_append_rotated(const KvRotateArgs& a, cudaStream_t s);
 
 struct KvAttentionArgs {
   KvView cache;

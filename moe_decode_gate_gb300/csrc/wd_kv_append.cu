@@ -16,167 +16,13 @@
 // leave 32 registers, which every instance spills beyond (28 bytes of stores and 40 of loads here,
 // 68 and 88 for FP32).  One token of 32 sequences: 2.9 us.  Tried: loads ahead, other numbers of tokens to a CTA (37 to 41 us).
 #include "wd_device.cuh"
-#include "wd_kv.cuh"
+#include "wd_kv_quant.cuh"
 
 namespace wd {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 16;  // tokens of a CTA
-
-template <typename T>
-struct alignas(16) Eight {
-  T v[8];
-};
-
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
-
-// Eight inputs as floats, and the bits of the largest magnitude as a float (NaN above Inf).
-template <typename T>
-struct Widen;
-template <>
-struct Widen<float> {
-  static __device__ __forceinline__ uint32_t run(const Eight<float>& x, float (&f)[8]) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      f[k] = x.v[k];
-      top = max(top, __float_as_uint(f[k]) & 0x7FFFFFFFu);
-    }
-    return top;
-  }
-};
-template <typename T>
-__device__ __forceinline__ uint32_t top_half(const Eight<T>& x) {
-  const uint4 w = *reinterpret_cast<const uint4*>(&x);
-  const uint32_t m = max_u16x2(max_u16x2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                               max_u16x2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
-  return max(m & 0xFFFFu, m >> 16);
-}
-template <>
-struct Widen<__nv_bfloat16> {
-  static __device__ __forceinline__ uint32_t run(const Eight<__nv_bfloat16>& x, float (&f)[8]) {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&x);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      f[2 * k] = __uint_as_float(w[k] << 16);
-      f[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-    }
-    return top_half(x) << 16;
-  }
-};
-template <>
-struct Widen<__half> {
-  static __device__ __forceinline__ uint32_t run(const Eight<__half>& x, float (&f)[8]) {
-    const __half2* h = reinterpret_cast<const __half2*>(&x);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 p = __half22float2(h[k]);
-      f[2 * k] = p.x;
-      f[2 * k + 1] = p.y;
-    }
-    const uint32_t top = top_half(x);
-    return __float_as_uint(__half2float(__ushort_as_half((unsigned short)top))) & 0x7FFFFFFFu;
-  }
-};
-
-template <typename T>
-__device__ __forceinline__ Eight<T> narrow(const float (&f)[8]);
-template <>
-__device__ __forceinline__ Eight<float> narrow(const float (&f)[8]) {
-  Eight<float> y;
-#pragma unroll
-  for (int k = 0; k < 8; ++k) y.v[k] = f[k];
-  return y;
-}
-template <>
-__device__ __forceinline__ Eight<__nv_bfloat16> narrow(const float (&f)[8]) {
-  Eight<__nv_bfloat16> y;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    reinterpret_cast<__nv_bfloat162*>(&y)[k] = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
-  return y;
-}
-template <>
-__device__ __forceinline__ Eight<__half> narrow(const float (&f)[8]) {
-  Eight<__half> y;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    reinterpret_cast<__half2*>(&y)[k] = __floats2half2_rn(f[2 * k], f[2 * k + 1]);
-  return y;
-}
-
-// Eight values -> eight E2M1 codes (round to nearest even, saturating), the first in the low bits.
-__device__ __forceinline__ uint32_t e2m1x8_of(const float (&f)[8]) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
-      "mov.b32 %0, {a, b, c, d};\n\t}"
-      : "=r"(r)
-      : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
-  return r;
-}
-
-// ... and back.
-__device__ __forceinline__ void e2m1x8_values(uint32_t w, float (&f)[8]) {
-  uint32_t r[4];
-  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-      : "r"(w));
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&r[k]));
-    f[2 * k] = p.x;
-    f[2 * k + 1] = p.y;
-  }
-}
-
-// 2^e for e in [-127, 127], the lowest a subnormal.
-__device__ __forceinline__ float power_of_two(int e) {
-  return e < -126 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(e + 127) << 23);
-}
-
-struct Place {
-  uint8_t* group;  // K head 0's group of the token, null to skip it
-  int t;           // token within the group
-};
-
-// Where a token of the batch goes.
-template <int D>
-__device__ __forceinline__ Place find_place(const KvAppendArgs& a, int token) {
-  const KvView& c = a.cache;
-  Place p{nullptr, 0};
-  int b = token;  // the last entry that starts at or before this token
-  if (a.batch.q_start) {
-    int lo = 0, hi = a.batch.entries;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (a.batch.q_start[mid] <= token) lo = mid + 1; else hi = mid;
-    }
-    b = lo - 1;
-  }
-  if (b < 0 || b >= a.batch.entries) return p;
-  int first, n;
-  kv_tokens(c, a.batch, b, first, n);
-  const int s = kv_slot(c, a.batch, b);
-  if (s < 0 || token >= first + n) return p;
-  const int pos = kv_length(c, s) - n + token - first;
-  if (pos < 0) {
-    atomicOr(c.flag, WD_KV_FLAG_BAD_INDEX);
-    return p;
-  }
-  const int id = c.table[(long long)s * c.columns + (pos >> c.page_shift)];
-  if ((unsigned)id >= (unsigned)c.num_pages) {
-    atomicOr(c.flag, WD_KV_FLAG_BAD_INDEX);
-    return p;
-  }
-  p.group = kv_group(c, id, a.layer, 0, pos, KvGroup<D>::kBytes);
-  p.t = pos & 15;
-  return p;
-}
 
 // per_cta: tokens of a CTA.  A thread stays with one head and side (or a few, if there are more than
 // the CTA has rows of threads) and goes from token to token.
@@ -222,7 +68,7 @@ __global__ void __launch_bounds__(kThreads, 8) kv_append(const KvAppendArgs a, i
     Eight<T> next;
     if (here && token0 < n) next = fetch(src);  // on its way while the places are found
     if (!placed) {
-      if ((int)threadIdx.x < n) place[threadIdx.x] = find_place<D>(a, base + threadIdx.x);
+      if ((int)threadIdx.x < n) place[threadIdx.x] = find_place<D>(c, a.batch, a.layer, base + threadIdx.x);
       __syncthreads();
       placed = true;
     }
@@ -306,8 +152,8 @@ cudaError_t run(const KvAppendArgs& a, cudaStream_t s) {
   const bool vec = aligned16(a.k) && aligned16(a.v) && aligned16(a.k_out) && aligned16(a.v_out) &&
                    a.k_token % u == 0 && a.k_head % u == 0 && a.v_token % u == 0 &&
                    a.v_head % u == 0;
-  return kv_launch(vec ? kv_append<T, D, true> : kv_append<T, D, false>, ctas, kThreads, 0, s, a,
-                   per_cta);
+  return launch_dependent(vec ? kv_append<T, D, true> : kv_append<T, D, false>, ctas, kThreads, 0, s,
+                          a, per_cta);
 }
 
 template <typename T>

@@ -1,0 +1,315 @@
+// wd_kv_append_rotated.cu - queries and keys rotated by their positions; keys and
+// values quantised to MXFP4 into the pages (declared in include/wd_kv.h).
+//
+// A pair (x1, x2) of a head's channels becomes (x1 c - x2 s, x2 c + x1 s), c and s from the row of the
+// table that the token's position names. Products and sums are rounded to FP32 one by one, not
+// contracted: the codes of a key are then the same whatever kernel computes them, and
+// its quantising sees the FP32 values (they are not rounded to the key's type on the way).
+//
+// One launch, two kinds of CTA. The first ones take keys and values, 8 channels of one token, head and side
+// to a thread as in wd_kv_append.cu; a key's thread reads its partner's channels too, half a rotation away.
+// The others take queries, which are most of the bytes: a thread has the 8 + 8 channels
+// of 8 pairs (16 neighbours where pairs are neighbours), so that each cosine and sine is read once for both.
+//
+// To read and write: q in and out, k and v in, 4.25 bits a channel of them out, the table's rows.
+#include "wd_device.cuh"
+#include "wd_kv_quant.cuh"
+
+namespace wd {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 16;  // tokens of a CTA
+
+template <typename T, bool kVec>
+__device__ __forceinline__ Eight<T> fetch(const T* src) {
+  Eight<T> x;
+  if (kVec) {
+    x = *reinterpret_cast<const Eight<T>*>(src);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x.v[k] = src[k];
+  }
+  return x;
+}
+
+template <typename T, bool kVec>
+__device__ __forceinline__ void put(T* dst, const Eight<T>& x) {
+  if (kVec) {
+    *reinterpret_cast<Eight<T>*>(dst) = x;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dst[k] = x.v[k];
+  }
+}
+
+template <int kN>
+__device__ __forceinline__ void load_floats(const float* p, float (&f)[kN]) {
+#pragma unroll
+  for (int k = 0; k < kN / 4; ++k) {
+    const float4 v = *reinterpret_cast<const float4*>(p + 4 * k);
+    f[4 * k] = v.x;
+    f[4 * k + 1] = v.y;
+    f[4 * k + 2] = v.z;
+    f[4 * k + 3] = v.w;
+  }
+}
+
+__device__ __forceinline__ float first_of(float x1, float x2, float c, float s) {
+  return __fsub_rn(__fmul_rn(x1, c), __fmul_rn(x2, s));
+}
+__device__ __forceinline__ float second_of(float x1, float x2, float c, float s) {
+  return __fadd_rn(__fmul_rn(x2, c), __fmul_rn(x1, s));
+}
+
+// Four neighbouring pairs, with their cosines and sines.
+__device__ __forceinline__ void rotate_neighbours(float (&f)[8], const float (&c)[4], const float (&s)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float a = f[2 * k], b = f[2 * k + 1];
+    f[2 * k] = first_of(a, b, c[k], s[k]);
+    f[2 * k + 1] = second_of(a, b, c[k], s[k]);
+  }
+}
+
+// The token's place, none if the table has no row for its position.
+template <int D>
+__device__ __forceinline__ Place rotated_place(const KvRotateArgs& a, int token) {
+  Place p = find_place<D>(a.kv.cache, a.kv.batch, a.kv.layer, token);
+  if (p.pos >= a.positions) {
+    atomicOr(a.kv.cache.flag, WD_KV_FLAG_BAD_INDEX);
+    p.group = nullptr;
+    p.pos = -1;
+  }
+  return p;
+}
+
+// Channels 8e .. 8e + 7 of one token, head and side (v: values, else keys): the largest magnitude of
+// their block from the row's `lanes` (`top`: the bits of these eight's), codes and scales to the token's place,
+// and what they stand for to `out` if `back`.
+template <typename T, int D, bool kVec>
+__device__ __forceinline__ void store_eight(const float (&f)[8], uint32_t top, unsigned lanes, int e, bool v, const Place* at,
+                                            long long head_at, bool back, T* out) {
+  using G = KvGroup<D>;
+  const int block = e >> 2, t8 = e & 3;
+  top = max(top, __shfl_xor_sync(lanes, top, 1));
+  top = max(top, __shfl_xor_sync(lanes, top, 2));
+  const bool bad = top >= 0x7F800000u;
+  // floor(log2(top)) - 2, at least -127; a subnormal's floor(log2) is below -126
+  const int ex = (int)(top >> 23);
+  const int exp2 = top == 0 || bad ? 0 : (ex <= 2 ? -127 : ex - 129);
+  const float inv = power_of_two(-exp2);
+  float y[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) y[k] = f[k] * inv;
+  const uint32_t word = bad ? 0u : e2m1x8_of(y);
+  // the scales of the row's blocks side by side
+  uint32_t scales = (bad ? 255u : (uint32_t)(exp2 + 127)) << (8 * (block & 3));
+  scales |= __shfl_xor_sync(lanes, scales, 4);
+  if (G::kBlocks >= 4) scales |= __shfl_xor_sync(lanes, scales, 8);
+  // V: blocks c and c ^ 1 swap halves, so that the even one has channels 4g .. of both for
+  // g = 2 t8 and the odd one for g = 2 t8 + 1
+  const uint32_t other = __shfl_xor_sync(lanes, word, 4);
+  const Place p = *at;
+  if (p.group) {
+    uint8_t* g = p.group + head_at;
+    uint8_t* scale_to = g + (v ? G::kVScale : G::kKScale) + p.t * G::kBlocks + block;
+    if (!v) {
+      *reinterpret_cast<uint32_t*>(g + G::k_word(p.t, block, t8)) = word;
+    } else {
+      const uint32_t both = block & 1 ? __byte_perm(other, word, 0x7632)
+                                      : __byte_perm(word, other, 0x5410);
+      *reinterpret_cast<uint32_t*>(g + G::v_half(p.t, block & ~1, 2 * t8 + (block & 1))) = both;
+    }
+    if ((e & 15) == 0) {
+      if (G::kBlocks == 2)
+        *reinterpret_cast<uint16_t*>(scale_to) = (uint16_t)scales;
+      else
+        *reinterpret_cast<uint32_t*>(scale_to) = scales;
+    }
+    if (back) {
+      const float unit = bad ? __uint_as_float(0x7FC00000u) : power_of_two(exp2);
+      e2m1x8_values(word, y);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] *= unit;
+      const Eight<T> z = narrow<T>(y);
+      if (kVec) {
+        *reinterpret_cast<Eight<T>*>(out) = z;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) out[k] = z.v[k];
+      }
+    }
+  }
+}
+
+// Queries of tokens [base, base + n).
+template <typename T, int D, bool kVec>
+__device__ __forceinline__ void queries(const KvRotateArgs& a, int base, int n, Place* place) {
+  constexpr int kPerRow = D / 16;  // threads to a token and head
+  constexpr int kRowsOfThreads = kThreads / kPerRow;
+  const int half = a.rot / 2;
+  const int e = threadIdx.x % kPerRow, row0 = threadIdx.x / kPerRow;
+  const bool turned = 16 * e < a.rot;  // else 16 channels that stay as they are
+  // this thread's two runs of 8 channels
+  const int c0 = turned && !a.paired ? 8 * e : 16 * e;
+  const int c1 = turned && !a.paired ? 8 * e + half : 16 * e + 8;
+  const int at_once = max(1, kRowsOfThreads / a.q_heads);  // tokens
+  const int token0 = row0 / a.q_heads;                     // (0 if there are more heads than threads for them)
+  if ((int)threadIdx.x < n) place[threadIdx.x] = rotated_place<D>(a, base + threadIdx.x);
+  __syncthreads();
+  if (token0 >= at_once) return;
+  for (int h = row0 - token0 * a.q_heads; h < a.q_heads; h += kRowsOfThreads) {
+    for (int token = token0; token < n; token += at_once) {
+      const int pos = place[token].pos;
+      if (pos < 0) continue;
+      const T* src = static_cast<const T*>(a.q) + (base + token) * a.q_token + h * a.q_head;
+      T* dst = static_cast<T*>(a.q_out) + ((long long)(base + token) * a.q_heads + h) * D;
+      Eight<T> x0 = fetch<T, kVec>(src + c0), x1 = fetch<T, kVec>(src + c1);
+      if (turned) {
+        float c[8], s[8], f[8], g[8];
+        const float* row = a.cos_sin + (long long)pos * a.rot + 8 * e;
+        load_floats(row, c);
+        load_floats(row + half, s);
+        Widen<T>::run(x0, f);
+        Widen<T>::run(x1, g);
+        if (a.paired) {
+          const float lo_c[4] = {c[0], c[1], c[2], c[3]}, hi_c[4] = {c[4], c[5], c[6], c[7]};
+          const float lo_s[4] = {s[0], s[1], s[2], s[3]}, hi_s[4] = {s[4], s[5], s[6], s[7]};
+          rotate_neighbours(f, lo_c, lo_s);
+          rotate_neighbours(g, hi_c, hi_s);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float u = f[k], v = g[k];
+            f[k] = first_of(u, v, c[k], s[k]);
+            g[k] = second_of(u, v, c[k], s[k]);
+          }
+        }
+        x0 = narrow<T>(f);
+        x1 = narrow<T>(g);
+      }
+      put<T, kVec>(dst + c0, x0);
+      put<T, kVec>(dst + c1, x1);
+    }
+  }
+}
+
+// Keys and values of tokens [base, base + n).
+template <typename T, int D, bool kVec>
+__device__ __forceinline__ void keys_and_values(const KvRotateArgs& a, int base, int n, Place* place) {
+  constexpr int kPerRow = D / 8;  // threads to a token, head and side
+  constexpr int kRowsOfThreads = kThreads / kPerRow;
+  const KvView& c = a.kv.cache;
+  const int rows = 2 * c.kv_heads;  // of a token: the heads' K, then the heads' V
+  const int half = a.rot / 2;
+  const int e = threadIdx.x % kPerRow;  // channels 8e .. 8e + 7
+  const int row0 = threadIdx.x / kPerRow;
+  const int at_once = max(1, kRowsOfThreads / rows);  // tokens
+  const int token0 = row0 / rows;
+  // a row's lanes are all here, or none: kPerRow divides the warp or is a warp
+  const unsigned lanes = kPerRow >= 32 ? 0xFFFFFFFFu
+                                       : ((1u << (kPerRow % 32)) - 1u) << (threadIdx.x & 31 & ~(kPerRow - 1));
+  const bool lower = 8 * e < half;  // of the two halves that a rotation pairs
+  if ((int)threadIdx.x < n) place[threadIdx.x] = rotated_place<D>(a, base + threadIdx.x);
+  __syncthreads();
+  if (token0 >= at_once) return;
+  for (int hs = row0 - token0 * rows; hs < rows; hs += kRowsOfThreads) {
+    const bool v = hs >= c.kv_heads;
+    const int head = v ? hs - c.kv_heads : hs;
+    const bool turned = !v && 8 * e < a.rot;
+    for (int token = token0; token < n; token += at_once) {
+      const Place p = place[token];
+      const T* src = static_cast<const T*>(v ? a.kv.v : a.kv.k) + (base + token) * (v ? a.kv.v_token : a.kv.k_token) +
+                     head * (v ? a.kv.v_head : a.kv.k_head) + 8 * e;
+      const Eight<T> x = fetch<T, kVec>(src);
+      float f[8];
+      uint32_t top = Widen<T>::run(x, f);
+      if (turned && p.group) {
+        const float* row = a.cos_sin + (long long)p.pos * a.rot;
+        if (a.paired) {
+          float co[4], si[4];
+          load_floats(row + 4 * e, co);
+          load_floats(row + half + 4 * e, si);
+          rotate_neighbours(f, co, si);
+        } else {
+          const int i = lower ? 8 * e : 8 * e - half;
+          float g[8], co[8], si[8];
+          Widen<T>::run(fetch<T, kVec>(lower ? src + half : src - half), g);
+          load_floats(row + i, co);
+          load_floats(row + half + i, si);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            f[k] = lower ? first_of(f[k], g[k], co[k], si[k]) : second_of(g[k], f[k], co[k], si[k]);
+        }
+        top = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(f[k]) & 0x7FFFFFFFu);
+      }
+      T* out = static_cast<T*>(v ? a.kv.v_out : a.kv.k_out) + ((long long)(base + token) * c.kv_heads + head) * D + 8 * e;
+      store_eight<T, D, kVec>(f, top, lanes, e, v, &place[token], (long long)head * c.head_bytes, a.kv.k_out != nullptr, out);
+    }
+  }
+}
+
+// The first kv_ctas CTAs take keys and values of kv_tokens tokens each, the others queries of q_tokens.
+template <typename T, int D, bool kVec>
+__global__ void __launch_bounds__(kThreads) kv_append_rotated(const KvRotateArgs a, int kv_ctas, int kv_tokens, int q_tokens) {
+  __shared__ Place place[kMaxTokens];
+  grid_dependency_wait();  // nothing above reads what an earlier kernel may write
+  grid_launch_dependents();
+  if ((int)blockIdx.x < kv_ctas) {
+    const int base = blockIdx.x * kv_tokens;
+    keys_and_values<T, D, kVec>(a, base, min(kv_tokens, a.kv.batch.tokens - base), place);
+  } else {
+    const int base = (blockIdx.x - kv_ctas) * q_tokens;
+    queries<T, D, kVec>(a, base, min(q_tokens, a.kv.batch.tokens - base), place);
+  }
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Tokens of a CTA: few are spread over the SMs, a pass of the threads to each CTA at least; many get kMaxTokens.
+int tokens_of(int tokens, int rows, int per_row) {
+  const int one_pass = (kThreads / per_row + rows - 1) / rows;
+  int n = (tokens + 8 * kKvSms - 1) / (8 * kKvSms);
+  n = n < one_pass ? one_pass : n;
+  return n > kMaxTokens ? kMaxTokens : n;
+}
+
+template <typename T, int D>
+cudaError_t run(const KvRotateArgs& a, cudaStream_t s) {
+  const KvAppendArgs& kv = a.kv;
+  const int tokens = kv.batch.tokens;
+  const int kv_tokens = tokens_of(tokens, 2 * kv.cache.kv_heads, D / 8);
+  const int kv_ctas = (tokens + kv_tokens - 1) / kv_tokens;
+  const int q_tokens = a.q ? tokens_of(tokens, a.q_heads, D / 16) : 1;
+  const int q_ctas = a.q ? (tokens + q_tokens - 1) / q_tokens : 0;
+  constexpr long long u = 16 / sizeof(T);  // elements to 16 bytes
+  const bool vec = aligned16(kv.k) && aligned16(kv.v) && aligned16(kv.k_out) && aligned16(kv.v_out) && aligned16(a.q) &&
+                   aligned16(a.q_out) && kv.k_token % u == 0 && kv.k_head % u == 0 && kv.v_token % u == 0 &&
+                   kv.v_head % u == 0 && a.q_token % u == 0 && a.q_head % u == 0;
+  return launch_dependent(vec ? kv_append_rotated<T, D, true> : kv_append_rotated<T, D, false>, kv_ctas + q_ctas, kThreads, 0,
+                          s, a, kv_ctas, kv_tokens, q_tokens);
+}
+
+template <typename T>
+cudaError_t run_dim(const KvRotateArgs& a, cudaStream_t s) {
+  switch (a.kv.cache.head_dim) {
+    case 64: return run<T, 64>(a, s);
+    case 128: return run<T, 128>(a, s);
+    default: return run<T, 256>(a, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append_rotated(const KvRotateArgs& a, cudaStream_t s) {
+  switch (a.kv.dtype) {
+    case WD_KV_BF16: return run_dim<__nv_bfloat16>(a, s);
+    case WD_KV_FP16: return run_dim<__half>(a, s);
+    default: return run_dim<float>(a, s);
+  }
+}
+
+}  // namespace wd

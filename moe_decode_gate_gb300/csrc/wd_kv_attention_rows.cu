@@ -1227,7 +1227,7 @@ cudaError_t run(const KvAttentionArgs& a, cudaStream_t s) {
   const void* fn = reinterpret_cast<const void*>(kv_attention_rows<D>);
   const cudaError_t e = ensure_dynamic_smem(fn, bytes);
   if (e != cudaSuccess) return e;
-  return kv_launch(kv_attention_rows<D>, kKvSms, kThreads, bytes, s, a);
+  return launch_dependent(kv_attention_rows<D>, kKvSms, kThreads, bytes, s, a);
 }
 
 }  // namespace

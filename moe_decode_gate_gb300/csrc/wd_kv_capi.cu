@@ -53,6 +53,36 @@ wd_status check_batch(const wd_kv_cache* c, int layer, const int32_t* seqs, cons
   return WD_OK;
 }
 
+// What wd_kv_append and wd_kv_append_rotated share; nothing to do is WD_OK.
+wd_status append_args(KvAppendArgs& a, const wd_kv_cache* cache, int layer, const void* k, const void* v,
+                      wd_kv_dtype dtype, int64_t k_stride_token, int64_t k_stride_head, int64_t v_stride_token,
+                      int64_t v_stride_head, void* k_out, void* v_out, const int32_t* seqs, const int32_t* q_start,
+                      int entries, int tokens) {
+  wd_status st = check_cache(cache);
+  if (st != WD_OK) return st;
+  st = check_batch(cache, layer, seqs, q_start, entries, tokens);
+  if (st != WD_OK) return st;
+  if (dtype != WD_KV_BF16 && dtype != WD_KV_FP16 && dtype != WD_KV_FP32) return WD_ERR_INVALID_ARG;
+  const uintptr_t size = dtype == WD_KV_FP32 ? 4 : 2;
+  if (tokens == 0 || entries == 0) return WD_OK;
+  if (!k || !v || !k_out != !v_out) return WD_ERR_INVALID_ARG;
+  if (!aligned(k, size) || !aligned(v, size) || !aligned(k_out, size) || !aligned(v_out, size))
+    return WD_ERR_INVALID_ARG;
+  a.cache = kv_view(*cache);
+  a.batch = KvBatch{seqs, q_start, entries, tokens};
+  a.layer = layer;
+  a.k = k;
+  a.v = v;
+  a.k_token = k_stride_token;
+  a.k_head = k_stride_head;
+  a.v_token = v_stride_token;
+  a.v_head = v_stride_head;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.dtype = dtype;
+  return WD_OK;
+}
+
 }  // namespace
 
 KvScratch kv_scratch(const wd_kv_cache& c) {
@@ -166,30 +196,38 @@ wd_status wd_kv_append(const wd_kv_cache* cache, int layer, const void* k, const
                        int64_t v_stride_token, int64_t v_stride_head, void* k_out, void* v_out,
                        const int32_t* seqs, const int32_t* q_start, int entries, int tokens,
                        wd_stream_t stream) {
-  wd_status st = check_cache(cache);
-  if (st != WD_OK) return st;
-  st = check_batch(cache, layer, seqs, q_start, entries, tokens);
-  if (st != WD_OK) return st;
-  if (dtype != WD_KV_BF16 && dtype != WD_KV_FP16 && dtype != WD_KV_FP32) return WD_ERR_INVALID_ARG;
-  const uintptr_t size = dtype == WD_KV_FP32 ? 4 : 2;
-  if (tokens == 0 || entries == 0) return WD_OK;
-  if (!k || !v || !k_out != !v_out) return WD_ERR_INVALID_ARG;
-  if (!aligned(k, size) || !aligned(v, size) || !aligned(k_out, size) || !aligned(v_out, size))
-    return WD_ERR_INVALID_ARG;
   KvAppendArgs a{};
-  a.cache = kv_view(*cache);
-  a.batch = KvBatch{seqs, q_start, entries, tokens};
-  a.layer = layer;
-  a.k = k;
-  a.v = v;
-  a.k_token = k_stride_token;
-  a.k_head = k_stride_head;
-  a.v_token = v_stride_token;
-  a.v_head = v_stride_head;
-  a.k_out = k_out;
-  a.v_out = v_out;
-  a.dtype = dtype;
+  const wd_status st = append_args(a, cache, layer, k, v, dtype, k_stride_token, k_stride_head, v_stride_token,
+                                   v_stride_head, k_out, v_out, seqs, q_start, entries, tokens);
+  if (st != WD_OK || tokens == 0 || entries == 0) return st;
   return cuda_status(launch_kv_append(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+wd_status wd_kv_append_rotated(const wd_kv_cache* cache, int layer, const void* q, const void* k, const void* v,
+                               wd_kv_dtype dtype, int64_t q_stride_token, int64_t q_stride_head, int q_heads,
+                               int64_t k_stride_token, int64_t k_stride_head, int64_t v_stride_token,
+                               int64_t v_stride_head, void* q_out, void* k_out, void* v_out, const float* cos_sin,
+                               int positions, int rot, int paired, const int32_t* seqs, const int32_t* q_start,
+                               int entries, int tokens, wd_stream_t stream) {
+  KvRotateArgs a{};
+  const wd_status st = append_args(a.kv, cache, layer, k, v, dtype, k_stride_token, k_stride_head, v_stride_token,
+                                   v_stride_head, k_out, v_out, seqs, q_start, entries, tokens);
+  if (st != WD_OK) return st;
+  if (positions < 1 || !q != !q_out || (q && (q_heads < 1 || q_heads > 4096))) return WD_ERR_INVALID_ARG;
+  if (rot < 16 || rot > cache->head_dim || rot % 16) return WD_ERR_UNSUPPORTED_SHAPE;
+  if (tokens == 0 || entries == 0) return WD_OK;
+  const uintptr_t size = dtype == WD_KV_FP32 ? 4 : 2;
+  if (!cos_sin || !aligned(cos_sin, 16) || !aligned(q, size) || !aligned(q_out, size)) return WD_ERR_INVALID_ARG;
+  a.q = q;
+  a.q_token = q ? q_stride_token : 0;
+  a.q_head = q ? q_stride_head : 0;
+  a.q_heads = q_heads;
+  a.q_out = q_out;
+  a.cos_sin = cos_sin;
+  a.positions = positions;
+  a.rot = rot;
+  a.paired = paired != 0;
+  return cuda_status(launch_kv_append_rotated(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 wd_status wd_kv_attention(const wd_kv_cache* cache, int layer, const void* q, wd_kv_dtype dtype,

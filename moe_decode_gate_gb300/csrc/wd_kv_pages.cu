@@ -705,7 +705,7 @@ cudaError_t compact_one(const KvView& v, const KvScratch& w, int32_t* table_out,
   const cudaError_t e =
       ensure_dynamic_smem(reinterpret_cast<const void*>(kv_compact_one<kEach>), kBytes);
   if (e != cudaSuccess) return e;
-  return kv_launch(kv_compact_one<kEach>, copying_ctas(v, v.num_pages / 2), kPlan, kBytes, s, v,
+  return launch_dependent(kv_compact_one<kEach>, copying_ctas(v, v.num_pages / 2), kPlan, kBytes, s, v,
                    w.counters, table_out, refs_out, page_map);
 }
 
@@ -713,17 +713,17 @@ cudaError_t compact_one(const KvView& v, const KvScratch& w, int32_t* table_out,
 
 cudaError_t launch_kv_reserve(const KvView& v, const KvScratch& w, const int32_t* seqs,
                               const int32_t* counts, int n, int32_t* ok, cudaStream_t s) {
-  return kv_launch(kv_reserve, 1, kPlan, 0, s, v, w, seqs, counts, n, ok);
+  return launch_dependent(kv_reserve, 1, kPlan, 0, s, v, w, seqs, counts, n, ok);
 }
 
 cudaError_t launch_kv_fork(const KvView& v, const KvScratch& w, const int32_t* src,
                            const int32_t* dst, int n, int32_t* ok, cudaStream_t s) {
   if (n <= kOneRequests && v.num_pages <= kOnePages && (long long)n * v.columns <= kOneCells &&
       few_bytes(v, n))
-    return kv_launch(kv_fork_one, copying_ctas(v, n), kPlan, 0, s, v, w, src, dst, n, ok);
-  cudaError_t e = kv_launch(kv_fork_plan, 1, kPlan, 0, s, v, w, src, dst, n, ok);
-  if (e == cudaSuccess) e = kv_launch(kv_fork_work, kWorkCtas, kCopy, 0, s, v, w, src, dst, n);
-  if (e == cudaSuccess) e = kv_launch(kv_fork_rows, n < 1024 ? n : 1024, kCopy, 0, s, v, w, dst, n);
+    return launch_dependent(kv_fork_one, copying_ctas(v, n), kPlan, 0, s, v, w, src, dst, n, ok);
+  cudaError_t e = launch_dependent(kv_fork_plan, 1, kPlan, 0, s, v, w, src, dst, n, ok);
+  if (e == cudaSuccess) e = launch_dependent(kv_fork_work, kWorkCtas, kCopy, 0, s, v, w, src, dst, n);
+  if (e == cudaSuccess) e = launch_dependent(kv_fork_rows, n < 1024 ? n : 1024, kCopy, 0, s, v, w, dst, n);
   return e;
 }
 
@@ -734,10 +734,10 @@ cudaError_t launch_kv_compact(const KvView& v, const KvScratch& w, int32_t* tabl
     return v.num_pages <= 4 * kPlan ? compact_one<4>(v, w, table_out, refs_out, page_map, s)
                                     : compact_one<16>(v, w, table_out, refs_out, page_map, s);
   const int chunks = (v.num_pages + kKvChunkPages - 1) / kKvChunkPages;
-  cudaError_t e = kv_launch(kv_compact_count, chunks, kPlan, 0, s, v, w);
-  if (e == cudaSuccess) e = kv_launch(kv_compact_plan, chunks, kPlan, 0, s, v, w, chunks);
+  cudaError_t e = launch_dependent(kv_compact_count, chunks, kPlan, 0, s, v, w);
+  if (e == cudaSuccess) e = launch_dependent(kv_compact_plan, chunks, kPlan, 0, s, v, w, chunks);
   if (e == cudaSuccess)
-    e = kv_launch(kv_compact_work, kWorkCtas, kCopy, 0, s, v, w, chunks, table_out, refs_out,
+    e = launch_dependent(kv_compact_work, kWorkCtas, kCopy, 0, s, v, w, chunks, table_out, refs_out,
                   page_map);
   return e;
 }

@@ -1,0 +1,356 @@
+// wd_route.cu - routing of tokens to experts (declared in include/wd_step.h).
+//
+// A warp takes a token. Its lanes hold the experts in order: a group of experts (there are 1 to 32)
+// has 32 / groups lanes, rounded down to a power of two, and each of them kV consecutive ones, so that
+// a group's value is a few shuffles within its lanes and the first lane of several with equal
+// keys has the lowest index. K times the warp's largest key is found (one redux on keys
+// whose integer order is their order), taken by the first lane that has it, and struck out.
+//
+// Keys are exact where no bias and no sums of groups are asked for: they are the logits. Else they
+// carry FP32's errors (margin() below); a token of which two keys that the choice hangs on are nearer
+// than that is chosen again from keys in 64 bits, which only those experts need that can be chosen.
+//
+// Bounded by the instructions of a token (about 25 for each of the K rounds), not by its bytes.
+#include "wd_device.cuh"
+#include "wd_step.cuh"
+#include "wd_vec.cuh"
+
+namespace wd {
+namespace {
+
+constexpr int kWarps = 4;  // tokens of a CTA
+constexpr unsigned kAll = 0xFFFFFFFFu;
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+
+// Integers in the order of the numbers; 0 stands below -inf. NaN is not asked for, -0 is 0.
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t u) {
+  return __uint_as_float(u ^ ((u & 0x80000000u) ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ unsigned long long order_of(double x) {
+  const long long u = __double_as_longlong(x + 0.0);
+  return (unsigned long long)(u ^ ((u >> 63) | (long long)0x8000000000000000ull));
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+  return value_of(__reduce_max_sync(kAll, order_of(v)));
+}
+__device__ __forceinline__ float warp_min(float v) { return -warp_max(-v); }
+__device__ __forceinline__ uint32_t largest(uint32_t v) { return __reduce_max_sync(kAll, v); }
+__device__ __forceinline__ unsigned long long largest(unsigned long long v) {
+  const uint32_t hi = __reduce_max_sync(kAll, (uint32_t)(v >> 32));
+  const uint32_t lo = __reduce_max_sync(kAll, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+  return (unsigned long long)hi << 32 | lo;
+}
+
+// Where the experts of a lane begin, and how many it has.
+struct Span {
+  int first, n;
+};
+struct Lanes {
+  int per_group;  // lanes of a group
+  int per_lane;   // experts of a lane
+};
+__host__ __device__ inline Lanes lanes_of(int E, int groups) {
+  int up = 1;
+  while (up < groups) up *= 2;
+  const int per_group = 32 / up, size = E / groups;
+  return Lanes{per_group, (size + per_group - 1) / per_group};
+}
+
+// The value of a group from its lanes' two largest keys, in each of its lanes. A masked second
+// key takes no part.
+template <typename F>
+__device__ __forceinline__ F group_value(F a, F b, int lanes, int best) {
+  for (int off = 1; off < lanes; off *= 2) {
+    const F c = __shfl_xor_sync(kAll, a, off), d = __shfl_xor_sync(kAll, b, off);
+    const F low = a < c ? a : c;
+    a = a < c ? c : a;
+    b = b < d ? d : b;
+    b = b < low ? low : b;
+  }
+  return best == 2 && b > -INFINITY ? a + b : a;
+}
+
+// Whether this lane's group is among the `top` largest, ties to the lowest index.
+template <typename F>
+__device__ __forceinline__ bool group_chosen(F value, int group, int groups, int lanes, int top) {
+  int before = 0;
+  for (int g = 0; g < groups; ++g) {
+    const F other = __shfl_sync(kAll, value, g * lanes);
+    before += other > value || (other == value && g < group);
+  }
+  return before < top;
+}
+
+// The K largest keys of the warp, largest first: entry r in lane r % 32, place r / 32 of `ids`. Keys are struck
+// out of k. With `check` (keys of 32 bits), whether two neighbours of the order, the first that was not taken
+// among them, are nearer than `margin`.
+template <int kV, typename Key>
+__device__ __forceinline__ bool take(Key (&k)[kV], const Span& mine, int K, int lane, bool check, float margin,
+                                     int (&ids)[2], uint32_t (&keys)[2]) {
+  bool near = false;
+  Key last = 0;
+  for (int r = 0; r < K + check; ++r) {
+    Key top = k[0];
+#pragma unroll
+    for (int i = 1; i < kV; ++i) top = top < k[i] ? k[i] : top;
+    const Key all = largest(top);
+    if (check && r && all) near |= value_of((uint32_t)last) - value_of((uint32_t)all) < margin;
+    if (r == K) break;
+    last = all;
+    const int winner = __ffs(__ballot_sync(kAll, top == all)) - 1;
+    int at = 0;
+#pragma unroll
+    for (int i = kV - 1; i >= 0; --i)
+      if (k[i] == all) at = i;
+    if (lane == winner) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i)
+        if (i == at) k[i] = 0;
+    }
+    const int id = __shfl_sync(kAll, mine.first + at, winner);
+    if (lane == (r & 31)) {
+      if (r < 32) {
+        ids[0] = id;
+        keys[0] = (uint32_t)all;
+      } else {
+        ids[1] = id;
+        keys[1] = (uint32_t)all;
+      }
+    }
+  }
+  return near;
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+
+// exp(x - top), where top is at least x; 1 for the largest even if infinite, 0 for masked ones.
+__device__ __forceinline__ float exp_below(float x, float top) {
+  return x == -INFINITY ? 0.f : x == top ? 1.f : expf(x - top);
+}
+
+// The token's choice from keys in 64 bits. Experts whose FP32 key is below `least` are out of question
+// unless all are needed for the groups. Rare, so it is kept out of the way of the other registers.
+template <typename T, int kV>
+__device__ __noinline__ void choose_again(const RouteArgs& a, const T* x, const Span mine, const Lanes lanes, int lane,
+                                          float least, float top, bool all_needed, bool chosen, int (&ids)[2]) {
+  const int group = lane / lanes.per_group;
+  unsigned long long k[kV];
+  double sum = 0.0, best = -INFINITY, second = -INFINITY;
+  const bool sums = a.groups > 1 && a.group_best == 2;
+  if (!a.sigmoid) {
+    for (int i = 0; i < mine.n; ++i) {
+      const float l = to_float(x[mine.first + i]);
+      if (l > -INFINITY) sum += l == top ? 1.0 : exp((double)l - (double)top);
+    }
+    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
+  }
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    k[i] = 0;
+    if (i >= mine.n) continue;
+    const float l = to_float(x[mine.first + i]);
+    const float b = a.bias ? a.bias[mine.first + i] : 0.f;
+    double key = -INFINITY;
+    if (l > -INFINITY) {
+      const float rough = (a.sigmoid ? sigmoid(l) : exp_below(l, top) / (float)sum) + b;
+      if (all_needed || rough >= least) {
+        const double score = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : l == top ? 1.0 / sum : exp((double)l - (double)top) / sum;
+        key = score + (double)b;
+        if (!(key == key)) key = -INFINITY;
+      }
+    }
+    second = second > key ? second : best < key ? best : key;
+    best = best < key ? key : best;
+    // where nothing is added, keys are ordered by the logits
+    k[i] = order_of(a.bias ? key : (double)(l > -INFINITY ? l : -INFINITY));
+  }
+  if (a.groups > 1) {
+    if (all_needed) {
+      const double value = sums ? group_value(best, second, lanes.per_group, 2) : group_value(best, second, lanes.per_group, 1);
+      chosen = group_chosen(group < a.groups ? value : -(double)INFINITY, group, a.groups, lanes.per_group, a.top_groups);
+    }
+    if (!chosen)
+#pragma unroll
+      for (int i = 0; i < kV; ++i) k[i] = 0;
+  }
+  uint32_t unused[2];
+  take<kV>(k, mine, a.K, lane, false, 0.f, ids, unused);
+}
+
+template <typename T, int kV, bool kVec>
+__global__ void __launch_bounds__(32 * kWarps) route(const RouteArgs a, const Lanes lanes) {
+  const int lane = threadIdx.x & 31;
+  const int token = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int size = a.E / a.groups;
+  const int group = lane / lanes.per_group, j = lane % lanes.per_group;
+  Span mine{group * size + j * lanes.per_lane, 0};
+  if (group < a.groups) mine.n = max(0, min(lanes.per_lane, size - j * lanes.per_lane));
+  grid_dependency_wait();  // nothing above reads what an earlier kernel may write
+  grid_launch_dependents();
+  if (token >= a.tokens) return;
+  const T* x = static_cast<const T*>(a.logits) + (long long)token * a.stride;
+  float l[kV];
+  if constexpr (kVec) {  // every lane has kV experts
+    struct alignas(sizeof(T) * kV < 16 ? sizeof(T) * kV : 16) Pack {
+      T v[kV];
+    };
+    const Pack p = *reinterpret_cast<const Pack*>(x + mine.first);
+#pragma unroll
+    for (int i = 0; i < kV; ++i) l[i] = to_float(p.v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) l[i] = i < mine.n ? to_float(x[mine.first + i]) : -INFINITY;
+  }
+  float top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    if (!(l[i] == l[i])) l[i] = -INFINITY;
+    top = fmaxf(top, l[i]);
+  }
+  top = warp_max(top);
+  const bool sums = a.groups > 1 && a.group_best == 2;
+  const bool inexact = a.bias || sums;  // keys that are not the logits
+  float s[kV];
+  float sum = 0.f;
+  if (!a.sigmoid && (inexact || !a.renormalise)) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      s[i] = exp_below(l[i], top);
+      sum += s[i];
+    }
+    sum = warp_sum(sum);
+  }
+  uint32_t k[kV];
+  float best = -INFINITY, second = -INFINITY, margin = 0.f;
+  const float unit = a.sigmoid ? 1.f : sum > 0.f ? 1.f / sum : 0.f;  // the largest score there may be
+  float most = 0.f;  // largest magnitude of a key
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    float key = l[i];
+    if (inexact && l[i] > -INFINITY) {
+      key = a.sigmoid ? sigmoid(l[i]) : s[i] * unit;
+      if (a.bias) key += a.bias[mine.first + i];
+      if (!(key == key)) key = -INFINITY;
+      if (fabsf(key) < INFINITY) most = fmaxf(most, fabsf(key));
+    }
+    second = fmaxf(second, fminf(best, key));
+    best = fmaxf(best, key);
+    // without a bias the choice goes by the logits even where the groups' goes by sums of scores
+    k[i] = i < mine.n ? order_of(a.bias ? key : l[i]) : 0u;
+  }
+  bool again = false, chosen = true;
+  if (inexact) {
+    // In units of 2^-24, a score is off by 2 (expf), 1 (its argument), 2 (quotient), 1 (the product by it) and the sum
+    // of all of them, kV + 5 roundings at most; a key by half a unit of its own more. Two keys are compared.
+    most = warp_max(most);
+    margin = 0x1p-23f * (a.sigmoid ? 12 : kV + 12) * unit + 0x1p-23f * most;
+  }
+  if (a.groups > 1) {
+    float value = group_value(best, second, lanes.per_group, a.group_best);
+    if (group >= a.groups) value = -INFINITY;
+    chosen = group_chosen(value, group, a.groups, lanes.per_group, a.top_groups);  // (all lanes take part)
+    if (group >= a.groups) chosen = false;
+    if (inexact) {
+      const float in = warp_min(chosen ? value : INFINITY);
+      const float out = warp_max(chosen ? -INFINITY : value);
+      again = in - out < 2.f * margin;
+    }
+    if (!chosen)
+#pragma unroll
+      for (int i = 0; i < kV; ++i) k[i] = 0;
+  }
+  int ids[2] = {0, 0};
+  uint32_t keys[2] = {0, 0};
+  const bool groups_again = again;
+  again |= take<kV>(k, mine, a.K, lane, a.bias != nullptr, margin, ids, keys);
+  if (again) {
+    int chosen_again[2] = {0, 0};
+    const uint32_t lowest = __shfl_sync(kAll, a.K > 32 ? keys[1] : keys[0], (a.K - 1) & 31);
+    choose_again<T, kV>(a, x, mine, lanes, lane, value_of(lowest) - 2.f * margin, top, groups_again, chosen,
+                        chosen_again);
+    ids[0] = chosen_again[0];
+    ids[1] = chosen_again[1];
+  }
+  // the weights, from the chosen experts' logits
+  float y[2], w[2] = {0.f, 0.f};
+  float high = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    y[e] = -INFINITY;
+    if (lane + 32 * e < a.K) {
+      y[e] = to_float(x[ids[e]]);
+      if (!(y[e] == y[e])) y[e] = -INFINITY;
+    }
+    high = fmaxf(high, y[e]);
+  }
+  high = warp_max(high);
+  float total = 0.f;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if (a.renormalise)  // scaled alike: far below 0 a sigmoid is an exponential, to all of FP32's bits
+      w[e] = a.sigmoid && high > -40.f ? (y[e] > -INFINITY ? sigmoid(y[e]) : 0.f) : exp_below(y[e], high);
+    else
+      w[e] = y[e] > -INFINITY ? (a.sigmoid ? sigmoid(y[e]) : exp_below(y[e], top) * unit) : 0.f;
+    total += w[e];
+  }
+  if (a.renormalise) {
+    total = warp_sum(total);
+    const float f = total > 0.f ? a.scale / total : 0.f;
+    w[0] *= f;
+    w[1] *= f;
+  } else {
+    w[0] *= a.scale;
+    w[1] *= a.scale;
+  }
+  const long long at = (long long)token * a.K + lane;
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    if (lane + 32 * e < a.K) {
+      a.ids[at + 32 * e] = ids[e];
+      a.weights[at + 32 * e] = w[e];
+    }
+}
+
+template <typename T, int kV>
+cudaError_t run(const RouteArgs& a, const Lanes lanes, cudaStream_t s) {
+  constexpr int kBytes = sizeof(T) * kV < 16 ? sizeof(T) * kV : 16;
+  const bool vec = lanes.per_lane == kV && a.groups * lanes.per_group == 32 && a.E == 32 * kV &&
+                   reinterpret_cast<uintptr_t>(a.logits) % kBytes == 0 && a.stride * (long long)sizeof(T) % kBytes == 0;
+  const int ctas = (a.tokens + kWarps - 1) / kWarps;
+  return launch_dependent(vec ? route<T, kV, true> : route<T, kV, false>, ctas, 32 * kWarps, 0, s, a, lanes);
+}
+
+template <typename T>
+cudaError_t run_type(const RouteArgs& a, cudaStream_t s) {
+  const Lanes lanes = lanes_of(a.E, a.groups);
+  if (lanes.per_lane <= 1) return run<T, 1>(a, lanes, s);
+  if (lanes.per_lane <= 2) return run<T, 2>(a, lanes, s);
+  if (lanes.per_lane <= 4) return run<T, 4>(a, lanes, s);
+  if (lanes.per_lane <= 8) return run<T, 8>(a, lanes, s);
+  if (lanes.per_lane <= 16) return run<T, 16>(a, lanes, s);
+  return run<T, 32>(a, lanes, s);
+}
+
+}  // namespace
+
+bool route_supported(int E, int groups) {
+  return E <= WD_ROUTE_MAX_EXPERTS && groups <= 32 && E % groups == 0 && lanes_of(E, groups).per_lane <= 32;
+}
+
+cudaError_t launch_route(const RouteArgs& a, wd_dtype dtype, cudaStream_t s) {
+  switch (dtype) {
+    case WD_BF16: return run_type<__nv_bfloat16>(a, s);
+    case WD_FP16: return run_type<__half>(a, s);
+    default: return run_type<float>(a, s);
+  }
+}
+
+}  // namespace wd

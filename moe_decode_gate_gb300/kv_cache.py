@@ -31,6 +31,30 @@ def wd_kv_page_bytes(layers: int, kv_heads: int, head_dim: int, page_size: int) 
     return int(lib().wd_kv_page_bytes(layers, kv_heads, head_dim, page_size))
 
 
+def rotation_table(positions: int, rot: int, base: float = 10000.0, frequencies=None, scale: float = 1.0,
+                   device="cuda"):
+    """cos_sin of ``KVCache.append_rotated``: FP32 [positions, rot], row p the cosines and then the sines of the
+    angles p * frequencies[i], i < rot / 2, times ``scale``.
+
+    ``frequencies`` (a sequence or tensor of rot / 2 angles per position) defaults to base ** (-2 i / rot).  Angles
+    are taken in 64 bits, so that far positions are as exact as near ones."""
+    if rot < 16 or rot % 16 or positions < 1:
+        raise ValueError(f"unsupported rotation: {positions} positions, {rot} channels")
+    if frequencies is None:
+        f = base ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+    else:
+        f = torch.as_tensor(frequencies, dtype=torch.float64, device=device)
+        if f.shape != (rot // 2,):
+            raise ValueError(f"frequencies must be {rot // 2} numbers")
+    table = torch.empty(positions, rot, dtype=torch.float32, device=device)
+    for a in range(0, positions, 65536):
+        b = min(positions, a + 65536)
+        angle = torch.arange(a, b, dtype=torch.float64, device=device)[:, None] * f
+        table[a:b, :rot // 2] = scale * angle.cos()
+        table[a:b, rot // 2:] = scale * angle.sin()
+    return table
+
+
 class KVCache:
     """Keys and values of ``slots`` sequences in pages of ``page_size`` tokens, MXFP4.
 
@@ -231,6 +255,66 @@ class KVCache:
             _check("wd_kv_append", st)
         self._keep(stream, k, v, seqs, q_start, values)
         return values.unbind(0) if return_values else None
+
+    def append_rotated(self, layer, q, k, v, cos_sin, seqs=None, q_start=None, paired=False, return_values=False,
+                       q_out=None, stream=None):
+        """``append``, with queries and keys rotated by their positions on the way.
+
+        q: [tokens, q_heads, head_dim] of k's type, any strides with contiguous channels (None: keys and values
+        alone); k, v, seqs, q_start as in ``append``.  cos_sin FP32 [positions, rot], as ``rotation_table`` makes
+        it: the cosines and then the sines of a position's rot / 2 angles.  The first ``rot`` channels of each
+        head are turned, channels i and i + rot / 2 together, or with ``paired`` 2i and 2i + 1.  Returns the turned queries
+        (in ``q_out`` if given, which may be q), and with ``return_values`` what the cache now holds, (q, k, v);
+        tokens of no entry, and those at positions that cos_sin does not have, are undefined in them."""
+        dtype, shape = k.dtype, k.shape
+        code = _DTYPES.get(dtype)
+        if code is None or len(shape) != 3 or shape[1] != self.kv_heads or \
+                shape[2] != self.head_dim or k.device != self.device:
+            self._refuse("k", k, self.kv_heads, _DTYPES)
+        if v.dtype is not dtype or v.shape != shape or v.device != self.device:
+            raise ValueError("v must have k's shape and type, on its device")
+        k_token, k_head, k_channel = k.stride()
+        v_token, v_head, v_channel = v.stride()
+        if k_channel != 1 or v_channel != 1:
+            raise ValueError("k and v must have contiguous channels")
+        tokens = shape[0]
+        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or cos_sin.device != self.device or \
+                not cos_sin.is_contiguous():
+            raise ValueError(f"cos_sin must be contiguous FP32 [positions, rot] on {self.device}")
+        positions, rot = cos_sin.shape
+        heads = q_token = q_head = 0
+        q_from = q_to = None
+        if q is not None:
+            if q.dtype is not dtype or q.dim() != 3 or q.shape[0] != tokens or q.shape[2] != self.head_dim or \
+                    q.device != self.device:
+                raise ValueError(f"q must be [{tokens}, heads, {self.head_dim}] of k's type, on its device")
+            q_token, q_head, q_channel = q.stride()
+            if q_channel != 1:
+                raise ValueError("q must have contiguous channels")
+            heads, q_from = q.shape[1], q.data_ptr()
+            if q_out is None:
+                q_out = self._output(q.shape, dtype, stream)
+            elif q_out.shape != q.shape or q_out.dtype is not dtype or not q_out.is_contiguous() or \
+                    q_out.device != self.device:
+                raise ValueError("q_out must be contiguous, of q's shape and type")
+            q_to = q_out.data_ptr()
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        s, qs, n = self._entries(seqs, q_start, tokens)
+        if return_values:
+            values = self._output((2, *shape), dtype, stream)
+            k_to = values.data_ptr()
+            v_to = k_to + values.nbytes // 2
+        else:
+            values = k_to = v_to = None
+        st = self._lib.wd_kv_append_rotated(
+            self._ref, layer, q_from, k.data_ptr(), v.data_ptr(), code, q_token, q_head, heads, k_token, k_head,
+            v_token, v_head, q_to, k_to, v_to, cos_sin.data_ptr(), positions, rot, paired, s, qs, n, tokens,
+            self._stream(stream))
+        if st:
+            _check("wd_kv_append_rotated", st)
+        self._keep(stream, q, k, v, cos_sin, seqs, q_start, q_out, values)
+        return (q_out, *values.unbind(0)) if return_values else q_out
 
     def attention(self, layer, q, seqs=None, q_start=None, max_q=0, scale=None, window=0, out=None,
                   return_lse=False, stream=None):
