@@ -1,12 +1,12 @@
 // wd_logits.cu - penalties, biases, temperature and masks on logits (declared
 // in include/wd_step.h).
 //
-// One pass: a CTA takes a slice of one row's vocabulary, counts in shared memory how often the row's
-// history names each of its tokens (every CTA of a row reads the whole history, which is
-// small beside the logits and comes from L2), notes which bias is the last for each, and then
-// streams its logits through: counts, biases and mask are looked up beside them. Nothing is
-// written but the result, no counts live from call to call, and counting whole numbers gives the same sums
-// in any order. Bytes bound it where rows are many, the history's scan where they are few.
+// One pass: a CTA takes a slice of one row's vocabulary, with its logits and their bits of the mask in registers. While
+// they are on their way it counts in shared memory how often the row's history names each of its
+// tokens (every CTA of a row reads the whole history, which is small beside the logits and comes from
+// L2) and notes which bias is the last for each. Nothing is written but the result, no counts live from call to call,
+// and counting whole numbers gives the same sums in any order. Bytes bound it where rows are many, the
+// history's scan where they are few.
 #include "wd_device.cuh"
 #include "wd_step.cuh"
 #include "wd_vec.cuh"
@@ -15,11 +15,10 @@ namespace wd {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFour = 4;               // elements of an access
-constexpr int kMinSlice = 1024;        // tokens of a CTA: one access to a thread
-constexpr int kMaxSlice = 4096;        // two arrays of it are 32 KB: seven CTAs to an SM
-constexpr int kCtasWanted = 4 * 152;   // for which slices are made smaller
-constexpr uint32_t kPrompt = 1u << 31;  // of a count: the prompt has the token
+constexpr int kFour = 4;                     // elements of an access
+constexpr int kUnit = kThreads * kFour;      // tokens of a slice: this, twice or four times
+constexpr int kCtasWanted = 4 * 152;         // for which slices are made smaller
+constexpr uint32_t kPrompt = 1u << 31;       // of a count: the prompt has the token
 constexpr uint32_t kAnswer = kPrompt - 1;
 
 __device__ __forceinline__ float to_float(float x) { return x; }
@@ -37,55 +36,111 @@ struct alignas(sizeof(T) * kFour) Four {
 // What a row's tokens go through.
 struct Row {
   float repetition, presence, frequency, scale;
-  const float* bias;      // the values of the row's biases
-  const int32_t* mask;    // its words
-  bool counts, biases;    // whether the slice has some
+  const float* bias;    // the values of the row's biases
+  const int32_t* mask;  // its words, null: all allowed
 };
 
-// Token `at` of the slice. count: how often its history has each; named: 1 + the last bias of each.
-__device__ __forceinline__ float adjusted(const Row& r, const uint32_t* count, const int32_t* named, float l, int at,
-                                          bool allowed) {
-  if (r.counts) {
-    const uint32_t c = count[at];
-    if (c) {
-      l = l > 0.f ? l / r.repetition : l * r.repetition;
-      const uint32_t n = c & kAnswer;
-      if (n) l -= (float)n * r.frequency + r.presence;
-    }
+// A logit with its token's count and 1 + its last bias (0: none).
+__device__ __forceinline__ float penalised(const Row& r, float l, uint32_t count, uint32_t named) {
+  if (count) {
+    l = l > 0.f ? l / r.repetition : l * r.repetition;
+    const uint32_t n = count & kAnswer;
+    if (n) l -= (float)n * r.frequency + r.presence;
   }
-  if (r.biases) {
-    const int e = named[at];
-    if (e) l += r.bias[e - 1];
-  }
-  l *= r.scale;
-  return allowed ? l : -INFINITY;
+  if (named) l += r.bias[named - 1];
+  return l;
 }
 
-// Slice `blockIdx.x % slices` of row `blockIdx.x / slices`. kVec: input and output of a row reach
-// the alignment of four elements at the same token.
-template <typename T, typename U, bool kVec>
-__global__ void __launch_bounds__(kThreads) adjust_logits(const LogitsArgs a, int slices, int slice) {
-  extern __shared__ uint32_t shared[];
+// The tokens of a row's history that are in [from, from + n), counted at `count`.
+__device__ __forceinline__ void count_tokens(const int32_t* tokens, int length, int prompt, int from, int n, uint32_t* count) {
+  const auto one = [&](int token, int i) {
+    const unsigned at = (unsigned)token - (unsigned)from;
+    if (at < (unsigned)n) {
+      if (i >= prompt)
+        atomicAdd(&count[at], 1u);
+      else if (!(count[at] & kPrompt))
+        atomicOr(&count[at], kPrompt);
+    }
+  };
+  // up to the first aligned one, then four to an access and four accesses on their way at a time
+  const int head = min(length, (int)((4 - (reinterpret_cast<uintptr_t>(tokens) >> 2) % 4) % 4));
+  const int fours = (length - head) / 4;
+  const int4* aligned = reinterpret_cast<const int4*>(tokens + head);
+  for (int i = threadIdx.x; i < fours; i += 4 * kThreads) {
+    int4 t[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      t[j] = i + j * kThreads < fours ? aligned[i + j * kThreads] : make_int4(-1, -1, -1, -1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = head + 4 * (i + j * kThreads);
+      one(t[j].x, at);
+      one(t[j].y, at + 1);
+      one(t[j].z, at + 2);
+      one(t[j].w, at + 3);
+    }
+  }
+  const int rest = length - head - 4 * fours;
+  if ((int)threadIdx.x < head + rest) {
+    const int i = (int)threadIdx.x < head ? threadIdx.x : threadIdx.x + 4 * fours;
+    one(tokens[i], i);
+  }
+}
+
+// Slice `blockIdx.x % slices` of row `blockIdx.x / slices`, kPer fours of tokens to a thread. kVec: input and output of a
+// row reach the alignment of four elements at the same token; slices begin there. The first one has what is
+// before that, too, and the one of the last four what is behind it.
+template <typename T, typename U, int kPer, bool kVec>
+__global__ void __launch_bounds__(kThreads) adjust_logits(const LogitsArgs a, int slices) {
+  constexpr int kSlice = kPer * kUnit;
+  constexpr int kPlaces = kSlice + 2 * kFour;  // of an array in shared memory: place 4 is the slice's first four
+  extern __shared__ uint4 shared[];
   const int b = blockIdx.x / slices, part = blockIdx.x % slices;
   const T* in = static_cast<const T*>(a.logits) + b * a.stride;
   U* out = static_cast<U*>(a.out) + b * a.out_stride;
-  // tokens [from, to): slices begin where four elements are aligned, the first with what is before that
-  const int lead = kVec ? (int)((kFour - (reinterpret_cast<uintptr_t>(in) / sizeof(T)) % kFour) % kFour) : 0;
-  const int from = part == 0 ? 0 : lead + part * slice;
-  const int to = part == slices - 1 ? a.V : min(a.V, lead + (part + 1) * slice);
-  const int n = to - from;
-  uint32_t* count = shared;
-  int32_t* named = reinterpret_cast<int32_t*>(shared + (a.history.tokens ? slice + kFour : 0));
+  const int lead =
+      kVec ? min(a.V, (int)((kFour - (reinterpret_cast<uintptr_t>(in) / sizeof(T)) % kFour) % kFour)) : 0;
+  const int last = lead + (a.V - lead) / kFour * kFour;  // behind the row's last four
+  const int begin = lead + part * kSlice, end = min(begin + kSlice, last);
+  const int closing = min((last - lead) / kSlice, slices - 1);  // the slice that the tokens behind the last four go to
+  const int from = part == 0 ? 0 : begin, to = part == closing ? a.V : end;
+  uint32_t* count = reinterpret_cast<uint32_t*>(shared);
+  int32_t* named = reinterpret_cast<int32_t*>(count + (a.history.tokens ? kPlaces : 0));
   grid_dependency_wait();  // nothing above reads what an earlier kernel may write
   grid_launch_dependents();
-  if (n <= 0) return;
+  if (to <= from) return;
   Row r;
+  r.mask = a.mask ? a.mask + b * a.mask_stride : nullptr;
+  // this thread's logits, and four bits of the mask for each access
+  Four<T> x[kPer];
+  uint32_t allowed = 0xFFFFFFFFu;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int v = begin + kFour * (threadIdx.x + j * kThreads);
+    if (v >= end) continue;
+    if constexpr (kVec) {
+      x[j] = *reinterpret_cast<const Four<T>*>(in + v);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kFour; ++k) x[j].v[k] = in[v + k];
+    }
+  }
+  if (r.mask) {
+    allowed = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int v = begin + kFour * (threadIdx.x + j * kThreads);
+      if (v >= end) continue;
+      const uint32_t word = r.mask[v >> 5];
+      const uint32_t next = (v & 31) > 32 - kFour ? r.mask[(v >> 5) + 1] : 0u;
+      allowed |= (__funnelshift_r(word, next, v & 31) & 15u) << (kFour * j);
+    }
+  }
   r.repetition = a.repetition ? a.repetition[b] : 1.f;
   r.presence = a.presence ? a.presence[b] : 0.f;
   r.frequency = a.frequency ? a.frequency[b] : 0.f;
   const float t = a.temperature ? a.temperature[b] : 1.f;
   r.scale = t > 0.f ? 1.f / t : 1.f;
-  r.mask = a.mask ? a.mask + b * a.mask_stride : nullptr;
   // the row's history, if it has one and its penalties are any
   const int32_t* tokens = nullptr;
   int length = 0, prompt = 0;
@@ -103,58 +158,65 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(const LogitsArgs a, in
     bias_to = a.bias_start[b + 1];
     if (bias_from < 0 || bias_to > a.biases) bias_to = bias_from;
   }
-  r.counts = length > 0;
-  r.biases = bias_to > bias_from;
   r.bias = a.bias_values + bias_from;
-  if (r.counts || r.biases) {
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      if (r.counts) count[i] = 0;
-      if (r.biases) named[i] = 0;
+  const bool counts = length > 0, biases = bias_to > bias_from;
+  if (counts || biases) {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < kPlaces / kFour; i += kThreads) {
+      if (counts) reinterpret_cast<uint4*>(count)[i] = zero;
+      if (biases) reinterpret_cast<uint4*>(named)[i] = zero;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < length; i += kThreads) {
-      const unsigned at = (unsigned)tokens[i] - (unsigned)from;
-      if (at < (unsigned)n) {
-        if (i < prompt)
-          atomicOr(&count[at], kPrompt);
-        else
-          atomicAdd(&count[at], 1u);
-      }
-    }
+    const int place = kFour - (begin - from);  // of token `from`
+    if (counts) count_tokens(tokens, length, prompt, from, to - from, count + place);
     for (int i = bias_from + threadIdx.x; i < bias_to; i += kThreads) {
       const unsigned at = (unsigned)a.bias_ids[i] - (unsigned)from;
-      if (at < (unsigned)n) atomicMax(&named[at], i - bias_from + 1);
+      if (at < (unsigned)(to - from)) atomicMax(&named[place + at], i - bias_from + 1);
     }
     __syncthreads();
   }
-  const auto bit = [&](int v) { return !r.mask || (r.mask[v >> 5] >> (v & 31)) & 1; };
-  if constexpr (kVec) {
-    const int head = part == 0 ? min(lead, n) : 0;
-    const int fours = (n - head) / kFour;
-    for (int i = threadIdx.x; i < fours; i += kThreads) {
-      const int at = head + kFour * i, v = from + at;
-      const Four<T> x = *reinterpret_cast<const Four<T>*>(in + v);
-      uint32_t bits = 15u;
-      if (r.mask) {
-        const uint32_t w = r.mask[v >> 5];
-        const uint32_t next = (v & 31) > 32 - kFour ? r.mask[(v >> 5) + 1] : 0u;
-        bits = __funnelshift_r(w, next, v & 31);
-      }
-      Four<U> y;
 #pragma unroll
-      for (int k = 0; k < kFour; ++k) put(&y.v[k], adjusted(r, count, named, to_float(x.v[k]), at + k, bits >> k & 1));
+  for (int j = 0; j < kPer; ++j) {
+    const int f = threadIdx.x + j * kThreads, v = begin + kFour * f;
+    if (v >= end) continue;
+    float l[kFour];
+#pragma unroll
+    for (int k = 0; k < kFour; ++k) l[k] = to_float(x[j].v[k]);
+    uint4 c = make_uint4(0, 0, 0, 0), e = c;
+    if (counts) c = reinterpret_cast<const uint4*>(count)[f + 1];
+    if (biases) e = reinterpret_cast<const uint4*>(named)[f + 1];
+    if (c.x | c.y | c.z | c.w | e.x | e.y | e.z | e.w) {
+      l[0] = penalised(r, l[0], c.x, e.x);
+      l[1] = penalised(r, l[1], c.y, e.y);
+      l[2] = penalised(r, l[2], c.z, e.z);
+      l[3] = penalised(r, l[3], c.w, e.w);
+    }
+    Four<U> y;
+#pragma unroll
+    for (int k = 0; k < kFour; ++k) put(&y.v[k], allowed >> (kFour * j + k) & 1 ? l[k] * r.scale : -INFINITY);
+    if constexpr (kVec) {
       *reinterpret_cast<Four<U>*>(out + v) = y;
+    } else {
+#pragma unroll
+      for (int k = 0; k < kFour; ++k) out[v + k] = y.v[k];
     }
-    // what is before and behind the aligned ones: at most three each
-    const int rest = n - head - kFour * fours;
-    if ((int)threadIdx.x < head + rest) {
-      const int at = (int)threadIdx.x < head ? threadIdx.x : threadIdx.x + kFour * fours;
-      put(&out[from + at], adjusted(r, count, named, to_float(in[from + at]), at, bit(from + at)));
-    }
-  } else {
-    for (int at = threadIdx.x; at < n; at += kThreads)
-      put(&out[from + at], adjusted(r, count, named, to_float(in[from + at]), at, bit(from + at)));
   }
+  // the loose tokens, at most three before the first four and three behind the last
+  const int before = begin - from > 0 ? min(begin, to) - from : 0, behind = max(0, to - max(end, begin));
+  if ((int)threadIdx.x < before + behind) {
+    const int v = (int)threadIdx.x < before ? from + threadIdx.x : max(end, begin) + threadIdx.x - before;
+    const int at = kFour + v - begin;
+    const float l = penalised(r, to_float(in[v]), counts ? count[at] : 0u, biases ? named[at] : 0u);
+    put(&out[v], !r.mask || (r.mask[v >> 5] >> (v & 31) & 1) ? l * r.scale : -INFINITY);
+  }
+}
+
+template <typename T, typename U, int kPer>
+cudaError_t run_slices(const LogitsArgs& a, bool vec, cudaStream_t s) {
+  const int slices = (a.V + kPer * kUnit - 1) / (kPer * kUnit);
+  const int arrays = (a.history.tokens ? 1 : 0) + (a.bias_start ? 1 : 0);
+  return launch_dependent(vec ? adjust_logits<T, U, kPer, true> : adjust_logits<T, U, kPer, false>, a.B * slices, kThreads,
+                          arrays * 4 * (kPer * kUnit + 2 * kFour), s, a, slices);
 }
 
 template <typename T, typename U>
@@ -163,14 +225,10 @@ cudaError_t run(const LogitsArgs& a, cudaStream_t s) {
   const auto same = [](long long x, long long y) { return ((x - y) % kFour) == 0; };
   const bool vec = same(place(a.logits, sizeof(T)), place(a.out, sizeof(U))) && (a.B == 1 || same(a.stride, a.out_stride));
   // Large slices where the rows fill the GPU (each reads the history once more), smaller ones where they do not.
-  int slice = kMaxSlice;
-  while (slice > kMinSlice && (long long)a.B * ((a.V + slice - 1) / slice) < kCtasWanted) slice /= 2;
-  const int slices = (a.V + slice - 1) / slice;
-  const long long ctas = (long long)a.B * slices;
-  const int arrays = (a.history.tokens ? 1 : 0) + (a.bias_start ? 1 : 0);
-  const int bytes = arrays * 4 * (slice + kFour);
-  const auto kernel = vec ? adjust_logits<T, U, true> : adjust_logits<T, U, false>;
-  return launch_dependent(kernel, (int)ctas, kThreads, bytes, s, a, slices, slice);
+  const auto ctas = [&](int per) { return (long long)a.B * ((a.V + per * kUnit - 1) / (per * kUnit)); };
+  if (ctas(4) >= kCtasWanted) return run_slices<T, U, 4>(a, vec, s);
+  if (ctas(2) >= kCtasWanted) return run_slices<T, U, 2>(a, vec, s);
+  return run_slices<T, U, 1>(a, vec, s);
 }
 
 template <typename T>

@@ -2,15 +2,17 @@
 //
 // A warp takes a token. Its lanes hold the experts in order: a group of experts (there are 1 to 32)
 // has 32 / groups lanes, rounded down to a power of two, and each of them kV consecutive ones, so that
-// a group's value is a few shuffles within its lanes and the first lane of several with equal
-// keys has the lowest index. K times the warp's largest key is found (one redux on keys
-// whose integer order is their order), taken by the first lane that has it, and struck out.
+// a group's value is a few shuffles within its lanes. K times the warp's largest key is found by one
+// redux over keys whose integer order is their order, and struck out.
 //
-// Keys are exact where no bias and no sums of groups are asked for: they are the logits. Else they
-// carry FP32's errors (margin() below); a token of which two keys that the choice hangs on are nearer
-// than that is chosen again from keys in 64 bits, which only those experts need that can be chosen.
+// Keys are exact where no bias and no sums of groups are asked for: they are the logits. Those of 16 bits
+// share a word with their expert's index, so that one redux gives both, the lowest index first of equal keys; a lane
+// sorts its words once and only its first one is looked at. Other keys need a second redux for the index.
+// Keys of scores and biases carry FP32's errors (margin below); a token of which two keys that the choice
+// hangs on are nearer than that is chosen again from keys in 64 bits: those of the K and
+// of what is as near to the last of them, one to a lane, or all of them where groups are in doubt.
 //
-// Bounded by the instructions of a token (about 25 for each of the K rounds), not by its bytes.
+// Bounded by the instructions of a token, not by its bytes.
 #include "wd_device.cuh"
 #include "wd_step.cuh"
 #include "wd_vec.cuh"
@@ -48,6 +50,20 @@ __device__ __forceinline__ unsigned long long largest(unsigned long long v) {
   const uint32_t lo = __reduce_max_sync(kAll, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
   return (unsigned long long)hi << 32 | lo;
 }
+
+// The same of 16-bit numbers, given as floats.
+__device__ __forceinline__ uint32_t half_order(float x, __nv_bfloat16) { return order_of(x) >> 16; }
+__device__ __forceinline__ float half_value(uint32_t u, __nv_bfloat16) {
+  return __uint_as_float((u << 16) ^ ((u & 0x8000u) ? 0x80000000u : 0xFFFF0000u));
+}
+__device__ __forceinline__ uint32_t half_order(float x, __half) {
+  const uint32_t u = __half_as_ushort(__float2half_rn(x + 0.f));
+  return (u ^ ((u & 0x8000u) ? 0xFFFFu : 0x8000u)) & 0xFFFFu;
+}
+__device__ __forceinline__ float half_value(uint32_t u, __half) {
+  return __half2float(__ushort_as_half((unsigned short)(u ^ ((u & 0x8000u) ? 0x8000u : 0xFFFFu))));
+}
+__device__ __forceinline__ uint32_t half_order(float, float) { return 0; }  // (no 16 bits, not used)
 
 // Where the experts of a lane begin, and how many it has.
 struct Span {
@@ -89,44 +105,72 @@ __device__ __forceinline__ bool group_chosen(F value, int group, int groups, int
   return before < top;
 }
 
-// The K largest keys of the warp, largest first: entry r in lane r % 32, place r / 32 of `ids`. Keys are struck
-// out of k. With `check` (keys of 32 bits), whether two neighbours of the order, the first that was not taken
-// among them, are nearer than `margin`.
+// The `n` largest keys of the warp, largest first: entry r in lane r % 32, place r / 32 of `ids`. Keys are
+// struck out of k. With a margin, goes on until the next key is further than that below the last one: returns how many it
+// took, kMany if that is more than 64; `near`: whether two neighbours of the order are nearer than the margin.
+constexpr int kMany = 65;
+
 template <int kV, typename Key>
-__device__ __forceinline__ bool take(Key (&k)[kV], const Span& mine, int K, int lane, bool check, float margin,
-                                     int (&ids)[2], uint32_t (&keys)[2]) {
-  bool near = false;
+__device__ __forceinline__ int take(Key (&k)[kV], const Span& mine, int n, int lane, float margin, bool& near,
+                                    int (&ids)[2]) {
   Key last = 0;
-  for (int r = 0; r < K + check; ++r) {
+  for (int r = 0;; ++r) {
+    if (r >= n && !(margin > 0.f)) return r;
     Key top = k[0];
 #pragma unroll
     for (int i = 1; i < kV; ++i) top = top < k[i] ? k[i] : top;
     const Key all = largest(top);
-    if (check && r && all) near |= value_of((uint32_t)last) - value_of((uint32_t)all) < margin;
-    if (r == K) break;
+    if (margin > 0.f && r > 0) {
+      const bool close = all && value_of((uint32_t)last) - value_of((uint32_t)all) < margin;
+      if (r >= n && (!close || r == 64)) return close ? kMany : r;
+      near |= close;
+    }
     last = all;
-    const int winner = __ffs(__ballot_sync(kAll, top == all)) - 1;
-    int at = 0;
+    int at = 1 << 20;  // of this lane's experts that have the key, the first
 #pragma unroll
     for (int i = kV - 1; i >= 0; --i)
-      if (k[i] == all) at = i;
-    if (lane == winner) {
+      if (k[i] == all) at = mine.first + i;
+    const int id = __reduce_min_sync(kAll, at);
 #pragma unroll
-      for (int i = 0; i < kV; ++i)
-        if (i == at) k[i] = 0;
-    }
-    const int id = __shfl_sync(kAll, mine.first + at, winner);
-    if (lane == (r & 31)) {
-      if (r < 32) {
-        ids[0] = id;
-        keys[0] = (uint32_t)all;
-      } else {
-        ids[1] = id;
-        keys[1] = (uint32_t)all;
-      }
-    }
+    for (int i = 0; i < kV; ++i)
+      if (mine.first + i == id) k[i] = 0;
+    if (lane == r) ids[0] = id;
+    if (lane + 32 == r) ids[1] = id;
   }
-  return near;
+}
+
+// Descending order of a lane's words (Batcher's merge exchange).
+template <int kV>
+__device__ __forceinline__ void sort_down(uint32_t (&k)[kV]) {
+#pragma unroll
+  for (int p = 1; p < kV; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < kV; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < kV && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const uint32_t a = k[i + j], b = k[i + j + q];
+            k[i + j] = max(a, b);
+            k[i + j + q] = min(a, b);
+          }
+}
+
+// The K largest words, as take(): of words that hold key and index no two are equal.
+template <int kV>
+__device__ __forceinline__ void take_words(uint32_t (&k)[kV], int K, int lane, uint32_t (&words)[2]) {
+  sort_down<kV>(k);
+  for (int r = 0; r < K; ++r) {
+    const uint32_t all = largest(k[0]);
+    if (k[0] == all) {
+#pragma unroll
+      for (int i = 0; i + 1 < kV; ++i) k[i] = k[i + 1];
+      k[kV - 1] = 0;
+    }
+    if (lane == r) words[0] = all;
+    if (lane + 32 == r) words[1] = all;
+  }
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
@@ -136,56 +180,89 @@ __device__ __forceinline__ float exp_below(float x, float top) {
   return x == -INFINITY ? 0.f : x == top ? 1.f : expf(x - top);
 }
 
-// The token's choice from keys in 64 bits. Experts whose FP32 key is below `least` are out of question
-// unless all are needed for the groups. Rare, so it is kept out of the way of the other registers.
+// The score's key in 64 bits of an expert whose logit is l. `top`: the token's largest logit, `sum`: of exp(l - top).
+__device__ __forceinline__ double exact_key(const RouteArgs& a, float l, int id, float top, double sum) {
+  if (!(l > -INFINITY)) return -(double)INFINITY;
+  const double score = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : l == top ? 1.0 / sum : exp((double)l - (double)top) / sum;
+  const double key = score + (a.bias ? (double)a.bias[id] : 0.0);
+  return key == key ? key : -(double)INFINITY;
+}
+
+// The sum of exp(l - top) over all experts, in 64 bits; not needed for sigmoids.
+template <typename T>
+__device__ __forceinline__ double exact_sum(const RouteArgs& a, const T* x, const Span& mine, float top) {
+  if (a.sigmoid) return 1.0;
+  double sum = 0.0;
+  for (int i = 0; i < mine.n; ++i) {
+    const float l = to_float(x[mine.first + i]);
+    if (l > -INFINITY) sum += l == top ? 1.0 : exp((double)l - (double)top);
+  }
+  for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
+  return sum;
+}
+
+// The order of the `n` <= 64 candidates that take() found, from keys in 64 bits. Rare, so it is kept out of the way
+// of the other registers.
+template <typename T>
+__device__ __noinline__ void order_again(const RouteArgs& a, const T* x, const Span mine, int lane, float top, int n,
+                                         int (&ids)[2]) {
+  const double sum = exact_sum(a, x, mine, top);
+  unsigned long long key[2];
+  int rank[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    key[e] = 0;
+    if (lane + 32 * e < n) key[e] = order_of(exact_key(a, to_float(x[ids[e]]), ids[e], top, sum));
+  }
+  for (int r = 0; r < n; ++r) {
+    const unsigned long long other = __shfl_sync(kAll, key[r >> 5], r & 31);
+    const int id = __shfl_sync(kAll, ids[r >> 5], r & 31);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) rank[e] += other > key[e] || (other == key[e] && id < ids[e]);
+  }
+  int sorted[2] = {0, 0};
+  for (int r = 0; r < n; ++r) {
+    const int to = __shfl_sync(kAll, rank[r >> 5], r & 31);
+    const int id = __shfl_sync(kAll, ids[r >> 5], r & 31);
+    if (to == lane) sorted[0] = id;
+    if (to == lane + 32) sorted[1] = id;
+  }
+  ids[0] = sorted[0];
+  ids[1] = sorted[1];
+}
+
+// The token's whole choice from keys in 64 bits.
 template <typename T, int kV>
 __device__ __noinline__ void choose_again(const RouteArgs& a, const T* x, const Span mine, const Lanes lanes, int lane,
-                                          float least, float top, bool all_needed, bool chosen, int (&ids)[2]) {
+                                          float top, int (&ids)[2]) {
   const int group = lane / lanes.per_group;
+  const double sum = exact_sum(a, x, mine, top);
   unsigned long long k[kV];
-  double sum = 0.0, best = -INFINITY, second = -INFINITY;
-  const bool sums = a.groups > 1 && a.group_best == 2;
-  if (!a.sigmoid) {
-    for (int i = 0; i < mine.n; ++i) {
-      const float l = to_float(x[mine.first + i]);
-      if (l > -INFINITY) sum += l == top ? 1.0 : exp((double)l - (double)top);
-    }
-    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
-  }
+  double best = -INFINITY, second = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kV; ++i) {
     k[i] = 0;
     if (i >= mine.n) continue;
     const float l = to_float(x[mine.first + i]);
-    const float b = a.bias ? a.bias[mine.first + i] : 0.f;
-    double key = -INFINITY;
-    if (l > -INFINITY) {
-      const float rough = (a.sigmoid ? sigmoid(l) : exp_below(l, top) / (float)sum) + b;
-      if (all_needed || rough >= least) {
-        const double score = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : l == top ? 1.0 / sum : exp((double)l - (double)top) / sum;
-        key = score + (double)b;
-        if (!(key == key)) key = -INFINITY;
-      }
-    }
+    const double key = exact_key(a, l, mine.first + i, top, sum);
     second = second > key ? second : best < key ? best : key;
     best = best < key ? key : best;
     // where nothing is added, keys are ordered by the logits
     k[i] = order_of(a.bias ? key : (double)(l > -INFINITY ? l : -INFINITY));
   }
   if (a.groups > 1) {
-    if (all_needed) {
-      const double value = sums ? group_value(best, second, lanes.per_group, 2) : group_value(best, second, lanes.per_group, 1);
-      chosen = group_chosen(group < a.groups ? value : -(double)INFINITY, group, a.groups, lanes.per_group, a.top_groups);
-    }
+    const double value = group_value(best, second, lanes.per_group, a.group_best);
+    const bool chosen = group_chosen(group < a.groups ? value : -(double)INFINITY, group, a.groups, lanes.per_group, a.top_groups);
     if (!chosen)
 #pragma unroll
       for (int i = 0; i < kV; ++i) k[i] = 0;
   }
-  uint32_t unused[2];
-  take<kV>(k, mine, a.K, lane, false, 0.f, ids, unused);
+  bool none;
+  take<kV>(k, mine, a.K, lane, 0.f, none, ids);
 }
 
-template <typename T, int kV, bool kVec>
+// kWords: logits of 16 bits, and no bias.
+template <typename T, int kV, bool kVec, bool kWords>
 __global__ void __launch_bounds__(32 * kWarps) route(const RouteArgs a, const Lanes lanes) {
   const int lane = threadIdx.x & 31;
   const int token = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -244,7 +321,12 @@ __global__ void __launch_bounds__(32 * kWarps) route(const RouteArgs a, const La
     second = fmaxf(second, fminf(best, key));
     best = fmaxf(best, key);
     // without a bias the choice goes by the logits even where the groups' goes by sums of scores
-    k[i] = i < mine.n ? order_of(a.bias ? key : l[i]) : 0u;
+    if (i >= mine.n)
+      k[i] = 0;
+    else if (kWords)
+      k[i] = half_order(l[i], T{}) << 16 | (0xFFFFu - (mine.first + i));
+    else
+      k[i] = order_of(a.bias ? key : l[i]);
   }
   bool again = false, chosen = true;
   if (inexact) {
@@ -268,29 +350,42 @@ __global__ void __launch_bounds__(32 * kWarps) route(const RouteArgs a, const La
       for (int i = 0; i < kV; ++i) k[i] = 0;
   }
   int ids[2] = {0, 0};
-  uint32_t keys[2] = {0, 0};
-  const bool groups_again = again;
-  again |= take<kV>(k, mine, a.K, lane, a.bias != nullptr, margin, ids, keys);
-  if (again) {
-    int chosen_again[2] = {0, 0};
-    const uint32_t lowest = __shfl_sync(kAll, a.K > 32 ? keys[1] : keys[0], (a.K - 1) & 31);
-    choose_again<T, kV>(a, x, mine, lanes, lane, value_of(lowest) - 2.f * margin, top, groups_again, chosen,
-                        chosen_again);
-    ids[0] = chosen_again[0];
-    ids[1] = chosen_again[1];
-  }
-  // the weights, from the chosen experts' logits
-  float y[2], w[2] = {0.f, 0.f};
-  float high = -INFINITY;
+  float y[2] = {-INFINITY, -INFINITY}, w[2] = {0.f, 0.f};  // logits and weights of the chosen
+  if constexpr (kWords) {
+    uint32_t words[2] = {0, 0};
+    take_words<kV>(k, a.K, lane, words);
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    y[e] = -INFINITY;
-    if (lane + 32 * e < a.K) {
-      y[e] = to_float(x[ids[e]]);
-      if (!(y[e] == y[e])) y[e] = -INFINITY;
+    for (int e = 0; e < 2; ++e)
+      if (lane + 32 * e < a.K) {
+        ids[e] = 0xFFFF - (words[e] & 0xFFFFu);
+        y[e] = half_value(words[e] >> 16, T{});
+      }
+  } else {
+    bool near = false;
+    const int n = take<kV>(k, mine, a.K, lane, a.bias ? margin : 0.f, near, ids);
+    if (n == kMany) again = true;
+    if (near && !again) {
+      int mended[2] = {ids[0], ids[1]};  // (its own, so that ids stay in registers)
+      order_again<T>(a, x, mine, lane, top, n, mended);
+      ids[0] = mended[0];
+      ids[1] = mended[1];
     }
-    high = fmaxf(high, y[e]);
   }
+  if (again) {
+    int mended[2] = {0, 0};
+    choose_again<T, kV>(a, x, mine, lanes, lane, top, mended);
+    ids[0] = mended[0];
+    ids[1] = mended[1];
+  }
+  if (!kWords || again) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (lane + 32 * e < a.K) {
+        y[e] = to_float(x[ids[e]]);
+        if (!(y[e] == y[e])) y[e] = -INFINITY;
+      }
+  }
+  float high = fmaxf(y[0], y[1]);
   high = warp_max(high);
   float total = 0.f;
 #pragma unroll
@@ -325,7 +420,10 @@ cudaError_t run(const RouteArgs& a, const Lanes lanes, cudaStream_t s) {
   const bool vec = lanes.per_lane == kV && a.groups * lanes.per_group == 32 && a.E == 32 * kV &&
                    reinterpret_cast<uintptr_t>(a.logits) % kBytes == 0 && a.stride * (long long)sizeof(T) % kBytes == 0;
   const int ctas = (a.tokens + kWarps - 1) / kWarps;
-  return launch_dependent(vec ? route<T, kV, true> : route<T, kV, false>, ctas, 32 * kWarps, 0, s, a, lanes);
+  constexpr bool kWords = sizeof(T) == 2;
+  const auto kernel = kWords && !a.bias ? (vec ? route<T, kV, true, kWords> : route<T, kV, false, kWords>)
+                                        : (vec ? route<T, kV, true, false> : route<T, kV, false, false>);
+  return launch_dependent(kernel, ctas, 32 * kWarps, 0, s, a, lanes);
 }
 
 template <typename T>
