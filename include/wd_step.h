@@ -102,7 +102,7 @@ typedef struct wd_history {
 
 /* What is done to logits before a token is chosen.  For each row b and token v:
  *
- *   1. v in the prompt or the answer:  l = l > 0 ? l / repetition[b] : l * repetition[b]
+ *   1. v in the prompt or the answer:  l = l > 0 ? l * (1 / repetition[b]) : l * repetition[b]
  *   2. v n > 0 times in the answer:    l = l - (n * frequency[b] + presence[b])
  *   3. v named by the row's biases:    l = l + its value (the last one, if it is named twice)
  *   4. temperature[b] > 0:             l = l * (1 / temperature[b])

@@ -10,6 +10,8 @@
 // to a thread as in wd_kv_append.cu; a key's thread reads its partner's channels too, half a rotation away.
 // The others take queries, which are most of the bytes: a thread has the 8 + 8 channels
 // of 8 pairs (16 neighbours where pairs are neighbours), so that each cosine and sine is read once for both.
+// The table's rows of a CTA's tokens stand in shared memory, and a thread's next token is on its way
+// while it turns one.
 //
 // To read and write: q in and out, k and v in, 4.25 bits a channel of them out, the table's rows.
 #include "wd_device.cuh"
@@ -43,33 +45,28 @@ __device__ __forceinline__ void put(T* dst, const Eight<T>& x) {
   }
 }
 
-template <int kN>
-__device__ __forceinline__ void load_floats(const float* p, float (&f)[kN]) {
-#pragma unroll
-  for (int k = 0; k < kN / 4; ++k) {
-    const float4 v = *reinterpret_cast<const float4*>(p + 4 * k);
-    f[4 * k] = v.x;
-    f[4 * k + 1] = v.y;
-    f[4 * k + 2] = v.z;
-    f[4 * k + 3] = v.w;
-  }
-}
-
-__device__ __forceinline__ float first_of(float x1, float x2, float c, float s) {
-  return __fsub_rn(__fmul_rn(x1, c), __fmul_rn(x2, s));
-}
-__device__ __forceinline__ float second_of(float x1, float x2, float c, float s) {
-  return __fadd_rn(__fmul_rn(x2, c), __fmul_rn(x1, s));
+// A pair's first and second channel: products and sums rounded one by one, never contracted (as pairs in packed
+// instructions, mul.rn.f32x2 and add.rn.f32x2, they are).
+__device__ __forceinline__ void turn(float& x1, float& x2, float c, float s) {
+  const float a = x1, b = x2;
+  x1 = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  x2 = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
 }
 
 // Four neighbouring pairs, with their cosines and sines.
-__device__ __forceinline__ void rotate_neighbours(float (&f)[8], const float (&c)[4], const float (&s)[4]) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float a = f[2 * k], b = f[2 * k + 1];
-    f[2 * k] = first_of(a, b, c[k], s[k]);
-    f[2 * k + 1] = second_of(a, b, c[k], s[k]);
-  }
+__device__ __forceinline__ void turn_neighbours(float (&f)[8], const float4 c, const float4 s) {
+  turn(f[0], f[1], c.x, s.x);
+  turn(f[2], f[3], c.y, s.y);
+  turn(f[4], f[5], c.z, s.z);
+  turn(f[6], f[7], c.w, s.w);
+}
+
+// Four pairs that are a run of first channels at x1 and one of second channels at x2.
+__device__ __forceinline__ void turn_runs(float* x1, float* x2, const float4 c, const float4 s) {
+  turn(x1[0], x2[0], c.x, s.x);
+  turn(x1[1], x2[1], c.y, s.y);
+  turn(x1[2], x2[2], c.z, s.z);
+  turn(x1[3], x2[3], c.w, s.w);
 }
 
 // The token's place, none if the table has no row for its position.
@@ -143,12 +140,30 @@ __device__ __forceinline__ void store_eight(const float (&f)[8], uint32_t top, u
   }
 }
 
+// The places of tokens [base, base + n), and the rows of the table at their positions: of eight pairs e, cosines 0 to 3
+// and 4 to 7 and sines alike are float4 e of the row's first, second, third and fourth quarter, so that a warp
+// reads each without bank conflicts.
+template <int D>
+__device__ __forceinline__ void stage(const KvRotateArgs& a, int base, int n, Place* place, float4* turns) {
+  if ((int)threadIdx.x < n) place[threadIdx.x] = rotated_place<D>(a, base + threadIdx.x);
+  __syncthreads();
+  const int eights = a.rot / 16, fours = a.rot / 4;
+  for (int i = threadIdx.x; i < n * fours; i += kThreads) {
+    const int token = i / fours, f = i - token * fours;
+    const int pos = place[token].pos;
+    if (pos < 0) continue;
+    const int quarter = (f & 1) + (f >= 2 * eights ? 2 : 0), e = (f >= 2 * eights ? f - 2 * eights : f) >> 1;
+    turns[token * fours + quarter * eights + e] = reinterpret_cast<const float4*>(a.cos_sin + (long long)pos * a.rot)[f];
+  }
+  __syncthreads();
+}
+
 // Queries of tokens [base, base + n).
 template <typename T, int D, bool kVec>
-__device__ __forceinline__ void queries(const KvRotateArgs& a, int base, int n, Place* place) {
+__device__ __forceinline__ void queries(const KvRotateArgs& a, int base, int n, Place* place, float4* turns) {
   constexpr int kPerRow = D / 16;  // threads to a token and head
   constexpr int kRowsOfThreads = kThreads / kPerRow;
-  const int half = a.rot / 2;
+  const int half = a.rot / 2, eights = a.rot / 16, fours = a.rot / 4;
   const int e = threadIdx.x % kPerRow, row0 = threadIdx.x / kPerRow;
   const bool turned = 16 * e < a.rot;  // else 16 channels that stay as they are
   // this thread's two runs of 8 channels
@@ -156,53 +171,61 @@ __device__ __forceinline__ void queries(const KvRotateArgs& a, int base, int n, 
   const int c1 = turned && !a.paired ? 8 * e + half : 16 * e + 8;
   const int at_once = max(1, kRowsOfThreads / a.q_heads);  // tokens
   const int token0 = row0 / a.q_heads;                     // (0 if there are more heads than threads for them)
-  if ((int)threadIdx.x < n) place[threadIdx.x] = rotated_place<D>(a, base + threadIdx.x);
-  __syncthreads();
-  if (token0 >= at_once) return;
-  for (int h = row0 - token0 * a.q_heads; h < a.q_heads; h += kRowsOfThreads) {
+  bool staged = false;
+  for (int h = row0 - token0 * a.q_heads; h < a.q_heads || !staged; h += kRowsOfThreads) {
+    const bool here = h < a.q_heads && token0 < at_once;
+    const T* src = static_cast<const T*>(a.q) + (base + token0) * a.q_token + h * a.q_head;
+    Eight<T> next0, next1;
+    if (here && token0 < n) {  // on their way while the places are found
+      next0 = fetch<T, kVec>(src + c0);
+      next1 = fetch<T, kVec>(src + c1);
+    }
+    if (!staged) {
+      stage<D>(a, base, n, place, turns);
+      staged = true;
+    }
+    if (!here) continue;
+    T* dst = static_cast<T*>(a.q_out) + ((long long)(base + token0) * a.q_heads + h) * D;
     for (int token = token0; token < n; token += at_once) {
-      const int pos = place[token].pos;
-      if (pos < 0) continue;
-      const T* src = static_cast<const T*>(a.q) + (base + token) * a.q_token + h * a.q_head;
-      T* dst = static_cast<T*>(a.q_out) + ((long long)(base + token) * a.q_heads + h) * D;
-      Eight<T> x0 = fetch<T, kVec>(src + c0), x1 = fetch<T, kVec>(src + c1);
-      if (turned) {
-        float c[8], s[8], f[8], g[8];
-        const float* row = a.cos_sin + (long long)pos * a.rot + 8 * e;
-        load_floats(row, c);
-        load_floats(row + half, s);
-        Widen<T>::run(x0, f);
-        Widen<T>::run(x1, g);
-        if (a.paired) {
-          const float lo_c[4] = {c[0], c[1], c[2], c[3]}, hi_c[4] = {c[4], c[5], c[6], c[7]};
-          const float lo_s[4] = {s[0], s[1], s[2], s[3]}, hi_s[4] = {s[4], s[5], s[6], s[7]};
-          rotate_neighbours(f, lo_c, lo_s);
-          rotate_neighbours(g, hi_c, hi_s);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float u = f[k], v = g[k];
-            f[k] = first_of(u, v, c[k], s[k]);
-            g[k] = second_of(u, v, c[k], s[k]);
-          }
-        }
-        x0 = narrow<T>(f);
-        x1 = narrow<T>(g);
+      Eight<T> x0 = next0, x1 = next1;
+      src += at_once * a.q_token;
+      if (token + at_once < n) {
+        next0 = fetch<T, kVec>(src + c0);
+        next1 = fetch<T, kVec>(src + c1);
       }
-      put<T, kVec>(dst + c0, x0);
-      put<T, kVec>(dst + c1, x1);
+      if (place[token].pos >= 0) {
+        if (turned) {
+          float f[8], g[8];
+          Widen<T>::run(x0, f);
+          Widen<T>::run(x1, g);
+          const float4* row = turns + token * fours + e;
+          const float4 ca = row[0], cb = row[eights], sa = row[2 * eights], sb = row[3 * eights];
+          if (a.paired) {
+            turn_neighbours(f, ca, sa);
+            turn_neighbours(g, cb, sb);
+          } else {
+            turn_runs(f, g, ca, sa);
+            turn_runs(f + 4, g + 4, cb, sb);
+          }
+          x0 = narrow<T>(f);
+          x1 = narrow<T>(g);
+        }
+        put<T, kVec>(dst + c0, x0);
+        put<T, kVec>(dst + c1, x1);
+      }
+      dst += (long long)at_once * a.q_heads * D;
     }
   }
 }
 
 // Keys and values of tokens [base, base + n).
 template <typename T, int D, bool kVec>
-__device__ __forceinline__ void keys_and_values(const KvRotateArgs& a, int base, int n, Place* place) {
+__device__ __forceinline__ void keys_and_values(const KvRotateArgs& a, int base, int n, Place* place, float4* turns) {
   constexpr int kPerRow = D / 8;  // threads to a token, head and side
   constexpr int kRowsOfThreads = kThreads / kPerRow;
   const KvView& c = a.kv.cache;
   const int rows = 2 * c.kv_heads;  // of a token: the heads' K, then the heads' V
-  const int half = a.rot / 2;
+  const int half = a.rot / 2, eights = a.rot / 16, fours = a.rot / 4;
   const int e = threadIdx.x % kPerRow;  // channels 8e .. 8e + 7
   const int row0 = threadIdx.x / kPerRow;
   const int at_once = max(1, kRowsOfThreads / rows);  // tokens
@@ -211,59 +234,75 @@ __device__ __forceinline__ void keys_and_values(const KvRotateArgs& a, int base,
   const unsigned lanes = kPerRow >= 32 ? 0xFFFFFFFFu
                                        : ((1u << (kPerRow % 32)) - 1u) << (threadIdx.x & 31 & ~(kPerRow - 1));
   const bool lower = 8 * e < half;  // of the two halves that a rotation pairs
-  if ((int)threadIdx.x < n) place[threadIdx.x] = rotated_place<D>(a, base + threadIdx.x);
-  __syncthreads();
-  if (token0 >= at_once) return;
-  for (int hs = row0 - token0 * rows; hs < rows; hs += kRowsOfThreads) {
+  bool staged = false;
+  for (int hs = row0 - token0 * rows; hs < rows || !staged; hs += kRowsOfThreads) {
+    const bool here = hs < rows && token0 < at_once;
     const bool v = hs >= c.kv_heads;
     const int head = v ? hs - c.kv_heads : hs;
-    const bool turned = !v && 8 * e < a.rot;
+    const bool turned = !v && 8 * e < a.rot, partnered = turned && !a.paired;
+    const long long stride = v ? a.kv.v_token : a.kv.k_token;
+    const T* src = static_cast<const T*>(v ? a.kv.v : a.kv.k) + (base + token0) * stride +
+                   head * (v ? a.kv.v_head : a.kv.k_head) + 8 * e;
+    const int partner = lower ? half : -half;
+    Eight<T> next, next_partner;
+    if (here && token0 < n) {  // on their way while the places are found
+      next = fetch<T, kVec>(src);
+      if (partnered) next_partner = fetch<T, kVec>(src + partner);
+    }
+    if (!staged) {
+      stage<D>(a, base, n, place, turns);
+      staged = true;
+    }
+    if (!here) continue;
+    const long long head_at = (long long)head * c.head_bytes;
+    T* out = static_cast<T*>(v ? a.kv.v_out : a.kv.k_out) + ((long long)(base + token0) * c.kv_heads + head) * D + 8 * e;
     for (int token = token0; token < n; token += at_once) {
-      const Place p = place[token];
-      const T* src = static_cast<const T*>(v ? a.kv.v : a.kv.k) + (base + token) * (v ? a.kv.v_token : a.kv.k_token) +
-                     head * (v ? a.kv.v_head : a.kv.k_head) + 8 * e;
-      const Eight<T> x = fetch<T, kVec>(src);
-      float f[8];
-      uint32_t top = Widen<T>::run(x, f);
-      if (turned && p.group) {
-        const float* row = a.cos_sin + (long long)p.pos * a.rot;
+      float f[8], g[8];
+      uint32_t top = Widen<T>::run(next, f);
+      if (partnered) Widen<T>::run(next_partner, g);
+      src += at_once * stride;
+      if (token + at_once < n) {
+        next = fetch<T, kVec>(src);
+        if (partnered) next_partner = fetch<T, kVec>(src + partner);
+      }
+      if (turned && place[token].pos >= 0) {
+        const float4* row = turns + token * fours;
         if (a.paired) {
-          float co[4], si[4];
-          load_floats(row + 4 * e, co);
-          load_floats(row + half + 4 * e, si);
-          rotate_neighbours(f, co, si);
+          row += (e & 1) * eights + (e >> 1);
+          turn_neighbours(f, row[0], row[2 * eights]);
         } else {
-          const int i = lower ? 8 * e : 8 * e - half;
-          float g[8], co[8], si[8];
-          Widen<T>::run(fetch<T, kVec>(lower ? src + half : src - half), g);
-          load_floats(row + i, co);
-          load_floats(row + half + i, si);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            f[k] = lower ? first_of(f[k], g[k], co[k], si[k]) : second_of(g[k], f[k], co[k], si[k]);
+          row += lower ? e : e - eights;
+          if (lower) {
+            turn_runs(f, g, row[0], row[2 * eights]);
+            turn_runs(f + 4, g + 4, row[eights], row[3 * eights]);
+          } else {
+            turn_runs(g, f, row[0], row[2 * eights]);
+            turn_runs(g + 4, f + 4, row[eights], row[3 * eights]);
+          }
         }
         top = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(f[k]) & 0x7FFFFFFFu);
       }
-      T* out = static_cast<T*>(v ? a.kv.v_out : a.kv.k_out) + ((long long)(base + token) * c.kv_heads + head) * D + 8 * e;
-      store_eight<T, D, kVec>(f, top, lanes, e, v, &place[token], (long long)head * c.head_bytes, a.kv.k_out != nullptr, out);
+      store_eight<T, D, kVec>(f, top, lanes, e, v, &place[token], head_at, a.kv.k_out != nullptr, out);
+      out += (long long)at_once * c.kv_heads * D;
     }
   }
 }
 
 // The first kv_ctas CTAs take keys and values of kv_tokens tokens each, the others queries of q_tokens.
 template <typename T, int D, bool kVec>
-__global__ void __launch_bounds__(kThreads) kv_append_rotated(const KvRotateArgs a, int kv_ctas, int kv_tokens, int q_tokens) {
+__global__ void __launch_bounds__(kThreads, 4) kv_append_rotated(const KvRotateArgs a, int kv_ctas, int kv_tokens, int q_tokens) {
   __shared__ Place place[kMaxTokens];
+  extern __shared__ float4 turns[];
   grid_dependency_wait();  // nothing above reads what an earlier kernel may write
   grid_launch_dependents();
   if ((int)blockIdx.x < kv_ctas) {
     const int base = blockIdx.x * kv_tokens;
-    keys_and_values<T, D, kVec>(a, base, min(kv_tokens, a.kv.batch.tokens - base), place);
+    keys_and_values<T, D, kVec>(a, base, min(kv_tokens, a.kv.batch.tokens - base), place, turns);
   } else {
     const int base = (blockIdx.x - kv_ctas) * q_tokens;
-    queries<T, D, kVec>(a, base, min(q_tokens, a.kv.batch.tokens - base), place);
+    queries<T, D, kVec>(a, base, min(q_tokens, a.kv.batch.tokens - base), place, turns);
   }
 }
 
@@ -289,8 +328,8 @@ cudaError_t run(const KvRotateArgs& a, cudaStream_t s) {
   const bool vec = aligned16(kv.k) && aligned16(kv.v) && aligned16(kv.k_out) && aligned16(kv.v_out) && aligned16(a.q) &&
                    aligned16(a.q_out) && kv.k_token % u == 0 && kv.k_head % u == 0 && kv.v_token % u == 0 &&
                    kv.v_head % u == 0 && a.q_token % u == 0 && a.q_head % u == 0;
-  return launch_dependent(vec ? kv_append_rotated<T, D, true> : kv_append_rotated<T, D, false>, kv_ctas + q_ctas, kThreads, 0,
-                          s, a, kv_ctas, kv_tokens, q_tokens);
+  return launch_dependent(vec ? kv_append_rotated<T, D, true> : kv_append_rotated<T, D, false>, kv_ctas + q_ctas, kThreads,
+                          4 * a.rot * (q_tokens > kv_tokens ? q_tokens : kv_tokens), s, a, kv_ctas, kv_tokens, q_tokens);
 }
 
 template <typename T>

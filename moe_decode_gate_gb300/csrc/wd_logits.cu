@@ -35,20 +35,22 @@ struct alignas(sizeof(T) * kFour) Four {
 
 // What a row's tokens go through.
 struct Row {
-  float repetition, presence, frequency, scale;
+  float repetition, presence, frequency;
+  float relief, scale;  // 1 / repetition, 1 / temperature
   const float* bias;    // the values of the row's biases
   const int32_t* mask;  // its words, null: all allowed
 };
 
-// A logit with its token's count and 1 + its last bias (0: none).
-__device__ __forceinline__ float penalised(const Row& r, float l, uint32_t count, uint32_t named) {
-  if (count) {
-    l = l > 0.f ? l / r.repetition : l * r.repetition;
-    const uint32_t n = count & kAnswer;
-    if (n) l -= (float)n * r.frequency + r.presence;
-  }
-  if (named) l += r.bias[named - 1];
-  return l;
+// A logit with its token's count.
+__device__ __forceinline__ float penalised(const Row& r, float l, uint32_t count) {
+  const float turned = l * (l > 0.f ? r.relief : r.repetition);
+  const uint32_t n = count & kAnswer;
+  const float less = n ? fmaf((float)n, r.frequency, r.presence) : 0.f;
+  return count ? turned - less : l;
+}
+// ... and with 1 + its last bias, 0 for none.
+__device__ __forceinline__ float biased(const Row& r, float l, uint32_t named) {
+  return named ? l + r.bias[named - 1] : l;
 }
 
 // The tokens of a row's history that are in [from, from + n), counted at `count`.
@@ -141,6 +143,7 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(const LogitsArgs a, in
   r.frequency = a.frequency ? a.frequency[b] : 0.f;
   const float t = a.temperature ? a.temperature[b] : 1.f;
   r.scale = t > 0.f ? 1.f / t : 1.f;
+  r.relief = 1.f / r.repetition;
   // the row's history, if it has one and its penalties are any
   const int32_t* tokens = nullptr;
   int length = 0, prompt = 0;
@@ -182,14 +185,23 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(const LogitsArgs a, in
     float l[kFour];
 #pragma unroll
     for (int k = 0; k < kFour; ++k) l[k] = to_float(x[j].v[k]);
-    uint4 c = make_uint4(0, 0, 0, 0), e = c;
-    if (counts) c = reinterpret_cast<const uint4*>(count)[f + 1];
-    if (biases) e = reinterpret_cast<const uint4*>(named)[f + 1];
-    if (c.x | c.y | c.z | c.w | e.x | e.y | e.z | e.w) {
-      l[0] = penalised(r, l[0], c.x, e.x);
-      l[1] = penalised(r, l[1], c.y, e.y);
-      l[2] = penalised(r, l[2], c.z, e.z);
-      l[3] = penalised(r, l[3], c.w, e.w);
+    if (counts) {
+      const uint4 c = reinterpret_cast<const uint4*>(count)[f + 1];
+      if (c.x | c.y | c.z | c.w) {
+        l[0] = penalised(r, l[0], c.x);
+        l[1] = penalised(r, l[1], c.y);
+        l[2] = penalised(r, l[2], c.z);
+        l[3] = penalised(r, l[3], c.w);
+      }
+    }
+    if (biases) {
+      const uint4 e = reinterpret_cast<const uint4*>(named)[f + 1];
+      if (e.x | e.y | e.z | e.w) {
+        l[0] = biased(r, l[0], e.x);
+        l[1] = biased(r, l[1], e.y);
+        l[2] = biased(r, l[2], e.z);
+        l[3] = biased(r, l[3], e.w);
+      }
     }
     Four<U> y;
 #pragma unroll
@@ -206,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) adjust_logits(const LogitsArgs a, in
   if ((int)threadIdx.x < before + behind) {
     const int v = (int)threadIdx.x < before ? from + threadIdx.x : max(end, begin) + threadIdx.x - before;
     const int at = kFour + v - begin;
-    const float l = penalised(r, to_float(in[v]), counts ? count[at] : 0u, biases ? named[at] : 0u);
+    const float l = biased(r, penalised(r, to_float(in[v]), counts ? count[at] : 0u), biases ? named[at] : 0u);
     put(&out[v], !r.mask || (r.mask[v >> 5] >> (v & 31) & 1) ? l * r.scale : -INFINITY);
   }
 }

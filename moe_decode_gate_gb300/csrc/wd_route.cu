@@ -286,18 +286,19 @@ __global__ void __launch_bounds__(32 * kWarps) route(const RouteArgs a, const La
 #pragma unroll
     for (int i = 0; i < kV; ++i) l[i] = i < mine.n ? to_float(x[mine.first + i]) : -INFINITY;
   }
-  float top = -INFINITY;
+  const bool sums = a.groups > 1 && a.group_best == 2;
+  const bool inexact = a.bias || sums;  // keys that are not the logits
+  float top = -INFINITY, sum = 0.f;     // of a softmax over all experts: the largest logit, the sum of exp(l - top)
+  float s[kV];                          // scores, then keys
 #pragma unroll
   for (int i = 0; i < kV; ++i) {
     if (!(l[i] == l[i])) l[i] = -INFINITY;
-    top = fmaxf(top, l[i]);
+    s[i] = l[i];
   }
-  top = warp_max(top);
-  const bool sums = a.groups > 1 && a.group_best == 2;
-  const bool inexact = a.bias || sums;  // keys that are not the logits
-  float s[kV];
-  float sum = 0.f;
   if (!a.sigmoid && (inexact || !a.renormalise)) {
+#pragma unroll
+    for (int i = 0; i < kV; ++i) top = fmaxf(top, l[i]);
+    top = warp_max(top);
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
       s[i] = exp_below(l[i], top);
@@ -305,37 +306,35 @@ __global__ void __launch_bounds__(32 * kWarps) route(const RouteArgs a, const La
     }
     sum = warp_sum(sum);
   }
-  uint32_t k[kV];
-  float best = -INFINITY, second = -INFINITY, margin = 0.f;
   const float unit = a.sigmoid ? 1.f : sum > 0.f ? 1.f / sum : 0.f;  // the largest score there may be
-  float most = 0.f;  // largest magnitude of a key
-#pragma unroll
-  for (int i = 0; i < kV; ++i) {
-    float key = l[i];
-    if (inexact && l[i] > -INFINITY) {
-      key = a.sigmoid ? sigmoid(l[i]) : s[i] * unit;
-      if (a.bias) key += a.bias[mine.first + i];
-      if (!(key == key)) key = -INFINITY;
-      if (fabsf(key) < INFINITY) most = fmaxf(most, fabsf(key));
-    }
-    second = fmaxf(second, fminf(best, key));
-    best = fmaxf(best, key);
-    // without a bias the choice goes by the logits even where the groups' goes by sums of scores
-    if (i >= mine.n)
-      k[i] = 0;
-    else if (kWords)
-      k[i] = half_order(l[i], T{}) << 16 | (0xFFFFu - (mine.first + i));
-    else
-      k[i] = order_of(a.bias ? key : l[i]);
-  }
-  bool again = false, chosen = true;
+  float margin = 0.f;
   if (inexact) {
+    float most = 0.f;  // largest magnitude of a key
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      if (l[i] > -INFINITY) {
+        s[i] = a.sigmoid ? sigmoid(l[i]) : s[i] * unit;
+        if (a.bias) s[i] += a.bias[mine.first + i];
+        if (!(s[i] == s[i])) s[i] = -INFINITY;
+        if (fabsf(s[i]) < INFINITY) most = fmaxf(most, fabsf(s[i]));
+      } else {
+        s[i] = -INFINITY;
+      }
+    }
     // In units of 2^-24, a score is off by 2 (expf), 1 (its argument), 2 (quotient), 1 (the product by it) and the sum
     // of all of them, kV + 5 roundings at most; a key by half a unit of its own more. Two keys are compared.
     most = warp_max(most);
     margin = 0x1p-23f * (a.sigmoid ? 12 : kV + 12) * unit + 0x1p-23f * most;
   }
+  bool again = false, chosen = true;
   if (a.groups > 1) {
+    float best = -INFINITY, second = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) {
+      const float key = inexact ? s[i] : l[i];
+      second = fmaxf(second, fminf(best, key));
+      best = fmaxf(best, key);
+    }
     float value = group_value(best, second, lanes.per_group, a.group_best);
     if (group >= a.groups) value = -INFINITY;
     chosen = group_chosen(value, group, a.groups, lanes.per_group, a.top_groups);  // (all lanes take part)
@@ -345,9 +344,17 @@ __global__ void __launch_bounds__(32 * kWarps) route(const RouteArgs a, const La
       const float out = warp_max(chosen ? -INFINITY : value);
       again = in - out < 2.f * margin;
     }
-    if (!chosen)
+  }
+  uint32_t k[kV];
 #pragma unroll
-      for (int i = 0; i < kV; ++i) k[i] = 0;
+  for (int i = 0; i < kV; ++i) {
+    // without a bias the choice goes by the logits even where the groups' goes by sums of scores
+    if (!chosen || (!kVec && i >= mine.n))
+      k[i] = 0;
+    else if (kWords)
+      k[i] = half_order(l[i], T{}) << 16 | (0xFFFFu - (mine.first + i));
+    else
+      k[i] = order_of(a.bias ? s[i] : l[i]);
   }
   int ids[2] = {0, 0};
   float y[2] = {-INFINITY, -INFINITY}, w[2] = {0.f, 0.f};  // logits and weights of the chosen
@@ -377,6 +384,7 @@ __global__ void __launch_bounds__(32 * kWarps) route(const RouteArgs a, const La
     ids[0] = mended[0];
     ids[1] = mended[1];
   }
+  const int halves = a.K > 32 ? 2 : 1;
   if (!kWords || again) {
 #pragma unroll
     for (int e = 0; e < 2; ++e)
@@ -385,11 +393,11 @@ __global__ void __launch_bounds__(32 * kWarps) route(const RouteArgs a, const La
         if (!(y[e] == y[e])) y[e] = -INFINITY;
       }
   }
-  float high = fmaxf(y[0], y[1]);
-  high = warp_max(high);
+  const float high = warp_max(fmaxf(y[0], y[1]));
   float total = 0.f;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
+    if (e >= halves) break;
     if (a.renormalise)  // scaled alike: far below 0 a sigmoid is an exponential, to all of FP32's bits
       w[e] = a.sigmoid && high > -40.f ? (y[e] > -INFINITY ? sigmoid(y[e]) : 0.f) : exp_below(y[e], high);
     else
