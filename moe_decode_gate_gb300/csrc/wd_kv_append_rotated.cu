@@ -23,25 +23,85 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 16;  // tokens of a CTA
 
+// Eight channels as whole words: as elements of 16 bits the compiler takes them apart and puts them together again.
+template <typename T>
+struct Words {
+  uint32_t w[2 * sizeof(T)];
+};
+
 template <typename T, bool kVec>
-__device__ __forceinline__ Eight<T> fetch(const T* src) {
-  Eight<T> x;
+__device__ __forceinline__ Words<T> fetch(const T* src) {
+  Words<T> x;
   if (kVec) {
-    x = *reinterpret_cast<const Eight<T>*>(src);
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(src)[i];
+      x.w[4 * i] = v.x, x.w[4 * i + 1] = v.y, x.w[4 * i + 2] = v.z, x.w[4 * i + 3] = v.w;
+    }
+  } else if (sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x.w[k] = reinterpret_cast<const uint32_t*>(src)[k];
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x.v[k] = src[k];
+    for (int k = 0; k < 4; ++k)
+      x.w[k] = reinterpret_cast<const uint16_t*>(src)[2 * k] | (uint32_t)reinterpret_cast<const uint16_t*>(src)[2 * k + 1] << 16;
   }
   return x;
 }
 
 template <typename T, bool kVec>
-__device__ __forceinline__ void put(T* dst, const Eight<T>& x) {
+__device__ __forceinline__ void put(T* dst, const Words<T>& x) {
   if (kVec) {
-    *reinterpret_cast<Eight<T>*>(dst) = x;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+      reinterpret_cast<uint4*>(dst)[i] = make_uint4(x.w[4 * i], x.w[4 * i + 1], x.w[4 * i + 2], x.w[4 * i + 3]);
+  } else if (sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) reinterpret_cast<uint32_t*>(dst)[k] = x.w[k];
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) dst[k] = x.v[k];
+    for (int k = 0; k < 4; ++k) {
+      reinterpret_cast<uint16_t*>(dst)[2 * k] = (uint16_t)x.w[k];
+      reinterpret_cast<uint16_t*>(dst)[2 * k + 1] = (uint16_t)(x.w[k] >> 16);
+    }
+  }
+}
+
+__device__ __forceinline__ void floats_of(const Words<float>& x, float (&f)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(x.w[k]);
+}
+__device__ __forceinline__ void floats_of(const Words<__nv_bfloat16>& x, float (&f)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f[2 * k] = __uint_as_float(x.w[k] << 16);
+    f[2 * k + 1] = __uint_as_float(x.w[k] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void floats_of(const Words<__half>& x, float (&f)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&x.w[k]));
+    f[2 * k] = p.x;
+    f[2 * k + 1] = p.y;
+  }
+}
+__device__ __forceinline__ void words_of(const float (&f)[8], Words<float>& x) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x.w[k] = __float_as_uint(f[k]);
+}
+__device__ __forceinline__ void words_of(const float (&f)[8], Words<__nv_bfloat16>& x) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+    x.w[k] = *reinterpret_cast<const uint32_t*>(&p);
+  }
+}
+__device__ __forceinline__ void words_of(const float (&f)[8], Words<__half>& x) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __half2 p = __floats2half2_rn(f[2 * k], f[2 * k + 1]);
+    x.w[k] = *reinterpret_cast<const uint32_t*>(&p);
   }
 }
 
@@ -129,13 +189,9 @@ __device__ __forceinline__ void store_eight(const float (&f)[8], uint32_t top, u
       e2m1x8_values(word, y);
 #pragma unroll
       for (int k = 0; k < 8; ++k) y[k] *= unit;
-      const Eight<T> z = narrow<T>(y);
-      if (kVec) {
-        *reinterpret_cast<Eight<T>*>(out) = z;
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) out[k] = z.v[k];
-      }
+      Words<T> z;
+      words_of(y, z);
+      put<T, kVec>(out, z);
     }
   }
 }
@@ -175,7 +231,7 @@ __device__ __forceinline__ void queries(const KvRotateArgs& a, int base, int n, 
   for (int h = row0 - token0 * a.q_heads; h < a.q_heads || !staged; h += kRowsOfThreads) {
     const bool here = h < a.q_heads && token0 < at_once;
     const T* src = static_cast<const T*>(a.q) + (base + token0) * a.q_token + h * a.q_head;
-    Eight<T> next0, next1;
+    Words<T> next0, next1;
     if (here && token0 < n) {  // on their way while the places are found
       next0 = fetch<T, kVec>(src + c0);
       next1 = fetch<T, kVec>(src + c1);
@@ -187,7 +243,7 @@ __device__ __forceinline__ void queries(const KvRotateArgs& a, int base, int n, 
     if (!here) continue;
     T* dst = static_cast<T*>(a.q_out) + ((long long)(base + token0) * a.q_heads + h) * D;
     for (int token = token0; token < n; token += at_once) {
-      Eight<T> x0 = next0, x1 = next1;
+      Words<T> x0 = next0, x1 = next1;
       src += at_once * a.q_token;
       if (token + at_once < n) {
         next0 = fetch<T, kVec>(src + c0);
@@ -196,8 +252,8 @@ __device__ __forceinline__ void queries(const KvRotateArgs& a, int base, int n, 
       if (place[token].pos >= 0) {
         if (turned) {
           float f[8], g[8];
-          Widen<T>::run(x0, f);
-          Widen<T>::run(x1, g);
+          floats_of(x0, f);
+          floats_of(x1, g);
           const float4* row = turns + token * fours + e;
           const float4 ca = row[0], cb = row[eights], sa = row[2 * eights], sb = row[3 * eights];
           if (a.paired) {
@@ -207,8 +263,8 @@ __device__ __forceinline__ void queries(const KvRotateArgs& a, int base, int n, 
             turn_runs(f, g, ca, sa);
             turn_runs(f + 4, g + 4, cb, sb);
           }
-          x0 = narrow<T>(f);
-          x1 = narrow<T>(g);
+          words_of(f, x0);
+          words_of(g, x1);
         }
         put<T, kVec>(dst + c0, x0);
         put<T, kVec>(dst + c1, x1);
@@ -244,7 +300,7 @@ __device__ __forceinline__ void keys_and_values(const KvRotateArgs& a, int base,
     const T* src = static_cast<const T*>(v ? a.kv.v : a.kv.k) + (base + token0) * stride +
                    head * (v ? a.kv.v_head : a.kv.k_head) + 8 * e;
     const int partner = lower ? half : -half;
-    Eight<T> next, next_partner;
+    Words<T> next, next_partner;
     if (here && token0 < n) {  // on their way while the places are found
       next = fetch<T, kVec>(src);
       if (partnered) next_partner = fetch<T, kVec>(src + partner);
@@ -258,8 +314,8 @@ __device__ __forceinline__ void keys_and_values(const KvRotateArgs& a, int base,
     T* out = static_cast<T*>(v ? a.kv.v_out : a.kv.k_out) + ((long long)(base + token0) * c.kv_heads + head) * D + 8 * e;
     for (int token = token0; token < n; token += at_once) {
       float f[8], g[8];
-      uint32_t top = Widen<T>::run(next, f);
-      if (partnered) Widen<T>::run(next_partner, g);
+      floats_of(next, f);
+      if (partnered) floats_of(next_partner, g);
       src += at_once * stride;
       if (token + at_once < n) {
         next = fetch<T, kVec>(src);
@@ -272,18 +328,17 @@ __device__ __forceinline__ void keys_and_values(const KvRotateArgs& a, int base,
           turn_neighbours(f, row[0], row[2 * eights]);
         } else {
           row += lower ? e : e - eights;
-          if (lower) {
-            turn_runs(f, g, row[0], row[2 * eights]);
-            turn_runs(f + 4, g + 4, row[eights], row[3 * eights]);
-          } else {
-            turn_runs(g, f, row[0], row[2 * eights]);
-            turn_runs(g + 4, f + 4, row[eights], row[3 * eights]);
-          }
-        }
-        top = 0;
+          const float4 ca = row[0], cb = row[eights], sa = row[2 * eights], sb = row[3 * eights];
+          const float co[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
+          const float si[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(f[k]) & 0x7FFFFFFFu);
+          for (int k = 0; k < 8; ++k)  // x1 c - x2 s, or x2 c + x1 s
+            f[k] = __fadd_rn(__fmul_rn(f[k], co[k]), __fmul_rn(g[k], lower ? -si[k] : si[k]));
+        }
       }
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(f[k]) & 0x7FFFFFFFu);
       store_eight<T, D, kVec>(f, top, lanes, e, v, &place[token], head_at, a.kv.k_out != nullptr, out);
       out += (long long)at_once * c.kv_heads * D;
     }

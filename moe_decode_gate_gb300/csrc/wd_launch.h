@@ -95,10 +95,10 @@ cudaError_t ensure_dynamic_smem(const void* func, int bytes);
 // on the stream drains.  Each of them waits for the results of that one before its first
 // read of memory.
 template <typename... Params, typename... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), int grid, int block, int shared, cudaStream_t s,
+cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, int block, int shared, cudaStream_t s,
                       const Args&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3((unsigned)block);
   cfg.dynamicSmemBytes = (size_t)shared;
   cfg.stream = s;

@@ -1,246 +1,377 @@
 // wd_logits.cu - penalties, biases, temperature and masks on logits (declared
 // in include/wd_step.h).
 //
-// One pass: a CTA takes a slice of one row's vocabulary, with its logits and their bits of the mask in registers. While
-// they are on their way it counts in shared memory how often the row's history names each of its
-// tokens (every CTA of a row reads the whole history, which is small beside the logits and comes from
-// L2) and notes which bias is the last for each. Nothing is written but the result, no counts live from call to call,
-// and counting whole numbers gives the same sums in any order. Bytes bound it where rows are many, the
-// history's scan where they are few.
+// One pass: a CTA takes a slice of one row's vocabulary. While its first logits are on their way it counts in shared
+// memory how often the row's history names each of the slice's tokens (every CTA of a row reads the whole
+// history, which is small beside the logits and comes from L2) and notes which bias is the last for each. Then it
+// streams its logits through, the next ones always on their way. Nothing is written but the result, no counts
+// live from call to call, and counting whole numbers gives the same sums in any order.
+//
+// Bytes bound it where rows are many and little else is asked for, its instructions (about
+// NNN) else; the chain of a CTA's loads (settings and slot, lengths, history) where rows are few.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
 #include "wd_device.cuh"
 #include "wd_step.cuh"
-#include "wd_vec.cuh"
 
 namespace wd {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kFour = 4;                     // elements of an access
-constexpr int kUnit = kThreads * kFour;      // tokens of a slice: this, twice or four times
+constexpr int kUnit = kThreads * kFour;      // tokens that the threads take with one access each
 constexpr int kCtasWanted = 4 * 152;         // for which slices are made smaller
-constexpr uint32_t kPrompt = 1u << 31;       // of a count: the prompt has the token
-constexpr uint32_t kAnswer = kPrompt - 1;
 
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+// What shared memory has of a token. Narrow: one word, the bias in its upper half (1 + its index in the row, 0: none), below
+// it a bit for the prompt and 15 for the count. Wide, for longer histories or more biases: a word for each, in two arrays.
+constexpr int kNarrowHistory = 32767, kNarrowBiases = 65535;
+template <bool kWide>
+struct Layout {
+  static constexpr uint32_t kPrompt = kWide ? 1u << 31 : 1u << 15;
+  static constexpr int kBiasShift = kWide ? 0 : 16;
+};
+
+// Four elements as whole words: as elements of 16 bits the compiler takes them apart and puts them together again.
+template <typename T>
+struct Four {
+  uint32_t w[sizeof(T)];
+};
+
+template <typename T, bool kVec>
+__device__ __forceinline__ Four<T> get_four(const T* p) {
+  Four<T> x;
+  if constexpr (sizeof(T) == 4) {
+    if (kVec) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      x.w[0] = v.x, x.w[1] = v.y, x.w[2] = v.z, x.w[3] = v.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x.w[k] = reinterpret_cast<const uint32_t*>(p)[k];
+    }
+  } else {
+    if (kVec) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      x.w[0] = v.x, x.w[1] = v.y;
+    } else {
+      const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+      x.w[0] = h[0] | (uint32_t)h[1] << 16;
+      x.w[1] = h[2] | (uint32_t)h[3] << 16;
+    }
+  }
+  return x;
+}
+
+__device__ __forceinline__ void floats_of(const Four<float>& x, float (&f)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(x.w[k]);
+}
+__device__ __forceinline__ void floats_of(const Four<__nv_bfloat16>& x, float (&f)[4]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    f[2 * k] = __uint_as_float(x.w[k] << 16);
+    f[2 * k + 1] = __uint_as_float(x.w[k] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void floats_of(const Four<__half>& x, float (&f)[4]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&x.w[k]));
+    f[2 * k] = p.x;
+    f[2 * k + 1] = p.y;
+  }
+}
+
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void put(__half* p, float x) { *p = __float2half_rn(x); }
+__device__ __forceinline__ float get(const float* p) { return *p; }
+__device__ __forceinline__ float get(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float get(const __half* p) { return __half2float(*p); }
 
-template <typename T>
-struct alignas(sizeof(T) * kFour) Four {
-  T v[kFour];
-};
+template <bool kVec>
+__device__ __forceinline__ void put_four(float* p, const float (&f)[4]) {
+  if (kVec) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) p[k] = f[k];
+  }
+}
+template <bool kVec, typename U>
+__device__ __forceinline__ void put_four(U* p, const float (&f)[4]) {
+  if (kVec) {
+    uint2 v;
+    if constexpr (std::is_same<U, __half>::value) {
+      const __half2 lo = __floats2half2_rn(f[0], f[1]), hi = __floats2half2_rn(f[2], f[3]);
+      v = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    } else {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(f[0], f[1]), hi = __floats2bfloat162_rn(f[2], f[3]);
+      v = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
+    *reinterpret_cast<uint2*>(p) = v;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) put(p + k, f[k]);
+  }
+}
 
 // What a row's tokens go through.
 struct Row {
   float repetition, presence, frequency;
   float relief, scale;  // 1 / repetition, 1 / temperature
   const float* bias;    // the values of the row's biases
-  const int32_t* mask;  // its words, null: all allowed
 };
 
-// A logit with its token's count.
-__device__ __forceinline__ float penalised(const Row& r, float l, uint32_t count) {
+// A logit with its token's prompt bit and count, and 1 + its last bias.
+template <bool kWide>
+__device__ __forceinline__ float penalised(const Row& r, float l, uint32_t count, uint32_t named) {
+  if (!kWide) {
+    named = count >> 16;
+    count &= 0xFFFFu;
+  }
   const float turned = l * (l > 0.f ? r.relief : r.repetition);
-  const uint32_t n = count & kAnswer;
+  const uint32_t n = count & (Layout<kWide>::kPrompt - 1);
   const float less = n ? fmaf((float)n, r.frequency, r.presence) : 0.f;
-  return count ? turned - less : l;
-}
-// ... and with 1 + its last bias, 0 for none.
-__device__ __forceinline__ float biased(const Row& r, float l, uint32_t named) {
+  l = count ? turned - less : l;
   return named ? l + r.bias[named - 1] : l;
 }
 
-// The tokens of a row's history that are in [from, from + n), counted at `count`.
-__device__ __forceinline__ void count_tokens(const int32_t* tokens, int length, int prompt, int from, int n, uint32_t* count) {
-  const auto one = [&](int token, int i) {
-    const unsigned at = (unsigned)token - (unsigned)from;
-    if (at < (unsigned)n) {
-      if (i >= prompt)
-        atomicAdd(&count[at], 1u);
-      else if (!(count[at] & kPrompt))
-        atomicOr(&count[at], kPrompt);
-    }
-  };
-  // up to the first aligned one, then four to an access and four accesses on their way at a time
-  const int head = min(length, (int)((4 - (reinterpret_cast<uintptr_t>(tokens) >> 2) % 4) % 4));
-  const int fours = (length - head) / 4;
-  const int4* aligned = reinterpret_cast<const int4*>(tokens + head);
-  for (int i = threadIdx.x; i < fours; i += 4 * kThreads) {
-    int4 t[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      t[j] = i + j * kThreads < fours ? aligned[i + j * kThreads] : make_int4(-1, -1, -1, -1);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int at = head + 4 * (i + j * kThreads);
-      one(t[j].x, at);
-      one(t[j].y, at + 1);
-      one(t[j].z, at + 2);
-      one(t[j].w, at + 3);
-    }
+// Tokens `first` .. `first` + 3 of a history of `columns`; -1 behind its end.
+__device__ __forceinline__ int4 four_tokens(const int32_t* tokens, bool aligned, int first, int columns) {
+  int4 v = make_int4(-1, -1, -1, -1);
+  if (aligned && first + 4 <= columns) {
+    v = *reinterpret_cast<const int4*>(tokens + first);
+  } else {
+    if (first < columns) v.x = tokens[first];
+    if (first + 1 < columns) v.y = tokens[first + 1];
+    if (first + 2 < columns) v.z = tokens[first + 2];
+    if (first + 3 < columns) v.w = tokens[first + 3];
   }
-  const int rest = length - head - 4 * fours;
-  if ((int)threadIdx.x < head + rest) {
-    const int i = (int)threadIdx.x < head ? threadIdx.x : threadIdx.x + 4 * fours;
-    one(tokens[i], i);
-  }
+  return v;
 }
 
-// Slice `blockIdx.x % slices` of row `blockIdx.x / slices`, kPer fours of tokens to a thread. kVec: input and output of a
-// row reach the alignment of four elements at the same token; slices begin there. The first one has what is
+// Marks a token as the prompt's, or counts it, if it is one of the n of the slice; `words`: the shared address of the first
+// one's. Without a branch: most accesses of a warp have a token for most slices.
+__device__ __forceinline__ void mark(uint32_t words, uint32_t at, int n, uint32_t bit) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.lo.u32 p, %1, %2;\n\t@p red.shared.or.b32 [%0], %3;\n\t}"
+               :: "r"(words + 4 * at), "r"(at), "r"(n), "r"(bit) : "memory");
+}
+__device__ __forceinline__ void add(uint32_t words, uint32_t at, int n) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.lo.u32 p, %1, %2;\n\t@p red.shared.add.u32 [%0], 1;\n\t}"
+               :: "r"(words + 4 * at), "r"(at), "r"(n) : "memory");
+}
+__device__ __forceinline__ void raise(uint32_t words, uint32_t at, int n, uint32_t to) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.lo.u32 p, %1, %2;\n\t@p red.shared.max.u32 [%0], %3;\n\t}"
+               :: "r"(words + 4 * at), "r"(at), "r"(n), "r"(to) : "memory");
+}
+
+// Slice blockIdx.x of row blockIdx.y: `chunks` times kPer fours of tokens to a thread. kVec: input and output of a row reach
+// the alignment of four elements at the same token; slices begin there. The first one has what is
 // before that, too, and the one of the last four what is behind it.
-template <typename T, typename U, int kPer, bool kVec>
-__global__ void __launch_bounds__(kThreads) adjust_logits(const LogitsArgs a, int slices) {
-  constexpr int kSlice = kPer * kUnit;
-  constexpr int kPlaces = kSlice + 2 * kFour;  // of an array in shared memory: place 4 is the slice's first four
+template <typename T, typename U, int kPer, bool kVec, bool kWide>
+__global__ void __launch_bounds__(kThreads, 4) adjust_logits(const LogitsArgs a, int chunks) {
+  constexpr int kChunk = kPer * kUnit;
+  constexpr int kBatch = 4;  // accesses of a thread to the history that are on their way at a time
   extern __shared__ uint4 shared[];
-  const int b = blockIdx.x / slices, part = blockIdx.x % slices;
+  const int slice = chunks * kChunk, places = slice + 2 * kFour;  // place 4 of an array is the slice's first four
+  const int b = blockIdx.y, part = blockIdx.x;
   const T* in = static_cast<const T*>(a.logits) + b * a.stride;
   U* out = static_cast<U*>(a.out) + b * a.out_stride;
   const int lead =
       kVec ? min(a.V, (int)((kFour - (reinterpret_cast<uintptr_t>(in) / sizeof(T)) % kFour) % kFour)) : 0;
   const int last = lead + (a.V - lead) / kFour * kFour;  // behind the row's last four
-  const int begin = lead + part * kSlice, end = min(begin + kSlice, last);
-  const int closing = min((last - lead) / kSlice, slices - 1);  // the slice that the tokens behind the last four go to
-  const int from = part == 0 ? 0 : begin, to = part == closing ? a.V : end;
-  uint32_t* count = reinterpret_cast<uint32_t*>(shared);
-  int32_t* named = reinterpret_cast<int32_t*>(count + (a.history.tokens ? kPlaces : 0));
+  const int begin = lead + part * slice, end = min(begin + slice, last);
+  const int before = part == 0 ? lead : 0;  // loose tokens that are this slice's
+  const int behind = begin <= last && last < begin + slice ? a.V - last : 0;
   grid_dependency_wait();  // nothing above reads what an earlier kernel may write
   grid_launch_dependents();
-  if (to <= from) return;
-  Row r;
-  r.mask = a.mask ? a.mask + b * a.mask_stride : nullptr;
-  // this thread's logits, and four bits of the mask for each access
-  Four<T> x[kPer];
-  uint32_t allowed = 0xFFFFFFFFu;
+  // A chunk's logits of this thread, and the words of the mask that hold the bits of each access (nothing is done
+  // with them yet: a use waits for what it needs, and the loads behind it wait, too).
+  struct Chunk {
+    Four<T> x[kPer];
+    uint32_t word[kPer], next[kPer];
+  };
+  const int32_t* mask = a.mask ? a.mask + b * a.mask_stride : nullptr;
+  const bool astride = lead % kFour;  // some fours' bits are in two words
+  const int shift = (begin + kFour * threadIdx.x) & 31;  // kUnit tokens are whole words: the same for all accesses
+  const auto fetch = [&](int at) {  // the chunk that begins at token `at`
+    Chunk c;
+    const int mine = at + kFour * threadIdx.x;
+    if (end - at >= kChunk) {
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int v = begin + kFour * (threadIdx.x + j * kThreads);
-    if (v >= end) continue;
-    if constexpr (kVec) {
-      x[j] = *reinterpret_cast<const Four<T>*>(in + v);
+      for (int j = 0; j < kPer; ++j) c.x[j] = get_four<T, kVec>(in + mine + j * kUnit);
     } else {
 #pragma unroll
-      for (int k = 0; k < kFour; ++k) x[j].v[k] = in[v + k];
+      for (int j = 0; j < kPer; ++j)
+        if (mine + j * kUnit < end) c.x[j] = get_four<T, kVec>(in + mine + j * kUnit);
     }
-  }
-  if (r.mask) {
-    allowed = 0;
+    if (mask) {
+      const int32_t* words = mask + (mine >> 5);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int v = begin + kFour * (threadIdx.x + j * kThreads);
-      if (v >= end) continue;
-      const uint32_t word = r.mask[v >> 5];
-      const uint32_t next = (v & 31) > 32 - kFour ? r.mask[(v >> 5) + 1] : 0u;
-      allowed |= (__funnelshift_r(word, next, v & 31) & 15u) << (kFour * j);
+      for (int j = 0; j < kPer; ++j)
+        if (mine + j * kUnit < end) c.word[j] = words[j * (kUnit / 32)];
+      if (astride) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (mine + j * kUnit < end && shift > 32 - kFour) c.next[j] = words[j * (kUnit / 32) + 1];
+      }
     }
-  }
+    return c;
+  };
+  Chunk next = fetch(begin);
+  Row r;
   r.repetition = a.repetition ? a.repetition[b] : 1.f;
   r.presence = a.presence ? a.presence[b] : 0.f;
   r.frequency = a.frequency ? a.frequency[b] : 0.f;
   const float t = a.temperature ? a.temperature[b] : 1.f;
-  r.scale = t > 0.f ? 1.f / t : 1.f;
-  r.relief = 1.f / r.repetition;
-  // the row's history, if it has one and its penalties are any
-  const int32_t* tokens = nullptr;
-  int length = 0, prompt = 0;
-  if (a.history.tokens && (r.repetition != 1.f || r.presence != 0.f || r.frequency != 0.f)) {
-    const int s = a.history.seqs ? a.history.seqs[b] : b;
-    if ((unsigned)s < (unsigned)a.history.slots) {
-      tokens = a.history.tokens + s * a.history.stride;
-      length = max(0, min(a.history.lengths[s], a.history.columns));
-      prompt = a.history.prompt_lengths ? max(0, min(a.history.prompt_lengths[s], length)) : 0;
-    }
-  }
-  int bias_from = 0, bias_to = 0;
+  int slot = -1, bias_from = 0, bias_to = 0;
+  if (a.history.tokens) slot = a.history.seqs ? a.history.seqs[b] : b;
   if (a.bias_start) {
     bias_from = a.bias_start[b];
     bias_to = a.bias_start[b + 1];
     if (bias_from < 0 || bias_to > a.biases) bias_to = bias_from;
   }
   r.bias = a.bias_values + bias_from;
-  const bool counts = length > 0, biases = bias_to > bias_from;
+  // the row's history, if it has one and its penalties are any
+  const bool penalties = r.repetition != 1.f || r.presence != 0.f || r.frequency != 0.f;
+  const bool counts = penalties && (unsigned)slot < (unsigned)a.history.slots, biases = bias_to > bias_from;
   if (counts || biases) {
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    for (int i = threadIdx.x; i < kPlaces / kFour; i += kThreads) {
-      if (counts) reinterpret_cast<uint4*>(count)[i] = zero;
-      if (biases) reinterpret_cast<uint4*>(named)[i] = zero;
+    const int from = begin - before, n = max(0, end - begin) + before + behind;  // the slice's tokens
+    const uint32_t words = (uint32_t)__cvta_generic_to_shared(shared) + 4 * (kFour - before);  // of token `from`
+    int4 tokens[kBatch];
+    const int32_t* history = nullptr;
+    int length = 0, prompt = 0;
+    const int columns = a.history.columns;
+    const auto ask = [&](int base) {
+      const bool aligned = reinterpret_cast<uintptr_t>(history) % 16 == 0;
+      if (aligned && base + 4 * kBatch * kThreads <= columns) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          tokens[j] = reinterpret_cast<const int4*>(history + base)[threadIdx.x + j * kThreads];
+      } else {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          tokens[j] = four_tokens(history, aligned, base + 4 * (threadIdx.x + j * kThreads), columns);
+      }
+    };
+    if (counts) {
+      history = a.history.tokens + slot * a.history.stride;
+      ask(0);  // beside the lengths
+      length = max(0, min(a.history.lengths[slot], columns));
+      prompt = a.history.prompt_lengths ? max(0, min(a.history.prompt_lengths[slot], length)) : 0;
     }
+    int id = -1;  // this thread's first bias
+    if (bias_from + (int)threadIdx.x < bias_to) id = a.bias_ids[bias_from + threadIdx.x];
+    const int fours = places / kFour * (kWide ? 2 : 1);
+    for (int i = threadIdx.x; i < fours; i += kThreads) shared[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    const int place = kFour - (begin - from);  // of token `from`
-    if (counts) count_tokens(tokens, length, prompt, from, to - from, count + place);
-    for (int i = bias_from + threadIdx.x; i < bias_to; i += kThreads) {
-      const unsigned at = (unsigned)a.bias_ids[i] - (unsigned)from;
-      if (at < (unsigned)(to - from)) atomicMax(&named[place + at], i - bias_from + 1);
+    if (biases) {
+      for (int i = threadIdx.x;;) {
+        raise(words + (kWide ? 4 * places : 0), (uint32_t)(id - from), id < 0 ? 0 : n, (uint32_t)(i + 1) << Layout<kWide>::kBiasShift);
+        i += kThreads;
+        if (bias_from + i >= bias_to) break;
+        id = a.bias_ids[bias_from + i];
+      }
+      if (!kWide) __syncthreads();  // before the lower halves change
+    }
+    for (int base = 0; base < length;) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = base + 4 * (threadIdx.x + j * kThreads);
+        if (i >= length) break;
+        const uint32_t at[4] = {(uint32_t)(tokens[j].x - from), (uint32_t)(tokens[j].y - from),
+                                (uint32_t)(tokens[j].z - from), (uint32_t)(tokens[j].w - from)};
+        if (i + 4 <= prompt) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mark(words, at[k], n, Layout<kWide>::kPrompt);
+        } else if (i >= prompt && i + 4 <= length) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) add(words, at[k], n);
+        } else {  // what holds the end of one of the two
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (i + k < prompt) mark(words, at[k], n, Layout<kWide>::kPrompt);
+            else if (i + k < length) add(words, at[k], n);
+          }
+        }
+      }
+      base += 4 * kBatch * kThreads;
+      if (base < length) ask(base);
     }
     __syncthreads();
   }
+  r.scale = t > 0.f ? 1.f / t : 1.f;
+  r.relief = 1.f / r.repetition;
+  const uint4* noted = shared + 1 + threadIdx.x;
+  for (int at = begin; at < end; at += kChunk, noted += kPer * kThreads) {
+    const Chunk c = next;
+    if (at + kChunk < end) next = fetch(at + kChunk);
+    const int mine = at + kFour * threadIdx.x;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int f = threadIdx.x + j * kThreads, v = begin + kFour * f;
-    if (v >= end) continue;
-    float l[kFour];
-#pragma unroll
-    for (int k = 0; k < kFour; ++k) l[k] = to_float(x[j].v[k]);
-    if (counts) {
-      const uint4 c = reinterpret_cast<const uint4*>(count)[f + 1];
-      if (c.x | c.y | c.z | c.w) {
-        l[0] = penalised(r, l[0], c.x);
-        l[1] = penalised(r, l[1], c.y);
-        l[2] = penalised(r, l[2], c.z);
-        l[3] = penalised(r, l[3], c.w);
+    for (int j = 0; j < kPer; ++j) {
+      if (mine + j * kUnit >= end) break;
+      float l[kFour];
+      floats_of(c.x[j], l);
+      if (counts || biases) {
+        const uint4 w = noted[j * kThreads];
+        uint4 e = make_uint4(0, 0, 0, 0);
+        if (kWide) e = noted[places / kFour + j * kThreads];
+        if (w.x | w.y | w.z | w.w | e.x | e.y | e.z | e.w) {
+          l[0] = penalised<kWide>(r, l[0], w.x, e.x);
+          l[1] = penalised<kWide>(r, l[1], w.y, e.y);
+          l[2] = penalised<kWide>(r, l[2], w.z, e.z);
+          l[3] = penalised<kWide>(r, l[3], w.w, e.w);
+        }
       }
-    }
-    if (biases) {
-      const uint4 e = reinterpret_cast<const uint4*>(named)[f + 1];
-      if (e.x | e.y | e.z | e.w) {
-        l[0] = biased(r, l[0], e.x);
-        l[1] = biased(r, l[1], e.y);
-        l[2] = biased(r, l[2], e.z);
-        l[3] = biased(r, l[3], e.w);
+#pragma unroll
+      for (int k = 0; k < kFour; ++k) l[k] *= r.scale;
+      if (mask) {
+        const uint32_t allowed = astride ? __funnelshift_r(c.word[j], c.next[j], shift) : c.word[j] >> shift;
+#pragma unroll
+        for (int k = 0; k < kFour; ++k) l[k] = allowed & (1u << k) ? l[k] : -INFINITY;
       }
-    }
-    Four<U> y;
-#pragma unroll
-    for (int k = 0; k < kFour; ++k) put(&y.v[k], allowed >> (kFour * j + k) & 1 ? l[k] * r.scale : -INFINITY);
-    if constexpr (kVec) {
-      *reinterpret_cast<Four<U>*>(out + v) = y;
-    } else {
-#pragma unroll
-      for (int k = 0; k < kFour; ++k) out[v + k] = y.v[k];
+      put_four<kVec>(out + mine + j * kUnit, l);
     }
   }
   // the loose tokens, at most three before the first four and three behind the last
-  const int before = begin - from > 0 ? min(begin, to) - from : 0, behind = max(0, to - max(end, begin));
   if ((int)threadIdx.x < before + behind) {
-    const int v = (int)threadIdx.x < before ? from + threadIdx.x : max(end, begin) + threadIdx.x - before;
-    const int at = kFour + v - begin;
-    const float l = biased(r, penalised(r, to_float(in[v]), counts ? count[at] : 0u), biases ? named[at] : 0u);
-    put(&out[v], !r.mask || (r.mask[v >> 5] >> (v & 31) & 1) ? l * r.scale : -INFINITY);
+    const int v = (int)threadIdx.x < before ? threadIdx.x : last + threadIdx.x - before;
+    const uint32_t* word = reinterpret_cast<const uint32_t*>(shared) + kFour + v - begin;
+    float l = get(in + v);
+    if (counts || biases) l = penalised<kWide>(r, l, word[0], kWide ? word[places] : 0u);
+    put(&out[v], !mask || (mask[v >> 5] >> (v & 31) & 1) ? l * r.scale : -INFINITY);
   }
 }
 
 template <typename T, typename U, int kPer>
-cudaError_t run_slices(const LogitsArgs& a, bool vec, cudaStream_t s) {
-  const int slices = (a.V + kPer * kUnit - 1) / (kPer * kUnit);
-  const int arrays = (a.history.tokens ? 1 : 0) + (a.bias_start ? 1 : 0);
-  return launch_dependent(vec ? adjust_logits<T, U, kPer, true> : adjust_logits<T, U, kPer, false>, a.B * slices, kThreads,
-                          arrays * 4 * (kPer * kUnit + 2 * kFour), s, a, slices);
+cudaError_t run_slices(const LogitsArgs& a, int chunks, cudaStream_t s) {
+  const auto place = [](const void* p, size_t size) { return (long long)(reinterpret_cast<uintptr_t>(p) / size % kFour); };
+  const auto same = [](long long x, long long y) { return ((x - y) % kFour) == 0; };
+  const bool vec = same(place(a.logits, sizeof(T)), place(a.out, sizeof(U))) && (a.B == 1 || same(a.stride, a.out_stride));
+  const bool noted = a.history.tokens || a.bias_start;
+  const bool wide = noted && (a.history.columns > kNarrowHistory || a.biases > kNarrowBiases);
+  const int slice = chunks * kPer * kUnit;
+  const auto kernel = vec ? (wide ? adjust_logits<T, U, kPer, true, true> : adjust_logits<T, U, kPer, true, false>)
+                          : (wide ? adjust_logits<T, U, kPer, false, true> : adjust_logits<T, U, kPer, false, false>);
+  const int bytes = noted ? 4 * (slice + 2 * kFour) * (wide ? 2 : 1) : 0;
+  if (bytes > 48 * 1024) {
+    const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), bytes);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_dependent(kernel, dim3((unsigned)((a.V + slice - 1) / slice), (unsigned)a.B), kThreads, bytes, s, a, chunks);
 }
 
 template <typename T, typename U>
 cudaError_t run(const LogitsArgs& a, cudaStream_t s) {
-  const auto place = [](const void* p, size_t size) { return (long long)(reinterpret_cast<uintptr_t>(p) / size % kFour); };
-  const auto same = [](long long x, long long y) { return ((x - y) % kFour) == 0; };
-  const bool vec = same(place(a.logits, sizeof(T)), place(a.out, sizeof(U))) && (a.B == 1 || same(a.stride, a.out_stride));
   // Large slices where the rows fill the GPU (each reads the history once more), smaller ones where they do not.
-  const auto ctas = [&](int per) { return (long long)a.B * ((a.V + per * kUnit - 1) / (per * kUnit)); };
-  if (ctas(4) >= kCtasWanted) return run_slices<T, U, 4>(a, vec, s);
-  if (ctas(2) >= kCtasWanted) return run_slices<T, U, 2>(a, vec, s);
-  return run_slices<T, U, 1>(a, vec, s);
+  const auto enough = [&](int slice) { return (long long)a.B * ((a.V + slice - 1) / slice) >= kCtasWanted; };
+  if (enough(8 * kUnit)) return run_slices<T, U, 4>(a, 2, s);
+  if (enough(4 * kUnit)) return run_slices<T, U, 4>(a, 1, s);
+  if (enough(2 * kUnit)) return run_slices<T, U, 1>(a, 2, s);
+  return run_slices<T, U, 1>(a, 1, s);
 }
 
 template <typename T>

@@ -70,14 +70,16 @@ struct Span {
   int first, n;
 };
 struct Lanes {
+  int shift;      // log2 of per_group
   int per_group;  // lanes of a group
   int per_lane;   // experts of a lane
+  int size;       // experts of a group
 };
-__host__ __device__ inline Lanes lanes_of(int E, int groups) {
-  int up = 1;
-  while (up < groups) up *= 2;
+Lanes lanes_of(int E, int groups) {
+  int up = 1, shift = 5;
+  while (up < groups) up *= 2, --shift;
   const int per_group = 32 / up, size = E / groups;
-  return Lanes{per_group, (size + per_group - 1) / per_group};
+  return Lanes{shift, per_group, (size + per_group - 1) / per_group, size};
 }
 
 // The value of a group from its lanes' two largest keys, in each of its lanes. A masked second
@@ -235,7 +237,7 @@ __device__ __noinline__ void order_again(const RouteArgs& a, const T* x, const S
 template <typename T, int kV>
 __device__ __noinline__ void choose_again(const RouteArgs& a, const T* x, const Span mine, const Lanes lanes, int lane,
                                           float top, int (&ids)[2]) {
-  const int group = lane / lanes.per_group;
+  const int group = lane >> lanes.shift;
   const double sum = exact_sum(a, x, mine, top);
   unsigned long long k[kV];
   double best = -INFINITY, second = -INFINITY;
@@ -263,13 +265,12 @@ __device__ __noinline__ void choose_again(const RouteArgs& a, const T* x, const 
 
 // kWords: logits of 16 bits, and no bias.
 template <typename T, int kV, bool kVec, bool kWords>
-__global__ void __launch_bounds__(32 * kWarps) route(const RouteArgs a, const Lanes lanes) {
+__global__ void __launch_bounds__(32 * kWarps) route(const __grid_constant__ RouteArgs a, const Lanes lanes) {
   const int lane = threadIdx.x & 31;
   const int token = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int size = a.E / a.groups;
-  const int group = lane / lanes.per_group, j = lane % lanes.per_group;
-  Span mine{group * size + j * lanes.per_lane, 0};
-  if (group < a.groups) mine.n = max(0, min(lanes.per_lane, size - j * lanes.per_lane));
+  const int group = lane >> lanes.shift, j = lane & (lanes.per_group - 1);
+  Span mine{group * lanes.size + j * lanes.per_lane, 0};
+  if (group < a.groups) mine.n = max(0, min(lanes.per_lane, lanes.size - j * lanes.per_lane));
   grid_dependency_wait();  // nothing above reads what an earlier kernel may write
   grid_launch_dependents();
   if (token >= a.tokens) return;
