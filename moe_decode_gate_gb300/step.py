@@ -83,14 +83,32 @@ def _vector(name, t, n, dtype, device):
     return t.data_ptr()
 
 
-def _rows(name, t, device):
-    """Strides (token, head) of [tokens, H] or [tokens, heads, H] with contiguous channels."""
+def _setting(name, t, n, device):
+    """_vector for one FP32 number to each of n rows, which are few look-ups where it is right."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.shape != (n,) or t.device != device or not t.is_contiguous():
+        return _vector(name, t, n, torch.float32, device)
+    return t.data_ptr()
+
+
+# As in kv_cache.py each call checks its tensors with as few attribute look-ups as it can (a call costs the host some ten
+# microseconds, most of it the results' allocation and the launch), and says what is wrong in the slow path.
+
+def _refuse_rows(name, t, device):
+    """Says what is wrong with a tensor that should be [tokens, H] or [tokens, heads, H] with contiguous channels."""
+    if t.dtype not in _DTYPES or t.device.type != "cuda":
+        raise ValueError(f"{name} must be a BF16, FP16 or FP32 CUDA tensor")
     if t.device != device or t.dim() not in (2, 3):
         raise ValueError(f"{name} must be [tokens, H] or [tokens, heads, H] on {device}")
-    stride = t.stride()
-    if stride[-1] != 1 and t.shape[-1] != 1:
-        raise ValueError(f"{name} must have contiguous channels")
-    return stride[0], stride[1] if len(stride) == 3 else 0
+    raise ValueError(f"{name} must have contiguous channels")
+
+
+def _refuse_matrix(name, t, columns):
+    """Says what is wrong with a tensor that should be [rows, columns] with contiguous rows."""
+    if t.dtype not in _DTYPES or t.device.type != "cuda" or t.dim() != 2:
+        raise ValueError(f"{name} must be a BF16, FP16 or FP32 CUDA tensor {columns}")
+    raise ValueError(f"{name} must have contiguous rows")
 
 
 def rms_norm(x, weight=None, residual=None, *, eps=1e-6, mxfp8=False, out=None, residual_out=None, stream=None):
@@ -102,11 +120,12 @@ def rms_norm(x, weight=None, residual=None, *, eps=1e-6, mxfp8=False, out=None, 
     sum in x's type comes last.  ``out`` receives the norm in x's type (with ``mxfp8`` in addition to the codes),
     ``residual_out`` the sum; they may be x and residual where those are contiguous."""
     dtype, shape, device = x.dtype, x.shape, x.device
-    code = _DTYPES.get(dtype)
-    if code is None or device.type != "cuda":
-        raise ValueError("x must be a BF16, FP16 or FP32 CUDA tensor")
-    token, head = _rows("x", x, device)
-    H, heads = shape[-1], shape[1] if len(shape) == 3 else 1
+    code, index, strides = _DTYPES.get(dtype), device.index, x.stride()
+    n = len(shape)
+    if code is None or index is None or not 1 < n < 4 or (strides[-1] != 1 and shape[-1] != 1):
+        _refuse_rows("x", x, device)
+    tokens, H = shape[0], shape[-1]
+    token, head, heads = strides[0], strides[1] if n == 3 else 0, shape[1] if n == 3 else 1
     weight_code, w = code, None
     if weight is not None:
         if weight.dtype is not dtype:
@@ -117,10 +136,14 @@ def rms_norm(x, weight=None, residual=None, *, eps=1e-6, mxfp8=False, out=None, 
     if residual is not None:
         if residual.shape != shape or residual.dtype is not dtype:
             raise ValueError("residual must have x's shape and type")
-        res_token, res_head = _rows("residual", residual, device)
+        strides = residual.stride()
+        if residual.device != device or (strides[-1] != 1 and H != 1):
+            _refuse_rows("residual", residual, device)
+        res_token, res_head = strides[0], strides[1] if n == 3 else 0
         res = residual.data_ptr()
         if residual_out is None:
-            residual_out = _output(shape, dtype, device, stream)
+            residual_out = torch.empty(shape, dtype=dtype, device=device) if stream is None else \
+                _output(shape, dtype, device, stream)
             res_to = residual_out.data_ptr()
         else:
             res_to = _given("residual_out", residual_out, shape, dtype, device)
@@ -136,11 +159,13 @@ def rms_norm(x, weight=None, residual=None, *, eps=1e-6, mxfp8=False, out=None, 
         scales = _output((*shape[:-1], H // 32), torch.uint8, device, stream)
         codes_to, scales_to = codes.data_ptr(), scales.data_ptr()
     elif out is None:
-        out = _output(shape, dtype, device, stream)
+        out = torch.empty(shape, dtype=dtype, device=device) if stream is None else \
+            _output(shape, dtype, device, stream)
         y = out.data_ptr()
-    if shape[0] and heads:
-        st = _library().wd_rms_norm(x.data_ptr(), code, token, head, shape[0], heads, H, w, weight_code, res, res_token,
-                                    res_head, res_to, eps, y, codes_to, scales_to, _raw_stream(device, stream))
+    if tokens and heads:
+        st = (_LIB or _library()).wd_rms_norm(x.data_ptr(), code, token, head, tokens, heads, H, w, weight_code, res,
+                                              res_token, res_head, res_to, eps, y, codes_to, scales_to,
+                                              _raw_stream(device, stream))
         if st:
             _check("wd_rms_norm", st)
         if stream is not None:
@@ -159,31 +184,33 @@ def route(logits, K, *, scores="softmax", bias=None, groups=1, top_groups=None, 
     (default: all) with the largest sums of their ``group_best`` (1 or 2) best are open.  Weights are divided by
     their sum if ``renormalise``, and multiplied by ``scale``.  A logit of -inf or NaN masks its expert.  Returns (ids
     int32, weights FP32) [tokens, K], largest key first, the lowest index first of equal ones."""
-    dtype, device = logits.dtype, logits.device
-    code, kind = _DTYPES.get(dtype), _SCORES.get(scores)
-    if code is None or device.type != "cuda" or logits.dim() != 2:
-        raise ValueError("logits must be a BF16, FP16 or FP32 CUDA tensor [tokens, E]")
+    shape, device = logits.shape, logits.device
+    code, kind = _DTYPES.get(logits.dtype), _SCORES.get(scores)
+    if code is None or device.index is None or len(shape) != 2:
+        _refuse_matrix("logits", logits, "[tokens, E]")
     if kind is None:
         raise ValueError(f"scores must be one of {', '.join(_SCORES)}")
-    tokens, E = logits.shape
+    tokens, E = shape
     stride, last = logits.stride()
     if last != 1 and E != 1:
-        raise ValueError("logits must have contiguous rows")
+        _refuse_matrix("logits", logits, "[tokens, E]")
     b = None if bias is None else _vector("bias", bias, E, torch.float32, device)
     shape = (tokens, K)
     if ids is None:
-        ids = _output(shape, torch.int32, device, stream)
+        ids = torch.empty(shape, dtype=torch.int32, device=device) if stream is None else \
+            _output(shape, torch.int32, device, stream)
         ids_to = ids.data_ptr()
     else:
         ids_to = _given("ids", ids, shape, torch.int32, device)
     if weights is None:
-        weights = _output(shape, torch.float32, device, stream)
+        weights = torch.empty(shape, dtype=torch.float32, device=device) if stream is None else \
+            _output(shape, torch.float32, device, stream)
         weights_to = weights.data_ptr()
     else:
         weights_to = _given("weights", weights, shape, torch.float32, device)
-    st = _library().wd_route(logits.data_ptr(), code, stride, tokens, E, K, kind, b, groups,
-                             groups if top_groups is None else top_groups, group_best, renormalise, scale, ids_to,
-                             weights_to, _raw_stream(device, stream))
+    st = (_LIB or _library()).wd_route(logits.data_ptr(), code, stride, tokens, E, K, kind, b, groups,
+                                       groups if top_groups is None else top_groups, group_best, renormalise, scale,
+                                       ids_to, weights_to, _raw_stream(device, stream))
     if st:
         _check("wd_route", st)
     if stream is not None:
@@ -201,25 +228,24 @@ def adjust_logits(logits, *, history=None, lengths=None, prompt_lengths=None, se
     ``temperature`` are FP32 [B]; ``bias`` is (start int32 [B + 1], ids int32 [N], values FP32 [N]); ``mask`` int32 words
     [B, ceil(V / 32)], a token to a bit.  Steps and order: include/wd_step.h.  Returns [B, V] of ``dtype`` (logits' own
     type, the default, or FP32), in ``out`` if given, which may be logits."""
-    kind, device = logits.dtype, logits.device
+    kind, shape, device = logits.dtype, logits.shape, logits.device
     code = _DTYPES.get(kind)
-    if code is None or device.type != "cuda" or logits.dim() != 2:
-        raise ValueError("logits must be a BF16, FP16 or FP32 CUDA tensor [B, V]")
-    B, V = logits.shape
+    if code is None or device.index is None or len(shape) != 2:
+        _refuse_matrix("logits", logits, "[B, V]")
+    B, V = shape
     stride, last = logits.stride()
     if last != 1 and V != 1:
-        raise ValueError("logits must have contiguous rows")
+        _refuse_matrix("logits", logits, "[B, V]")
     to = kind if dtype is None else dtype
     if out is not None and dtype is None:
         to = out.dtype
     if to is not kind and to is not torch.float32:
         raise ValueError(f"dtype must be {kind} or {torch.float32}")
     if out is None:
-        out = _output((B, V), to, device, stream)
+        out = torch.empty(shape, dtype=to, device=device) if stream is None else _output(shape, to, device, stream)
         out_stride = V
     else:
-        if out.shape != logits.shape or out.dtype is not to or out.device != device or \
-                (out.stride(1) != 1 and V != 1):
+        if out.shape != shape or out.dtype is not to or out.device != device or (out.stride(1) != 1 and V != 1):
             raise ValueError(f"out must be {to} {[B, V]} with contiguous rows on {device}")
         out_stride = out.stride(0)
     h = None
@@ -255,12 +281,11 @@ def adjust_logits(logits, *, history=None, lengths=None, prompt_lengths=None, se
                 (mask.stride(1) != 1 and mask.shape[1] != 1):
             raise ValueError(f"mask must be int32 {[B, (V + 31) // 32]} with contiguous rows on {device}")
         m, mask_stride = mask.data_ptr(), mask.stride(0)
-    f32 = torch.float32
-    st = _library().wd_adjust_logits(
+    st = (_LIB or _library()).wd_adjust_logits(
         logits.data_ptr(), code, stride, B, V, None if h is None else ctypes.byref(h),
-        _vector("repetition", repetition, B, f32, device), _vector("presence", presence, B, f32, device),
-        _vector("frequency", frequency, B, f32, device), start, ids, values, n,
-        _vector("temperature", temperature, B, f32, device), m, mask_stride, out.data_ptr(), _DTYPES[to], out_stride,
+        _setting("repetition", repetition, B, device), _setting("presence", presence, B, device),
+        _setting("frequency", frequency, B, device), start, ids, values, n,
+        _setting("temperature", temperature, B, device), m, mask_stride, out.data_ptr(), _DTYPES[to], out_stride,
         _raw_stream(device, stream))
     if st:
         _check("wd_adjust_logits", st)
