@@ -200,88 +200,100 @@ __device__ __forceinline__ void store_eight(const float (&f)[8], uint32_t top, u
 // and 4 to 7 and sines alike are float4 e of the row's first, second, third and fourth quarter, so that a warp
 // reads each without bank conflicts.
 template <int D>
-__device__ __forceinline__ void stage(const KvRotateArgs& a, int base, int n, Place* place, float4* turns) {
+__device__ __forceinline__ void stage(const KvRotateArgs& a, int base, int n, int rot, Place* place, float4* turns) {
   if ((int)threadIdx.x < n) place[threadIdx.x] = rotated_place<D>(a, base + threadIdx.x);
   __syncthreads();
-  const int eights = a.rot / 16, fours = a.rot / 4;
+  const int eights = rot / 16, fours = rot / 4;
   for (int i = threadIdx.x; i < n * fours; i += kThreads) {
     const int token = i / fours, f = i - token * fours;
     const int pos = place[token].pos;
     if (pos < 0) continue;
     const int quarter = (f & 1) + (f >= 2 * eights ? 2 : 0), e = (f >= 2 * eights ? f - 2 * eights : f) >> 1;
-    turns[token * fours + quarter * eights + e] = reinterpret_cast<const float4*>(a.cos_sin + (long long)pos * a.rot)[f];
+    turns[token * fours + quarter * eights + e] = reinterpret_cast<const float4*>(a.cos_sin + (long long)pos * rot)[f];
   }
   __syncthreads();
 }
 
+// kWhole: all channels are turned, in runs (rot = D, not paired); else as the arguments say.
+
 // Queries of tokens [base, base + n).
-template <typename T, int D, bool kVec>
+template <typename T, int D, bool kVec, bool kWhole>
 __device__ __forceinline__ void queries(const KvRotateArgs& a, int base, int n, Place* place, float4* turns) {
   constexpr int kPerRow = D / 16;  // threads to a token and head
   constexpr int kRowsOfThreads = kThreads / kPerRow;
-  const int half = a.rot / 2, eights = a.rot / 16, fours = a.rot / 4;
+  const int rot = kWhole ? D : a.rot;
+  const bool paired = !kWhole && a.paired;
+  const int half = rot / 2, eights = rot / 16, fours = rot / 4;
   const int e = threadIdx.x % kPerRow, row0 = threadIdx.x / kPerRow;
-  const bool turned = 16 * e < a.rot;  // else 16 channels that stay as they are
+  const bool turned = kWhole || 16 * e < rot;  // else 16 channels that stay as they are
   // this thread's two runs of 8 channels
-  const int c0 = turned && !a.paired ? 8 * e : 16 * e;
-  const int c1 = turned && !a.paired ? 8 * e + half : 16 * e + 8;
+  const int c0 = turned && !paired ? 8 * e : 16 * e;
+  const int apart = turned && !paired ? half : 8;
   const int at_once = max(1, kRowsOfThreads / a.q_heads);  // tokens
   const int token0 = row0 / a.q_heads;                     // (0 if there are more heads than threads for them)
+  const long long src_step = at_once * a.q_token, dst_step = (long long)at_once * a.q_heads * D;
   bool staged = false;
   for (int h = row0 - token0 * a.q_heads; h < a.q_heads || !staged; h += kRowsOfThreads) {
     const bool here = h < a.q_heads && token0 < at_once;
-    const T* src = static_cast<const T*>(a.q) + (base + token0) * a.q_token + h * a.q_head;
+    const T* src = static_cast<const T*>(a.q) + (base + token0) * a.q_token + h * a.q_head + c0;
     Words<T> next0, next1;
     if (here && token0 < n) {  // on their way while the places are found
-      next0 = fetch<T, kVec>(src + c0);
-      next1 = fetch<T, kVec>(src + c1);
+      next0 = fetch<T, kVec>(src);
+      next1 = fetch<T, kVec>(src + apart);
     }
     if (!staged) {
-      stage<D>(a, base, n, place, turns);
+      stage<D>(a, base, n, rot, place, turns);
       staged = true;
     }
     if (!here) continue;
-    T* dst = static_cast<T*>(a.q_out) + ((long long)(base + token0) * a.q_heads + h) * D;
+    T* dst = static_cast<T*>(a.q_out) + ((long long)(base + token0) * a.q_heads + h) * D + c0;
+    const float4* row = turns + token0 * fours + e;
     for (int token = token0; token < n; token += at_once) {
-      Words<T> x0 = next0, x1 = next1;
-      src += at_once * a.q_token;
+      const bool write = place[token].pos >= 0;
+      float f[8], g[8];
+      if (turned) {
+        floats_of(next0, f);
+        floats_of(next1, g);
+      } else if (write) {
+        put<T, kVec>(dst, next0);
+        put<T, kVec>(dst + apart, next1);
+      }
+      src += src_step;
       if (token + at_once < n) {
-        next0 = fetch<T, kVec>(src + c0);
-        next1 = fetch<T, kVec>(src + c1);
+        next0 = fetch<T, kVec>(src);
+        next1 = fetch<T, kVec>(src + apart);
       }
-      if (place[token].pos >= 0) {
-        if (turned) {
-          float f[8], g[8];
-          floats_of(x0, f);
-          floats_of(x1, g);
-          const float4* row = turns + token * fours + e;
-          const float4 ca = row[0], cb = row[eights], sa = row[2 * eights], sb = row[3 * eights];
-          if (a.paired) {
-            turn_neighbours(f, ca, sa);
-            turn_neighbours(g, cb, sb);
-          } else {
-            turn_runs(f, g, ca, sa);
-            turn_runs(f + 4, g + 4, cb, sb);
-          }
-          words_of(f, x0);
-          words_of(g, x1);
+      if (turned && write) {
+        const float4 ca = row[0], cb = row[eights], sa = row[2 * eights], sb = row[3 * eights];
+        if (paired) {
+          turn_neighbours(f, ca, sa);
+          turn_neighbours(g, cb, sb);
+        } else {
+          turn_runs(f, g, ca, sa);
+          turn_runs(f + 4, g + 4, cb, sb);
         }
-        put<T, kVec>(dst + c0, x0);
-        put<T, kVec>(dst + c1, x1);
+        Words<T> x;
+        words_of(f, x);
+        put<T, kVec>(dst, x);
+        words_of(g, x);
+        put<T, kVec>(dst + apart, x);
       }
-      dst += (long long)at_once * a.q_heads * D;
+      dst += dst_step;
+      row += at_once * fours;
     }
   }
 }
 
 // Keys and values of tokens [base, base + n).
-template <typename T, int D, bool kVec>
+template <typename T, int D, bool kVec, bool kWhole>
 __device__ __forceinline__ void keys_and_values(const KvRotateArgs& a, int base, int n, Place* place, float4* turns) {
   constexpr int kPerRow = D / 8;  // threads to a token, head and side
   constexpr int kRowsOfThreads = kThreads / kPerRow;
   const KvView& c = a.kv.cache;
   const int rows = 2 * c.kv_heads;  // of a token: the heads' K, then the heads' V
-  const int half = a.rot / 2, eights = a.rot / 16, fours = a.rot / 4;
+  const int rot = kWhole ? D : a.rot;
+  const bool paired = !kWhole && a.paired;
+  const int half = rot / 2, eights = rot / 16, fours = rot / 4;
   const int e = threadIdx.x % kPerRow;  // channels 8e .. 8e + 7
   const int row0 = threadIdx.x / kPerRow;
   const int at_once = max(1, kRowsOfThreads / rows);  // tokens
@@ -290,12 +302,13 @@ __device__ __forceinline__ void keys_and_values(const KvRotateArgs& a, int base,
   const unsigned lanes = kPerRow >= 32 ? 0xFFFFFFFFu
                                        : ((1u << (kPerRow % 32)) - 1u) << (threadIdx.x & 31 & ~(kPerRow - 1));
   const bool lower = 8 * e < half;  // of the two halves that a rotation pairs
+  const uint32_t sign = lower ? 0x80000000u : 0u;
   bool staged = false;
   for (int hs = row0 - token0 * rows; hs < rows || !staged; hs += kRowsOfThreads) {
     const bool here = hs < rows && token0 < at_once;
     const bool v = hs >= c.kv_heads;
     const int head = v ? hs - c.kv_heads : hs;
-    const bool turned = !v && 8 * e < a.rot, partnered = turned && !a.paired;
+    const bool turned = !v && (kWhole || 8 * e < rot), partnered = turned && !paired;
     const long long stride = v ? a.kv.v_token : a.kv.k_token;
     const T* src = static_cast<const T*>(v ? a.kv.v : a.kv.k) + (base + token0) * stride +
                    head * (v ? a.kv.v_head : a.kv.k_head) + 8 * e;
@@ -306,7 +319,7 @@ __device__ __forceinline__ void keys_and_values(const KvRotateArgs& a, int base,
       if (partnered) next_partner = fetch<T, kVec>(src + partner);
     }
     if (!staged) {
-      stage<D>(a, base, n, place, turns);
+      stage<D>(a, base, n, rot, place, turns);
       staged = true;
     }
     if (!here) continue;
@@ -323,7 +336,7 @@ __device__ __forceinline__ void keys_and_values(const KvRotateArgs& a, int base,
       }
       if (turned && place[token].pos >= 0) {
         const float4* row = turns + token * fours;
-        if (a.paired) {
+        if (paired) {
           row += (e & 1) * eights + (e >> 1);
           turn_neighbours(f, row[0], row[2 * eights]);
         } else {
@@ -333,7 +346,8 @@ __device__ __forceinline__ void keys_and_values(const KvRotateArgs& a, int base,
           const float si[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
 #pragma unroll
           for (int k = 0; k < 8; ++k)  // x1 c - x2 s, or x2 c + x1 s
-            f[k] = __fadd_rn(__fmul_rn(f[k], co[k]), __fmul_rn(g[k], lower ? -si[k] : si[k]));
+            f[k] = __fadd_rn(__fmul_rn(f[k], co[k]),
+                             __fmul_rn(g[k], __uint_as_float(__float_as_uint(si[k]) ^ sign)));
         }
       }
       uint32_t top = 0;
@@ -345,19 +359,22 @@ __device__ __forceinline__ void keys_and_values(const KvRotateArgs& a, int base,
   }
 }
 
-// The first kv_ctas CTAs take keys and values of kv_tokens tokens each, the others queries of q_tokens.
-template <typename T, int D, bool kVec>
-__global__ void __launch_bounds__(kThreads, 4) kv_append_rotated(const KvRotateArgs a, int kv_ctas, int kv_tokens, int q_tokens) {
+// CTAs of kv_tokens tokens' keys and values and of q_tokens' queries by turns (the first have more to compute, the others
+// more to move), and the rest of either behind them.
+template <typename T, int D, bool kVec, bool kWhole>
+__global__ void __launch_bounds__(kThreads, 4)
+    kv_append_rotated(const KvRotateArgs a, int kv_ctas, int kv_tokens, int q_ctas, int q_tokens) {
   __shared__ Place place[kMaxTokens];
   extern __shared__ float4 turns[];
   grid_dependency_wait();  // nothing above reads what an earlier kernel may write
   grid_launch_dependents();
-  if ((int)blockIdx.x < kv_ctas) {
-    const int base = blockIdx.x * kv_tokens;
-    keys_and_values<T, D, kVec>(a, base, min(kv_tokens, a.kv.batch.tokens - base), place, turns);
+  const int i = blockIdx.x, both = 2 * min(kv_ctas, q_ctas);
+  if (i < both ? i % 2 == 0 : kv_ctas > q_ctas) {
+    const int base = (i < both ? i / 2 : i - both / 2) * kv_tokens;
+    keys_and_values<T, D, kVec, kWhole>(a, base, min(kv_tokens, a.kv.batch.tokens - base), place, turns);
   } else {
-    const int base = (blockIdx.x - kv_ctas) * q_tokens;
-    queries<T, D, kVec>(a, base, min(q_tokens, a.kv.batch.tokens - base), place, turns);
+    const int base = (i < both ? i / 2 : i - both / 2) * q_tokens;
+    queries<T, D, kVec, kWhole>(a, base, min(q_tokens, a.kv.batch.tokens - base), place, turns);
   }
 }
 
@@ -383,8 +400,11 @@ cudaError_t run(const KvRotateArgs& a, cudaStream_t s) {
   const bool vec = aligned16(kv.k) && aligned16(kv.v) && aligned16(kv.k_out) && aligned16(kv.v_out) && aligned16(a.q) &&
                    aligned16(a.q_out) && kv.k_token % u == 0 && kv.k_head % u == 0 && kv.v_token % u == 0 &&
                    kv.v_head % u == 0 && a.q_token % u == 0 && a.q_head % u == 0;
-  return launch_dependent(vec ? kv_append_rotated<T, D, true> : kv_append_rotated<T, D, false>, kv_ctas + q_ctas, kThreads,
-                          4 * a.rot * (q_tokens > kv_tokens ? q_tokens : kv_tokens), s, a, kv_ctas, kv_tokens, q_tokens);
+  const auto kernel = !vec ? kv_append_rotated<T, D, false, false>
+                      : a.rot == D && !a.paired ? kv_append_rotated<T, D, true, true>
+                                                : kv_append_rotated<T, D, true, false>;
+  return launch_dependent(kernel, kv_ctas + q_ctas, kThreads, 4 * a.rot * (q_tokens > kv_tokens ? q_tokens : kv_tokens), s,
+                          a, kv_ctas, kv_tokens, q_ctas, q_tokens);
 }
 
 template <typename T>

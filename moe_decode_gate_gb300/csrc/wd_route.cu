@@ -163,19 +163,29 @@ __device__ __forceinline__ void sort_down(uint32_t (&k)[kV]) {
 template <int kV>
 __device__ __forceinline__ void take_words(uint32_t (&k)[kV], int K, int lane, uint32_t (&words)[2]) {
   sort_down<kV>(k);
-  for (int r = 0; r < K; ++r) {
+  const auto next = [&] {  // the largest of all, taken from the lane that has it
     const uint32_t all = largest(k[0]);
-    if (k[0] == all) {
+    const bool taken = k[0] == all;
 #pragma unroll
-      for (int i = 0; i + 1 < kV; ++i) k[i] = k[i + 1];
-      k[kV - 1] = 0;
-    }
-    if (lane == r) words[0] = all;
-    if (lane + 32 == r) words[1] = all;
+    for (int i = 0; i < kV; ++i) k[i] = taken ? (i + 1 < kV ? k[i + 1] : 0u) : k[i];
+    return all;
+  };
+#pragma unroll 4
+  for (int r = 0; r < min(K, 32); ++r) {
+    const uint32_t all = next();
+    words[0] = lane == r ? all : words[0];
+  }
+  for (int r = 32; r < K; ++r) {
+    const uint32_t all = next();
+    words[1] = lane + 32 == r ? all : words[1];
   }
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+
+// For keys, which are compared as they are: __expf is off by |x| units relative to itself, s (1 - s) of which reaches the
+// sigmoid s, at most one unit of 1; the quotient by two.
+__device__ __forceinline__ float sigmoid_key(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
 // exp(x - top), where top is at least x; 1 for the largest even if infinite, 0 for masked ones.
 __device__ __forceinline__ float exp_below(float x, float top) {
@@ -314,7 +324,7 @@ __global__ void __launch_bounds__(32 * kWarps) route(const __grid_constant__ Rou
 #pragma unroll
     for (int i = 0; i < kV; ++i) {
       if (l[i] > -INFINITY) {
-        s[i] = a.sigmoid ? sigmoid(l[i]) : s[i] * unit;
+        s[i] = a.sigmoid ? sigmoid_key(l[i]) : s[i] * unit;
         if (a.bias) s[i] += a.bias[mine.first + i];
         if (!(s[i] == s[i])) s[i] = -INFINITY;
         if (fabsf(s[i]) < INFINITY) most = fmaxf(most, fabsf(s[i]));
@@ -322,8 +332,9 @@ __global__ void __launch_bounds__(32 * kWarps) route(const __grid_constant__ Rou
         s[i] = -INFINITY;
       }
     }
-    // In units of 2^-24, a score is off by 2 (expf), 1 (its argument), 2 (quotient), 1 (the product by it) and the sum
-    // of all of them, kV + 5 roundings at most; a key by half a unit of its own more. Two keys are compared.
+    // In units of 2^-24, a softmax' score is off by 2 (expf), 1 (its argument), 2 (quotient), 1 (the product by it) and the
+    // sum of all of them, kV + 5 roundings at most; a sigmoid's by less than 12 of 1; a key by half a unit of its own more.
+    // Two keys are compared.
     most = warp_max(most);
     margin = 0x1p-23f * (a.sigmoid ? 12 : kV + 12) * unit + 0x1p-23f * most;
   }
