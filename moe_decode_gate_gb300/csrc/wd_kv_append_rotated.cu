@@ -362,7 +362,7 @@ __device__ __forceinline__ void keys_and_values(const KvRotateArgs& a, int base,
 // CTAs of kv_tokens tokens' keys and values and of q_tokens' queries by turns (the first have more to compute, the others
 // more to move), and the rest of either behind them.
 template <typename T, int D, bool kVec, bool kWhole>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 5)
     kv_append_rotated(const KvRotateArgs a, int kv_ctas, int kv_tokens, int q_ctas, int q_tokens) {
   __shared__ Place place[kMaxTokens];
   extern __shared__ float4 turns[];

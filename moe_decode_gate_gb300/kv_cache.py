@@ -266,55 +266,54 @@ class KVCache:
         head are turned, channels i and i + rot / 2 together, or with ``paired`` 2i and 2i + 1.  Returns the turned queries
         (in ``q_out`` if given, which may be q), and with ``return_values`` what the cache now holds, (q, k, v);
         tokens of no entry, and those at positions that cos_sin does not have, are undefined in them."""
-        dtype, shape = k.dtype, k.shape
+        dtype, shape, device, dim = k.dtype, k.shape, self.device, self.head_dim
         code = _DTYPES.get(dtype)
-        if code is None or len(shape) != 3 or shape[1] != self.kv_heads or \
-                shape[2] != self.head_dim or k.device != self.device:
+        if code is None or len(shape) != 3 or shape[1] != self.kv_heads or shape[2] != dim or k.device != device:
             self._refuse("k", k, self.kv_heads, _DTYPES)
-        if v.dtype is not dtype or v.shape != shape or v.device != self.device:
+        if v.dtype is not dtype or v.shape != shape or v.device != device:
             raise ValueError("v must have k's shape and type, on its device")
         k_token, k_head, k_channel = k.stride()
         v_token, v_head, v_channel = v.stride()
         if k_channel != 1 or v_channel != 1:
             raise ValueError("k and v must have contiguous channels")
-        tokens = shape[0]
-        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or cos_sin.device != self.device or \
+        tokens, turns = shape[0], cos_sin.shape
+        if cos_sin.dtype is not torch.float32 or len(turns) != 2 or cos_sin.device != device or \
                 not cos_sin.is_contiguous():
-            raise ValueError(f"cos_sin must be contiguous FP32 [positions, rot] on {self.device}")
-        positions, rot = cos_sin.shape
+            raise ValueError(f"cos_sin must be contiguous FP32 [positions, rot] on {device}")
         heads = q_token = q_head = 0
         q_from = q_to = None
         if q is not None:
-            if q.dtype is not dtype or q.dim() != 3 or q.shape[0] != tokens or q.shape[2] != self.head_dim or \
-                    q.device != self.device:
-                raise ValueError(f"q must be [{tokens}, heads, {self.head_dim}] of k's type, on its device")
+            q_shape = q.shape
+            if q.dtype is not dtype or len(q_shape) != 3 or q_shape[0] != tokens or q_shape[2] != dim or \
+                    q.device != device:
+                raise ValueError(f"q must be [{tokens}, heads, {dim}] of k's type, on its device")
             q_token, q_head, q_channel = q.stride()
             if q_channel != 1:
                 raise ValueError("q must have contiguous channels")
-            heads, q_from = q.shape[1], q.data_ptr()
+            heads, q_from = q_shape[1], q.data_ptr()
             if q_out is None:
-                q_out = self._output(q.shape, dtype, stream)
-            elif q_out.shape != q.shape or q_out.dtype is not dtype or not q_out.is_contiguous() or \
-                    q_out.device != self.device:
+                q_out = torch.empty(q_shape, dtype=dtype, device=device) if stream is None else \
+                    self._output(q_shape, dtype, stream)
+            elif q_out.shape != q_shape or q_out.dtype is not dtype or not q_out.is_contiguous() or \
+                    q_out.device != device:
                 raise ValueError("q_out must be contiguous, of q's shape and type")
             q_to = q_out.data_ptr()
         elif q_out is not None:
             raise ValueError("q_out without q")
         s, qs, n = self._entries(seqs, q_start, tokens)
+        k_out = v_out = k_to = v_to = None
         if return_values:
-            values = self._output((2, *shape), dtype, stream)
-            k_to = values.data_ptr()
-            v_to = k_to + values.nbytes // 2
-        else:
-            values = k_to = v_to = None
+            k_out, v_out = self._output(shape, dtype, stream), self._output(shape, dtype, stream)
+            k_to, v_to = k_out.data_ptr(), v_out.data_ptr()
         st = self._lib.wd_kv_append_rotated(
             self._ref, layer, q_from, k.data_ptr(), v.data_ptr(), code, q_token, q_head, heads, k_token, k_head,
-            v_token, v_head, q_to, k_to, v_to, cos_sin.data_ptr(), positions, rot, paired, s, qs, n, tokens,
+            v_token, v_head, q_to, k_to, v_to, cos_sin.data_ptr(), turns[0], turns[1], paired, s, qs, n, tokens,
             self._stream(stream))
         if st:
             _check("wd_kv_append_rotated", st)
-        self._keep(stream, q, k, v, cos_sin, seqs, q_start, q_out, values)
-        return (q_out, *values.unbind(0)) if return_values else q_out
+        if stream is not None:
+            self._keep(stream, q, k, v, cos_sin, seqs, q_start, q_out, k_out, v_out)
+        return (q_out, k_out, v_out) if return_values else q_out
 
     def attention(self, layer, q, seqs=None, q_start=None, max_q=0, scale=None, window=0, out=None,
                   return_lse=False, stream=None):

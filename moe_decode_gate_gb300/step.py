@@ -83,12 +83,12 @@ def _vector(name, t, n, dtype, device):
     return t.data_ptr()
 
 
-def _setting(name, t, n, device):
-    """_vector for one FP32 number to each of n rows, which are few look-ups where it is right."""
+def _per(name, t, n, dtype, device):
+    """_vector of one number to each of n, with few look-ups where it is right."""
     if t is None:
         return None
-    if t.dtype is not torch.float32 or t.shape != (n,) or t.device != device or not t.is_contiguous():
-        return _vector(name, t, n, torch.float32, device)
+    if t.dtype is not dtype or t.shape != (n,) or t.device != device or not t.is_contiguous():
+        _vector(name, t, n, dtype, device)
     return t.data_ptr()
 
 
@@ -155,8 +155,10 @@ def rms_norm(x, weight=None, residual=None, *, eps=1e-6, mxfp8=False, out=None, 
     if mxfp8:
         if H % 32:
             raise ValueError(f"MXFP8 wants a multiple of 32 channels, not {H}")
-        codes = _output(shape, torch.uint8, device, stream)
-        scales = _output((*shape[:-1], H // 32), torch.uint8, device, stream)
+        u8, per_block = torch.uint8, (*shape[:-1], H // 32)
+        codes = torch.empty(shape, dtype=u8, device=device) if stream is None else _output(shape, u8, device, stream)
+        scales = torch.empty(per_block, dtype=u8, device=device) if stream is None else \
+            _output(per_block, u8, device, stream)
         codes_to, scales_to = codes.data_ptr(), scales.data_ptr()
     elif out is None:
         out = torch.empty(shape, dtype=dtype, device=device) if stream is None else \
@@ -256,9 +258,10 @@ def adjust_logits(logits, *, history=None, lengths=None, prompt_lengths=None, se
         if lengths is None:
             raise ValueError("history needs lengths")
         slots, columns = history.shape
-        h = _History(history.data_ptr(), _vector("lengths", lengths, slots, torch.int32, device),
-                     _vector("prompt_lengths", prompt_lengths, slots, torch.int32, device),
-                     _vector("seqs", seqs, B, torch.int32, device), history.stride(0), slots, columns)
+        i32 = torch.int32
+        h = _History(history.data_ptr(), _per("lengths", lengths, slots, i32, device),
+                     _per("prompt_lengths", prompt_lengths, slots, i32, device), _per("seqs", seqs, B, i32, device),
+                     history.stride(0), slots, columns)
         if not columns:  # nothing came before
             h = repetition = presence = frequency = None
     elif repetition is not None or presence is not None or frequency is not None:
@@ -270,9 +273,9 @@ def adjust_logits(logits, *, history=None, lengths=None, prompt_lengths=None, se
     if bias is not None:
         starts, tokens, amounts = bias
         n = tokens.shape[0]
-        start = _vector("bias start", starts, B + 1, torch.int32, device)
-        ids = _vector("bias ids", tokens, n, torch.int32, device)
-        values = _vector("bias values", amounts, n, torch.float32, device)
+        start = _per("bias start", starts, B + 1, torch.int32, device)
+        ids = _per("bias ids", tokens, n, torch.int32, device)
+        values = _per("bias values", amounts, n, torch.float32, device)
         if not n:
             start = ids = values = None
     m, mask_stride = None, 0
@@ -281,11 +284,12 @@ def adjust_logits(logits, *, history=None, lengths=None, prompt_lengths=None, se
                 (mask.stride(1) != 1 and mask.shape[1] != 1):
             raise ValueError(f"mask must be int32 {[B, (V + 31) // 32]} with contiguous rows on {device}")
         m, mask_stride = mask.data_ptr(), mask.stride(0)
+    f32 = torch.float32
     st = (_LIB or _library()).wd_adjust_logits(
         logits.data_ptr(), code, stride, B, V, None if h is None else ctypes.byref(h),
-        _setting("repetition", repetition, B, device), _setting("presence", presence, B, device),
-        _setting("frequency", frequency, B, device), start, ids, values, n,
-        _setting("temperature", temperature, B, device), m, mask_stride, out.data_ptr(), _DTYPES[to], out_stride,
+        _per("repetition", repetition, B, f32, device), _per("presence", presence, B, f32, device),
+        _per("frequency", frequency, B, f32, device), start, ids, values, n,
+        _per("temperature", temperature, B, f32, device), m, mask_stride, out.data_ptr(), _DTYPES[to], out_stride,
         _raw_stream(device, stream))
     if st:
         _check("wd_adjust_logits", st)

@@ -208,7 +208,7 @@ def rotated(cache, given=lambda t: t, stream=None, **kw):  # noqa: F811
 def test_rotated_on_another_stream(cache):  # noqa: F811
     side, given = test_kv_streams.Side(), []
     rotated(cache, lambda d: given.extend(d.values()), side, return_values=True, q_start=kv((5,), I32))
-    assert len(cache.made) == 2 and len(cache.launched) == 1
+    assert len(cache.made) == 3 and len(cache.launched) == 1
     for t in cache.made:
         assert t.made_on is side and "current" in t.used_on
     for t in (*(g for g in given if g is not True), cache.pool, cache.table, cache.lengths, cache.refs, cache.workspace):
