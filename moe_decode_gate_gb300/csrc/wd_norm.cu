@@ -1,13 +1,15 @@
 // wd_norm.cu - residual addition and root-mean-square norm, to the input's type
 // or to MXFP8 (declared in include/wd_step.h).
 //
-// A row stands in the registers of kTpr threads (a warp, or a CTA) from its one reading to
+// A row stands in the registers of its threads (8 or 16 lanes, a warp, or a CTA) from its one reading to
 // its one writing: r = x + residual, the sum of squares over the threads, y. Bytes bound it: x and
 // residual in, r and y out, and nothing else but the weights, which stay in L2.
 //
-// Rows of whole, aligned vectors give a thread 8 elements at a time; four neighbouring lanes then hold a
-// block of 32, whose largest magnitude is two shuffles away. Any other row (odd H, odd strides) is
-// taken one element to a lane, so that a warp's access stays contiguous, and a block is a warp.
+// A thread takes eight elements at a time, of 16 aligned bytes (32 in FP32). Where H is a multiple of eight and all is
+// aligned, four neighbouring lanes hold a block of 32, whose largest magnitude is two shuffles away. Where rows begin
+// anywhere but all tensors alike (odd H), the eights begin at the aligned place before the row, and the first and the
+// last of them are taken element by element. What is left (tensors of unlike alignment, MXFP8 of unaligned rows) is taken one element
+// to a lane, so that a warp's access stays contiguous, and a block is a warp.
 #include <float.h>
 
 #include "wd_device.cuh"
@@ -17,7 +19,8 @@
 namespace wd {
 namespace {
 
-constexpr int kMinThreads = 128;  // of a CTA: short rows share one
+constexpr int kThreads = 128;  // of a CTA whose rows are a warp's or less
+enum Mode { kAligned, kShifted, kSingle };
 
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -45,53 +48,77 @@ __device__ __forceinline__ float exp2_of(int e) {
   return e < -126 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// The sum over the kTpr threads of a row, the same bits in each of them.
+// The sum over the threads of a row (kTpr lanes; 0: the CTA), the same bits in each of them.
 template <int kTpr>
 __device__ __forceinline__ float row_sum(float v, float* part) {
-  v = warp_sum(v);
-  if (kTpr <= 32) return v;
-  constexpr int kWarps = kTpr / 32;
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0.f;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) v += part[i];
-  return v;
+  for (int off = kTpr ? kTpr / 2 : 16; off > 0; off /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+  if (kTpr) return v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_sum(lane < (int)(blockDim.x >> 5) ? part[lane] : 0.f);
 }
 
-// kPer: groups of 8 elements of a thread; kVec: they are consecutive and aligned.
-template <typename T, int kTpr, int kPer, bool kVec>
-__global__ void __launch_bounds__(kTpr < kMinThreads ? kMinThreads : kTpr)
-    rms_norm(const NormArgs a) {
-  constexpr int kThreads = kTpr < kMinThreads ? kMinThreads : kTpr;
-  __shared__ float part[2][kThreads / 32];
-  const int t = threadIdx.x % kTpr;
-  const long long row = (long long)blockIdx.x * (kThreads / kTpr) + threadIdx.x / kTpr;
+// Eights of a row of H elements: elements j .. j + 7, of which those count that are in the row.
+template <typename T, Mode kMode>
+__device__ __forceinline__ Eight<T> get_eight(const T* row, int j, int H) {
+  Eight<T> x;
+  if (kMode == kAligned || (j >= 0 && j + 8 <= H)) {
+    x = *reinterpret_cast<const Eight<T>*>(row + j);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x.v[k] = j + k >= 0 && j + k < H ? row[j + k] : T(0.f);
+  }
+  return x;
+}
+template <typename T, Mode kMode>
+__device__ __forceinline__ void put_eight(T* row, int j, int H, const float (&f)[8]) {
+  if (kMode == kAligned || (j >= 0 && j + 8 <= H)) {
+    *reinterpret_cast<Eight<T>*>(row + j) = narrow<T>(f);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (j + k >= 0 && j + k < H) narrow_to(row + j + k, f[k]);
+  }
+}
+
+// Rows of kTpr lanes (0: a CTA), kPer eights to a thread.
+template <typename T, int kTpr, int kPer, Mode kMode>
+__global__ void __launch_bounds__(kTpr ? kThreads : 512) rms_norm(const NormArgs a) {
+  __shared__ float part[2][32];
+  const int tpr = kTpr ? kTpr : blockDim.x;
+  const int t = kTpr ? threadIdx.x % (kTpr ? kTpr : 1) : threadIdx.x;
+  const long long row = kTpr ? (long long)blockIdx.x * (kThreads / (kTpr ? kTpr : 1)) + threadIdx.x / (kTpr ? kTpr : 1)
+                             : (long long)blockIdx.x;
   grid_dependency_wait();  // nothing above reads what an earlier kernel may write
   grid_launch_dependents();
-  if (row >= a.rows) return;  // a whole warp's row, or none: rows of several warps have a CTA each
-  const long long token = a.heads == 1 ? row : row / a.heads;
-  const int head = a.heads == 1 ? 0 : (int)(row - token * a.heads);
+  const bool live = !kTpr || row < a.rows;  // (lanes of no row take part in their warp's sums)
+  const unsigned token = a.heads == 1 ? (unsigned)row : (unsigned)row / (unsigned)a.heads;  // rows are below 2^31
+  const int head = a.heads == 1 ? 0 : (int)((unsigned)row - token * (unsigned)a.heads);
   const T* x = static_cast<const T*>(a.x) + token * a.x_token + head * a.x_head;
   const T* res = static_cast<const T*>(a.residual) + token * a.residual_token + head * a.residual_head;
   const long long at = row * a.H;
-  // element k of group i of this thread
-  const auto index = [&](int i, int k) { return kVec ? 8 * (i * kTpr + t) + k : (8 * i + k) * kTpr + t; };
+  constexpr int kUnit = 16 / sizeof(T);
+  const int lead = kMode == kShifted ? (int)(reinterpret_cast<uintptr_t>(x) / sizeof(T) % kUnit) : 0;
+  // the first element of eight i, or single element (i, k)
+  const auto eight = [&](int i) { return 8 * (i * tpr + t) - lead; };
+  const auto single = [&](int i, int k) { return (8 * i + k) * tpr + t; };
   float r[kPer][8];
   float sum = 0.f;
-  if constexpr (kVec) {
+  if constexpr (kMode != kSingle) {
     Eight<T> in[kPer], more[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (index(i, 0) < a.H) in[i] = *reinterpret_cast<const Eight<T>*>(x + index(i, 0));
+      if (live && eight(i) < a.H) in[i] = get_eight<T, kMode>(x, eight(i), a.H);
     if (a.residual) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (index(i, 0) < a.H) more[i] = *reinterpret_cast<const Eight<T>*>(res + index(i, 0));
+        if (live && eight(i) < a.H) more[i] = get_eight<T, kMode>(res, eight(i), a.H);
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const bool here = index(i, 0) < a.H;
+      const bool here = live && eight(i) < a.H;
       if (here) Widen<T>::run(in[i], r[i]);
       if (here && a.residual) {
         float f[8];
@@ -110,9 +137,9 @@ __global__ void __launch_bounds__(kTpr < kMinThreads ? kMinThreads : kTpr)
     for (int i = 0; i < kPer; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int j = index(i, k);
-        r[i][k] = j < a.H ? widen(x[j]) : 0.f;
-        if (a.residual && j < a.H) r[i][k] += widen(res[j]);
+        const int j = single(i, k);
+        r[i][k] = live && j < a.H ? widen(x[j]) : 0.f;
+        if (a.residual && live && j < a.H) r[i][k] += widen(res[j]);
       }
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
@@ -124,52 +151,60 @@ __global__ void __launch_bounds__(kTpr < kMinThreads ? kMinThreads : kTpr)
     T* to = static_cast<T*>(a.residual_out) + at;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      if constexpr (kVec) {
-        if (index(i, 0) < a.H) *reinterpret_cast<Eight<T>*>(to + index(i, 0)) = narrow<T>(r[i]);
+      if constexpr (kMode != kSingle) {
+        if (live && eight(i) < a.H) put_eight<T, kMode>(to, eight(i), a.H, r[i]);
       } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (index(i, k) < a.H) narrow_to(to + index(i, k), r[i][k]);
+          if (live && single(i, k) < a.H) narrow_to(to + single(i, k), r[i][k]);
       }
     }
   }
   float rstd = rsqrtf(sum / a.H + a.eps);
-  if (!(sum <= FLT_MAX)) {
-    // Squares beyond FP32: once more with r 2^-72 (2^128 2^-72 squared, 2^14 times, is below 2^127); eps is
-    // then below the last bit. A row that holds what is not finite comes out as NaN.
-    sum = 0.f;
+  // Squares beyond FP32: once more with r 2^-72 (2^128 2^-72 squared, 2^14 times, is below 2^127); eps is
+  // then below the last bit. A row that holds what is not finite comes out as NaN.
+  const bool beyond = !(sum <= FLT_MAX);
+  if (kTpr && kTpr < 32 ? __any_sync(0xFFFFFFFFu, beyond) : beyond) {
+    float small = 0.f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        r[i][k] *= 0x1p-72f;
-        sum += r[i][k] * r[i][k];
+        if (beyond) r[i][k] *= 0x1p-72f;
+        small += r[i][k] * r[i][k];
       }
-    sum = row_sum<kTpr>(sum, part[1]);
-    rstd = sum <= FLT_MAX ? rsqrtf(sum / a.H) : __uint_as_float(0x7FC00000u);
+    small = row_sum<kTpr>(small, part[1]);
+    if (beyond) rstd = small <= FLT_MAX ? rsqrtf(small / a.H) : __uint_as_float(0x7FC00000u);
   }
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    if constexpr (kVec) {
-      const int j = index(i, 0);
-      const bool here = j < a.H;
+    if constexpr (kMode != kSingle) {
+      const int j = eight(i);
+      const bool here = live && j < a.H;
       float w[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) w[k] = 1.f;
       if (here && a.weight) {
-        if (a.weight_fp32)
-          Widen<float>::run(*reinterpret_cast<const Eight<float>*>(static_cast<const float*>(a.weight) + j), w);
-        else
-          Widen<T>::run(*reinterpret_cast<const Eight<T>*>(static_cast<const T*>(a.weight) + j), w);
-      }
-      uint32_t top = 0;
+        if (kMode == kAligned || (lead == 0 && j + 8 <= a.H && a.weight_aligned)) {
+          if (a.weight_fp32)
+            Widen<float>::run(*reinterpret_cast<const Eight<float>*>(static_cast<const float*>(a.weight) + j), w);
+          else
+            Widen<T>::run(*reinterpret_cast<const Eight<T>*>(static_cast<const T*>(a.weight) + j), w);
+        } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        r[i][k] = r[i][k] * rstd * w[k];
-        top = max(top, __float_as_uint(r[i][k]) & 0x7FFFFFFFu);
+          for (int k = 0; k < 8; ++k)
+            if (j + k >= 0 && j + k < a.H)
+              w[k] = a.weight_fp32 ? static_cast<const float*>(a.weight)[j + k]
+                                   : widen(static_cast<const T*>(a.weight)[j + k]);
+        }
       }
-      if (a.y && here) *reinterpret_cast<Eight<T>*>(static_cast<T*>(a.y) + at + j) = narrow<T>(r[i]);
-      if (a.codes) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) r[i][k] = r[i][k] * rstd * w[k];
+      if (a.y && here) put_eight<T, kMode>(static_cast<T*>(a.y) + at, j, a.H, r[i]);
+      if (kMode == kAligned && a.codes) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(r[i][k]) & 0x7FFFFFFFu);
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
         bool bad;
@@ -187,8 +222,8 @@ __global__ void __launch_bounds__(kTpr < kMinThreads ? kMinThreads : kTpr)
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int j = index(i, k);
-        const bool here = j < a.H;
+        const int j = single(i, k);
+        const bool here = live && j < a.H;
         float w = 1.f;
         if (here && a.weight)
           w = a.weight_fp32 ? static_cast<const float*>(a.weight)[j] : widen(static_cast<const T*>(a.weight)[j]);
@@ -210,31 +245,62 @@ __global__ void __launch_bounds__(kTpr < kMinThreads ? kMinThreads : kTpr)
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-template <typename T, int kTpr, int kPer>
+template <typename T, int kTpr, int kPer, Mode kMode>
 cudaError_t run(const NormArgs& a, cudaStream_t s) {
-  constexpr int kThreads = kTpr < kMinThreads ? kMinThreads : kTpr;
-  constexpr int kRows = kThreads / kTpr;
+  const int rows = kTpr ? kThreads / (kTpr ? kTpr : 1) : 1;  // of a CTA
+  const int eights = (a.H + (kMode == kShifted ? 14 : 7)) / 8;
+  const int threads = kTpr ? kThreads : ((eights + kPer - 1) / kPer + 31) / 32 * 32;
+  return launch_dependent(rms_norm<T, kTpr, kPer, kMode>, (int)(((long long)a.rows + rows - 1) / rows), threads, 0, s, a);
+}
+
+// A row's threads have two eights each (one, where there are two of each, x's and the residual's: about as much on its way)
+// up to 32 lanes, then a warp with up to four each, then a CTA with one or two, four at the longest.
+template <typename T, Mode kMode>
+cudaError_t run_mode(const NormArgs& a, cudaStream_t s) {
+  const int eights = (a.H + (kMode == kShifted ? 14 : 7)) / 8;
+  const bool alone = !a.residual && a.rows >= 152 * 64;  // (fewer rows want their threads)
+  if constexpr (kMode == kAligned) {
+    if (alone && eights == 8) return run<T, 4, 2, kMode>(a, s);
+    if (alone && eights > 8 && eights <= 16) return run<T, 8, 2, kMode>(a, s);
+    if (alone && eights > 16 && eights <= 32) return run<T, 16, 2, kMode>(a, s);
+  }
+  if constexpr (kMode != kSingle) {
+    if (eights <= 8) return run<T, 8, 1, kMode>(a, s);
+    if (eights <= 16) return run<T, 16, 1, kMode>(a, s);
+    if (eights <= 32) return run<T, 32, 1, kMode>(a, s);
+  }
+  if (eights <= 64) return run<T, 32, 2, kMode>(a, s);
+  if constexpr (kMode == kAligned) {
+    if (eights <= 96) return run<T, 32, 3, kMode>(a, s);
+  }
+  if constexpr (kMode != kSingle) {
+    if (eights <= 128) return run<T, 32, 4, kMode>(a, s);
+  }
+  if (eights <= (alone ? 256 : 512)) return run<T, 0, 1, kMode>(a, s);
+  if (eights <= 1024) return run<T, 0, 2, kMode>(a, s);
+  return run<T, 0, kMode == kShifted ? 5 : 4, kMode>(a, s);
+}
+
+template <typename T>
+cudaError_t run_type(const NormArgs& a, cudaStream_t s) {
   constexpr int kUnit = 16 / sizeof(T);  // elements to 16 bytes
+  const auto place = [](const void* p) { return (long long)(reinterpret_cast<uintptr_t>(p) / sizeof(T) % kUnit); };
   const bool vec = a.H % 8 == 0 && aligned(a.x, 16) && aligned(a.residual, 16) && aligned(a.weight, 16) &&
                    aligned(a.residual_out, 16) && aligned(a.y, 16) && aligned(a.codes, 8) &&
                    a.x_token % kUnit == 0 && a.x_head % kUnit == 0 && a.residual_token % kUnit == 0 &&
                    a.residual_head % kUnit == 0;
-  const int ctas = (int)(((long long)a.rows + kRows - 1) / kRows);
-  return launch_dependent(vec ? rms_norm<T, kTpr, kPer, true> : rms_norm<T, kTpr, kPer, false>, ctas, kThreads,
-                          0, s, a);
-}
-
-// Rows up to 512 elements have a warp, longer ones a CTA of so many threads that each holds
-// 8 to 16 elements, 32 at the longest.
-template <typename T>
-cudaError_t run_type(const NormArgs& a, cudaStream_t s) {
-  if (a.H <= 256) return run<T, 32, 1>(a, s);
-  if (a.H <= 512) return run<T, 32, 2>(a, s);
-  if (a.H <= 1024) return run<T, 128, 1>(a, s);
-  if (a.H <= 2048) return run<T, 256, 1>(a, s);
-  if (a.H <= 4096) return run<T, 512, 1>(a, s);
-  if (a.H <= 8192) return run<T, 512, 2>(a, s);
-  return run<T, 512, 4>(a, s);
+  if (vec) return run_mode<T, kAligned>(a, s);
+  NormArgs b = a;
+  b.weight_aligned = aligned(a.weight, 16);
+  // rows that begin at the same place of 16 bytes in every tensor, whichever place that is
+  const long long per_token = (long long)a.heads * a.H;
+  const auto alike = [&](const void* p, long long token, long long head) {
+    return !p || (place(p) == place(a.x) && (token - a.x_token) % kUnit == 0 && (a.heads == 1 || (head - a.x_head) % kUnit == 0));
+  };
+  if (!a.codes && alike(a.residual, a.residual_token, a.residual_head) && alike(a.residual_out, per_token, a.H) &&
+      alike(a.y, per_token, a.H))
+    return run_mode<T, kShifted>(b, s);
+  return run_mode<T, kSingle>(b, s);
 }
 
 }  // namespace

@@ -170,7 +170,7 @@ __device__ __forceinline__ void take_words(uint32_t (&k)[kV], int K, int lane, u
     for (int i = 0; i < kV; ++i) k[i] = taken ? (i + 1 < kV ? k[i + 1] : 0u) : k[i];
     return all;
   };
-#pragma unroll 4
+#pragma unroll(kV <= 8 ? 4 : 1)
   for (int r = 0; r < min(K, 32); ++r) {
     const uint32_t all = next();
     words[0] = lane == r ? all : words[0];
@@ -251,7 +251,7 @@ __device__ __noinline__ void choose_again(const RouteArgs& a, const T* x, const 
   const double sum = exact_sum(a, x, mine, top);
   unsigned long long k[kV];
   double best = -INFINITY, second = -INFINITY;
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < kV; ++i) {
     k[i] = 0;
     if (i >= mine.n) continue;
@@ -441,8 +441,9 @@ cudaError_t run(const RouteArgs& a, const Lanes lanes, cudaStream_t s) {
                    reinterpret_cast<uintptr_t>(a.logits) % kBytes == 0 && a.stride * (long long)sizeof(T) % kBytes == 0;
   const int ctas = (a.tokens + kWarps - 1) / kWarps;
   constexpr bool kWords = sizeof(T) == 2;
-  const auto kernel = kWords && !a.bias ? (vec ? route<T, kV, true, kWords> : route<T, kV, false, kWords>)
-                                        : (vec ? route<T, kV, true, false> : route<T, kV, false, false>);
+  constexpr bool kPacks = kV <= 16;  // (1024 experts are rare enough for single loads)
+  const auto kernel = kWords && !a.bias ? (vec ? route<T, kV, kPacks, kWords> : route<T, kV, false, kWords>)
+                                        : (vec ? route<T, kV, kPacks, false> : route<T, kV, false, false>);
   return launch_dependent(kernel, ctas, 32 * kWarps, 0, s, a, lanes);
 }
 

@@ -16,7 +16,7 @@ struct NormArgs {
   const void* residual;       // null: none
   long long residual_token, residual_head;
   const void* weight;  // null: ones
-  bool weight_fp32;
+  bool weight_fp32, weight_aligned;  // (the second is launch_rms_norm's own)
   void *residual_out, *y;  // null: not wanted
   uint8_t *codes, *scales;
   int rows, heads, H;
