@@ -253,16 +253,22 @@ cudaError_t run(const NormArgs& a, cudaStream_t s) {
   return launch_dependent(rms_norm<T, kTpr, kPer, kMode>, (int)(((long long)a.rows + rows - 1) / rows), threads, 0, s, a);
 }
 
-// A row's threads have two eights each (one, where there are two of each, x's and the residual's: about as much on its way)
-// up to 32 lanes, then a warp with up to four each, then a CTA with one or two, four at the longest.
+// How many eights a thread has. Few rows want all the threads that they can have: one eight each, up to 512 threads. Many rows
+// fill the GPU, and then each thread wants much on its way and each row few warps that wait for each other: two
+// eights where there is no residual and rows are up to 32 lanes (32 heads of 64 elements 34.4 -> 23.5 us), up to four to a warp's
+// lane for up to 1024 elements, and four beyond that (16 bits, aligned; 4096 x 8192 with residual 48.2 -> 45.6 us, 8192 x
+// 4096 without 35.5 -> 30.1) or two (FP32, whose four cost registers: 49.5 against 46.4 us for 4096 x 4096; rows that begin
+// anywhere: 85.9 against 55.4 for 22369 x 1500).
 template <typename T, Mode kMode>
 cudaError_t run_mode(const NormArgs& a, cudaStream_t s) {
   const int eights = (a.H + (kMode == kShifted ? 14 : 7)) / 8;
-  const bool alone = !a.residual && a.rows >= 152 * 64;  // (fewer rows want their threads)
+  const bool many = a.rows >= 152 * 8;
   if constexpr (kMode == kAligned) {
-    if (alone && eights == 8) return run<T, 4, 2, kMode>(a, s);
-    if (alone && eights > 8 && eights <= 16) return run<T, 8, 2, kMode>(a, s);
-    if (alone && eights > 16 && eights <= 32) return run<T, 16, 2, kMode>(a, s);
+    if (!a.residual && a.rows >= 152 * 64) {
+      if (eights == 8) return run<T, 4, 2, kMode>(a, s);
+      if (eights > 8 && eights <= 16) return run<T, 8, 2, kMode>(a, s);
+      if (eights > 16 && eights <= 32) return run<T, 16, 2, kMode>(a, s);
+    }
   }
   if constexpr (kMode != kSingle) {
     if (eights <= 8) return run<T, 8, 1, kMode>(a, s);
@@ -276,7 +282,8 @@ cudaError_t run_mode(const NormArgs& a, cudaStream_t s) {
   if constexpr (kMode != kSingle) {
     if (eights <= 128) return run<T, 32, 4, kMode>(a, s);
   }
-  if (eights <= (alone ? 256 : 512)) return run<T, 0, 1, kMode>(a, s);
+  if (kMode == kAligned && sizeof(T) == 2 && many) return run<T, 0, 4, kMode>(a, s);
+  if (eights <= 512 && !many) return run<T, 0, 1, kMode>(a, s);
   if (eights <= 1024) return run<T, 0, 2, kMode>(a, s);
   return run<T, 0, kMode == kShifted ? 5 : 4, kMode>(a, s);
 }

@@ -167,6 +167,42 @@ def test_many_rows(cuda_device):
     assert y.shape == r.shape == (0, 64)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+@pytest.mark.parametrize("T,H", [(9800, 64), (9800, 72), (9801, 128), (9800, 200), (9803, 256), (9800, 100), (1217, 1040),
+                                 (1300, 1500), (1216, 2048), (1217, 2049), (1216, 4104), (1216, 9000)])
+def test_many_rows_of(T, H, dtype, cuda_device):
+    """Where rows are many a thread has more of each."""
+    x, xv = make((T, H), dtype, cuda_device, 16)
+    w, wv = make((H,), dtype, cuda_device, 17)
+    check_y(wd.rms_norm(x, w), ref.rms_norm(xv, wv, None, 1e-6)[0], dtype)
+    res, rv = make((T, H), dtype, cuda_device, 18, 3.0)
+    want, r = ref.rms_norm(xv, wv, rv, 1e-6)
+    y, total = wd.rms_norm(x, w, res)
+    check_y(y, want, dtype)
+    check_sum(total, r, dtype)
+    if H % 32 == 0:
+        check_mxfp8(*wd.rms_norm(x, w, mxfp8=True), ref.rms_norm(xv, wv, None, 1e-6)[0])
+
+
+@pytest.mark.parametrize("H", [37, 500, 777, 3001])
+@pytest.mark.parametrize("shift", range(9))
+def test_rows_that_begin_anywhere(H, shift, cuda_device):
+    """All tensors alike, and each at a place of its own; nothing around the results changes."""
+    T = 5
+    for dtype in (BF16, FP32):
+        flat, fv = make((T * H + shift,), dtype, cuda_device, 19)
+        x, xv = flat[shift:].view(T, H), fv[shift:].reshape(T, H)
+        res, rv = make((T, H), dtype, cuda_device, 20)
+        want, r = ref.rms_norm(xv, None, rv, 1e-6)
+        for at in (shift, 3):
+            room = torch.full((2, T * H + 20,), 7.0, dtype=dtype, device=cuda_device)
+            y, total = (t[at:at + T * H].view(T, H) for t in room)
+            wd.rms_norm(x, None, res, out=y, residual_out=total)
+            check_y(y, want, dtype)
+            check_sum(total, r, dtype)
+            assert bool((room[:, :at] == 7).all()) and bool((room[:, at + T * H:] == 7).all())
+
+
 def test_offsets_beyond_32_bits(cuda_device):
     """Rows so far apart that their offsets in elements pass 2^32."""
     base = torch.empty(2 ** 33 + 128, dtype=torch.uint8, device=cuda_device).view(BF16)
