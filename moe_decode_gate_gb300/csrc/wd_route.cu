@@ -141,22 +141,21 @@ __device__ __forceinline__ int take(Key (&k)[kV], const Span& mine, int n, int l
   }
 }
 
-// Descending order of a lane's words (Batcher's merge exchange).
+// Descending order of a lane's words (Batcher's bitonic sort: its loops are plain enough to be unrolled at any kV).
 template <int kV>
 __device__ __forceinline__ void sort_down(uint32_t (&k)[kV]) {
 #pragma unroll
-  for (int p = 1; p < kV; p *= 2)
+  for (int run = 2; run <= kV; run *= 2)
 #pragma unroll
-    for (int q = p; q >= 1; q /= 2)
+    for (int apart = run / 2; apart > 0; apart /= 2)
 #pragma unroll
-      for (int j = q % p; j + q < kV; j += 2 * q)
-#pragma unroll
-        for (int i = 0; i < q; ++i)
-          if (i + j + q < kV && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
-            const uint32_t a = k[i + j], b = k[i + j + q];
-            k[i + j] = max(a, b);
-            k[i + j + q] = min(a, b);
-          }
+      for (int i = 0; i < kV; ++i) {
+        if (i & apart) continue;
+        const uint32_t a = k[i], b = k[i + apart];
+        const bool down = (i & run) == 0;
+        k[i] = down ? max(a, b) : min(a, b);
+        k[i + apart] = down ? min(a, b) : max(a, b);
+      }
 }
 
 // The K largest words, as take(): of words that hold key and index no two are equal.
