@@ -5,14 +5,17 @@
 // a group's value is a few shuffles within its lanes. K times the warp's largest key is found by one
 // redux over keys whose integer order is their order, and struck out.
 //
-// Keys are exact where no bias and no sums of groups are asked for: they are the logits. Those of 16 bits
-// share a word with their expert's index, so that one redux gives both, the lowest index first of equal keys; a lane
-// sorts its words once and only its first one is looked at. Other keys need a second redux for the index.
-// Keys of scores and biases carry FP32's errors (margin below); a token of which two keys that the choice
-// hangs on are nearer than that is chosen again from keys in 64 bits: those of the K and
-// of what is as near to the last of them, one to a lane, or all of them where groups are in doubt.
+// A lane sorts its keys once, and of them only the first is looked at.
 //
-// Bounded by the instructions of a token, not by its bytes.
+// Keys are exact where no bias and no sums of groups are asked for: they are the logits. Those of 16 bits
+// share a word with their expert's index, so that one redux gives both, the lowest index first of equal keys. Keys
+// of 32 bits share one with their place in the lane, which takes their last few bits. Keys of scores and biases carry FP32's errors
+// besides. A token of which two keys that the choice hangs on are nearer than that is looked at again with keys in
+// 64 bits, of those experts alone that are in doubt, one to a lane: the best of each group, the K and what is
+// as near to the last of them. (With all keys in 64 bits one token takes 12 us at 496 experts, and the call waits for it.)
+//
+// Bounded by the instructions of a token, most of them for the half-rate pipe that compares and selects, not by
+// its bytes.
 #include "wd_device.cuh"
 #include "wd_step.cuh"
 #include "wd_vec.cuh"
@@ -82,10 +85,9 @@ Lanes lanes_of(int E, int groups) {
   return Lanes{shift, per_group, (size + per_group - 1) / per_group, size};
 }
 
-// The value of a group from its lanes' two largest keys, in each of its lanes. A masked second
-// key takes no part.
+// The two largest keys of a group from its lanes' two largest, in each of its lanes.
 template <typename F>
-__device__ __forceinline__ F group_value(F a, F b, int lanes, int best) {
+__device__ __forceinline__ void two_of_group(F& a, F& b, int lanes) {
   for (int off = 1; off < lanes; off *= 2) {
     const F c = __shfl_xor_sync(kAll, a, off), d = __shfl_xor_sync(kAll, b, off);
     const F low = a < c ? a : c;
@@ -93,6 +95,10 @@ __device__ __forceinline__ F group_value(F a, F b, int lanes, int best) {
     b = b < d ? d : b;
     b = b < low ? low : b;
   }
+}
+// ... and its value. A masked second key takes no part.
+__device__ __forceinline__ double group_value(double a, double b, int lanes, int best) {
+  two_of_group(a, b, lanes);
   return best == 2 && b > -INFINITY ? a + b : a;
 }
 
@@ -107,27 +113,15 @@ __device__ __forceinline__ bool group_chosen(F value, int group, int groups, int
   return before < top;
 }
 
-// The `n` largest keys of the warp, largest first: entry r in lane r % 32, place r / 32 of `ids`. Keys are
-// struck out of k. With a margin, goes on until the next key is further than that below the last one: returns how many it
-// took, kMany if that is more than 64; `near`: whether two neighbours of the order are nearer than the margin.
-constexpr int kMany = 65;
-
-template <int kV, typename Key>
-__device__ __forceinline__ int take(Key (&k)[kV], const Span& mine, int n, int lane, float margin, bool& near,
-                                    int (&ids)[2]) {
-  Key last = 0;
-  for (int r = 0;; ++r) {
-    if (r >= n && !(margin > 0.f)) return r;
-    Key top = k[0];
+// The `n` largest keys of 64 bits, largest first, the lowest index first of equal ones: entry r in lane r % 32, place r / 32
+// of `ids`. Keys are struck out of k.
+template <int kV>
+__device__ __forceinline__ void take_exact(unsigned long long (&k)[kV], const Span& mine, int n, int lane, int (&ids)[2]) {
+  for (int r = 0; r < n; ++r) {
+    unsigned long long top = k[0];
 #pragma unroll
     for (int i = 1; i < kV; ++i) top = top < k[i] ? k[i] : top;
-    const Key all = largest(top);
-    if (margin > 0.f && r > 0) {
-      const bool close = all && value_of((uint32_t)last) - value_of((uint32_t)all) < margin;
-      if (r >= n && (!close || r == 64)) return close ? kMany : r;
-      near |= close;
-    }
-    last = all;
+    const unsigned long long all = largest(top);
     int at = 1 << 20;  // of this lane's experts that have the key, the first
 #pragma unroll
     for (int i = kV - 1; i >= 0; --i)
@@ -158,33 +152,77 @@ __device__ __forceinline__ void sort_down(uint32_t (&k)[kV]) {
       }
 }
 
-// The K largest words, as take(): of words that hold key and index no two are equal.
+// A lane's words in descending order, of which the first is looked at: the others stand in shared memory (the columns of a
+// warp's `rows` of 32), where taking one is a load of the next instead of a move of all.
 template <int kV>
-__device__ __forceinline__ void take_words(uint32_t (&k)[kV], int K, int lane, uint32_t (&words)[2]) {
-  sort_down<kV>(k);
-  const auto next = [&] {  // the largest of all, taken from the lane that has it
-    const uint32_t all = largest(k[0]);
-    const bool taken = k[0] == all;
+struct Sorted {
+  uint32_t head;
+  const uint32_t* next;
+  // (of lanes that are not `open` none is taken)
+  __device__ __forceinline__ Sorted(uint32_t (&k)[kV], uint32_t* rows, int lane, bool open) {
+    sort_down<kV>(k);
+    head = open ? k[0] : 0;
+    next = rows + lane;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) k[i] = taken ? (i + 1 < kV ? k[i + 1] : 0u) : k[i];
-    return all;
-  };
-#pragma unroll(kV <= 8 ? 4 : 1)
-  for (int r = 0; r < min(K, 32); ++r) {
-    const uint32_t all = next();
-    words[0] = lane == r ? all : words[0];
+    for (int i = 1; i < kV; ++i) rows[32 * (i - 1) + lane] = k[i];
+    rows[32 * (kV - 1) + lane] = 0;  // (a lane reads its own column alone)
   }
-  for (int r = 32; r < K; ++r) {
-    const uint32_t all = next();
-    words[1] = lane + 32 == r ? all : words[1];
+  __device__ __forceinline__ void take(bool mine) {
+    if (mine) {
+      head = *next;
+      next += 32;
+    }
   }
+};
+
+// The K largest words, to taken[0] .. taken[K - 1]: of words that hold key and index no two are equal.
+template <int kV>
+__device__ __forceinline__ void take_words(Sorted<kV>& sorted, int K, uint32_t* taken) {
+#pragma unroll 2
+  for (int r = 0; r < K; ++r) {
+    const uint32_t all = largest(sorted.head);
+    const bool mine = all && sorted.head == all;  // (nothing is open while groups are in doubt)
+    if (mine) taken[r] = all;
+    sorted.take(mine);
+  }
+  __syncwarp();
+}
+
+// Takes the largest word of key and place in the lane, and its expert, to taken[r] and ids[r] (0 if there is none).
+template <int kV>
+__device__ __forceinline__ void take_place(Sorted<kV>& sorted, const Span& mine, int lane, int r, uint32_t* taken,
+                                           uint32_t* ids) {
+  const uint32_t all = largest(sorted.head);
+  const int winner = __ffs(__ballot_sync(kAll, sorted.head == all)) - 1;  // (words of two lanes may be the same)
+  const bool take = lane == winner;
+  if (take) {
+    taken[r] = all;
+    ids[r] = mine.first + (kV - 1 - (int)(all & (kV - 1)));
+  }
+  sorted.take(take && all);
+}
+
+// Whether word b may stand before its neighbour a: the two are the same but for the place or, where keys are off by `off` and
+// `part` of themselves, nearer than that. Masked ones are like nothing else; infinite ones' words are no numbers (no
+// comparison with them is true).
+template <int kV>
+__device__ __forceinline__ bool too_near(uint32_t a, uint32_t b, float off, float part) {
+  if (!b) return false;
+  if ((a ^ b) < (uint32_t)kV) return true;
+  const float x = value_of(a), y = value_of(b);
+  return off > 0.f && b > order_of(-INFINITY) && !(x - y >= fmaf(part, fmaxf(fabsf(x), fabsf(y)), off));
 }
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
 
-// For keys, which are compared as they are: __expf is off by |x| units relative to itself, s (1 - s) of which reaches the
-// sigmoid s, at most one unit of 1; the quotient by two.
-__device__ __forceinline__ float sigmoid_key(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// For keys, which are compared as they are: the exponential is off by |x| units relative to itself, s (1 - s) of which reaches
+// the sigmoid s, at most one unit of 1; the reciprocal by two.
+__device__ __forceinline__ float sigmoid_key(float x) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return s;
+}
 
 // exp(x - top), where top is at least x; 1 for the largest even if infinite, 0 for masked ones.
 __device__ __forceinline__ float exp_below(float x, float top) {
@@ -212,18 +250,21 @@ __device__ __forceinline__ double exact_sum(const RouteArgs& a, const T* x, cons
   return sum;
 }
 
-// The order of the `n` <= 64 candidates that take() found, from keys in 64 bits. Rare, so it is kept out of the way
+// The order of `n` <= 64 experts, from keys in 64 bits. Rare, so it is kept out of the way
 // of the other registers.
 template <typename T>
 __device__ __noinline__ void order_again(const RouteArgs& a, const T* x, const Span mine, int lane, float top, int n,
                                          int (&ids)[2]) {
-  const double sum = exact_sum(a, x, mine, top);
+  const double sum = a.bias ? exact_sum(a, x, mine, top) : 1.0;
   unsigned long long key[2];
   int rank[2] = {0, 0};
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     key[e] = 0;
-    if (lane + 32 * e < n) key[e] = order_of(exact_key(a, to_float(x[ids[e]]), ids[e], top, sum));
+    if (lane + 32 * e < n) {
+      const float l = to_float(x[ids[e]]);
+      key[e] = order_of(a.bias ? exact_key(a, l, ids[e], top, sum) : (double)(l > -INFINITY ? l : -INFINITY));
+    }
   }
   for (int r = 0; r < n; ++r) {
     const unsigned long long other = __shfl_sync(kAll, key[r >> 5], r & 31);
@@ -242,12 +283,54 @@ __device__ __noinline__ void order_again(const RouteArgs& a, const T* x, const S
   ids[1] = sorted[1];
 }
 
-// The token's whole choice from keys in 64 bits.
+// Whether this lane's group is chosen, from the keys in 64 bits of those experts that may be the best of a group: whose
+// key is not below `least`. False in `sure` if those are more than 64. Rare, too.
+template <typename T, int kV>
+__device__ __noinline__ bool groups_again(const RouteArgs& a, const T* x, const Span mine, const Lanes lanes, int lane,
+                                          float top, const float (&keys)[kV], float least, uint32_t* list, bool& sure) {
+  const int group = lane >> lanes.shift;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    const bool may = i < mine.n && keys[i] > -INFINITY && keys[i] >= least;
+    const uint32_t who = __ballot_sync(kAll, may);
+    const int at = n + __popc(who & ((1u << lane) - 1));
+    if (may && at < 64) list[at] = mine.first + i;
+    n += __popc(who);
+  }
+  __syncwarp();
+  sure = n <= 64;
+  if (!sure) return false;
+  const double sum = exact_sum(a, x, mine, top);
+  double key[2] = {0.0, 0.0};
+  int id[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    if (lane + 32 * e < n) {
+      id[e] = list[lane + 32 * e];
+      key[e] = exact_key(a, to_float(x[id[e]]), id[e], top, sum);
+    }
+  __syncwarp();
+  double best = -INFINITY, second = -INFINITY;
+  for (int r = 0; r < n; ++r) {
+    const double k = __shfl_sync(kAll, r < 32 ? key[0] : key[1], r & 31);
+    const int of = __shfl_sync(kAll, r < 32 ? id[0] : id[1], r & 31) / lanes.size;
+    if (of != group) continue;
+    second = second > k ? second : best < k ? best : k;
+    best = best < k ? k : best;
+  }
+  const double value = a.group_best == 2 && second > -INFINITY ? best + second : best;
+  const bool chosen = group_chosen(group < a.groups ? value : -(double)INFINITY, group, a.groups, lanes.per_group, a.top_groups);
+  return chosen && group < a.groups;
+}
+
+// The choice of a token's experts from all their keys in 64 bits, in the chosen groups.
 template <typename T, int kV>
 __device__ __noinline__ void choose_again(const RouteArgs& a, const T* x, const Span mine, const Lanes lanes, int lane,
-                                          float top, int (&ids)[2]) {
+                                          float top, bool groups_too, bool chosen, int (&ids)[2]) {
   const int group = lane >> lanes.shift;
-  const double sum = exact_sum(a, x, mine, top);
+  const bool scores = a.bias || groups_too;  // else the logits are the keys
+  const double sum = scores ? exact_sum(a, x, mine, top) : 1.0;
   unsigned long long k[kV];
   double best = -INFINITY, second = -INFINITY;
 #pragma unroll 1
@@ -255,21 +338,21 @@ __device__ __noinline__ void choose_again(const RouteArgs& a, const T* x, const 
     k[i] = 0;
     if (i >= mine.n) continue;
     const float l = to_float(x[mine.first + i]);
-    const double key = exact_key(a, l, mine.first + i, top, sum);
+    const double logit = l > -INFINITY ? l : -INFINITY;
+    const double key = scores ? exact_key(a, l, mine.first + i, top, sum) : logit;
     second = second > key ? second : best < key ? best : key;
     best = best < key ? key : best;
     // where nothing is added, keys are ordered by the logits
-    k[i] = order_of(a.bias ? key : (double)(l > -INFINITY ? l : -INFINITY));
+    k[i] = order_of(a.bias ? key : logit);
   }
-  if (a.groups > 1) {
+  if (groups_too) {
     const double value = group_value(best, second, lanes.per_group, a.group_best);
-    const bool chosen = group_chosen(group < a.groups ? value : -(double)INFINITY, group, a.groups, lanes.per_group, a.top_groups);
-    if (!chosen)
-#pragma unroll
-      for (int i = 0; i < kV; ++i) k[i] = 0;
+    chosen = group_chosen(group < a.groups ? value : -(double)INFINITY, group, a.groups, lanes.per_group, a.top_groups);
   }
-  bool none;
-  take<kV>(k, mine, a.K, lane, 0.f, none, ids);
+  if (!chosen)
+#pragma unroll
+    for (int i = 0; i < kV; ++i) k[i] = 0;
+  take_exact<kV>(k, mine, a.K, lane, ids);
 }
 
 // kWords: logits of 16 bits, and no bias.
@@ -280,6 +363,9 @@ __global__ void __launch_bounds__(32 * kWarps) route(const __grid_constant__ Rou
   const int group = lane >> lanes.shift, j = lane & (lanes.per_group - 1);
   Span mine{group * lanes.size + j * lanes.per_lane, 0};
   if (group < a.groups) mine.n = max(0, min(lanes.per_lane, lanes.size - j * lanes.per_lane));
+  __shared__ uint32_t shared[kWarps][32 * kV + (kWords ? 64 : 131)];
+  uint32_t* rows = shared[threadIdx.x >> 5];
+  uint32_t* taken = rows + 32 * kV;  // the words that were taken, in order, and behind them the experts of them
   grid_dependency_wait();  // nothing above reads what an earlier kernel may write
   grid_launch_dependents();
   if (token >= a.tokens) return;
@@ -302,7 +388,7 @@ __global__ void __launch_bounds__(32 * kWarps) route(const __grid_constant__ Rou
   float s[kV];                          // scores, then keys
 #pragma unroll
   for (int i = 0; i < kV; ++i) {
-    if (!(l[i] == l[i])) l[i] = -INFINITY;
+    l[i] = fmaxf(l[i], -INFINITY);  // (NaN is the other of two)
     s[i] = l[i];
   }
   if (!a.sigmoid && (inexact || !a.renormalise)) {
@@ -317,27 +403,29 @@ __global__ void __launch_bounds__(32 * kWarps) route(const __grid_constant__ Rou
     sum = warp_sum(sum);
   }
   const float unit = a.sigmoid ? 1.f : sum > 0.f ? 1.f / sum : 0.f;  // the largest score there may be
-  float margin = 0.f;
+  // In units of 2^-24, a softmax' score is off by 2 (expf), 1 (its argument), 2 (quotient), 1 (the product by it) and the
+  // sum of all of them, kV + 5 roundings at most; a sigmoid's by less than 12 of 1; a key by half a unit of its own more, and by
+  // the kV units that its place takes. Two keys are compared.
+  float off = 0.f;
+  constexpr float kPart = 0x1p-23f * (1 + kV);
   if (inexact) {
-    float most = 0.f;  // largest magnitude of a key
+    off = 0x1p-23f * (a.sigmoid ? 12 : kV + 12) * unit;
+    if (a.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-      if (l[i] > -INFINITY) {
-        s[i] = a.sigmoid ? sigmoid_key(l[i]) : s[i] * unit;
-        if (a.bias) s[i] += a.bias[mine.first + i];
-        if (!(s[i] == s[i])) s[i] = -INFINITY;
-        if (fabsf(s[i]) < INFINITY) most = fmaxf(most, fabsf(s[i]));
-      } else {
-        s[i] = -INFINITY;
-      }
+      for (int i = 0; i < kV; ++i) s[i] = sigmoid_key(l[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) s[i] *= unit;
     }
-    // In units of 2^-24, a softmax' score is off by 2 (expf), 1 (its argument), 2 (quotient), 1 (the product by it) and the
-    // sum of all of them, kV + 5 roundings at most; a sigmoid's by less than 12 of 1; a key by half a unit of its own more.
-    // Two keys are compared.
-    most = warp_max(most);
-    margin = 0x1p-23f * (a.sigmoid ? 12 : kV + 12) * unit + 0x1p-23f * most;
+    if (!kWords && a.bias) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i)
+        if (kVec || i < mine.n) s[i] = fmaxf(s[i] + a.bias[mine.first + i], -INFINITY);
+    }
+#pragma unroll
+    for (int i = 0; i < kV; ++i) s[i] = l[i] > -INFINITY ? s[i] : -INFINITY;
   }
-  bool again = false, chosen = true;
+  bool again = false, groups_too = false, chosen = true;  // what is chosen again with all keys
   if (a.groups > 1) {
     float best = -INFINITY, second = -INFINITY;
 #pragma unroll
@@ -346,52 +434,86 @@ __global__ void __launch_bounds__(32 * kWarps) route(const __grid_constant__ Rou
       second = fmaxf(second, fminf(best, key));
       best = fmaxf(best, key);
     }
-    float value = group_value(best, second, lanes.per_group, a.group_best);
+    two_of_group(best, second, lanes.per_group);
+    float value = a.group_best == 2 && second > -INFINITY ? best + second : best;
     if (group >= a.groups) value = -INFINITY;
     chosen = group_chosen(value, group, a.groups, lanes.per_group, a.top_groups);  // (all lanes take part)
     if (group >= a.groups) chosen = false;
-    if (inexact) {
+    if (inexact) {  // sums of two keys each
       const float in = warp_min(chosen ? value : INFINITY);
       const float out = warp_max(chosen ? -INFINITY : value);
-      again = in - out < 2.f * margin;
+      const float most = warp_max(fmaxf(best > -INFINITY ? fabsf(best) : 0.f, second > -INFINITY ? fabsf(second) : 0.f));
+      const float margin = 2.f * fmaf(kPart, most, off);
+      if (in - out < margin) {
+        float keys[kV];  // (their own, so that s stays in registers)
+#pragma unroll
+        for (int i = 0; i < kV; ++i) keys[i] = s[i];
+        const float low = a.group_best == 2 && second > -INFINITY ? second : best;
+        bool sure;
+        chosen = groups_again<T, kV>(a, x, mine, lanes, lane, top, keys, low - margin, taken, sure);
+        again = groups_too = !sure;
+      }
     }
   }
   uint32_t k[kV];
 #pragma unroll
   for (int i = 0; i < kV; ++i) {
     // without a bias the choice goes by the logits even where the groups' goes by sums of scores
-    if (!chosen || (!kVec && i >= mine.n))
-      k[i] = 0;
-    else if (kWords)
+    if (kWords)
       k[i] = half_order(l[i], T{}) << 16 | (0xFFFFu - (mine.first + i));
     else
-      k[i] = order_of(a.bias ? s[i] : l[i]);
+      k[i] = (order_of(a.bias ? s[i] : l[i]) & ~(uint32_t)(kV - 1)) | (kV - 1 - i);
+    if (!kVec && i >= mine.n) k[i] = 0;
   }
+  Sorted<kV> sorted(k, rows, lane, chosen);
   int ids[2] = {0, 0};
   float y[2] = {-INFINITY, -INFINITY}, w[2] = {0.f, 0.f};  // logits and weights of the chosen
   if constexpr (kWords) {
-    uint32_t words[2] = {0, 0};
-    take_words<kV>(k, a.K, lane, words);
+    take_words<kV>(sorted, a.K, taken);
 #pragma unroll
     for (int e = 0; e < 2; ++e)
       if (lane + 32 * e < a.K) {
-        ids[e] = 0xFFFF - (words[e] & 0xFFFFu);
-        y[e] = half_value(words[e] >> 16, T{});
+        const uint32_t word = taken[lane + 32 * e];
+        ids[e] = 0xFFFF - (word & 0xFFFFu);
+        y[e] = half_value(word >> 16, T{});
       }
   } else {
-    bool near = false;
-    const int n = take<kV>(k, mine, a.K, lane, a.bias ? margin : 0.f, near, ids);
-    if (n == kMany) again = true;
-    if (near && !again) {
-      int mended[2] = {ids[0], ids[1]};  // (its own, so that ids stay in registers)
-      order_again<T>(a, x, mine, lane, top, n, mended);
-      ids[0] = mended[0];
-      ids[1] = mended[1];
+    uint32_t* order = taken + 66;
+    const float part = kPart, apart = a.bias ? off : 0.f;
+    for (int r = 0; r <= a.K; ++r) take_place<kV>(sorted, mine, lane, r, taken, order);
+    __syncwarp();
+    bool near = false;  // two neighbours among the K and the one behind them
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (lane + 32 * e < a.K) near |= too_near<kV>(taken[lane + 32 * e], taken[lane + 32 * e + 1], apart, part);
+    if (__any_sync(kAll, near)) {
+      // as many more as are too near to the K-th
+      int n = a.K;
+      while (n <= 64 && too_near<kV>(taken[n - 1], taken[n], apart, part)) {
+        ++n;
+        if (n <= 64) take_place<kV>(sorted, mine, lane, n, taken, order);
+        __syncwarp();
+      }
+      if (n > 64) {
+        again = true;
+      } else if (!again) {
+        int mended[2] = {0, 0};  // (its own, so that ids stay in registers)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (lane + 32 * e < n) mended[e] = order[lane + 32 * e];
+        order_again<T>(a, x, mine, lane, top, n, mended);
+        ids[0] = mended[0];
+        ids[1] = mended[1];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (lane + 32 * e < a.K) ids[e] = order[lane + 32 * e];
     }
   }
   if (again) {
     int mended[2] = {0, 0};
-    choose_again<T, kV>(a, x, mine, lanes, lane, top, mended);
+    choose_again<T, kV>(a, x, mine, lanes, lane, top, groups_too, chosen, mended);
     ids[0] = mended[0];
     ids[1] = mended[1];
   }

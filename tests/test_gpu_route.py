@@ -95,6 +95,37 @@ def test_keys_nearer_than_32_bits_tell(scores, groups, top, best, E, cuda_device
     check(x, 10, cuda_device, bias, scores=scores, groups=groups, top_groups=top, group_best=best)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("groups,top,best,E", [(1, 1, 2, 256), (8, 3, 2, 256), (8, 3, 1, 256), (4, 2, 2, 1000), (32, 9, 2, 64)])
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+def test_all_alike(scores, groups, top, best, E, dtype, cuda_device):
+    """All logits the same, or of two values, with no bias, the same for all, or one in doubt: more ties than are looked at
+    one by one."""
+    r = np.random.RandomState(11)
+    x = torch.from_numpy(np.stack([np.full(E, 0.5), np.where(r.rand(E) < 0.5, 0.5, 0.25), np.full(E, -60.0),
+                                   np.where(np.arange(E) % 7 == 3, 1.0, 0.5)])).to(dtype).to(cuda_device)
+    kw = dict(scores=scores, groups=groups, top_groups=top, group_best=best)
+    for K in (1, 9):
+        if K <= top * (E // groups):
+            check(x, K, cuda_device, **kw)
+            check(x, K, cuda_device, np.zeros(E), **kw)
+            check(x, K, cuda_device, np.full(E, 0.125), **kw)
+            check(x, K, cuda_device, np.where(np.arange(E) % 50 == 49, 0.125 + 2.0 ** -24, 0.125), **kw)
+
+
+@pytest.mark.parametrize("E,K", [(256, 8), (1000, 12), (64, 60)])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_logits_of_neighbouring_bits(E, K, dtype, cuda_device):
+    """FP32 logits that differ in their last bits alone, and such pairs among others."""
+    r = np.random.RandomState(12)
+    one = np.float32(1.0) + np.float32(2.0 ** -23) * r.permutation(E).astype(np.float32)
+    pairs = np.repeat(r.standard_normal(E // 2).astype(np.float32), 2)
+    pairs[1::2] = np.nextafter(pairs[1::2], np.float32(10))
+    x = torch.from_numpy(np.stack([one, -one, pairs, pairs[r.permutation(E)]])).to(dtype).to(cuda_device)
+    for scores in ("softmax", "sigmoid"):
+        check(x, K, cuda_device, scores=scores)
+
+
 @pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("biased", [False, True])
 @pytest.mark.parametrize("renormalise", [False, True])
