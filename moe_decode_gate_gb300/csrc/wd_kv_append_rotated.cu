@@ -13,7 +13,10 @@
 // The table's rows of a CTA's tokens stand in shared memory, and a thread's next token is on its way
 // while it turns one.
 //
-// To read and write: q in and out, k and v in, 4.25 bits a channel of them out, the table's rows.
+// To read and write: q in and out, k and v in, 4.25 bits a channel of them out, the table's rows. Measured: eight prompts,
+// 15,841 tokens of 32 query and 4 key heads of 128 in BF16 with the values back, 335 MB, 58.9 us, 5.7 TB/s, 0.84 of the copy
+// rate; one token of 32 sequences 3.0 us. Tried: the table's rows from L1 for each token (70.9), 3, 4 and 6 CTAs to
+// an SM for 5 (67.5, 61.7, 59.8), 8 and 32 tokens to a CTA (61.0, 59.1), first all keys and then all queries (63.9).
 #include "wd_device.cuh"
 #include "wd_kv_quant.cuh"
 

@@ -7,8 +7,13 @@
 // streams its logits through, the next ones always on their way. Nothing is written but the result, no counts
 // live from call to call, and counting whole numbers gives the same sums in any order.
 //
-// Bytes bound it where rows are many and little else is asked for, its instructions (about
-// NNN) else; the chain of a CTA's loads (settings and slot, lengths, history) where rows are few.
+// Measured (BF16 to FP32): 64 rows of 131,072 with histories of 300 to 8192, biases, masks and temperatures 16.6 us, of
+// which the logits alone take 6.4 (50 MB, in part from L2), masks 0.5, and the histories 8: their counting and what their
+// tokens go through is half of the 540 instructions that a warp has for 16 tokens a lane. One row of 32,768
+// 2.6 us. Seven rows of 100,003 with a history of up to 32,768 11.9 us: all CTAs of a row read its history at the same time.
+// Tried: the CTAs of a cluster sharing the history and counting in each other's shared memory (its two barriers cost more
+// than the reading: 24.4 against 21.1 us then); one slice after the other in smaller slices (19 to 24); five CTAs to an
+// SM for four (16.8); eight accesses to the history at a time (13.0 for the long ones).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -366,7 +371,8 @@ cudaError_t run_slices(const LogitsArgs& a, int chunks, cudaStream_t s) {
 
 template <typename T, typename U>
 cudaError_t run(const LogitsArgs& a, cudaStream_t s) {
-  // Large slices where the rows fill the GPU (each reads the history once more), smaller ones where they do not.
+  // Large slices where the rows fill the GPU (each reads the history once more; 64 x 131,072 in slices of 4096 took 27.4
+  // us where those of 8192 took 23.6), smaller ones where they do not.
   const auto enough = [&](int slice) { return (long long)a.B * ((a.V + slice - 1) / slice) >= kCtasWanted; };
   if (enough(8 * kUnit)) return run_slices<T, U, 4>(a, 2, s);
   if (enough(4 * kUnit)) return run_slices<T, U, 4>(a, 1, s);

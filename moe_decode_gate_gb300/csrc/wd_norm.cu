@@ -10,6 +10,11 @@
 // anywhere but all tensors alike (odd H), the eights begin at the aligned place before the row, and the first and the
 // last of them are taken element by element. What is left (tensors of unlike alignment, MXFP8 of unaligned rows) is taken one element
 // to a lane, so that a warp's access stays contiguous, and a block is a warp.
+// Measured (BF16, with residual): 16384 x 2048 41.5 us, 6.5 TB/s, 0.95 of the copy rate; 2048 x 16384 50.7 us (0.78: few CTAs
+// of many warps that wait for each other); 16376 x 2049 63 us (0.63: the weights are then taken one by one); into
+// MXFP8 42.7 us (0.81). Without residual 32 heads of 128 of 8192 tokens 23.3 us (0.85), 8192 x 4096 30 us (0.66: half as
+// much on its way). One row of 2048: 1.6 us. Tried: groups of rows after each other in a CTA that stays (registers for two,
+// 10 to 50 % slower), CTAs of 1024 threads (2048 x 16384 64.8), eight to sixteen eights in one warp (51.8 for 8192 x 2048 of FP32).
 #include <float.h>
 
 #include "wd_device.cuh"
