@@ -275,7 +275,8 @@ __global__ void __launch_bounds__(kThreads, 4) adjust_logits(const LogitsArgs a,
     __syncthreads();
     if (biases) {
       for (int i = threadIdx.x;;) {
-        raise(words + (kWide ? 4 * places : 0), (uint32_t)(id - from), id < 0 ? 0 : n, (uint32_t)(i + 1) << Layout<kWide>::kBiasShift);
+        raise(words + (kWide ? 4 * places : 0), (uint32_t)id - (uint32_t)from, id < 0 ? 0 : n,
+              (uint32_t)(i + 1) << Layout<kWide>::kBiasShift);
         i += kThreads;
         if (bias_from + i >= bias_to) break;
         id = a.bias_ids[bias_from + i];
@@ -287,8 +288,8 @@ __global__ void __launch_bounds__(kThreads, 4) adjust_logits(const LogitsArgs a,
       for (int j = 0; j < kBatch; ++j) {
         const int i = base + 4 * (threadIdx.x + j * kThreads);
         if (i >= length) break;
-        const uint32_t at[4] = {(uint32_t)(tokens[j].x - from), (uint32_t)(tokens[j].y - from),
-                                (uint32_t)(tokens[j].z - from), (uint32_t)(tokens[j].w - from)};
+        const uint32_t at[4] = {(uint32_t)tokens[j].x - (uint32_t)from, (uint32_t)tokens[j].y - (uint32_t)from,
+                                (uint32_t)tokens[j].z - (uint32_t)from, (uint32_t)tokens[j].w - (uint32_t)from};
         if (i + 4 <= prompt) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) mark(words, at[k], n, Layout<kWide>::kPrompt);

@@ -217,8 +217,8 @@ __device__ __forceinline__ bool too_near(uint32_t a, uint32_t b, float off, floa
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
 
-// For keys, which are compared as they are: the exponential is off by |x| units relative to itself, s (1 - s) of which reaches
-// the sigmoid s, at most one unit of 1; the reciprocal by two.
+// For keys, which are compared as they are: the exponential is off by 4 + 1.5 |x| units of 2^-24 relative to itself, s (1 - s)
+// of which reaches the sigmoid s, little more than one unit of 1; the sum and the reciprocal by three.
 __device__ __forceinline__ float sigmoid_key(float x) {
   float e, s;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
@@ -405,13 +405,13 @@ __global__ void __launch_bounds__(32 * kWarps) route(const __grid_constant__ Rou
     sum = warp_sum(sum);
   }
   const float unit = a.sigmoid ? 1.f : sum > 0.f ? 1.f / sum : 0.f;  // the largest score there may be
-  // In units of 2^-24, a softmax' score is off by 2 (expf), 1 (its argument), 2 (quotient), 1 (the product by it) and the
-  // sum of all of them, kV + 5 roundings at most; a sigmoid's by less than 12 of 1; a key by half a unit of its own more, and by
-  // the kV units that its place takes. Two keys are compared.
+  // In units of 2^-24, a softmax' score is off by 4 (expf), 1 (its argument), 2 (quotient and product) and the sum, itself by
+  // 4, 3 (the arguments) and kV + 5 roundings at most; a sigmoid's by less than 12 of 1; a key by one of its own
+  // more, and by the kV times two that its place takes. Two keys are compared.
   float off = 0.f;
   constexpr float kPart = 0x1p-23f * (1 + kV);
   if (inexact) {
-    off = 0x1p-23f * (a.sigmoid ? 12 : kV + 12) * unit;
+    off = 0x1p-23f * (a.sigmoid ? 12 : kV + 20) * unit;
     if (a.sigmoid) {
 #pragma unroll
       for (int i = 0; i < kV; ++i) s[i] = sigmoid_key(l[i]);

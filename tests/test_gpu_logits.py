@@ -41,8 +41,9 @@ def check(x, dev, dtype=None, out=None, bias=None, **kw):
     assert np.array_equal(np.isnan(g), np.isnan(want))
     assert np.array_equal(np.isinf(g), np.isinf(want)) and np.array_equal(g[np.isinf(g)], want[np.isinf(g)])
     fine = np.isfinite(want)
+    g, want, mag = g[fine], want[fine], mag[fine]
     tol = 8 * 2.0 ** -24 * mag + torch.finfo(to).eps / 2 * np.abs(want) * (1 + 2.0 ** -10) + LEAST[to]
-    assert (np.abs(g - want)[fine] <= tol[fine]).all()
+    assert (np.abs(g - want) <= tol).all()
     return got
 
 
@@ -141,6 +142,31 @@ def test_a_token_a_million_times(cuda_device):
     kw = dict(history=h, lengths=np.array([n]), frequency=np.array([1e-3]), presence=np.array([0.5]))
     got = check(make(1, 5000, FP32, cuda_device, 7), cuda_device, **kw)
     assert float(got[0, 1234]) < -1000
+
+
+@pytest.mark.parametrize("columns", [32767, 32768, 32770])
+@pytest.mark.parametrize("prompt", [0, 5, 32767])
+def test_as_many_tokens_as_a_word_counts(columns, prompt, cuda_device):
+    """Histories up to the longest that a count of 15 bits beside the prompt's bit holds, and just beyond, with a bias of
+    each token in the same words."""
+    V = 1500
+    h = np.full((2, columns), 1234, np.int32)
+    h[1] = np.arange(columns) % 3
+    kw = dict(history=h, lengths=np.array([columns, columns - 1]), prompt_lengths=np.array([prompt, prompt]),
+              repetition=np.array([1.25, 0.5]), frequency=np.array([1e-3, 2e-3]), presence=np.array([0.5, -0.25]),
+              bias=(np.array([0, V, 2 * V]), np.tile(np.arange(V), 2), np.linspace(-1, 1, 2 * V)))
+    check(make(2, V, FP32, cuda_device, 11), cuda_device, **kw)
+
+
+@pytest.mark.parametrize("n", [65535, 65536, 70001])
+def test_as_many_biases_as_a_word_counts(n, cuda_device):
+    r = np.random.RandomState(n)
+    V = 9000
+    ids = r.randint(0, V, n)
+    ids[-1] = 4321
+    kw = request(1, V, 100, 12)
+    kw["bias"] = (np.array([0, n]), ids, r.standard_normal(n))
+    check(make(1, V, FP32, cuda_device, 12), cuda_device, **kw)
 
 
 def test_temperatures(cuda_device):
