@@ -7,12 +7,12 @@
 //
 // A thread takes eight elements at a time, of 16 aligned bytes (32 in FP32). Where H is a multiple of eight and all is
 // aligned, four neighbouring lanes hold a block of 32, whose largest magnitude is two shuffles away. Where rows begin
-// anywhere but all tensors alike (odd H), the eights begin at the aligned place before the row, and the first and the
-// last of them are taken element by element. What is left (tensors of unlike alignment, MXFP8 of unaligned rows) is taken one element
+// anywhere but all tensors alike (odd H), the eights begin at the first aligned place, and the up to 14 elements around them
+// are taken by a lane each. What is left (tensors of unlike alignment, MXFP8 of unaligned rows) is taken one element
 // to a lane, so that a warp's access stays contiguous, and a block is a warp.
 // Measured (BF16, with residual): 16384 x 2048 41.5 us, 6.5 TB/s, 0.95 of the copy rate; 2048 x 16384 50.7 us (0.78: few CTAs
-// of many warps that wait for each other); 16376 x 2049 63 us (0.63: the weights are then taken one by one); into
-// MXFP8 42.7 us (0.81). Without residual 32 heads of 128 of 8192 tokens 23.3 us (0.85), 8192 x 4096 30 us (0.66: half as
+// of many warps that wait for each other); 16376 x 2049 45.3 us (0.87: the weights are then taken one by one, 3.7 us of
+// it), 100,764 x 333 53.8 (0.73); into MXFP8 42.7 us (0.81). Without residual 32 heads of 128 of 8192 tokens 23.3 us (0.85), 8192 x 4096 30 us (0.66: half as
 // much on its way). One row of 2048: 1.6 us. Tried: groups of rows after each other in a CTA that stays (registers for two,
 // 10 to 50 % slower), CTAs of 1024 threads (2048 x 16384 64.8), eight to sixteen eights in one warp (51.8 for 8192 x 2048 of FP32).
 #include <float.h>
@@ -65,29 +65,6 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   return warp_sum(lane < (int)(blockDim.x >> 5) ? part[lane] : 0.f);
 }
 
-// Eights of a row of H elements: elements j .. j + 7, of which those count that are in the row.
-template <typename T, Mode kMode>
-__device__ __forceinline__ Eight<T> get_eight(const T* row, int j, int H) {
-  Eight<T> x;
-  if (kMode == kAligned || (j >= 0 && j + 8 <= H)) {
-    x = *reinterpret_cast<const Eight<T>*>(row + j);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x.v[k] = j + k >= 0 && j + k < H ? row[j + k] : T(0.f);
-  }
-  return x;
-}
-template <typename T, Mode kMode>
-__device__ __forceinline__ void put_eight(T* row, int j, int H, const float (&f)[8]) {
-  if (kMode == kAligned || (j >= 0 && j + 8 <= H)) {
-    *reinterpret_cast<Eight<T>*>(row + j) = narrow<T>(f);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (j + k >= 0 && j + k < H) narrow_to(row + j + k, f[k]);
-  }
-}
-
 // Rows of kTpr lanes (0: a CTA), kPer eights to a thread.
 template <typename T, int kTpr, int kPer, Mode kMode>
 __global__ void __launch_bounds__(kTpr ? kThreads : 512) rms_norm(const NormArgs a) {
@@ -105,25 +82,33 @@ __global__ void __launch_bounds__(kTpr ? kThreads : 512) rms_norm(const NormArgs
   const T* res = static_cast<const T*>(a.residual) + token * a.residual_token + head * a.residual_head;
   const long long at = row * a.H;
   constexpr int kUnit = 16 / sizeof(T);
-  const int lead = kMode == kShifted ? (int)(reinterpret_cast<uintptr_t>(x) / sizeof(T) % kUnit) : 0;
+  // kShifted: the eights' elements are [begin, stop), and lane t has loose element `loose` of those around them
+  const int begin =
+      kMode == kShifted ? min(a.H, (int)((kUnit - reinterpret_cast<uintptr_t>(x) / sizeof(T) % kUnit) % kUnit)) : 0;
+  const int stop = kMode == kShifted ? begin + (a.H - begin) / 8 * 8 : a.H;
+  const int loose = t < begin ? t : stop + t - begin;
+  const bool loosed = kMode == kShifted && live && loose < a.H;
   // the first element of eight i, or single element (i, k)
-  const auto eight = [&](int i) { return 8 * (i * tpr + t) - lead; };
+  const auto eight = [&](int i) { return begin + 8 * (i * tpr + t); };
   const auto single = [&](int i, int k) { return (8 * i + k) * tpr + t; };
-  float r[kPer][8];
+  float r[kPer][8], rl = 0.f;
   float sum = 0.f;
   if constexpr (kMode != kSingle) {
     Eight<T> in[kPer], more[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (live && eight(i) < a.H) in[i] = get_eight<T, kMode>(x, eight(i), a.H);
+      if (live && eight(i) < stop) in[i] = *reinterpret_cast<const Eight<T>*>(x + eight(i));
+    if (loosed) rl = widen(x[loose]);
     if (a.residual) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if (live && eight(i) < a.H) more[i] = get_eight<T, kMode>(res, eight(i), a.H);
+        if (live && eight(i) < stop) more[i] = *reinterpret_cast<const Eight<T>*>(res + eight(i));
+      if (loosed) rl += widen(res[loose]);
     }
+    sum = rl * rl;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const bool here = live && eight(i) < a.H;
+      const bool here = live && eight(i) < stop;
       if (here) Widen<T>::run(in[i], r[i]);
       if (here && a.residual) {
         float f[8];
@@ -157,20 +142,22 @@ __global__ void __launch_bounds__(kTpr ? kThreads : 512) rms_norm(const NormArgs
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       if constexpr (kMode != kSingle) {
-        if (live && eight(i) < a.H) put_eight<T, kMode>(to, eight(i), a.H, r[i]);
+        if (live && eight(i) < stop) *reinterpret_cast<Eight<T>*>(to + eight(i)) = narrow<T>(r[i]);
       } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (live && single(i, k) < a.H) narrow_to(to + single(i, k), r[i][k]);
       }
     }
+    if (loosed) narrow_to(to + loose, rl);
   }
   float rstd = rsqrtf(sum / a.H + a.eps);
   // Squares beyond FP32: once more with r 2^-72 (2^128 2^-72 squared, 2^14 times, is below 2^127); eps is
   // then below the last bit. A row that holds what is not finite comes out as NaN.
   const bool beyond = !(sum <= FLT_MAX);
   if (kTpr && kTpr < 32 ? __any_sync(0xFFFFFFFFu, beyond) : beyond) {
-    float small = 0.f;
+    if (beyond) rl *= 0x1p-72f;
+    float small = rl * rl;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
 #pragma unroll
@@ -185,12 +172,12 @@ __global__ void __launch_bounds__(kTpr ? kThreads : 512) rms_norm(const NormArgs
   for (int i = 0; i < kPer; ++i) {
     if constexpr (kMode != kSingle) {
       const int j = eight(i);
-      const bool here = live && j < a.H;
+      const bool here = live && j < stop;
       float w[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) w[k] = 1.f;
       if (here && a.weight) {
-        if (kMode == kAligned || (lead == 0 && j + 8 <= a.H && a.weight_aligned)) {
+        if (kMode == kAligned || (begin == 0 && a.weight_aligned)) {
           if (a.weight_fp32)
             Widen<float>::run(*reinterpret_cast<const Eight<float>*>(static_cast<const float*>(a.weight) + j), w);
           else
@@ -198,14 +185,13 @@ __global__ void __launch_bounds__(kTpr ? kThreads : 512) rms_norm(const NormArgs
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            if (j + k >= 0 && j + k < a.H)
-              w[k] = a.weight_fp32 ? static_cast<const float*>(a.weight)[j + k]
-                                   : widen(static_cast<const T*>(a.weight)[j + k]);
+            w[k] = a.weight_fp32 ? static_cast<const float*>(a.weight)[j + k]
+                                 : widen(static_cast<const T*>(a.weight)[j + k]);
         }
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) r[i][k] = r[i][k] * rstd * w[k];
-      if (a.y && here) put_eight<T, kMode>(static_cast<T*>(a.y) + at, j, a.H, r[i]);
+      if (a.y && here) *reinterpret_cast<Eight<T>*>(static_cast<T*>(a.y) + at + j) = narrow<T>(r[i]);
       if (kMode == kAligned && a.codes) {
         uint32_t top = 0;
 #pragma unroll
@@ -246,14 +232,22 @@ __global__ void __launch_bounds__(kTpr ? kThreads : 512) rms_norm(const NormArgs
       }
     }
   }
+  if (loosed && a.y) {
+    float w = 1.f;
+    if (a.weight)
+      w = a.weight_fp32 ? static_cast<const float*>(a.weight)[loose] : widen(static_cast<const T*>(a.weight)[loose]);
+    narrow_to(static_cast<T*>(a.y) + at + loose, rl * rstd * w);
+  }
 }
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+int eights_of(int H, Mode mode) { return mode == kShifted ? (H / 8 ? H / 8 : 1) : (H + 7) / 8; }
+
 template <typename T, int kTpr, int kPer, Mode kMode>
 cudaError_t run(const NormArgs& a, cudaStream_t s) {
   const int rows = kTpr ? kThreads / (kTpr ? kTpr : 1) : 1;  // of a CTA
-  const int eights = (a.H + (kMode == kShifted ? 14 : 7)) / 8;
+  const int eights = eights_of(a.H, kMode);
   const int threads = kTpr ? kThreads : ((eights + kPer - 1) / kPer + 31) / 32 * 32;
   return launch_dependent(rms_norm<T, kTpr, kPer, kMode>, (int)(((long long)a.rows + rows - 1) / rows), threads, 0, s, a);
 }
@@ -266,7 +260,7 @@ cudaError_t run(const NormArgs& a, cudaStream_t s) {
 // anywhere: 85.9 against 55.4 for 22369 x 1500).
 template <typename T, Mode kMode>
 cudaError_t run_mode(const NormArgs& a, cudaStream_t s) {
-  const int eights = (a.H + (kMode == kShifted ? 14 : 7)) / 8;
+  const int eights = eights_of(a.H, kMode);
   const bool many = a.rows >= 152 * 8;
   if constexpr (kMode == kAligned) {
     if (!a.residual && a.rows >= 152 * 64) {
@@ -275,9 +269,11 @@ cudaError_t run_mode(const NormArgs& a, cudaStream_t s) {
       if (eights > 16 && eights <= 32) return run<T, 16, 2, kMode>(a, s);
     }
   }
-  if constexpr (kMode != kSingle) {
+  if constexpr (kMode == kAligned) {
     if (eights <= 8) return run<T, 8, 1, kMode>(a, s);
-    if (eights <= 16) return run<T, 16, 1, kMode>(a, s);
+  }
+  if constexpr (kMode != kSingle) {
+    if (eights <= 16) return run<T, 16, 1, kMode>(a, s);  // (as many lanes as there may be loose elements)
     if (eights <= 32) return run<T, 32, 1, kMode>(a, s);
   }
   if (eights <= 64) return run<T, 32, 2, kMode>(a, s);
@@ -290,7 +286,7 @@ cudaError_t run_mode(const NormArgs& a, cudaStream_t s) {
   if (kMode == kAligned && sizeof(T) == 2 && many) return run<T, 0, 4, kMode>(a, s);
   if (eights <= 512 && !many) return run<T, 0, 1, kMode>(a, s);
   if (eights <= 1024) return run<T, 0, 2, kMode>(a, s);
-  return run<T, 0, kMode == kShifted ? 5 : 4, kMode>(a, s);
+  return run<T, 0, 4, kMode>(a, s);
 }
 
 template <typename T>
