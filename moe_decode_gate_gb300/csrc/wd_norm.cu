@@ -92,9 +92,16 @@ __global__ void __launch_bounds__(kTpr ? kThreads : 512) rms_norm(const NormArgs
   const auto eight = [&](int i) { return begin + 8 * (i * tpr + t); };
   const auto single = [&](int i, int k) { return (8 * i + k) * tpr + t; };
   float r[kPer][8], rl = 0.f;
+  // A thread with one eight asks for its weights with the row (one row of 2048 1.6 -> 1.5 us, 200 of 4096 to MXFP8 2.7 -> 2.5);
+  // with more, their registers cost more than the wait (2048 x 16384 50.7 -> 62 us).
+  constexpr bool kEarly = kMode == kAligned && kPer == 1;
+  const bool early = kEarly && a.weight && !a.weight_fp32;
+  Eight<T> wt[1];
   float sum = 0.f;
   if constexpr (kMode != kSingle) {
     Eight<T> in[kPer], more[kPer];
+    if (early && live && eight(0) < stop)
+      wt[0] = *reinterpret_cast<const Eight<T>*>(static_cast<const T*>(a.weight) + eight(0));
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       if (live && eight(i) < stop) in[i] = *reinterpret_cast<const Eight<T>*>(x + eight(i));
@@ -180,6 +187,8 @@ __global__ void __launch_bounds__(kTpr ? kThreads : 512) rms_norm(const NormArgs
         if (kMode == kAligned || (begin == 0 && a.weight_aligned)) {
           if (a.weight_fp32)
             Widen<float>::run(*reinterpret_cast<const Eight<float>*>(static_cast<const float*>(a.weight) + j), w);
+          else if (early)
+            Widen<T>::run(wt[0], w);
           else
             Widen<T>::run(*reinterpret_cast<const Eight<T>*>(static_cast<const T*>(a.weight) + j), w);
         } else {
