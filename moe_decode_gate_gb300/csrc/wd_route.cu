@@ -77,14 +77,16 @@ struct Span {
 struct Lanes {
   int shift;      // log2 of per_group
   int per_group;  // lanes of a group
-  int per_lane;   // experts of a lane
+  int per_lane;   // experts of a lane, a power of two; the last lanes of a group have fewer or none
   int size;       // experts of a group
+  bool packs, bias_packs;  // logits and biases of a lane that has all its experts may be loaded as vectors
 };
 Lanes lanes_of(int E, int groups) {
-  int up = 1, shift = 5;
+  int up = 1, shift = 5, per_lane = 1;
   while (up < groups) up *= 2, --shift;
   const int per_group = 32 / up, size = E / groups;
-  return Lanes{shift, per_group, (size + per_group - 1) / per_group, size};
+  while (per_lane * per_group < size) per_lane *= 2;
+  return Lanes{shift, per_group, per_lane, size, false, false};
 }
 
 // The two largest keys of a group from its lanes' two largest, in each of its lanes.
@@ -373,7 +375,7 @@ __global__ void __launch_bounds__(32 * kWarps) route(const __grid_constant__ Rou
   if (token >= a.tokens) return;
   const T* x = static_cast<const T*>(a.logits) + (long long)token * a.stride;
   float l[kV];
-  if constexpr (kVec) {  // every lane has kV experts
+  if (kVec || (lanes.packs && mine.n == kV)) {  // (kVec: every lane has kV experts)
     struct alignas(sizeof(T) * kV < 16 ? sizeof(T) * kV : 16) Pack {
       T v[kV];
     };
@@ -420,9 +422,18 @@ __global__ void __launch_bounds__(32 * kWarps) route(const __grid_constant__ Rou
       for (int i = 0; i < kV; ++i) s[i] *= unit;
     }
     if (!kWords && a.bias) {
+      if (lanes.bias_packs && (kVec || mine.n == kV)) {
+        struct alignas(4 * kV < 16 ? 4 * kV : 16) Pack {
+          float v[kV];
+        };
+        const Pack p = *reinterpret_cast<const Pack*>(a.bias + mine.first);
 #pragma unroll
-      for (int i = 0; i < kV; ++i)
-        if (kVec || i < mine.n) s[i] = fmaxf(s[i] + a.bias[mine.first + i], -INFINITY);
+        for (int i = 0; i < kV; ++i) s[i] = fmaxf(s[i] + p.v[i], -INFINITY);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kV; ++i)
+          if (i < mine.n) s[i] = fmaxf(s[i] + a.bias[mine.first + i], -INFINITY);
+      }
     }
 #pragma unroll
     for (int i = 0; i < kV; ++i) s[i] = l[i] > -INFINITY ? s[i] : -INFINITY;
@@ -558,16 +569,18 @@ __global__ void __launch_bounds__(32 * kWarps) route(const __grid_constant__ Rou
 }
 
 template <typename T, int kV>
-cudaError_t run(const RouteArgs& a, const Lanes lanes, cudaStream_t s) {
-  constexpr int kBytes = sizeof(T) * kV < 16 ? sizeof(T) * kV : 16;
-  const bool vec = lanes.per_lane == kV && a.groups * lanes.per_group == 32 && a.E == 32 * kV &&
-                   reinterpret_cast<uintptr_t>(a.logits) % kBytes == 0 && a.stride * (long long)sizeof(T) % kBytes == 0;
-  const int ctas = (a.tokens + kWarps - 1) / kWarps;
-  constexpr bool kWords = sizeof(T) == 2;
-  constexpr bool kPacks = kV <= 16;  // (1024 experts are rare enough for single loads)
+cudaError_t run(const RouteArgs& a, Lanes lanes, cudaStream_t s) {
+  constexpr int kBytes = sizeof(T) * kV < 16 ? sizeof(T) * kV : 16, kBiasBytes = 4 * kV < 16 ? 4 * kV : 16;
+  const bool one = a.groups == 1;  // (else groups begin at places of their own)
+  lanes.packs = reinterpret_cast<uintptr_t>(a.logits) % kBytes == 0 && a.stride * (long long)sizeof(T) % kBytes == 0 &&
+                (one || lanes.size * sizeof(T) % kBytes == 0);
+  lanes.bias_packs = reinterpret_cast<uintptr_t>(a.bias) % kBiasBytes == 0 && (one || lanes.size * 4 % kBiasBytes == 0);
+  // experts that fill the lanes get an instance of their own (1024 are rare enough without)
+  const bool vec = kV <= 16 && lanes.packs && a.E == 32 * kV;
+  constexpr bool kWords = sizeof(T) == 2, kPacks = kV <= 16;
   const auto kernel = kWords && !a.bias ? (vec ? route<T, kV, kPacks, kWords> : route<T, kV, false, kWords>)
                                         : (vec ? route<T, kV, kPacks, false> : route<T, kV, false, false>);
-  return launch_dependent(kernel, ctas, 32 * kWarps, 0, s, a, lanes);
+  return launch_dependent(kernel, (a.tokens + kWarps - 1) / kWarps, 32 * kWarps, 0, s, a, lanes);
 }
 
 template <typename T>
