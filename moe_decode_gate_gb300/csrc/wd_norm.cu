@@ -12,9 +12,10 @@
 // to a lane, so that a warp's access stays contiguous, and a block is a warp.
 // Measured (BF16, with residual): 16384 x 2048 41.5 us, 6.5 TB/s, 0.95 of the copy rate; 2048 x 16384 50.7 us (0.78: few CTAs
 // of many warps that wait for each other); 16376 x 2049 45.3 us (0.87: the weights are then taken one by one, 3.7 us of
-// it), 100,764 x 333 53.8 (0.73); into MXFP8 42.7 us (0.81). Without residual 32 heads of 128 of 8192 tokens 23.3 us (0.85), 8192 x 4096 30 us (0.66: half as
-// much on its way). One row of 2048: 1.6 us. Tried: groups of rows after each other in a CTA that stays (registers for two,
-// 10 to 50 % slower), CTAs of 1024 threads (2048 x 16384 64.8), eight to sixteen eights in one warp (51.8 for 8192 x 2048 of FP32).
+// it), 100,764 x 333 53.8 (0.73); 16384 x 2048 into MXFP8 43.3 us (0.80). Without residual 32 heads of 128 of 8192 tokens
+// 23.3 us (0.85), 8192 x 4096 30 us (0.66: half as much on its way). One row of 2048: 1.4 us. Tried: groups of rows after
+// each other in a CTA that stays (registers for two, 10 to 50 % slower), CTAs of 1024 threads (2048 x 16384 64.8), eight
+// eights in one warp (51.8 for 8192 x 2048 of FP32).
 #include <float.h>
 
 #include "wd_device.cuh"
@@ -266,7 +267,7 @@ cudaError_t run(const NormArgs& a, cudaStream_t s) {
 // eights where there is no residual and rows are up to 32 lanes (32 heads of 64 elements 34.4 -> 23.5 us), up to four to a warp's
 // lane for up to 1024 elements, and four beyond that (16 bits, aligned; 4096 x 8192 with residual 48.2 -> 45.6 us, 8192 x
 // 4096 without 35.5 -> 30.1) or two (FP32, whose four cost registers: 49.5 against 46.4 us for 4096 x 4096; rows that begin
-// anywhere: 85.9 against 55.4 for 22369 x 1500).
+// anywhere: 51.6 against 45.0 for 22369 x 1500, with one 47.9).
 template <typename T, Mode kMode>
 cudaError_t run_mode(const NormArgs& a, cudaStream_t s) {
   const int eights = eights_of(a.H, kMode);

@@ -16,8 +16,9 @@
 //
 // Bounded by the instructions of a token, most of them for the half-rate pipe that compares and selects, not by
 // its bytes. Measured: 16384 tokens of 128 experts, 8 of them, BF16 7.3 us (FP32 11.0); of 256 in 8 groups with a bias
-// 20.6 us; of 512 13.5 us; 32 tokens of 128 1.9 us. Tried: a warp that goes from token to token with the biases in registers
-// (20.6 -> 30.7 us of the groups then, 7.0 -> 7.8), lanes' lists moved up in registers (15.8 against 13.5 us at 512 experts).
+// 19.9 us; of 512 13.5 us, of 1000 30.9; 32 tokens of 128 1.9 us. Tried: a warp that goes from token to token with the biases
+// in registers (27 -> 30.7 us of the groups then, 7.0 -> 7.8), lanes' lists moved up in registers (15.8 against 13.5 us at 512
+// experts, the same at 128).
 #include "wd_device.cuh"
 #include "wd_step.cuh"
 #include "wd_vec.cuh"
