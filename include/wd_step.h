@@ -104,7 +104,7 @@ typedef struct wd_history {
  *
  *   1. v in the prompt or the answer:  l = l > 0 ? l * (1 / repetition[b]) : l * repetition[b]
  *   2. v n > 0 times in the answer:    l = l - (n * frequency[b] + presence[b])
- *   3. v named by the row's biases:    l = l + its value (the last one, if it is named twice)
+ *   3. v named by the row's biases:    l = l + its value (the sum of them in their order, if it is named several times)
  *   4. temperature[b] > 0:             l = l * (1 / temperature[b])
  *   5. bit v of the row's mask is 0:   l = -inf
  *

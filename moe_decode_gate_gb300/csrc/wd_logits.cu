@@ -3,17 +3,18 @@
 //
 // One pass: a CTA takes a slice of one row's vocabulary. While its first logits are on their way it counts in shared
 // memory how often the row's history names each of the slice's tokens (every CTA of a row reads the whole
-// history, which is small beside the logits and comes from L2) and notes which bias is the last for each. Then it
+// history, which is small beside the logits and comes from L2) and notes which bias is each one's. Then it
 // streams its logits through, the next ones always on their way. Nothing is written but the result, no counts
 // live from call to call, and counting whole numbers gives the same sums in any order.
 //
-// Measured (BF16 to FP32): 64 rows of 131,072 with histories of 300 to 8192, biases, masks and temperatures 16.6 us, of
+// Measured (BF16 to FP32): 64 rows of 131,072 with histories of 300 to 8192, biases, masks and temperatures 17.1 us, of
 // which the logits alone take 6.4 (50 MB, in part from L2), masks 0.5, and the histories 8: their counting and what their
 // tokens go through is half of the 540 instructions that a warp has for 16 tokens a lane. One row of 32,768
-// 2.6 us. Seven rows of 100,003 with a history of up to 32,768 11.9 us: all CTAs of a row read its history at the same time.
+// 2.8 us. Seven rows of 100,003 with a history of up to 32,768 11.9 us: all CTAs of a row read its history at the same time.
 // Tried: the CTAs of a cluster sharing the history and counting in each other's shared memory (its two barriers cost more
 // than the reading: 24.4 against 21.1 us then); one slice after the other in smaller slices (19 to 24); five CTAs to an
-// SM for four (16.8); eight accesses to the history at a time (13.0 for the long ones).
+// SM for four (no faster); eight accesses to the history at a time (13.0 for the long ones); sums and biases behind one
+// pointer that is chosen for each token (19.1 for 17.1).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -30,13 +31,17 @@ constexpr int kFour = 4;                     // elements of an access
 constexpr int kUnit = kThreads * kFour;      // tokens that the threads take with one access each
 constexpr int kCtasWanted = 4 * 152;         // for which slices are made smaller
 
-// What shared memory has of a token. Narrow: one word, the bias in its upper half (1 + its index in the row, 0: none), below
-// it a bit for the prompt and 15 for the count. Wide, for longer histories or more biases: a word for each, in two arrays.
-constexpr int kNarrowHistory = 32767, kNarrowBiases = 65535;
+// What shared memory has of a token. Narrow: one word, in its upper half the bias (1 + its index in the row, 0: none), below it
+// a bit for the prompt and 15 for the count. Wide, for longer histories or more biases: a word for each half, in two
+// arrays. A token of several biases has the half's highest bit, and below it 1 + the place of their sum, or ones if the places
+// are all taken.
+constexpr int kNarrowHistory = 32767, kNarrowBiases = 32767;
+constexpr int kSums = 512;
 template <bool kWide>
 struct Layout {
   static constexpr uint32_t kPrompt = kWide ? 1u << 31 : 1u << 15;
   static constexpr int kBiasShift = kWide ? 0 : 16;
+  static constexpr uint32_t kSeveral = kWide ? 1u << 31 : 1u << 15;  // above the bias
 };
 
 // Four elements as whole words: as elements of 16 bits the compiler takes them apart and puts them together again.
@@ -130,7 +135,42 @@ struct Row {
   const float* bias;    // the values of the row's biases
 };
 
-// A logit with its token's prompt bit and count, and 1 + its last bias.
+// The sum of row b's biases of a token, in the order in which they stand.
+__device__ __forceinline__ float sum_of_biases(const LogitsArgs& a, int b, int token) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (int i = a.bias_start[b], to = a.bias_start[b + 1]; i < to; ++i)
+    if (a.bias_ids[i] == token) sum += a.bias_values[i];
+  return sum;
+}
+
+// The same for a token of each lane of a warp. A lane reads every 32nd bias and hands it to the others: for 300 biases that
+// takes 4 us where lanes that read them all took 11.
+__device__ __forceinline__ float sums_of_biases(const LogitsArgs& a, int from, int to, int token) {
+  float sum = 0.f;
+  int id = -1;
+  float value = 0.f;
+  const auto ask = [&](int i) {
+    id = i < to ? a.bias_ids[i] : -1;
+    value = i < to ? a.bias_values[i] : 0.f;
+  };
+  ask(from + (int)(threadIdx.x & 31));
+#pragma unroll 1
+  for (int at = from; at < to; at += 32) {
+    const int ids = id;
+    const float values = value;
+    if (to - at > 32) ask(at + 32 + (int)(threadIdx.x & 31));
+#pragma unroll 8
+    for (int k = 0; k < 32; ++k) {
+      const int other = __shfl_sync(~0u, ids, k);
+      const float its = __shfl_sync(~0u, values, k);
+      sum = other == token ? sum + its : sum;
+    }
+  }
+  return sum;
+}
+
+// The logit of a token with its prompt bit and count, and its bias unless it has several.
 template <bool kWide>
 __device__ __forceinline__ float penalised(const Row& r, float l, uint32_t count, uint32_t named) {
   if (!kWide) {
@@ -141,7 +181,7 @@ __device__ __forceinline__ float penalised(const Row& r, float l, uint32_t count
   const uint32_t n = count & (Layout<kWide>::kPrompt - 1);
   const float less = n ? fmaf((float)n, r.frequency, r.presence) : 0.f;
   l = count ? turned - less : l;
-  return named ? l + r.bias[named - 1] : l;
+  return named - 1 < Layout<kWide>::kSeveral - 1 ? l + r.bias[named - 1] : l;
 }
 
 // Tokens `first` .. `first` + 3 of a history of `columns`; -1 behind its end.
@@ -168,10 +208,6 @@ __device__ __forceinline__ void add(uint32_t words, uint32_t at, int n) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.lo.u32 p, %1, %2;\n\t@p red.shared.add.u32 [%0], 1;\n\t}"
                :: "r"(words + 4 * at), "r"(at), "r"(n) : "memory");
 }
-__device__ __forceinline__ void raise(uint32_t words, uint32_t at, int n, uint32_t to) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.lo.u32 p, %1, %2;\n\t@p red.shared.max.u32 [%0], %3;\n\t}"
-               :: "r"(words + 4 * at), "r"(at), "r"(n), "r"(to) : "memory");
-}
 
 // Slice blockIdx.x of row blockIdx.y: `chunks` times kPer fours of tokens to a thread. kVec: input and output of a row reach
 // the alignment of four elements at the same token; slices begin there. The first one has what is
@@ -180,7 +216,12 @@ template <typename T, typename U, int kPer, bool kVec, bool kWide>
 __global__ void __launch_bounds__(kThreads, 4) adjust_logits(const LogitsArgs a, int chunks) {
   constexpr int kChunk = kPer * kUnit;
   constexpr int kBatch = 4;  // accesses of a thread to the history that are on their way at a time
+  constexpr uint32_t kSeveral = Layout<kWide>::kSeveral << Layout<kWide>::kBiasShift;
+  static_assert(kSeveral == 1u << 31, "the highest bit of its word");
+  constexpr uint32_t kIndex = kSeveral - (1u << Layout<kWide>::kBiasShift);  // the bits of an index
   extern __shared__ uint4 shared[];
+  __shared__ float sums[kSums];  // of the slice's tokens of several biases
+  __shared__ int places_taken;
   const int slice = chunks * kChunk, places = slice + 2 * kFour;  // place 4 of an array is the slice's first four
   const int b = blockIdx.y, part = blockIdx.x;
   const T* in = static_cast<const T*>(a.logits) + b * a.stride;
@@ -272,16 +313,40 @@ __global__ void __launch_bounds__(kThreads, 4) adjust_logits(const LogitsArgs a,
     if (bias_from + (int)threadIdx.x < bias_to) id = a.bias_ids[bias_from + threadIdx.x];
     const int fours = places / kFour * (kWide ? 2 : 1);
     for (int i = threadIdx.x; i < fours; i += kThreads) shared[i] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x == 0) places_taken = 0;
     __syncthreads();
+    uint32_t* named = reinterpret_cast<uint32_t*>(shared) + kFour - before + (kWide ? places : 0);
+    const auto add_up = [&] {  // the biases of the tokens that have several, all of which are noted
+      const int several = min(places_taken, kSums);
+      if (!several) return;
+      for (int first = threadIdx.x & ~31; first < several; first += kThreads) {  // whole warps
+        const int i = first + (threadIdx.x & 31);
+        const int token = i < several ? __float_as_int(sums[i]) : -1;
+        const float sum = sums_of_biases(a, bias_from, bias_to, token);
+        if (i < several) {
+          named[token - from] = kSeveral | (uint32_t)(i + 1) << Layout<kWide>::kBiasShift;
+          sums[i] = sum;
+        }
+      }
+      __syncthreads();
+    };
     if (biases) {
       for (int i = threadIdx.x;;) {
-        raise(words + (kWide ? 4 * places : 0), (uint32_t)id - (uint32_t)from, id < 0 ? 0 : n,
-              (uint32_t)(i + 1) << Layout<kWide>::kBiasShift);
+        const uint32_t at = (uint32_t)id - (uint32_t)from;
+        if (id >= 0 && at < (uint32_t)n && atomicMax(&named[at], (uint32_t)(i + 1) << Layout<kWide>::kBiasShift) &&
+            !(atomicOr(&named[at], kSeveral) & kSeveral)) {  // the second one of its token
+          const int place = atomicAdd(&places_taken, 1);
+          if (place < kSums) sums[place] = __int_as_float(id);
+          else atomicOr(&named[at], kIndex);
+        }
         i += kThreads;
         if (bias_from + i >= bias_to) break;
         id = a.bias_ids[bias_from + i];
       }
-      if (!kWide) __syncthreads();  // before the lower halves change
+      if (!kWide) {  // before the lower halves change
+        __syncthreads();
+        add_up();
+      }
     }
     for (int base = 0; base < length;) {
 #pragma unroll
@@ -308,11 +373,15 @@ __global__ void __launch_bounds__(kThreads, 4) adjust_logits(const LogitsArgs a,
       if (base < length) ask(base);
     }
     __syncthreads();
+    if (kWide && biases) add_up();
   }
   r.scale = t > 0.f ? 1.f / t : 1.f;
   r.relief = 1.f / r.repetition;
+  const bool repeats = biases && places_taken > 0;
+  const bool too_many = repeats && places_taken > kSums;  // the whole slice is taken like loose tokens
+  const auto sum_of = [&](uint32_t its) { return its & kSeveral ? sums[((its & kIndex) >> Layout<kWide>::kBiasShift) - 1] : 0.f; };
   const uint4* noted = shared + 1 + threadIdx.x;
-  for (int at = begin; at < end; at += kChunk, noted += kPer * kThreads) {
+  for (int at = too_many ? end : begin; at < end; at += kChunk, noted += kPer * kThreads) {
     const Chunk c = next;
     if (at + kChunk < end) next = fetch(at + kChunk);
     const int mine = at + kFour * threadIdx.x;
@@ -330,6 +399,13 @@ __global__ void __launch_bounds__(kThreads, 4) adjust_logits(const LogitsArgs a,
           l[1] = penalised<kWide>(r, l[1], w.y, e.y);
           l[2] = penalised<kWide>(r, l[2], w.z, e.z);
           l[3] = penalised<kWide>(r, l[3], w.w, e.w);
+          if (repeats) {
+            if (!kWide) e = w;
+            l[0] += sum_of(e.x);
+            l[1] += sum_of(e.y);
+            l[2] += sum_of(e.z);
+            l[3] += sum_of(e.w);
+          }
         }
       }
 #pragma unroll
@@ -343,11 +419,16 @@ __global__ void __launch_bounds__(kThreads, 4) adjust_logits(const LogitsArgs a,
     }
   }
   // the loose tokens, at most three before the first four and three behind the last
-  if ((int)threadIdx.x < before + behind) {
-    const int v = (int)threadIdx.x < before ? threadIdx.x : last + threadIdx.x - before;
+  const int loose = before + behind + (too_many ? max(0, end - begin) : 0);
+  for (int i = threadIdx.x; i < loose; i += kThreads) {
+    const int v = too_many ? begin - before + i : i < before ? i : last + i - before;
     const uint32_t* word = reinterpret_cast<const uint32_t*>(shared) + kFour + v - begin;
     float l = get(in + v);
-    if (counts || biases) l = penalised<kWide>(r, l, word[0], kWide ? word[places] : 0u);
+    if (counts || biases) {
+      const uint32_t named = word[kWide ? places : 0];
+      l = penalised<kWide>(r, l, word[0], named);
+      if (named & kSeveral) l += (named & kIndex) == kIndex ? sum_of_biases(a, b, v) : sum_of(named);
+    }
     put(&out[v], !mask || (mask[v >> 5] >> (v & 31) & 1) ? l * r.scale : -INFINITY);
   }
 }

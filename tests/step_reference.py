@@ -104,11 +104,10 @@ def adjust_logits(x, history=None, lengths=None, prompt_lengths=None, seqs=None,
                 start, ids, values = bias
                 lo, hi = int(start[b]), int(start[b + 1])
                 if 0 <= lo <= hi <= len(ids):
-                    last = {int(v): float(z) for v, z in zip(ids[lo:hi], values[lo:hi])}
-                    for v, z in last.items():
+                    for v, z in zip(ids[lo:hi], values[lo:hi]):
                         if 0 <= v < V:
-                            l[v] += z
-                            m[v] += abs(z)
+                            l[v] += float(z)
+                            m[v] += abs(float(z))
             if temperature is not None and temperature[b] > 0:
                 l /= temperature[b]
                 m /= temperature[b]

@@ -2,7 +2,7 @@
 
 Tolerance: each of the steps is one or two FP32 roundings of what is summed up to then (quotient, product and sum of
 the penalties, their difference, the bias' sum, the temperature's reciprocal and product), 8 2^-24 of the magnitudes in
-all, and one rounding to the output's type.
+all, one more for each further bias of the same token, and one rounding to the output's type.
 """
 import numpy as np
 import pytest
@@ -42,7 +42,12 @@ def check(x, dev, dtype=None, out=None, bias=None, **kw):
     assert np.array_equal(np.isinf(g), np.isinf(want)) and np.array_equal(g[np.isinf(g)], want[np.isinf(g)])
     fine = np.isfinite(want)
     g, want, mag = g[fine], want[fine], mag[fine]
-    tol = 8 * 2.0 ** -24 * mag + torch.finfo(to).eps / 2 * np.abs(want) * (1 + 2.0 ** -10) + LEAST[to]
+    further = 0
+    if bias is not None:
+        start, ids = np.asarray(bias[0]), np.asarray(bias[1])
+        rows = [ids[max(0, lo):max(0, hi)] for lo, hi in zip(start[:-1], start[1:])]
+        further = max([int(np.unique(i, return_counts=True)[1].max()) - 1 for i in rows if i.size], default=0)
+    tol = (8 + further) * 2.0 ** -24 * mag + torch.finfo(to).eps / 2 * np.abs(want) * (1 + 2.0 ** -10) + LEAST[to]
     assert (np.abs(g - want) <= tol).all()
     return got
 
@@ -127,11 +132,38 @@ def test_what_is_out_of_range_counts_for_nothing(cuda_device):
     check(make(6, V, BF16, cuda_device, 5), cuda_device, dtype=FP32, **{**kw, "bias": (start, ids, values)})
 
 
-def test_a_token_named_twice_gets_the_last_bias(cuda_device):
-    r = np.random.RandomState(6)
-    ids = np.concatenate((np.full(500, 77), r.randint(0, 100, 3000), np.full(3, 4000)))
-    values = r.standard_normal(ids.size)
-    check(make(1, 4001, FP32, cuda_device, 6), cuda_device, bias=(np.array([0, ids.size]), ids, values))
+@pytest.mark.parametrize("columns", [10, 40000])
+@pytest.mark.parametrize("B,V", [(1, 203), (3, 9001), (80, 16411)])
+@pytest.mark.parametrize("times", [2, 3, 50])
+def test_biases_of_a_token_add_up(times, B, V, columns, cuda_device):
+    """In their order, the same from run to run; for histories of both kinds and slices of all sizes."""
+    r = np.random.RandomState(times)
+    rows = []
+    for b in range(B):
+        ids = np.concatenate((np.full(times, 77 + b), np.full(3, V - 1), np.zeros(2), r.randint(0, V, 40), [-1, -1, V]))
+        rows.append(r.permutation(ids).astype(np.int32))
+    start, ids = rows[0].size * np.arange(B + 1), np.concatenate(rows)
+    kw = request(B, V, columns, 6)
+    kw["bias"] = (start, ids, 100 * r.standard_normal(ids.size))
+    x = make(B, V, FP32, cuda_device, 6)
+    got = check(x, cuda_device, **kw)
+    for _ in range(3):
+        assert torch.equal(check(x, cuda_device, **kw), got)
+    wide = torch.empty((B, V + 3), device=cuda_device)[:, 1:V + 1]  # rows that reach an alignment elsewhere than the input's
+    assert torch.equal(check(x, cuda_device, out=wide, **kw), got)
+
+
+@pytest.mark.parametrize("columns", [10, 40000])
+def test_many_tokens_of_several_biases(columns, cuda_device):
+    """More than a CTA keeps the sums of, in large slices and with small ones."""
+    r = np.random.RandomState(15)
+    for B, V, tokens in ((608, 8192, 1300), (1, 1024, 1024), (2, 1500, 1100)):
+        ids = r.permutation(np.concatenate((r.permutation(V)[:tokens], r.permutation(V)[:tokens], r.permutation(V)[:tokens])))
+        kw = request(B, V, columns, 16)
+        kw["bias"] = (ids.size * (np.arange(B + 1) > B // 2), ids, 10 * r.standard_normal(ids.size))
+        x = make(B, V, FP32, cuda_device, 17)
+        got = check(x, cuda_device, **kw)
+        assert torch.equal(check(x, cuda_device, **kw), got)
 
 
 def test_a_token_a_million_times(cuda_device):
@@ -158,12 +190,12 @@ def test_as_many_tokens_as_a_word_counts(columns, prompt, cuda_device):
     check(make(2, V, FP32, cuda_device, 11), cuda_device, **kw)
 
 
-@pytest.mark.parametrize("n", [65535, 65536, 70001])
+@pytest.mark.parametrize("n", [32767, 32768, 70001])
 def test_as_many_biases_as_a_word_counts(n, cuda_device):
     r = np.random.RandomState(n)
-    V = 9000
-    ids = r.randint(0, V, n)
-    ids[-1] = 4321
+    V = 80000
+    ids = r.permutation(V)[:n]
+    ids[-3:] = ids[0]  # and one token four times
     kw = request(1, V, 100, 12)
     kw["bias"] = (np.array([0, n]), ids, r.standard_normal(n))
     check(make(1, V, FP32, cuda_device, 12), cuda_device, **kw)
