@@ -7,14 +7,14 @@
 // streams its logits through, the next ones always on their way. Nothing is written but the result, no counts
 // live from call to call, and counting whole numbers gives the same sums in any order.
 //
-// Measured (BF16 to FP32): 64 rows of 131,072 with histories of 300 to 8192, biases, masks and temperatures 17.1 us, of
+// Measured (BF16 to FP32): 64 rows of 131,072 with histories of 300 to 8192, biases, masks and temperatures 16.9 us, of
 // which the logits alone take 6.4 (50 MB, in part from L2), masks 0.5, and the histories 8: their counting and what their
 // tokens go through is half of the 540 instructions that a warp has for 16 tokens a lane. One row of 32,768
 // 2.8 us. Seven rows of 100,003 with a history of up to 32,768 11.9 us: all CTAs of a row read its history at the same time.
 // Tried: the CTAs of a cluster sharing the history and counting in each other's shared memory (its two barriers cost more
 // than the reading: 24.4 against 21.1 us then); one slice after the other in smaller slices (19 to 24); five CTAs to an
 // SM for four (no faster); eight accesses to the history at a time (13.0 for the long ones); sums and biases behind one
-// pointer that is chosen for each token (19.1 for 17.1).
+// pointer that is chosen for each token (19.1).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -181,7 +181,7 @@ __device__ __forceinline__ float penalised(const Row& r, float l, uint32_t count
   const uint32_t n = count & (Layout<kWide>::kPrompt - 1);
   const float less = n ? fmaf((float)n, r.frequency, r.presence) : 0.f;
   l = count ? turned - less : l;
-  return named - 1 < Layout<kWide>::kSeveral - 1 ? l + r.bias[named - 1] : l;
+  return named ? l + r.bias[named - 1] : l;
 }
 
 // Tokens `first` .. `first` + 3 of a history of `columns`; -1 behind its end.
@@ -377,11 +377,26 @@ __global__ void __launch_bounds__(kThreads, 4) adjust_logits(const LogitsArgs a,
   }
   r.scale = t > 0.f ? 1.f / t : 1.f;
   r.relief = 1.f / r.repetition;
-  const bool repeats = biases && places_taken > 0;
-  const bool too_many = repeats && places_taken > kSums;  // the whole slice is taken like loose tokens
-  const auto sum_of = [&](uint32_t its) { return its & kSeveral ? sums[((its & kIndex) >> Layout<kWide>::kBiasShift) - 1] : 0.f; };
+  // A slice with tokens of several biases is taken one by one: what their sums ask of registers would cost
+  // the others (64 x 131,072 FP32 13.3 against 12.3 us).
+  if (biases && places_taken) {
+    const int from = begin - before, n = max(0, end - begin) + before + behind;
+#pragma unroll 1
+    for (int v = from + threadIdx.x; v < from + n; v += kThreads) {
+      const uint32_t* word = reinterpret_cast<const uint32_t*>(shared) + kFour + v - begin;
+      const uint32_t named = word[kWide ? places : 0], place = named & kIndex;
+      float l = get(in + v);
+      if (named & kSeveral)
+        l = penalised<kWide>(r, l, kWide ? word[0] : word[0] & 0xFFFFu, 0u) +
+            (place == kIndex ? sum_of_biases(a, b, v) : sums[(place >> Layout<kWide>::kBiasShift) - 1]);
+      else
+        l = penalised<kWide>(r, l, word[0], named);
+      put(&out[v], !mask || (mask[v >> 5] >> (v & 31) & 1) ? l * r.scale : -INFINITY);
+    }
+    return;
+  }
   const uint4* noted = shared + 1 + threadIdx.x;
-  for (int at = too_many ? end : begin; at < end; at += kChunk, noted += kPer * kThreads) {
+  for (int at = begin; at < end; at += kChunk, noted += kPer * kThreads) {
     const Chunk c = next;
     if (at + kChunk < end) next = fetch(at + kChunk);
     const int mine = at + kFour * threadIdx.x;
@@ -399,13 +414,6 @@ __global__ void __launch_bounds__(kThreads, 4) adjust_logits(const LogitsArgs a,
           l[1] = penalised<kWide>(r, l[1], w.y, e.y);
           l[2] = penalised<kWide>(r, l[2], w.z, e.z);
           l[3] = penalised<kWide>(r, l[3], w.w, e.w);
-          if (repeats) {
-            if (!kWide) e = w;
-            l[0] += sum_of(e.x);
-            l[1] += sum_of(e.y);
-            l[2] += sum_of(e.z);
-            l[3] += sum_of(e.w);
-          }
         }
       }
 #pragma unroll
@@ -419,16 +427,11 @@ __global__ void __launch_bounds__(kThreads, 4) adjust_logits(const LogitsArgs a,
     }
   }
   // the loose tokens, at most three before the first four and three behind the last
-  const int loose = before + behind + (too_many ? max(0, end - begin) : 0);
-  for (int i = threadIdx.x; i < loose; i += kThreads) {
-    const int v = too_many ? begin - before + i : i < before ? i : last + i - before;
+  if ((int)threadIdx.x < before + behind) {
+    const int v = (int)threadIdx.x < before ? threadIdx.x : last + threadIdx.x - before;
     const uint32_t* word = reinterpret_cast<const uint32_t*>(shared) + kFour + v - begin;
     float l = get(in + v);
-    if (counts || biases) {
-      const uint32_t named = word[kWide ? places : 0];
-      l = penalised<kWide>(r, l, word[0], named);
-      if (named & kSeveral) l += (named & kIndex) == kIndex ? sum_of_biases(a, b, v) : sum_of(named);
-    }
+    if (counts || biases) l = penalised<kWide>(r, l, word[0], kWide ? word[places] : 0u);
     put(&out[v], !mask || (mask[v >> 5] >> (v & 31) & 1) ? l * r.scale : -INFINITY);
   }
 }
