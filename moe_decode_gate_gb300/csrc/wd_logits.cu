@@ -150,16 +150,17 @@ __device__ __forceinline__ float sums_of_biases(const LogitsArgs& a, int from, i
   float sum = 0.f;
   int id = -1;
   float value = 0.f;
-  const auto ask = [&](int i) {
-    id = i < to ? a.bias_ids[i] : -1;
-    value = i < to ? a.bias_values[i] : 0.f;
+  const unsigned n = to - from;  // (places are counted from `from`, unsigned: those behind the last bias may pass 2^31)
+  const auto ask = [&](unsigned i) {
+    id = i < n ? a.bias_ids[from + (int)i] : -1;
+    value = i < n ? a.bias_values[from + (int)i] : 0.f;
   };
-  ask(from + (int)(threadIdx.x & 31));
+  ask(threadIdx.x & 31);
 #pragma unroll 1
-  for (int at = from; at < to; at += 32) {
+  for (unsigned at = 0; at < n; at += 32) {
     const int ids = id;
     const float values = value;
-    if (to - at > 32) ask(at + 32 + (int)(threadIdx.x & 31));
+    if (n - at > 32) ask(at + 32 + (threadIdx.x & 31));
 #pragma unroll 8
     for (int k = 0; k < 32; ++k) {
       const int other = __shfl_sync(~0u, ids, k);
@@ -278,12 +279,13 @@ __global__ void __launch_bounds__(kThreads, 4) adjust_logits(const LogitsArgs a,
   if (a.bias_start) {
     bias_from = a.bias_start[b];
     bias_to = a.bias_start[b + 1];
-    if (bias_from < 0 || bias_to > a.biases) bias_to = bias_from;
+    if (bias_from < 0 || bias_to > a.biases || bias_to < bias_from) bias_from = bias_to = 0;
   }
+  const unsigned listed = bias_to - bias_from;  // the row's biases (bias_from + a place behind them may pass 2^31)
   r.bias = a.bias_values + bias_from;
   // the row's history, if it has one and its penalties are any
   const bool penalties = r.repetition != 1.f || r.presence != 0.f || r.frequency != 0.f;
-  const bool counts = penalties && (unsigned)slot < (unsigned)a.history.slots, biases = bias_to > bias_from;
+  const bool counts = penalties && (unsigned)slot < (unsigned)a.history.slots, biases = listed > 0;
   if (counts || biases) {
     const int from = begin - before, n = max(0, end - begin) + before + behind;  // the slice's tokens
     const uint32_t words = (uint32_t)__cvta_generic_to_shared(shared) + 4 * (kFour - before);  // of token `from`
@@ -310,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 4) adjust_logits(const LogitsArgs a,
       prompt = a.history.prompt_lengths ? max(0, min(a.history.prompt_lengths[slot], length)) : 0;
     }
     int id = -1;  // this thread's first bias
-    if (bias_from + (int)threadIdx.x < bias_to) id = a.bias_ids[bias_from + threadIdx.x];
+    if (threadIdx.x < listed) id = a.bias_ids[bias_from + (int)threadIdx.x];
     const int fours = places / kFour * (kWide ? 2 : 1);
     for (int i = threadIdx.x; i < fours; i += kThreads) shared[i] = make_uint4(0, 0, 0, 0);
     if (threadIdx.x == 0) places_taken = 0;
@@ -331,17 +333,17 @@ __global__ void __launch_bounds__(kThreads, 4) adjust_logits(const LogitsArgs a,
       __syncthreads();
     };
     if (biases) {
-      for (int i = threadIdx.x;;) {
+      for (unsigned i = threadIdx.x;;) {
         const uint32_t at = (uint32_t)id - (uint32_t)from;
-        if (id >= 0 && at < (uint32_t)n && atomicMax(&named[at], (uint32_t)(i + 1) << Layout<kWide>::kBiasShift) &&
+        if (id >= 0 && at < (uint32_t)n && atomicMax(&named[at], (i + 1) << Layout<kWide>::kBiasShift) &&
             !(atomicOr(&named[at], kSeveral) & kSeveral)) {  // the second one of its token
           const int place = atomicAdd(&places_taken, 1);
           if (place < kSums) sums[place] = __int_as_float(id);
           else atomicOr(&named[at], kIndex);
         }
         i += kThreads;
-        if (bias_from + i >= bias_to) break;
-        id = a.bias_ids[bias_from + i];
+        if (i >= listed) break;
+        id = a.bias_ids[bias_from + (int)i];
       }
       if (!kWide) {  // before the lower halves change
         __syncthreads();
