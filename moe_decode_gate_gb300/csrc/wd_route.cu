@@ -207,14 +207,15 @@ __device__ __forceinline__ void take_place(Sorted<kV>& sorted, const Span& mine,
   sorted.take(take && all);
 }
 
-// Whether word b may stand before its neighbour a: the two are the same but for the place or, where keys are off by `off` and
-// `part` of themselves, nearer than that. Masked ones are like nothing else; infinite ones' words are no numbers (no
-// comparison with them is true).
+// Whether the key of word b may be before that of its neighbour a: the two words are the same but for the place or, where keys
+// are off by `off` and `part` of themselves, nearer than that. Masked ones are like nothing else, infinite ones far from all
+// that are not.
 template <int kV>
 __device__ __forceinline__ bool too_near(uint32_t a, uint32_t b, float off, float part) {
   if (!b) return false;
+  constexpr uint32_t kKey = ~(uint32_t)(kV - 1);  // without the place, which may lift b as far as a's next step
   if ((a ^ b) < (uint32_t)kV) return true;
-  const float x = value_of(a), y = value_of(b);
+  const float x = value_of(a & kKey), y = value_of(b & kKey);
   return off > 0.f && b > order_of(-INFINITY) && !(x - y >= fmaf(part, fmaxf(fabsf(x), fabsf(y)), off));
 }
 
@@ -410,7 +411,8 @@ __global__ void __launch_bounds__(32 * kWarps) route(const __grid_constant__ Rou
   const float unit = a.sigmoid ? 1.f : sum > 0.f ? 1.f / sum : 0.f;  // the largest score there may be
   // In units of 2^-24, a softmax' score is off by 4 (expf), 1 (its argument), 2 (quotient and product) and the sum, itself by
   // 4, 3 (the arguments) and kV + 5 roundings at most; a sigmoid's by less than 12 of 1; a key by one of its own
-  // more, and by the kV times two that its place takes. Two keys are compared.
+  // more, and its word, once the place is cleared, by less than 2 kV: one way, so that the difference of two
+  // words is off by 2 kV and not by twice that. Two keys are compared.
   float off = 0.f;
   constexpr float kPart = 0x1p-23f * (1 + kV);
   if (inexact) {
