@@ -74,7 +74,7 @@ wd_status wd_route(const void* logits, wd_dtype dtype, int64_t stride_token, int
   a.K = K;
   a.groups = top_groups == groups ? 1 : groups;  // all of them: no choice
   a.top_groups = top_groups == groups ? 1 : top_groups;
-  a.group_best = group_best;
+  a.group_best = E == groups ? 1 : group_best;  // of one expert: its key, which without a bias its logit orders
   a.sigmoid = scores == WD_SIGMOID;
   a.renormalise = renormalise != 0;
   a.scale = scale;
