@@ -290,7 +290,7 @@ __device__ __noinline__ void order_again(const RouteArgs& a, const T* x, const S
 }
 
 // Whether this lane's group is chosen, from the keys in 64 bits of those experts that may be the best of a group: whose
-// key is not below `least`. False in `sure` if those are more than 64. Rare, too.
+// key is not below `least` (NaN where biases are infinite: all of the group). False in `sure` if those are more than 64. Rare, too.
 template <typename T, int kV>
 __device__ __noinline__ bool groups_again(const RouteArgs& a, const T* x, const Span mine, const Lanes lanes, int lane,
                                           float top, const float (&keys)[kV], float least, uint32_t* list, bool& sure) {
@@ -298,7 +298,7 @@ __device__ __noinline__ bool groups_again(const RouteArgs& a, const T* x, const 
   int n = 0;
 #pragma unroll
   for (int i = 0; i < kV; ++i) {
-    const bool may = i < mine.n && keys[i] > -INFINITY && keys[i] >= least;
+    const bool may = i < mine.n && keys[i] > -INFINITY && !(keys[i] < least);
     const uint32_t who = __ballot_sync(kAll, may);
     const int at = n + __popc(who & ((1u << lane) - 1));
     if (may && at < 64) list[at] = mine.first + i;
@@ -460,7 +460,8 @@ __global__ void __launch_bounds__(32 * kWarps) route(const __grid_constant__ Rou
       const float out = warp_max(chosen ? -INFINITY : value);
       const float most = warp_max(fmaxf(best > -INFINITY ? fabsf(best) : 0.f, second > -INFINITY ? fabsf(second) : 0.f));
       const float margin = 2.f * fmaf(kPart, most, off);
-      if (in - out < margin) {
+      // (keys of which two may leave FP32 in a sum are always looked at again)
+      if (in - out < margin || !(most < 0x1p126f)) {
         float keys[kV];  // (their own, so that s stays in registers)
 #pragma unroll
         for (int i = 0; i < kV; ++i) keys[i] = s[i];
