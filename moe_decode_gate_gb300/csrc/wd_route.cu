@@ -556,7 +556,12 @@ __global__ void __launch_bounds__(32 * kWarps) route(const __grid_constant__ Rou
   }
   if (a.renormalise) {
     total = warp_sum(total);
-    const float f = total > 0.f ? a.scale / total : 0.f;
+    float f = total > 0.f ? a.scale / total : 0.f;
+    if (isinf(f)) {  // a large scale over a small sum
+      w[0] /= total;
+      w[1] /= total;
+      f = a.scale;
+    }
     w[0] *= f;
     w[1] *= f;
   } else {

@@ -59,3 +59,17 @@ def test_infinite_and_huge_biases_in_groups(E, groups, top, best, scores, cuda_d
     low = -np.linspace(2.9e38, 3.3e38, E)
     compare(x, 4, low, cuda_device, **kw)
     compare(x, 4, low[::-1].copy(), cuda_device, **kw)
+
+
+@pytest.mark.parametrize("scale", [1e30, 3e38, -1e35])
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalise", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_any_scale(dtype, renormalise, scores, scale, cuda_device):
+    r = np.random.RandomState(5)
+    x = torch.from_numpy(np.stack([r.standard_normal(64), r.standard_normal(64) - 37.0, r.uniform(-39, -30, 64)])).to(dtype)
+    ids, w = wd.route(x.to(cuda_device), 6, scores=scores, renormalise=renormalise, scale=scale)
+    s = float(np.float32(scale))
+    want, want_w = ref.route(x.double().numpy(), 6, scores, None, 1, 1, 2, renormalise, s)
+    assert np.array_equal(ids.cpu().numpy(), want)
+    assert (np.abs(w.double().cpu().numpy() - want_w) <= 2.0 ** -18 * np.abs(want_w) + 2.0 ** -126).all()
