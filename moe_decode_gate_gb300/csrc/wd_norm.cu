@@ -159,10 +159,11 @@ __global__ void __launch_bounds__(kTpr ? kThreads : 512) rms_norm(const NormArgs
     }
     if (loosed) narrow_to(to + loose, rl);
   }
-  float rstd = rsqrtf(sum / a.H + a.eps);
-  // Squares beyond FP32: once more with r 2^-72 (2^128 2^-72 squared, 2^14 times, is below 2^127); eps is
-  // then below the last bit. A row that holds what is not finite comes out as NaN.
-  const bool beyond = !(sum <= FLT_MAX);
+  const float mean = sum / a.H + a.eps;
+  float rstd = rsqrtf(mean);
+  // Squares, or their mean and eps, beyond FP32: once more with r 2^-72 and eps 2^-144 (2^128 2^-72 squared, 2^14
+  // times, is below 2^127). A row that holds what is not finite comes out as NaN.
+  const bool beyond = !(mean <= FLT_MAX);
   if (kTpr && kTpr < 32 ? __any_sync(0xFFFFFFFFu, beyond) : beyond) {
     if (beyond) rl *= 0x1p-72f;
     float small = rl * rl;
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kTpr ? kThreads : 512) rms_norm(const NormArgs
         small += r[i][k] * r[i][k];
       }
     small = row_sum<kTpr>(small, part[1]);
-    if (beyond) rstd = small <= FLT_MAX ? rsqrtf(small / a.H) : __uint_as_float(0x7FC00000u);
+    if (beyond) rstd = small <= FLT_MAX ? rsqrtf(fmaf(a.eps, 0x1p-144f, small / a.H)) : __uint_as_float(0x7FC00000u);
   }
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
