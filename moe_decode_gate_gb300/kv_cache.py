@@ -277,6 +277,8 @@ class KVCache:
         if k_channel != 1 or v_channel != 1:
             raise ValueError("k and v must have contiguous channels")
         tokens, turns = shape[0], cos_sin.shape
+        if tokens > 2 ** 31 - 1:  # (ctypes would cut it to its low bits)
+            raise ValueError(f"unsupported sizes: {tokens} tokens")
         if cos_sin.dtype is not torch.float32 or len(turns) != 2 or cos_sin.device != device or \
                 not cos_sin.is_contiguous():
             raise ValueError(f"cos_sin must be contiguous FP32 [positions, rot] on {device}")

@@ -16,6 +16,7 @@ from ._native import _check, lib
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _LIB = None
+_MOST = 2 ** 31 - 1  # what the library's int parameters hold: ctypes would cut a larger number to its low bits
 
 
 class _History(ctypes.Structure):
@@ -126,6 +127,8 @@ def rms_norm(x, weight=None, residual=None, *, eps=1e-6, mxfp8=False, out=None, 
         _refuse_rows("x", x, device)
     tokens, H = shape[0], shape[-1]
     token, head, heads = strides[0], strides[1] if n == 3 else 0, shape[1] if n == 3 else 1
+    if H > _MOST or heads > _MOST:
+        raise ValueError(f"unsupported sizes: {list(shape)}")
     weight_code, w = code, None
     if weight is not None:
         if weight.dtype is not dtype:
@@ -193,6 +196,8 @@ def route(logits, K, *, scores="softmax", bias=None, groups=1, top_groups=None, 
     if kind is None:
         raise ValueError(f"scores must be one of {', '.join(_SCORES)}")
     tokens, E = shape
+    if E > _MOST or K > _MOST:
+        raise ValueError(f"unsupported sizes: {K} of {E} experts")
     stride, last = logits.stride()
     if last != 1 and E != 1:
         _refuse_matrix("logits", logits, "[tokens, E]")
@@ -235,6 +240,8 @@ def adjust_logits(logits, *, history=None, lengths=None, prompt_lengths=None, se
     if code is None or device.index is None or len(shape) != 2:
         _refuse_matrix("logits", logits, "[B, V]")
     B, V = shape
+    if B > _MOST or V > _MOST:
+        raise ValueError(f"unsupported sizes: {list(shape)}")
     stride, last = logits.stride()
     if last != 1 and V != 1:
         _refuse_matrix("logits", logits, "[B, V]")
@@ -258,6 +265,8 @@ def adjust_logits(logits, *, history=None, lengths=None, prompt_lengths=None, se
         if lengths is None:
             raise ValueError("history needs lengths")
         slots, columns = history.shape
+        if slots > _MOST or columns > _MOST:
+            raise ValueError(f"unsupported sizes: a history of {list(history.shape)}")
         i32 = torch.int32
         h = _History(history.data_ptr(), _per("lengths", lengths, slots, i32, device),
                      _per("prompt_lengths", prompt_lengths, slots, i32, device), _per("seqs", seqs, B, i32, device),
@@ -273,6 +282,8 @@ def adjust_logits(logits, *, history=None, lengths=None, prompt_lengths=None, se
     if bias is not None:
         starts, tokens, amounts = bias
         n = tokens.shape[0]
+        if n > _MOST:
+            raise ValueError(f"unsupported sizes: {n} biases")
         start = _per("bias start", starts, B + 1, torch.int32, device)
         ids = _per("bias ids", tokens, n, torch.int32, device)
         values = _per("bias values", amounts, n, torch.float32, device)
