@@ -76,11 +76,13 @@ typedef enum wd_scores { WD_SOFTMAX = 0, WD_SIGMOID = 1 } wd_scores;
  * [tokens, K], contiguous.  A logit of -inf or NaN masks its expert: score 0, chosen
  * after all that are not masked whatever its bias, and without part in its group's
  * value.  Logits of +inf share the softmax among them.  Where the scores of
- * the chosen are all 0, the weights are 0.
+ * the chosen are all 0, the weights are 0.  Weights are made of FP32 scores: one below 2^-126
+ * loses bits or counts as 0 (but sigmoids that are renormalised keep theirs if all of the K are below e^-40).
  *
  * Without a bias keys are compared by their logits, which order as they do.  Where keys or
  * groups' sums have to be compared, the FP32 ones decide unless two are nearer to each other than their
  * error; that token's are then compared in 64 bits, so that ids are those of the definition.
+ * Groups of one expert and no bias go by the logits, too.
  *
  * E <= WD_ROUTE_MAX_EXPERTS, groups <= 32 divides E, a group has at most 1024 / groups
  * experts with groups rounded up to a power of two; K <= min(WD_ROUTE_MAX_K, top_groups * E / groups);
@@ -113,9 +115,10 @@ typedef struct wd_history {
  * repetition, presence, frequency, temperature: FP32 [B], each NULL to leave its step out.
  * Biases: row b's are entries bias_start[b] .. bias_start[b + 1] - 1 of bias_ids and
  * bias_values (all NULL for none; `biases` entries in all).  mask: int32 words, rows mask_stride words
- * apart, bit v % 32 of word v / 32 (NULL: all allowed).  Steps are FP32, rounded once
- * to out_dtype.  What is out of range counts for nothing: tokens and biases outside the
- * vocabulary, slots, entries of bias_start; lengths are cut to 0 .. columns. */
+ * apart, bit v % 32 of word v / 32 (NULL: all allowed).  Steps and reciprocals are FP32
+ * (1 / x of x below 2^-128 is infinite), and the result is rounded once to out_dtype.  What is out of range counts
+ * for nothing: tokens and biases outside the vocabulary, slots, a row's biases if its entries of bias_start are no
+ * range 0 <= from <= to <= biases; lengths are cut to 0 .. columns. */
 WD_API wd_status wd_adjust_logits(const void* logits, wd_dtype dtype, int64_t stride, int B, int V,
                                   const wd_history* history, const float* repetition,
                                   const float* presence, const float* frequency,

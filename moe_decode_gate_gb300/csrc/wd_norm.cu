@@ -12,8 +12,9 @@
 // to a lane, so that a warp's access stays contiguous, and a block is a warp.
 // Measured (BF16, with residual): 16384 x 2048 41.5 us, 6.5 TB/s, 0.95 of the copy rate; 2048 x 16384 50.7 us (0.78: few CTAs
 // of many warps that wait for each other); 16376 x 2049 45.3 us (0.87: the weights are then taken one by one, 3.7 us of
-// it), 100,764 x 333 53.8 (0.73); 16384 x 2048 into MXFP8 43.3 us (0.80). Without residual 32 heads of 128 of 8192 tokens
-// 23.3 us (0.85), 8192 x 4096 30 us (0.66: half as much on its way). One row of 2048: 1.4 us. Tried: groups of rows after
+// it), 100,764 x 333 53.8 (0.73); 16384 x 2048 into MXFP8 43.3 us (0.80), 2048 x 16384 52.8 (0.66). FP32 up to 4096 elements
+// 0.84 to 0.97, 1024 x 16384 62 us (0.64). Without residual 32 heads of 128 of 8192 tokens 23.3 us (0.85), 16384 x 2048 27.8
+// (0.71), 8192 x 4096 30.7 (0.64: half as much on its way), 4096 x 8192 32.8 (0.60). One row of 2048: 1.4 us. Tried: groups of rows after
 // each other in a CTA that stays (registers for two, 10 to 50 % slower), CTAs of 1024 threads (2048 x 16384 64.8), eight
 // eights in one warp (51.8 for 8192 x 2048 of FP32).
 #include <float.h>
